@@ -45,8 +45,10 @@
 extern "C" {
 #endif
 
-/* Logit element types. */
-typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
+/* Element types.  Logits are SV_F32 or SV_BF16; SV_F16 and SV_E4M3 (8-bit
+ * floating point: 4 exponent and 3 mantissa bits, largest value 448, no
+ * infinity) occur in the cache-side calls at the end of this file only. */
+typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2, SV_E4M3 = 3 } sv_dtype;
 
 /* Host-side return codes. */
 typedef enum {
@@ -68,6 +70,8 @@ typedef enum {
 #define SV_FLAG_BOUNDS 64u           /* bounds-checked builds (SV_DEBUG_BOUNDS) only: a
                                         kernel formed an index outside its buffer; the
                                         access was skipped and the outputs are invalid */
+#define SV_FLAG_INVALID_PAGE 128u    /* a page table entry that a call needed was outside
+                                        [0, num_pages) */
 
 /*
  * Bytes of workspace that calls with these sizes need (any mode, any dtype).
@@ -392,6 +396,194 @@ int spec_verify_greedy_noalloc(const void *target_logits, int t_dtype, int64_t t
  */
 int spec_verify_greedy_noalloc_read_device_status(uint32_t *flags_host, int clear,
                                                   void *stream);
+
+/* ======================================================================
+ * The cache side of a decoding step
+ *
+ * "Accelerating Sonar through speculation", section "Speculative decoding":
+ * one target forward scores all drafted tokens at once.  The calls below are
+ * the parts of that forward which depend on the draft's shape: rotary
+ * positions, the write of the drafted tokens' keys and values into a paged
+ * cache, attention of the drafted tokens (a chain, or a tree given by
+ * `parent` as for spec_verify_tree_greedy) over the cache, and, after
+ * verification, the move of the accepted path's rows into place.
+ *
+ * A sequence's cached token at position t lives in page
+ * page_table[b*table_stride + t / page_size], place t % page_size.  Node j of
+ * the draft (node 0: the last committed token) is written at position
+ * L + j, L = cache_len[b] (a negative one reads as 0); its rotary position
+ * is L + its depth in the tree, which is its cache position once
+ * spec_verify_cache_commit has moved the accepted path.
+ *
+ * Shared conventions: `workspace` is nullable and only receives the SV_FLAG_*
+ * bits (as in spec_verify_commit: its first 256 bytes, any other verify
+ * workspace will do).  A page table entry outside [0, num_pages) is never
+ * followed (SV_FLAG_INVALID_PAGE); a token at or past max_pages * page_size
+ * has no place (SV_FLAG_CAPACITY).  What then happens to it is said at each
+ * call.  Entries that hold no token are not looked at.
+ * `count` [B], nullable: only the first count[b] (clamped to [0, N]) of the N
+ * nodes of sequence b exist; the others are padding.  B <= 65535, head_dim
+ * <= 256, num_heads <= 1024; strides are >= 0, pools at least one page.
+ * ====================================================================== */
+
+/* A paged cache pool: keys and values of one layer, or of several at equal
+ * distances.  Element (page, place, head, d) of layer l is at
+ * l*layer_stride + page*page_stride + place*token_stride + head*head_stride
+ * + d (in elements, the same for k and v).  SV_E4M3 pools have one scale for
+ * each (page, head, place), contiguous in that order, layers
+ * scale_layer_stride apart; a value is its code times its scale. */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale; /* SV_E4M3 only, else NULL */
+    int dtype;                /* SV_F32 (read, write and commit only), SV_BF16, SV_F16, SV_E4M3 */
+    int num_pages, page_size, num_heads, head_dim;
+    int64_t page_stride, token_stride, head_stride;
+    int num_layers; /* spec_verify_cache_commit moves rows in all; the other calls use layer 0 */
+    int64_t layer_stride, scale_layer_stride;
+} sv_kv_cache;
+
+/* Rows [B, N, H, D] of a strided tensor, head_dim contiguous (strides in elements). */
+typedef struct {
+    const void *data;
+    int64_t stride_b, stride_n, stride_h;
+} sv_rows;
+
+/* Rotary positions: pair i of the leading rotary_dim elements of a head turns
+ * by position * inv_freq[i].  The pair is elements (i, i + rotary_dim/2), or
+ * (2i, 2i+1) if `interleaved`; (a, b) -> magnitude (a cos - b sin, b cos +
+ * a sin).  inv_freq: rotary_dim/2 doubles on the DEVICE.  Angles are reduced
+ * in 64 bits, so far positions turn as exactly as near ones. */
+typedef struct {
+    const double *inv_freq;
+    int rotary_dim; /* even, 2 .. head_dim */
+    int interleaved;
+    float magnitude;
+} sv_rotary;
+
+/*
+ * Rotary frequencies base^(-2i/rotary_dim), scaled for long contexts, into
+ * `inv_freq` (rotary_dim/2 doubles) and the factor for sv_rotary.magnitude
+ * into `magnitude`; both HOST pointers.  Runs on the host only.
+ *  SV_ROPE_NONE    as they are
+ *  SV_ROPE_LINEAR  all divided by `factor` (position interpolation)
+ *  SV_ROPE_BANDS   by wavelength w = 2 pi / f over the original context
+ *                  length: f where original_len / w > high, f / factor where
+ *                  it is < low, linear in original_len / w between
+ *  SV_ROPE_YARN    (Peng et al. 2023) by pair index: f up to the pair that
+ *                  turns `high` times over original_len, f / factor from the
+ *                  one that turns `low` times, a linear ramp between;
+ *                  magnitude 0.1 ln(factor) + 1
+ * SV_ERR_INVALID_ARG: rotary_dim odd, < 2 or > 512; base <= 1; factor < 1,
+ * original_len <= 0 or not 0 < low < high where the form uses them.
+ */
+enum { SV_ROPE_NONE = 0, SV_ROPE_LINEAR = 1, SV_ROPE_BANDS = 2, SV_ROPE_YARN = 3 };
+
+int spec_verify_rotary_frequencies(double *inv_freq, float *magnitude, int rotary_dim,
+                                   double base, int scaling, double factor, double original_len,
+                                   double low, double high);
+
+/*
+ * Rotary positions of T tokens: out[t, h, :] = x[t, h, :] turned to
+ * positions[t] (int32, any sign), elements past rotary_dim copied.
+ * x: T*H rows of D elements, (t, h) at t*x_stride_t + h*x_stride_h; out the
+ * same with its own strides; out may be x (same strides), otherwise the two
+ * must not overlap.  dtype SV_F32, SV_BF16 or SV_F16; computed in 32 bits.
+ * `inverse` nonzero turns by the opposite angle with the same magnitude: the
+ * transposed map, which is also the gradient of x.
+ * 0 <= T < 2^31, 1 <= H <= 1024, 2 <= D <= 512.  One launch.
+ */
+int spec_verify_rotary(const void *x, int dtype, int64_t x_stride_t, int64_t x_stride_h,
+                       const int32_t *positions, const sv_rotary *rope, int inverse, int64_t T,
+                       int H, int D, void *out, int64_t o_stride_t, int64_t o_stride_h,
+                       void *stream);
+
+/*
+ * Write N new tokens of each sequence into the cache.
+ *
+ * k, v: [B, N, num_heads, head_dim] of `dtype` (SV_F32, SV_BF16, SV_F16).
+ * K is turned by `rope` (nullable: not turned) to position L + depth(j):
+ * depth in the tree `parent` [B, N], or j if `parent` is NULL; then N may be
+ * any prompt chunk's length, with `parent` N <= 64.  A node whose parent is
+ * outside [0, j) counts as a root (depth 0; SV_FLAG_INVALID_TREE).  The pool
+ * has the same type, or SV_E4M3: then each row (token, head) is held with
+ * scale = amax / 448 (rounded to float) and codes value / scale rounded to
+ * nearest, ties to even, as if in exact arithmetic; a row with an infinity
+ * or a NaN gets a NaN scale, an all-zero row scale 0.
+ * q (nullable): Hq heads [B, N, Hq, head_dim] of `dtype`, turned in the same
+ * launch into q_out [B, N, Hq, head_dim] contiguous (padding nodes are left
+ * as they were); needs `rope`.
+ * Tokens without a place or with an invalid page are not written.  Two nodes
+ * must not share a place (distinct sequences need distinct pages there).
+ */
+int spec_verify_cache_write(const sv_kv_cache *cache, const int32_t *page_table,
+                            int64_t table_stride, int max_pages, const int32_t *cache_len,
+                            const int32_t *parent, const int32_t *count, const sv_rows *k,
+                            const sv_rows *v, int dtype, int B, int N, const sv_rotary *rope,
+                            const sv_rows *q, int Hq, void *q_out, void *workspace,
+                            void *stream);
+
+/*
+ * Read cached rows back, packed: for offsets[b] <= r < offsets[b+1], rows
+ * k_out[r] and v_out[r] ([total, num_heads, head_dim] contiguous, of
+ * out_dtype SV_F32, SV_BF16 or SV_F16) are the cached token of sequence b at
+ * position start[b] + r - offsets[b] (start nullable: 0).  offsets: [B+1]
+ * int32, non-decreasing, on the device.  Rows outside [offsets[0],
+ * offsets[B]) are left as they were; a row without a place or with an
+ * invalid page is filled with zeros.
+ */
+int spec_verify_cache_read(const sv_kv_cache *cache, const int32_t *page_table,
+                           int64_t table_stride, int max_pages, const int32_t *offsets,
+                           const int32_t *start, int B, int64_t total, void *k_out, void *v_out,
+                           int out_dtype, void *workspace, void *stream);
+
+/*
+ * Attention of N drafted tokens of each sequence over the cache, in which
+ * their own keys and values have been written (spec_verify_cache_write):
+ *   out[b, i, h] = sum_t w_t v_t,  w = softmax_t(scale q[b, i, h] . k_t)
+ * over the cached positions t < L and over the positions L + j of node i's
+ * ancestors j and of itself; `parent` [B, N] as for the tree verify calls,
+ * NULL for a chain (node i sees nodes 0..i).  Head h reads cache head
+ * h / (Hq / num_heads).  q: [B, N, Hq, head_dim], SV_BF16 or SV_F16; the pool
+ * has the same type or is SV_E4M3.  out: [B, N, Hq, head_dim] contiguous, of
+ * q's type; lse (nullable) [B, N, Hq]: ln sum_t exp(scale q . k_t).
+ * A padding node, a node with an invalid parent (SV_FLAG_INVALID_TREE) and
+ * every node below one attend to nothing: zeros, lse -inf.  So does a row
+ * whose scores are all -inf.  Tokens without a place or with an invalid page
+ * are left out of the sums.  What a masked position holds does not matter,
+ * infinities and NaN included.
+ * 1 <= N <= 64, Hq a multiple of num_heads, Hq <= 1024, head_dim <= 256,
+ * scale finite.  Scores, softmax statistics and sums are held in 32 bits;
+ * the weights enter the second product rounded to the type of the values
+ * (to 16-bit floats for an SV_E4M3 pool).
+ * scratch: device memory of spec_verify_tree_attention_scratch_size bytes,
+ * 16-byte aligned, never read before it is written: no initialisation, but
+ * not shared by two calls that may run at the same time.
+ */
+size_t spec_verify_tree_attention_scratch_size(int B, int N, int Hq, int num_heads,
+                                               int head_dim);
+
+int spec_verify_tree_attention(const sv_rows *q, int q_dtype, const sv_kv_cache *cache,
+                               const int32_t *page_table, int64_t table_stride, int max_pages,
+                               const int32_t *cache_len, const int32_t *parent,
+                               const int32_t *count, int B, int N, int Hq, float scale,
+                               void *out, float *lse, void *workspace, void *scratch,
+                               size_t scratch_bytes, void *stream);
+
+/*
+ * After verification: move the accepted path's cache rows into place, in all
+ * layers of the pool, and advance the lengths.  With n = accepted_len[b]
+ * (clamped to [0, N-1]), the row at position L + path[b, j] moves to L + j
+ * for j = 1..n, and new_len[b] = L + n + 1 (new_len may be cache_len).
+ * path [B, N] as spec_verify_tree_greedy and spec_verify_tree_stochastic
+ * write it; NULL (a chain): nothing moves.  An entry outside [j, N) is not
+ * moved (SV_FLAG_INVALID_TREE), nor is one without a place or with an invalid
+ * page; new_len stops at the capacity (SV_FLAG_CAPACITY).
+ * 1 <= N <= 64.  One launch, two when rows may move and new_len is cache_len.
+ */
+int spec_verify_cache_commit(const sv_kv_cache *cache, const int32_t *page_table,
+                             int64_t table_stride, int max_pages, const int32_t *cache_len,
+                             const int32_t *accepted_len, const int32_t *path, int B, int N,
+                             int32_t *new_len, void *workspace, void *stream);
 
 #ifdef __cplusplus
 }

@@ -21,10 +21,11 @@ import torch
 
 from .build import LIB_PATH
 
-SV_F32, SV_BF16 = 0, 1
+SV_F32, SV_BF16, SV_F16, SV_E4M3 = 0, 1, 2, 3
 SV_FLAG_INVALID_TOKEN, SV_FLAG_RESIDUAL_FALLBACK, SV_FLAG_TIMEOUT = 1, 2, 4
 SV_FLAG_INVALID_ROW, SV_FLAG_CAPACITY, SV_FLAG_INVALID_TREE = 8, 16, 32
 SV_FLAG_BOUNDS = 64  # raised by the bounds-checked build only
+SV_FLAG_INVALID_PAGE = 128
 
 # Entry points declared in include/spec_verify.h.
 EXPORTS = (
@@ -36,10 +37,33 @@ EXPORTS = (
     "spec_verify_greedy_noalloc_read_device_status",
     "spec_verify_tree_stochastic_workspace_size", "spec_verify_tree_stochastic",
     "spec_verify_kernel_launches",
+    "spec_verify_rotary_frequencies", "spec_verify_rotary", "spec_verify_cache_write",
+    "spec_verify_cache_read", "spec_verify_tree_attention_scratch_size",
+    "spec_verify_tree_attention", "spec_verify_cache_commit",
 )
 
 _lib = None
 _lock = threading.Lock()
+
+
+class _Cache(ctypes.Structure):  # sv_kv_cache
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("num_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("num_layers", ctypes.c_int), ("layer_stride", ctypes.c_int64),
+                ("scale_layer_stride", ctypes.c_int64)]
+
+
+class _Rows(ctypes.Structure):  # sv_rows
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64), ("stride_h", ctypes.c_int64)]
+
+
+class _Rotary(ctypes.Structure):  # sv_rotary
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("magnitude", ctypes.c_float)]
 
 
 class SpecVerifyError(RuntimeError):
@@ -105,6 +129,24 @@ def load_library(path: str | None = None):
         lib.spec_verify_greedy_noalloc.restype = I
         lib.spec_verify_greedy_noalloc_read_device_status.argtypes = [ctypes.POINTER(U32), I, P]
         lib.spec_verify_greedy_noalloc_read_device_status.restype = I
+        C, R, X, D = (ctypes.POINTER(_Cache), ctypes.POINTER(_Rows), ctypes.POINTER(_Rotary),
+                      ctypes.c_double)
+        lib.spec_verify_rotary_frequencies.argtypes = [P, P, I, D, I, D, D, D, D]
+        lib.spec_verify_rotary_frequencies.restype = I
+        lib.spec_verify_rotary.argtypes = [P, I, I64, I64, P, X, I, I64, I, I, P, I64, I64, P]
+        lib.spec_verify_rotary.restype = I
+        lib.spec_verify_cache_write.argtypes = [C, P, I64, I, P, P, P, R, R, I, I, I, X, R, I, P,
+                                                P, P]
+        lib.spec_verify_cache_write.restype = I
+        lib.spec_verify_cache_read.argtypes = [C, P, I64, I, P, P, I, I64, P, P, I, P, P]
+        lib.spec_verify_cache_read.restype = I
+        lib.spec_verify_tree_attention_scratch_size.argtypes = [I, I, I, I, I]
+        lib.spec_verify_tree_attention_scratch_size.restype = SZ
+        lib.spec_verify_tree_attention.argtypes = [R, I, C, P, I64, I, P, P, P, I, I, I, F, P, P,
+                                                   P, P, SZ, P]
+        lib.spec_verify_tree_attention.restype = I
+        lib.spec_verify_cache_commit.argtypes = [C, P, I64, I, P, P, P, I, I, P, P, P]
+        lib.spec_verify_cache_commit.restype = I
         lib.spec_verify_kernel_launches.argtypes = []
         lib.spec_verify_kernel_launches.restype = U64
         if path is None:
@@ -507,3 +549,345 @@ def philox4x32_10(counters: torch.Tensor, seed: int, stream=None) -> torch.Tenso
                                               out.data_ptr(), _stream_ptr(stream, c.device))
     _check(code, "spec_verify_philox4x32_10")
     return out
+
+
+# ---------------------------------------------------------------- cache side
+
+_TYPES = {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float16: SV_F16,
+          torch.float8_e4m3fn: SV_E4M3}
+_ROPE = {"none": 0, "linear": 1, "bands": 2, "yarn": 3}
+
+
+def _on(device, stream):
+    """A guard that makes the device current, and the pointer of the stream to
+    launch on."""
+    return torch.cuda.device(device), _stream_ptr(stream, device)
+
+
+def _keep(t, stream):
+    """Memory made on the current stream and used on `stream`."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _ints(t, shape, device, name):
+    if (not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.int32 or
+            tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _optional_ints(t, shape, device, name):
+    return None if t is None else _ints(t, shape, device, name)
+
+
+def _rows(t, heads, dim, name, like=None):
+    """Code and descriptor of a [B, N, heads, dim] tensor (`like`: another one)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _TYPES:
+        raise TypeError(f"{name} must be a CUDA tensor of a floating type")
+    if t.dim() != 4 or (heads is not None and t.shape[2] != heads) or t.shape[3] != dim:
+        raise ValueError(f"{name} must be [B, N, {'H' if heads is None else heads}, {dim}], "
+                         f"got {tuple(t.shape)}")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device or
+                             t.shape[:2] != like.shape[:2]):
+        raise ValueError(f"{name} must match k's type, device, B and N")
+    sb, sn, sh, sd = t.stride()
+    if sd != 1 and t.numel() > 0 and dim > 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return _TYPES[t.dtype], _Rows(t.data_ptr(), sb, sn, sh)
+
+
+class KVCache:
+    """A paged cache pool: k and v [pages, page_size, heads, head_dim] (or
+    [layers, pages, ...]) of one floating type with any strides but a contiguous
+    last axis, the same for both; float8_e4m3fn pools come with float32 scales
+    [pages, heads, page_size] (or [layers, ...]).  Page tables are passed to the
+    calls.  `KVCache.empty` allocates one with each head's page contiguous."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "device", "page_size", "num_heads", "head_dim",
+                 "layers", "_c")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dtype not in _TYPES or not k.is_cuda or k.dim() not in (4, 5):
+            raise TypeError("k must be a CUDA tensor [(layers,) pages, page_size, heads, head_dim] "
+                            "of float32, bfloat16, float16 or float8_e4m3fn")
+        stride = k.stride()
+        if v.dtype != k.dtype or v.device != k.device or v.shape != k.shape or v.stride() != stride:
+            raise ValueError("v must have k's type, device, shape and strides")
+        *layers, pages, page_size, heads, dim = k.shape
+        if stride[-1] != 1 and dim > 1:
+            raise ValueError("the pool's last axis must be contiguous")
+        coded = k.dtype == torch.float8_e4m3fn
+        if coded != (k_scale is not None) or coded != (v_scale is not None):
+            raise ValueError("float8_e4m3fn pools, and only they, have k_scale and v_scale")
+        if coded:
+            want = (*layers, pages, heads, page_size)
+            for s in (k_scale, v_scale):
+                if (s.dtype != torch.float32 or s.device != k.device or tuple(s.shape) != want or
+                        s.stride()[-3:] != (heads * page_size, page_size, 1)):
+                    raise ValueError(f"scales must be float32 {want}, contiguous but for layers")
+            if layers and k_scale.stride(0) != v_scale.stride(0):
+                raise ValueError("k_scale and v_scale must have the same strides")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device, self.page_size, self.num_heads, self.head_dim = k.device, page_size, heads, dim
+        self.layers = layers[0] if layers else 1
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if coded else None,
+                         v_scale.data_ptr() if coded else None, _TYPES[k.dtype], pages, page_size,
+                         heads, dim, stride[-4], stride[-3], stride[-2], self.layers,
+                         stride[0] if layers else 0,
+                         k_scale.stride(0) if layers and coded else 0)
+
+    @classmethod
+    def empty(cls, num_pages, page_size, num_heads, head_dim, dtype=torch.bfloat16, device="cuda",
+              layers=None):
+        """A pool of zeros whose layout is [(layers,) pages, heads, page_size, head_dim]."""
+        lead = () if layers is None else (layers,)
+        shape = (*lead, num_pages, num_heads, page_size)
+        made = []
+        for _ in range(2):
+            t = torch.zeros((*shape, head_dim), device=device,
+                            dtype=torch.uint8 if dtype == torch.float8_e4m3fn else dtype)
+            made.append(t.view(dtype).transpose(-3, -2))
+        if dtype == torch.float8_e4m3fn:
+            made += [torch.zeros(shape, dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*made)
+
+    def layer(self, i):
+        """Layer i's pool (shares memory)."""
+        if self.k.dim() == 4:
+            raise ValueError("this pool has one layer")
+        return KVCache(self.k[i], self.v[i], None if self.k_scale is None else self.k_scale[i],
+                       None if self.v_scale is None else self.v_scale[i])
+
+
+class Rotary:
+    """Rotary positions: float64 frequencies [rotary_dim / 2] on the device, the
+    pair layout and the factor on cos and sin (see rotary_frequencies)."""
+
+    __slots__ = ("inv_freq", "interleaved", "magnitude", "_c")
+
+    def __init__(self, inv_freq, interleaved=False, magnitude=1.0):
+        if (inv_freq.dtype != torch.float64 or not inv_freq.is_cuda or inv_freq.dim() != 1 or
+                not inv_freq.is_contiguous()):
+            raise TypeError("inv_freq must be a contiguous float64 CUDA tensor [rotary_dim / 2]")
+        self.inv_freq, self.interleaved, self.magnitude = inv_freq, interleaved, magnitude
+        self._c = _Rotary(inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(interleaved), magnitude)
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "none",
+                       factor: float = 1.0, original_len: float = 0.0, low: float = 1.0,
+                       high: float = 0.0, interleaved: bool = False, device="cuda") -> Rotary:
+    """Rotary frequencies base^(-2i/rotary_dim) on `device`, scaled for long
+    contexts: "none", "linear" (all / factor), "bands" (by wavelength; low and
+    high bound original_len / wavelength) or "yarn" (a ramp over the pairs that
+    turn between `high` and `low` times over original_len).  `high` defaults to
+    4 for "bands" and 32 for "yarn"."""
+    if scaling not in _ROPE:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE)}, got {scaling!r}")
+    if high == 0.0:
+        high = 32.0 if scaling == "yarn" else 4.0
+    host = (ctypes.c_double * max(1, rotary_dim // 2))()
+    mag = ctypes.c_float(1.0)
+    _check(load_library().spec_verify_rotary_frequencies(
+        ctypes.addressof(host), ctypes.addressof(mag), rotary_dim, base, _ROPE[scaling], factor,
+        original_len, low, high), "spec_verify_rotary_frequencies")
+    return Rotary(torch.tensor(list(host), dtype=torch.float64, device=device), interleaved,
+                  float(mag.value))
+
+
+def rotary(x: torch.Tensor, positions: torch.Tensor, rope: Rotary, *, inverse: bool = False,
+           out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotary positions: x [T, H, D] or [B, N, H, D] (float32, bfloat16 or
+    float16; last axis contiguous), positions [T] or [B, N] int32.  `inverse`
+    turns back (the transposed map, hence the gradient).  `out` may be x."""
+    lib = load_library()
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype not in _TYPES or \
+            x.dtype == torch.float8_e4m3fn:
+        raise TypeError("x must be a CUDA tensor of float32, bfloat16 or float16")
+    if x.dim() not in (3, 4):
+        raise ValueError(f"x must be [T, H, D] or [B, N, H, D], got shape {tuple(x.shape)}")
+    dev = x.device
+    pos = _ints(positions, x.shape[:-2], dev, "positions")
+    if rope.inv_freq.device != dev:
+        raise ValueError("the rotary frequencies must be on x's device")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        _keep(out, stream)
+    elif out.dtype != x.dtype or out.device != dev or out.shape != x.shape:
+        raise ValueError("out must have x's type, device and shape")
+    if x.numel() == 0:
+        return out
+    H, D = x.shape[-2:]
+    strides = []
+    for t, name in ((x, "x"), (out, "out")):
+        s = t.stride()
+        if s[-1] != 1:
+            raise ValueError(f"{name}: the last axis must be contiguous")
+        if t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1 and s[0] != t.shape[1] * s[1]:
+            raise ValueError(f"{name}: tokens must be evenly spaced over B and N")
+        strides.append((s[1] if t.dim() == 4 and t.shape[1] > 1 else s[0], s[-2]))
+    guard, st = _on(dev, stream)
+    with guard:
+        code = lib.spec_verify_rotary(
+            x.data_ptr(), _TYPES[x.dtype], *strides[0], pos, rope._c, int(inverse),
+            x.numel() // (H * D), H, D, out.data_ptr(), *strides[1], st)
+    _check(code, "spec_verify_rotary")
+    return out
+
+
+def _table(page_table, B, device):
+    if (not isinstance(page_table, torch.Tensor) or page_table.dtype != torch.int32 or
+            page_table.device != device or page_table.dim() != 2 or page_table.shape[0] != B or
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        raise TypeError(f"page_table must be int32 [{B}, max_pages] on {device}, rows contiguous")
+    return page_table.data_ptr(), page_table.stride(0), page_table.shape[1]
+
+
+def _status(workspace, device, stream):
+    ws = workspace or default_workspace(device)
+    ws.ensure(256, stream)
+    return ws.buf.data_ptr()
+
+
+def cache_write(cache: KVCache, page_table: torch.Tensor, cache_len: torch.Tensor,
+                k: torch.Tensor, v: torch.Tensor, *, parent: torch.Tensor | None = None,
+                count: torch.Tensor | None = None, rope: Rotary | None = None,
+                q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                workspace: Workspace | None = None, stream=None) -> torch.Tensor | None:
+    """Write k and v [B, N, heads, head_dim] of N new tokens a sequence at
+    positions cache_len[b] + j of the paged cache, K turned by `rope` to
+    position cache_len[b] + depth (in the tree `parent` [B, N], else j), in 8
+    bits if the pool is float8_e4m3fn.  `q` [B, N, Hq, head_dim] is turned in
+    the same launch and returned.  Only the first count[b] tokens are written."""
+    lib = load_library()
+    code_t, kr = _rows(k, cache.num_heads, cache.head_dim, "k")
+    _, vr = _rows(v, cache.num_heads, cache.head_dim, "v", k)
+    B, N = k.shape[:2]
+    dev = cache.device
+    if k.device != dev:
+        raise ValueError("k and v must be on the cache's device")
+    if rope is not None and rope.inv_freq.device != dev:
+        raise ValueError("the rotary frequencies must be on the cache's device")
+    lens = _ints(cache_len, (B,), dev, "cache_len")
+    par = _optional_ints(parent, (B, N), dev, "parent")
+    cnt = _optional_ints(count, (B,), dev, "count")
+    table, tstride, pages = _table(page_table, B, dev)
+    qr, Hq, qo = None, 0, None
+    if q is not None:
+        if rope is None:
+            raise ValueError("q is turned by rope: pass both")
+        _, qr = _rows(q, None, cache.head_dim, "q", k)
+        Hq = q.shape[2]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            if cnt is not None:
+                q_out.zero_()  # padding rows are left as they were
+            _keep(q_out, stream)
+        elif (q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.device != dev or
+              not q_out.is_contiguous()):
+            raise ValueError("q_out must be a contiguous tensor like q")
+        qo = q_out.data_ptr()
+    guard, st = _on(dev, stream)
+    with guard:
+        code = lib.spec_verify_cache_write(
+            cache._c, table, tstride, pages, lens, par, cnt, kr, vr, code_t, B, N,
+            None if rope is None else rope._c, qr, Hq, qo, _status(workspace, dev, stream), st)
+    _check(code, "spec_verify_cache_write")
+    return q_out
+
+
+def cache_read(cache: KVCache, page_table: torch.Tensor, offsets: torch.Tensor, total: int,
+               dtype: torch.dtype = torch.bfloat16, *, start: torch.Tensor | None = None,
+               out: dict | None = None, workspace: Workspace | None = None, stream=None) -> dict:
+    """Cached rows as packed k and v [total, heads, head_dim] of `dtype`: row r
+    of offsets[b] <= r < offsets[b+1] is sequence b's token at position
+    start[b] + r - offsets[b].  Other rows are left as they were (unset, unless
+    `out` brings the tensors)."""
+    lib = load_library()
+    dev = cache.device
+    B = int(offsets.shape[0]) - 1
+    if B < 0 or dtype not in _TYPES or dtype == torch.float8_e4m3fn:
+        raise ValueError("offsets must be [B + 1] and dtype float32, bfloat16 or float16")
+    offs = _ints(offsets, (B + 1,), dev, "offsets")
+    st0 = _optional_ints(start, (B,), dev, "start")
+    table, tstride, pages = _table(page_table, B, dev)
+    shape = (int(total), cache.num_heads, cache.head_dim)
+    res = {x: _keep(_out(out, x, shape, dtype, dev), stream) for x in ("k", "v")}
+    if total == 0:
+        return res
+    guard, st = _on(dev, stream)
+    with guard:
+        code = lib.spec_verify_cache_read(
+            cache._c, table, tstride, pages, offs, st0, B, int(total), res["k"].data_ptr(),
+            res["v"].data_ptr(), _TYPES[dtype], _status(workspace, dev, stream), st)
+    _check(code, "spec_verify_cache_read")
+    return res
+
+
+def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
+                   cache_len: torch.Tensor, parent: torch.Tensor | None = None, *,
+                   count: torch.Tensor | None = None, scale: float | None = None,
+                   lse: bool = False, out: dict | None = None,
+                   workspace: Workspace | None = None, stream=None) -> dict:
+    """Attention of drafted tokens over the cache that holds them
+    (cache_write): q [B, N, Hq, head_dim] bfloat16 or float16, node i of the
+    tree `parent` [B, N] (None: a chain) sees cache_len[b] context tokens, its
+    ancestors and itself; Hq a multiple of the cache's heads; scale defaults to
+    head_dim ** -0.5.  Returns out [B, N, Hq, head_dim] (and lse [B, N, Hq])."""
+    lib = load_library()
+    code_t, qr = _rows(q, None, cache.head_dim, "q")
+    B, N, Hq, D = q.shape
+    dev = cache.device
+    if q.device != dev:
+        raise ValueError("q must be on the cache's device")
+    lens = _ints(cache_len, (B,), dev, "cache_len")
+    par = _optional_ints(parent, (B, N), dev, "parent")
+    cnt = _optional_ints(count, (B,), dev, "count")
+    table, tstride, pages = _table(page_table, B, dev)
+    res = {"out": _keep(_out(out, "out", (B, N, Hq, D), q.dtype, dev), stream)}
+    if lse:
+        res["lse"] = _keep(_out(out, "lse", (B, N, Hq), torch.float32, dev), stream)
+    if scale is None:
+        scale = D ** -0.5
+    need = lib.spec_verify_tree_attention_scratch_size(B, N, Hq, cache.num_heads, D)
+    scratch = _keep(torch.empty(max(need, 16), dtype=torch.uint8, device=dev), stream)
+    guard, st = _on(dev, stream)
+    with guard:
+        code = lib.spec_verify_tree_attention(
+            qr, code_t, cache._c, table, tstride, pages, lens, par, cnt, B, N, Hq, float(scale),
+            res["out"].data_ptr(), res["lse"].data_ptr() if lse else None,
+            _status(workspace, dev, stream), scratch.data_ptr(), scratch.numel(), st)
+    _check(code, "spec_verify_tree_attention")
+    return res
+
+
+def cache_commit(cache: KVCache, page_table: torch.Tensor, cache_len: torch.Tensor, result: dict,
+                 *, new_len: torch.Tensor | None = None, workspace: Workspace | None = None,
+                 stream=None) -> torch.Tensor:
+    """After a verify call: move the accepted path's cache rows, in all layers
+    of the pool, from positions cache_len[b] + path[b, j] to cache_len[b] + j,
+    and return the new lengths cache_len + accepted_len + 1 (in `new_len`,
+    which may be cache_len).  `result` is what tree_greedy or tree_stochastic
+    returned; results without a path (a chain) only advance the lengths."""
+    lib = load_library()
+    acc, path = result["accepted_len"], result.get("path")
+    dev = cache.device
+    B = int(acc.shape[0])
+    lens = _ints(cache_len, (B,), dev, "cache_len")
+    accepted = _ints(acc, (B,), dev, "accepted_len")
+    if path is not None:
+        N = int(path.shape[1]) if path.dim() == 2 else -1
+        path = _ints(path, (B, N), dev, "path")
+    else:
+        N = int(result["out_tokens"].shape[1]) if "out_tokens" in result else 64
+    table, tstride, pages = _table(page_table, B, dev)
+    if new_len is None:
+        new_len = _keep(torch.empty(B, dtype=torch.int32, device=dev), stream)
+    guard, st = _on(dev, stream)
+    with guard:
+        code = lib.spec_verify_cache_commit(
+            cache._c, table, tstride, pages, lens, accepted, path, B, N,
+            _ints(new_len, (B,), dev, "new_len"), _status(workspace, dev, stream), st)
+    _check(code, "spec_verify_cache_commit")
+    return new_len

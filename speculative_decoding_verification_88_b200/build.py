@@ -23,8 +23,10 @@ LIB_PATH = os.path.join(LIB_DIR, "libspecverify.so")
 # For tests, in place of a memory checker; never the default library.
 BOUNDS_LIB_PATH = os.path.join(LIB_DIR, "libspecverify_bounds.so")
 
-SOURCES = ["sv_api.cu", "sv_kernels.cu", "sv_noalloc.cu", "sv_tree_stoch.cu"]
-HEADERS = [os.path.join(CSRC, h) for h in ("sv_internal.h", "sv_device.cuh")] + [
+SOURCES = ["sv_api.cu", "sv_kernels.cu", "sv_noalloc.cu", "sv_tree_stoch.cu",
+           "sv_cache_api.cu", "sv_cache.cu", "sv_attention.cu"]
+HEADERS = [os.path.join(CSRC, h) for h in ("sv_internal.h", "sv_device.cuh", "sv_cache.h",
+                                               "sv_cache_device.cuh")] + [
     os.path.join(INCLUDE, "spec_verify.h")]
 
 NVCC_FLAGS = [
