@@ -24,7 +24,8 @@ LIB_PATH = os.path.join(LIB_DIR, "libspecverify.so")
 BOUNDS_LIB_PATH = os.path.join(LIB_DIR, "libspecverify_bounds.so")
 
 SOURCES = ["sv_api.cu", "sv_kernels.cu", "sv_noalloc.cu", "sv_tree_stoch.cu",
-           "sv_cache_api.cu", "sv_cache.cu", "sv_attention.cu"]
+           "sv_cache_api.cu", "sv_cache.cu", "sv_attention.cu",
+           "sv_attention_mma.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("sv_internal.h", "sv_device.cuh", "sv_cache.h",
                                                "sv_cache_device.cuh")] + [
     os.path.join(INCLUDE, "spec_verify.h")]

@@ -1,0 +1,1209 @@
+// sv_attention_mma.cu -- attention of drafted tokens over the paged cache on
+// the 5th-generation tensor cores.
+//
+// The N nodes of a sequence and the G query heads of one cache head make R =
+// N G rows that read the same keys and values.  An item is (sequence, cache
+// head, up to 256 of these rows); its cached tokens are cut into tiles of
+// 128, and all tiles of all items, in order, are dealt out evenly over one
+// block per SM, so that ragged lengths balance and a single long sequence
+// uses every SM.  A block's share is a run of segments (a range of one item's
+// tiles).  A segment that covers its item writes the result; any other leaves
+// (maximum, sum, unnormalised output) in scratch, and a second grid joins
+// them (at most two for each block, so the traffic is small).
+//
+// Per tile S = Q K^T (128 rows x 128 tokens) and O += P V, both by
+// tcgen05.mma from shared memory filled by TMA (P from tensor memory, where
+// it overlies S).  Two softmax warpgroups work in turn, each with its own S
+// and O in tensor memory: with at most 128 rows they take alternate tiles
+// (merged at the segment's end), with more each takes one half of the rows.
+// The MMA warp issues S of one while the other computes its exponentials.
+// A thread owns one row, so a row's maximum and sum need no shuffles.  The
+// running maximum is only raised when a score exceeds it by 2^8: O is then
+// rescaled in tensor memory; until then weights up to 2^8 are exact enough
+// in 16 bits, and the division by the sum at the end makes up for it.
+//
+// Weights enter the second product in the values' 16-bit type.  8-bit pools
+// are widened to 16-bit floats in shared memory (exact) by four converter
+// warps, K's scales multiply S and V's scales the weights; queries are scaled
+// by a power of two a row so that they fit 16-bit floats exactly, and the
+// weights by a power of two that follows the largest scale of V.
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "sv_cache_device.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kTile = 128;        // tokens a tile, rows a half item
+constexpr int kMaxCtas = 148;     // scratch is sized for this many blocks
+constexpr int kScaleRing = 4;     // tiles whose scales are held
+constexpr int kMaxStages = 8;
+constexpr int kConvStages = 3;    // widened tiles (8-bit pools)
+constexpr float kLazy = 8.0f;     // log2 of what a weight may exceed 1 by
+
+// Work split shared by the two grids: sequence b has tiles(b) * per_b tiles,
+// block c takes [T c / n, T (c + 1) / n).
+struct Split {
+  long long T;
+  int n;
+  __device__ __forceinline__ long long start(int c) const { return T * c / n; }
+};
+
+__host__ __device__ inline size_t slot_floats(int DP) { return static_cast<size_t>(kTile) * (DP + 2); }
+
+}  // namespace
+
+struct MmaParams {
+  AttnParams a;
+  int R;        // rows of a (sequence, cache head)
+  int halves;   // row tiles of 128
+  int pairs;    // items of a (sequence, cache head)
+  int box;      // tokens a TMA box: the largest power of two up to 128 that divides a page
+  int head_first;  // the tensor maps' second axis is the head, not the place
+  int stages;   // TMA ring entries
+  int qtiles;   // Q tiles in shared memory: 1 or 2
+  int negate;   // the scale is negative: Q is negated instead
+  int qvec;     // query rows start on 16-byte boundaries
+};
+
+namespace {
+
+__device__ __forceinline__ long long tokens_of(const AttnParams& a, int b, int& nodes, long long& len) {
+  nodes = a.count ? min(max(__ldg(a.count + b), 0), a.N) : a.N;
+  len = max(0, __ldg(a.cache_len + b));
+  const long long cap = min(static_cast<long long>(a.c.max_pages) * a.c.page_size, 0x7fffffffll);
+  const long long end = len + nodes;
+  return nodes == 0 ? 0 : end < cap ? end : cap;
+}
+__device__ __forceinline__ int tiles_of(const AttnParams& a, int b) {
+  int nodes;
+  long long len;
+  const long long t = (tokens_of(a, b, nodes, len) + kTile - 1) / kTile;
+  return t < 1 ? 1 : static_cast<int>(t);
+}
+
+// Total tiles, and the sequence and remainder of tile x(total), by the first
+// 256 threads of a block; all of them take part in the barriers.
+struct Found {
+  long long T;
+  int b;
+  long long rem;  // tiles into sequence b
+};
+template <typename At>
+__device__ __forceinline__ void find_tile(const AttnParams& a, int per_b, long long* sums, Found* f, At at) {
+  const int tid = threadIdx.x;
+  const int per = (a.B + 255) / 256;
+  long long mine = 0;
+  if (tid < 256) {
+    for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) mine += static_cast<long long>(tiles_of(a, b)) * per_b;
+    sums[tid] = mine;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    long long s[8], run = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s[i] = run;
+      run += sums[tid * 8 + i];
+    }
+    long long incl = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (tid >= o) incl += up;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[tid * 8 + i] = incl - run + s[i];
+    if (tid == 31) f->T = incl;
+  }
+  __syncthreads();
+  const long long x = at(f->T);
+  if (tid < 256 && mine > 0 && x >= sums[tid] && x < sums[tid] + mine) {
+    long long rem = x - sums[tid];
+    int b = tid * per;
+    for (;; ++b) {
+      const long long t = static_cast<long long>(tiles_of(a, b)) * per_b;
+      if (rem < t) break;
+      rem -= t;
+    }
+    f->b = b;
+    f->rem = rem;
+  }
+  __syncthreads();
+}
+
+// A block's segments in order, as every role walks them.
+struct Walk {
+  long long left;  // tiles of the share not yet walked
+  int b, item, items;
+  int tiles;       // of an item of b
+  int t0, t1;      // this segment's tiles
+  int nodes;
+  long long len, total;
+  bool first;
+  bool new_b;
+  __device__ __forceinline__ void load(const AttnParams& a) {
+    total = tokens_of(a, b, nodes, len);
+    const long long t = (total + kTile - 1) / kTile;
+    tiles = t < 1 ? 1 : static_cast<int>(t);
+    new_b = true;
+  }
+  __device__ __forceinline__ void begin(const AttnParams& a, int per_b, const Found& f, long long share) {
+    left = share;
+    items = per_b;
+    b = f.b;
+    first = true;
+    load(a);
+    item = static_cast<int>(f.rem / tiles);
+    t0 = static_cast<int>(f.rem - static_cast<long long>(item) * tiles);
+    t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + left));
+  }
+  __device__ __forceinline__ bool next(const AttnParams& a) {
+    left -= t1 - t0;
+    if (left <= 0) return false;
+    first = false;
+    new_b = false;
+    t0 = 0;
+    if (++item == items) {
+      item = 0;
+      ++b;
+      load(a);
+    }
+    t1 = static_cast<int>(min(static_cast<long long>(tiles), left));
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+};
+
+// ------------------------------------------------------------- PTX wrappers
+
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                       uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+      "%5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Shared-memory operand with 128-byte swizzle: rows of 128 bytes, groups of 8
+// rows `sbo` bytes apart; for an operand whose rows run along K (V), `lbo` is
+// the distance to the next 64 columns.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | static_cast<uint64_t>(lbo >> 4) << 16 |
+         static_cast<uint64_t>(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// f32 accumulator, 16-bit operands (bf16 or f16), M = 128; V is read
+// transposed (its columns are the fast axis).
+__host__ __device__ constexpr uint32_t mma_shape(bool bf16, int n, bool b_transposed) {
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_transposed ? 1u << 16 : 0u) |
+         static_cast<uint32_t>(n / 8) << 17 | 8u << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+// Arrives on `bar` once every MMA this thread has issued is complete.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of this warp's lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Two weights in the values' 16-bit type.
+template <typename M>
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack_weights<__nv_bfloat16>(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+template <>
+__device__ __forceinline__ uint32_t pack_weights<__half>(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// Whether any 16-bit element of a word is an infinity or a NaN.
+template <typename M>
+__device__ __forceinline__ bool odd_word(uint32_t w);
+template <>
+__device__ __forceinline__ bool odd_word<__nv_bfloat16>(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+template <>
+__device__ __forceinline__ bool odd_word<__half>(uint32_t w) {
+  return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+}
+
+struct Control {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t cfull[kConvStages], cempty[kConvStages];
+  uint64_t scale_full[kScaleRing];
+  uint64_t s_full[2], p_ready[2], o_done, q_full;
+  uint32_t tmem;
+  int abort;
+  int stop;              // abort, as the softmax warpgroups agreed on it
+  int bad[2];            // a page of the segment is missing (by segment parity)
+  unsigned int odd[2];   // tree tokens whose values hold an infinity or a NaN
+  unsigned long long mask[64];
+  float qscale[2 * kTile];
+  float2 ml[2][kTile];
+  float kscale[kScaleRing][kTile], vscale[kScaleRing][kTile];
+  float vmax[kScaleRing][4];
+  long long sums[256];
+  Found found;
+};
+
+// Bounded wait; once one has run out, every wait of the block returns at once
+// and the roles run to their ends on whatever is there.
+__device__ __forceinline__ void wait(Control* s, uint64_t* bar, uint32_t parity, Ctrl* ctrl) {
+  if (mbar_try_wait(bar, parity)) return;
+  const unsigned long long t0 = global_ns();
+  for (unsigned int spin = 1;; ++spin) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((spin & 63u) == 0u) {
+      if (*reinterpret_cast<volatile int*>(&s->abort)) return;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        *reinterpret_cast<volatile int*>(&s->abort) = 1;
+        raise_flag(ctrl, kFlagTimeout);
+        return;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool gave_up(const Control* s) { return *reinterpret_cast<const volatile int*>(&s->abort) != 0; }
+
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Ring entries of a segment of T tiles, in the order the MMA warp needs them:
+// alternate tiles (one row tile): K0 K1 V0 K2 V1 ...; two row tiles: K0 V0 K1 V1 ...
+__device__ __forceinline__ int k_entry(bool two, int t) { return two ? 2 * t : t == 0 ? 0 : 2 * t - 1; }
+__device__ __forceinline__ int v_entry(bool two, int t, int T) { return two ? 2 * t + 1 : t == T - 1 ? 2 * T - 1 : 2 * t + 2; }
+
+}  // namespace
+
+// DP: head_dim rounded up to 64 or 128.  QT: queries and output; E4: 8-bit pool.
+template <typename QT, int DP, bool E4>
+__global__ void __launch_bounds__(E4 ? 448 : 320, 1)
+    attention_mma_kernel(const MmaParams p, const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ksmap,
+                         const __grid_constant__ CUtensorMap vsmap) {
+  using MT = typename std::conditional<E4, __half, QT>::type;  // operands of the products
+  constexpr int kQBytes = kTile * DP * 2;
+  constexpr int kRow = E4 ? DP : DP * 2;             // bytes of a token's row in a TMA tile
+  constexpr int kData = kTile * kRow;
+  constexpr int kScaleBytes = E4 ? 16 * 128 : 0;     // one array's boxes, 128 bytes apart at least
+  constexpr int kEntry = kData + 2 * kScaleBytes;
+  constexpr int kConv = kTile * DP * 2;
+  constexpr int kChunks = DP / 64;
+  constexpr bool kBf16 = std::is_same<MT, __nv_bfloat16>::value;
+  constexpr uint32_t kShapeS = mma_shape(kBf16, kTile, false);
+  constexpr uint32_t kShapeO = mma_shape(kBf16, DP, true);
+
+  dep_enter();
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char* qs = smem;
+  unsigned char* conv = qs + p.qtiles * kQBytes;                          // E4 only
+  unsigned char* ring = conv + (E4 ? kConvStages * kConv : 0);
+  Control* s = reinterpret_cast<Control*>(ring + p.stages * kEntry);
+  const AttnParams& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per_b = a.c.heads * p.pairs;
+
+  if (tid == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&s->full[i], 1);
+      mbar_init(&s->empty[i], E4 ? 4 : 1);
+    }
+    for (int i = 0; i < kConvStages; ++i) {
+      mbar_init(&s->cfull[i], 4);
+      mbar_init(&s->cempty[i], 1);
+    }
+    for (int i = 0; i < kScaleRing; ++i) mbar_init(&s->scale_full[i], 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s->s_full[i], 1);
+      mbar_init(&s->p_ready[i], 4);
+      s->bad[i] = 0;
+      s->odd[i] = 0u;
+    }
+    mbar_init(&s->o_done, 1);
+    mbar_init(&s->q_full, 1);
+    s->abort = 0;
+    s->stop = 0;
+    mbar_fence_init();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&s->tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tmem_fence_before();
+  }
+  __syncthreads();
+  tmem_fence_after();
+  const int grid = gridDim.x;
+  const int cta = blockIdx.x;
+  find_tile(a, per_b, s->sums, &s->found, [&](long long T) {
+    const Split sp{T, static_cast<int>(min(static_cast<long long>(grid), T))};
+    return cta < sp.n ? sp.start(cta) : -1;
+  });
+  const uint32_t tmem = s->tmem;
+  const Split split{s->found.T, static_cast<int>(min(static_cast<long long>(grid), s->found.T))};
+  const long long share = cta < split.n ? split.start(cta + 1) - split.start(cta) : 0;
+
+  if (share > 0) {
+    Walk w;
+    w.begin(a, per_b, s->found, share);
+    if (warp == 8) {
+      // ------------------------------------------------ producer: TMA loads
+      const int nbox = kTile / p.box;
+      uint32_t e = 0;  // ring entries filled
+      bool stop = false;  // the same in all lanes
+      do {
+        const bool two = 2 * (w.item % p.pairs) + 1 < p.halves;
+        const int h = w.item / p.pairs;
+        const int T = w.t1 - w.t0;
+        // page (num_pages: none, which TMA fills with zeros) and place of this
+        // lane's box in two tiles running
+        const auto locate = [&](int t, int& page, int& place) {
+          page = a.c.num_pages;
+          place = 0;
+          const long long tok = static_cast<long long>(w.t0 + t) * kTile + lane * p.box;
+          if (t < T && lane < nbox && tok < w.total) {
+            const int pi = page_of(a.c, static_cast<int>(tok));
+            place = static_cast<int>(tok) - pi * a.c.page_size;
+            const int g = __ldg(a.c.table + static_cast<long long>(w.b) * a.c.table_stride + pi);
+            if (static_cast<unsigned int>(g) < static_cast<unsigned int>(a.c.num_pages)) page = g;
+          }
+        };
+        const auto load = [&](bool values, int page, int place) {
+          if (stop) return;
+          const uint32_t slot = e % p.stages, phase = (e / p.stages) & 1u;
+          wait(s, &s->empty[slot], phase ^ 1u, a.ctrl);
+          if (__any_sync(0xffffffffu, gave_up(s))) stop = true;
+          if (stop) return;
+          const uint32_t dst = smem_addr(ring + slot * kEntry);
+          if (lane == 0)
+            mbar_arrive_expect_tx(&s->full[slot], kData + (E4 && !values ? 2 * kTile * 4 : 0));
+          __syncwarp();
+          if (lane < nbox) {
+            const CUtensorMap* map = values ? &vmap : &kmap;
+            const int y = p.head_first ? h : place, z = p.head_first ? place : h;
+            if (E4) {
+              tma_4d(dst + lane * p.box * kRow, map, 0, y, z, page, &s->full[slot]);
+              if (!values) {
+                const uint32_t sd = dst + kData + lane * max(p.box * 4, 128);
+                tma_3d(sd, &ksmap, place, h, page, &s->full[slot]);
+                tma_3d(sd + kScaleBytes, &vsmap, place, h, page, &s->full[slot]);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < kChunks; ++c)
+                tma_4d(dst + c * kTile * 128 + lane * p.box * 128, map, c * 64, y, z, page, &s->full[slot]);
+            }
+          }
+          ++e;
+        };
+        int pg0, pl0, pg1, pl1;
+        locate(0, pg0, pl0);
+        if (!two) load(false, pg0, pl0);
+        for (int t = 0; t < T && !stop; ++t) {
+          locate(t + 1, pg1, pl1);
+          if (two) {
+            load(false, pg0, pl0);
+            load(true, pg0, pl0);
+          } else {
+            if (t + 1 < T) load(false, pg1, pl1);
+            load(true, pg0, pl0);
+          }
+          pg0 = pg1;
+          pl0 = pl1;
+        }
+      } while (!stop && w.next(a));
+      if (stop) {  // copies in flight land before the block ends
+        const unsigned long long t0 = global_ns();
+        const uint32_t n = min(e, static_cast<uint32_t>(p.stages));
+        for (uint32_t i = e - n; i < e; ++i)
+          while (!mbar_try_wait(&s->full[i % p.stages], (i / p.stages) & 1u) && global_ns() - t0 < kWaitLimitNs) {}
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------ MMA issue (one thread)
+      if (lane == 0) {
+        uint32_t base = 0;  // ring entries of earlier segments
+        uint32_t seg = 0, np[2] = {0, 0};
+        const uint32_t stages = E4 ? kConvStages : p.stages;
+        const uint32_t tiles = smem_addr(E4 ? conv : ring);
+        constexpr uint32_t kStep = E4 ? kConv : kEntry;
+        uint64_t* fullb = E4 ? s->cfull : s->full;
+        uint64_t* emptyb = E4 ? s->cempty : s->empty;
+        do {
+          const bool two = 2 * (w.item % p.pairs) + 1 < p.halves;
+          const int T = w.t1 - w.t0, U = two ? 2 * T : T;
+          wait(s, &s->q_full, seg & 1u, a.ctrl);
+          for (int x = 0; x <= U && !gave_up(s); ++x) {
+            if (x < U) {
+              const int g = x & 1, t = two ? x >> 1 : x;
+              const uint32_t e = base + k_entry(two, t), slot = e % stages;
+              wait(s, &fullb[slot], (e / stages) & 1u, a.ctrl);
+              tmem_fence_after();
+              if (gave_up(s)) break;
+              const uint64_t qd = operand(smem_addr(qs) + (two && g ? kQBytes : 0), 16, 1024);
+              const uint64_t kd = operand(tiles + slot * kStep, 16, 1024);
+#pragma unroll
+              for (int k = 0; k < DP / 16; ++k) {
+                // 16 elements are 32 bytes of a 128-byte row; 64 are the next block of rows
+                const uint64_t step = static_cast<uint64_t>(k / 4) * (kTile * 128 >> 4) + (k % 4) * 2;
+                mma_ss(tmem + g * kTile, qd + step, kd + step, kShapeS, k > 0);
+              }
+              mma_commit(&s->s_full[g]);
+              if (!two || g == 1) mma_commit(&emptyb[slot]);
+            }
+            if (x > 0) {
+              const int v = x - 1, g = v & 1, t = two ? v >> 1 : v;
+              const uint32_t e = base + v_entry(two, t, T), slot = e % stages;
+              wait(s, &fullb[slot], (e / stages) & 1u, a.ctrl);
+              wait(s, &s->p_ready[g], np[g] & 1u, a.ctrl);
+              ++np[g];
+              tmem_fence_after();
+              if (gave_up(s)) break;
+              const uint64_t vd = operand(tiles + slot * kStep, kTile * 128, 1024);
+              const uint32_t o = tmem + 2 * kTile + g * DP;
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k)
+                mma_ts(o, tmem + g * kTile + k * 8, vd + static_cast<uint64_t>(k) * (16 * 128 >> 4), kShapeO,
+                       v > 1 || k > 0);
+              if (!two || g == 1) mma_commit(&emptyb[slot]);
+            }
+          }
+          mma_commit(&s->o_done);
+          base += 2 * T;
+          ++seg;
+        } while (!gave_up(s) && w.next(a));
+        if (gave_up(s)) {  // MMAs in flight finish before their memory goes away
+          const unsigned long long t0 = global_ns();
+          while (!mbar_try_wait(&s->o_done, (seg - 1) & 1u) && global_ns() - t0 < kWaitLimitNs) {}
+        }
+      }
+      __syncwarp();
+    } else if (warp >= 10) {
+      // ------------------------------------------------ 8-bit to 16-bit tiles
+      if (E4) {
+        const int cw = warp - 10;
+        uint32_t e = 0, tile = 0;
+        bool stop = false;  // the same in all lanes
+        do {
+          const bool two = 2 * (w.item % p.pairs) + 1 < p.halves;
+          const int T = w.t1 - w.t0;
+          for (int i = 0; i < 2 * T && !stop; ++i, ++e) {
+            bool values;
+            int t;
+            if (two) {
+              values = i & 1;
+              t = i >> 1;
+            } else {
+              values = i == 2 * T - 1 || (i > 0 && (i & 1) == 0);
+              t = !values ? (i + 1) / 2 : i == 2 * T - 1 ? T - 1 : i / 2 - 1;
+            }
+            const uint32_t slot = e % p.stages, cslot = e % kConvStages;
+            wait(s, &s->full[slot], (e / p.stages) & 1u, a.ctrl);
+            wait(s, &s->cempty[cslot], ((e / kConvStages) & 1u) ^ 1u, a.ctrl);
+            stop = __any_sync(0xffffffffu, gave_up(s));
+            if (stop) break;
+            const unsigned char* src = ring + slot * kEntry;
+            unsigned char* dst = conv + cslot * kConv;
+            const long long tok0 = static_cast<long long>(w.t0 + t) * kTile;
+            if (!values) {
+              // scales of this warp's 32 tokens; places past the end count as 0
+              const uint32_t ti = (tile + t) % kScaleRing;
+              const int x = cw * 32 + lane;
+              const int off = x / p.box * max(p.box * 4, 128) + x % p.box * 4;
+              const bool in = tok0 + x < w.total;
+              const float ks = in ? *reinterpret_cast<const float*>(src + kData + off) : 0.0f;
+              const float vs = in ? *reinterpret_cast<const float*>(src + kData + kScaleBytes + off) : 0.0f;
+              s->kscale[ti][x] = ks;
+              s->vscale[ti][x] = vs;
+              const float top = warp_max(fabsf(vs) < INFINITY ? fabsf(vs) : 0.0f);
+              if (lane == 0) s->vmax[ti][cw] = top;
+            }
+            constexpr int kLanes = DP / 16;          // lanes a row, 16 codes each
+            constexpr int kRows = 32 / kLanes;       // rows an iteration
+            const int j = lane % kLanes;
+#pragma unroll
+            for (int it = 0; it < 32 / kRows; ++it) {
+              const int row = cw * 32 + it * kRows + lane / kLanes;
+              uint4 c = *reinterpret_cast<const uint4*>(src + row * DP + j * 16);
+              const long long tok = tok0 + row;
+              if (tok >= w.total) c = make_uint4(0u, 0u, 0u, 0u);
+              if (values && tok >= w.len) {
+                // a drafted token's NaN must reach its own descendants only:
+                // it goes by the scale, which multiplies their weights alone
+                const uint32_t words[4] = {c.x, c.y, c.z, c.w};
+                bool odd = false;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                  for (int z = 0; z < 4; ++z) odd |= (words[q] >> (8 * z) & 0x7fu) == 0x7fu;
+                if (odd) {
+                  c = make_uint4(0u, 0u, 0u, 0u);
+                  s->vscale[(tile + t) % kScaleRing][row] = __int_as_float(0x7fc00000);
+                }
+              }
+              uint32_t out[8];
+              const uint32_t words[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2(
+                    static_cast<__nv_fp8x2_storage_t>(words[q >> 1] >> (16 * (q & 1))), __NV_E4M3);
+                out[q] = static_cast<uint32_t>(v.x) | static_cast<uint32_t>(v.y) << 16;
+              }
+              unsigned char* line = dst + (j / 4) * kTile * 128 + row * 128;
+              const int first = 2 * (j % 4);
+              const uint4 lo = make_uint4(out[0], out[1], out[2], out[3]);
+              const uint4 hi = make_uint4(out[4], out[5], out[6], out[7]);
+              // lanes of the second 64 columns store their halves the other
+              // way round: the two blocks share banks
+              const bool swap = j >= 4;
+              *reinterpret_cast<uint4*>(line + (((first + (swap ? 1 : 0)) ^ (row & 7)) * 16)) = swap ? hi : lo;
+              *reinterpret_cast<uint4*>(line + (((first + (swap ? 0 : 1)) ^ (row & 7)) * 16)) = swap ? lo : hi;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&s->cfull[cslot]);
+              mbar_arrive(&s->empty[slot]);
+              if (!values) mbar_arrive(&s->scale_full[(tile + t) % kScaleRing]);
+            }
+          }
+          tile += T;
+        } while (!stop && w.next(a));
+      }
+    } else {
+      // ------------------------------------------------ softmax warpgroups
+      const int g = warp >> 2, r = tid & 127;
+      const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (warp % 4)
+      const uint32_t s_addr = tmem + lane_base + g * kTile;
+      uint32_t base = 0, tile_base = 0, ns = 0, seg = 0;
+      do {
+        const int pr = w.item % p.pairs, h = w.item / p.pairs;
+        const bool two = 2 * pr + 1 < p.halves;
+        const int T = w.t1 - w.t0;
+        const int row0 = pr * 2 * kTile;
+        const int rows = min(two ? 2 * kTile : kTile, p.R - row0);
+        // ---- ancestors, missing pages, queries
+        if (w.new_b && tid < 64) {
+          const int* par = a.parent ? a.parent + static_cast<long long>(w.b) * a.N : nullptr;
+          unsigned long long m = 0ull;
+          if (tid < w.nodes) {
+            if (!par) {
+              m = tid == 63 ? ~0ull : (2ull << tid) - 1ull;
+            } else {
+              m = 1ull << tid;
+              for (int i = tid; i > 0;) {
+                const int up = __ldg(par + i);
+                if (up < 0 || up >= i) {
+                  if (w.t0 == 0) raise_flag(a.ctrl, kFlagInvalidTree);
+                  m = 0ull;
+                  break;
+                }
+                m |= 1ull << up;
+                i = up;
+              }
+            }
+          }
+          s->mask[tid] = m;
+        }
+        if (tid == 0) {
+          if (w.t0 == 0 && w.nodes > 0 && w.len + w.nodes > w.total) raise_flag(a.ctrl, kFlagCapacity);
+          s->bad[(seg + 1) & 1] = 0;
+        }
+        {
+          const long long lo = static_cast<long long>(w.t0) * kTile, hi = min(static_cast<long long>(w.t1) * kTile, w.total);
+          bool miss = false;
+          if (lo < hi)
+            for (int pi = page_of(a.c, static_cast<int>(lo)) + tid; pi <= page_of(a.c, static_cast<int>(hi - 1)); pi += 256)
+              miss |= static_cast<unsigned int>(__ldg(a.c.table + static_cast<long long>(w.b) * a.c.table_stride + pi)) >=
+                      static_cast<unsigned int>(a.c.num_pages);
+          if (miss) {
+            s->bad[seg & 1] = 1;
+            raise_flag(a.ctrl, kFlagInvalidPage);
+          }
+        }
+        {
+          constexpr int kUnits = DP / 8;  // runs of 8 elements a row
+          const int D = a.c.dim;
+          for (int i0 = 0; i0 < rows * kUnits; i0 += 256) {
+            const int i = i0 + tid;
+            const bool in = i < rows * kUnits;
+            const int rr = in ? i / kUnits : 0, j = i % kUnits;
+            const int node = (row0 + rr) / a.G, head = h * a.G + (row0 + rr) % a.G;
+            const QT* src = static_cast<const QT*>(a.q.p) + w.b * a.q.sb + node * a.q.sn + head * a.q.sh + j * 8;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (in && j * 8 < D) {
+              if (p.qvec) {
+                v = *reinterpret_cast<const uint4*>(src);
+              } else {
+                const uint16_t* x = reinterpret_cast<const uint16_t*>(src);
+                uint32_t y[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) y[q] = x[2 * q] | static_cast<uint32_t>(x[2 * q + 1]) << 16;
+                v = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+            }
+            if (p.negate) v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
+            if (E4) {
+              // a power of two brings the row's largest element to 2^14..2^15
+              float f[8];
+              load8(reinterpret_cast<const QT*>(&v), f);
+              float top = 0.0f;
+#pragma unroll
+              for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(f[q]));
+#pragma unroll
+              for (int o = 1; o < kUnits; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+              ex = max(ex, -100);
+              const bool plain = top == 0.0f || !(top < INFINITY);
+              const float up = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(14 - ex + 127) << 23);
+              if (in && j == 0) s->qscale[rr] = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(ex - 14 + 127) << 23);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) f[q] *= up;
+              store8(reinterpret_cast<__half*>(&v), f);
+            }
+            if (in)
+              *reinterpret_cast<uint4*>(qs + (rr >> 7) * kQBytes + (j >> 3) * kTile * 128 + (rr & 127) * 128 +
+                                        (((j & 7) ^ (rr & 7)) * 16)) = v;
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        softmax_sync();
+        if (tid == 0) mbar_arrive(&s->q_full);
+        const bool missing = *reinterpret_cast<volatile int*>(&s->bad[seg & 1]) != 0;
+
+        const int row = two ? g * kTile + r : r;          // row within the item
+        const bool live = row < rows;
+        const bool warp_live = (two ? g * kTile : 0) + (warp & 3) * 32 < rows;
+        const int node = live ? (row0 + row) / a.G : 0;
+        const unsigned long long mask = live ? s->mask[node] : 0ull;
+        const float c2 = E4 ? a.c2 * (live ? s->qscale[row] : 0.0f) : a.c2;
+        const uint32_t o_addr = tmem + lane_base + 2 * kTile + g * DP;
+        float M = -INFINITY, l = 0.0f;
+        int vexp = -200;  // log2 of the weights' common factor (8-bit pools)
+
+        const int U = two ? 2 * T : T;
+        for (int x = g; x < U; x += 2) {
+          const int t = two ? x >> 1 : x;
+          const long long tok0 = static_cast<long long>(w.t0 + t) * kTile;
+          const bool tail = tok0 + kTile > w.len;           // drafted tokens or the end
+          const bool masked = tail || tok0 + kTile > w.total || missing;
+          const uint32_t ti = (tile_base + t) % kScaleRing;
+          wait(s, &s->s_full[g], ns & 1u, a.ctrl);
+          ++ns;
+          if (E4) {
+            wait(s, &s->scale_full[ti], ((tile_base + t) / kScaleRing) & 1u, a.ctrl);
+            if (tail) {  // the widening of drafted tokens' values may still mark a scale
+              const uint32_t e = base + v_entry(two, t, T);
+              wait(s, &s->cfull[e % kConvStages], (e / kConvStages) & 1u, a.ctrl);
+            }
+          }
+          __syncwarp();
+          tmem_fence_after();
+          if (warp_live) {
+            uint32_t words[4] = {~0u, ~0u, ~0u, ~0u};
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const long long off = tok0 + 32 * c - w.len, lim = w.total - (tok0 + 32 * c);
+                uint32_t y = ~0u;
+                if (off >= 64) y = 0u;
+                else if (off >= 0) y = static_cast<uint32_t>(mask >> off);
+                else if (off > -32) y = static_cast<uint32_t>(mask << -off) | ((1u << -off) - 1u);
+                if (lim <= 0) y = 0u;
+                else if (lim < 32) y &= (1u << lim) - 1u;
+                if (missing) {
+                  bool in = false;
+                  if (lane < lim) {
+                    const int pi = page_of(a.c, static_cast<int>(tok0 + 32 * c + lane));
+                    in = static_cast<unsigned int>(__ldg(a.c.table + static_cast<long long>(w.b) * a.c.table_stride + pi)) <
+                         static_cast<unsigned int>(a.c.num_pages);
+                  }
+                  y &= __ballot_sync(0xffffffffu, in);
+                }
+                words[c] = y;
+              }
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[32];
+              tmem_ld32(s_addr + c * 32, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                float f = __uint_as_float(v[i]);
+                if (E4) f *= s->kscale[ti][c * 32 + i];
+                if (masked) f = words[c] >> i & 1u ? f : -INFINITY;
+                top = fmaxf(top, f);
+              }
+            }
+            top = top == -INFINITY ? -INFINITY : top * c2;
+            bool raise;
+            float Mn = M;
+            if (E4) {
+              const float vm = fmaxf(fmaxf(s->vmax[ti][0], s->vmax[ti][1]), fmaxf(s->vmax[ti][2], s->vmax[ti][3]));
+              const int ve = max(vexp, min(max(static_cast<int>(__float_as_uint(vm) >> 23) - 126, -60), 100));  // vm <= 2^ve
+              raise = top > M - vexp + kLazy || ve > vexp;
+              if (__any_sync(0xffffffffu, raise)) Mn = fmaxf(M - vexp, top) + ve;
+              vexp = ve;
+            } else {
+              raise = top > M + kLazy;
+              if (__any_sync(0xffffffffu, raise)) Mn = fmaxf(M, top);
+            }
+            if (Mn != M) {
+              const float f = M == -INFINITY ? 0.0f : ex2f(M - Mn);
+              l *= f;
+            }
+            // the first tile's product overwrites O
+            if (x > 1 && __any_sync(0xffffffffu, Mn != M)) {
+              const float f = M == -INFINITY ? 0.0f : Mn == M ? 1.0f : ex2f(M - Mn);
+#pragma unroll
+              for (int c = 0; c < DP / 32; ++c) {
+                uint32_t v[32];
+                tmem_ld32(o_addr + c * 32, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(v[i]) * f);
+                tmem_st32(o_addr + c * 32, v);
+              }
+            }
+            M = Mn;
+            const float shift = M == -INFINITY ? 0.0f : M;
+            float sum = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[32], out[16];
+              tmem_ld32(s_addr + c * 32, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                float pw[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  float f = __uint_as_float(v[i + z]);
+                  if (E4) f *= s->kscale[ti][c * 32 + i + z];
+                  f = ex2f(fmaf(f, c2, -shift));
+                  if (masked) f = words[c] >> (i + z) & 1u ? f : 0.0f;
+                  sum += f;
+                  if (E4) {
+                    f *= s->vscale[ti][c * 32 + i + z];
+                    if (masked) f = words[c] >> (i + z) & 1u ? f : 0.0f;
+                  }
+                  pw[z] = f;
+                }
+                out[i >> 1] = pack_weights<MT>(pw[0], pw[1]);
+              }
+              tmem_st16(s_addr + c * 16, out);
+            }
+            l += sum;
+            tmem_wait_st();
+          }
+          if (!E4 && tail && (!two || g == 0)) {
+            // Values of places past the end may be anything: zeros, so that a
+            // zero weight stays zero.  A drafted token's infinities and NaN
+            // are taken out as well and added by hand to the rows that see it.
+            const uint32_t e = base + v_entry(two, t, T), slot = e % p.stages;
+            wait(s, &s->full[slot], (e / p.stages) & 1u, a.ctrl);
+            const long long tok = tok0 + r;
+            if (tok >= w.len) {
+              unsigned char* line = ring + slot * kEntry + r * 128;
+#pragma unroll 1
+              for (int c = 0; c < kChunks; ++c)
+#pragma unroll 1
+                for (int q = 0; q < 8; ++q) {
+                  uint4* at = reinterpret_cast<uint4*>(line + c * kTile * 128 + q * 16);
+                  if (tok >= w.total) {
+                    *at = make_uint4(0u, 0u, 0u, 0u);
+                  } else {
+                    uint4 v = *at;
+                    uint32_t y[4] = {v.x, v.y, v.z, v.w};
+                    bool odd = false;
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) odd |= odd_word<MT>(y[z]);
+                    if (odd) {
+#pragma unroll
+                      for (int z = 0; z < 4; ++z) {
+                        if (odd_word<MT>(y[z] & 0xffffu)) y[z] &= 0xffff0000u;
+                        if (odd_word<MT>(y[z] & 0xffff0000u)) y[z] &= 0xffffu;
+                      }
+                      *at = make_uint4(y[0], y[1], y[2], y[3]);
+                      atomicOr(&s->odd[(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
+                    }
+                  }
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s->p_ready[g]);
+        }
+
+        // ---- the segment's end: join the two groups, write
+        wait(s, &s->o_done, seg & 1u, a.ctrl);
+        __syncwarp();
+        tmem_fence_after();
+        if (mask == 0ull) M = -INFINITY, l = 0.0f;
+        s->ml[g][r] = make_float2(M, l);
+        softmax_sync();
+        const unsigned int odd0 = E4 ? 0u : s->odd[0], odd1 = E4 ? 0u : s->odd[1];
+        if (warp_live) {
+          float f0 = 1.0f, f1 = 0.0f;
+          if (!two) {
+            const float2 x0 = s->ml[0][r], x1 = s->ml[1][r];
+            M = fmaxf(x0.x, x1.x);
+            // a NaN sum comes with a maximum of -inf when every score was NaN
+            f0 = x0.x == M ? 1.0f : ex2f(x0.x - M);
+            f1 = x1.x == M ? 1.0f : ex2f(x1.x - M);
+            if (T < 2) f1 = 0.0f;
+            l = x0.y * f0 + (T < 2 ? 0.0f : x1.y * f1);
+          }
+          const bool whole = w.whole();
+          const bool none = mask == 0ull || l == 0.0f;
+          const float inv = none ? 0.0f : whole ? 1.0f / l : 1.0f;
+          const int col0 = two ? 0 : g * (DP / 2), ncol = two ? DP : DP / 2;
+          const int D = a.c.dim, head = h * a.G + (row0 + row) % a.G;
+          const long long out_row = (static_cast<long long>(w.b) * a.N + node) * a.Hq + head;
+          const int slot = 2 * cta + (w.first ? 0 : 1);
+          float* part = static_cast<float*>(a.scratch) +
+                        (static_cast<size_t>(slot) * p.qtiles + (row >> 7)) * slot_floats(DP);
+#pragma unroll 1
+          for (int c = 0; c < ncol; c += 32) {
+            uint32_t v[32], v1[32];
+            const uint32_t at = tmem + lane_base + 2 * kTile + col0 + c;
+            __syncwarp();
+            tmem_ld32(at + (two ? g * DP : 0), v);
+            if (!two) tmem_ld32(at + DP, v1);
+            tmem_wait_ld();
+            if (live) {
+              float o[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                float y = f0 == 0.0f ? 0.0f : __uint_as_float(v[i]) * f0;
+                if (!two && f1 != 0.0f) y = fmaf(__uint_as_float(v1[i]), f1, y);
+                o[i] = none ? 0.0f : y * inv;
+              }
+              if (!E4 && (odd0 | odd1) && !none) {
+                // weight times an infinity or a NaN: itself, whatever the weight
+                for (unsigned long long m = mask & (static_cast<unsigned long long>(odd1) << 32 | odd0); m; m &= m - 1) {
+                  const long long tok = w.len + __ffsll(static_cast<long long>(m)) - 1;
+                  int page, place;
+                  if (tok >= w.total || !find_place(a.c, w.b, tok, page, place, nullptr)) continue;
+                  const QT* x = static_cast<const QT*>(a.c.v) + page * a.c.page_stride + place * a.c.token_stride +
+                                h * a.c.head_stride + col0 + c;
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) {
+                    const float y = col0 + c + i < D ? elem_f32(x[i]) : 0.0f;
+                    if (!isfinite(y)) o[i] += y;
+                  }
+                }
+              }
+              if (whole) {
+                QT* dst = static_cast<QT*>(a.out) + out_row * D + col0 + c;
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                  if (col0 + c + i < D) {
+                    const float y[8] = {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]};
+                    store8(dst + i, y);
+                  }
+                }
+              } else {
+                float4* dst = reinterpret_cast<float4*>(part) + static_cast<size_t>((col0 + c) / 4) * kTile + (row & 127);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) dst[i / 4 * kTile] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              }
+            }
+          }
+          if (live && (two || g == 0)) {
+            if (whole) {
+              if (a.lse) a.lse[out_row] = none ? -INFINITY : (M + log2f(l)) * kLn2;
+            } else {
+              float2* ml = reinterpret_cast<float2*>(part + static_cast<size_t>(kTile) * DP);
+              ml[row & 127] = make_float2(none ? -INFINITY : M, none ? 0.0f : l);
+            }
+          }
+        }
+        tmem_fence_before();
+        if (tid == 0) s->stop = gave_up(s);
+        softmax_sync();  // O, Q, ml, mask and odd may be overwritten now
+        if (tid < 2) s->odd[tid] = 0u;
+        base += 2 * T;
+        tile_base += T;
+        ++seg;
+      } while (!*reinterpret_cast<volatile int*>(&s->stop) && w.next(a));
+    }
+  }
+  __syncthreads();
+  if (warp == 9) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// ----------------------------------------------------------------- joining
+//
+// Block j looks at the boundary between shares j and j + 1.  The blocks whose
+// boundaries cut one item share its rows' columns (runs of 8), so that each
+// reads about as much as one share wrote.
+template <typename QT, int DP>
+__global__ void __launch_bounds__(256) attention_join_kernel(const MmaParams p, int grid) {
+  griddep_wait();
+  __shared__ long long sums[256];
+  __shared__ Found found;
+  const AttnParams& a = p.a;
+  const int per_b = a.c.heads * p.pairs;
+  const int j = blockIdx.x + 1;
+  find_tile(a, per_b, sums, &found, [&](long long T) {
+    const Split sp{T, static_cast<int>(min(static_cast<long long>(grid), T))};
+    return j < sp.n ? sp.start(j) : -1;
+  });
+  const Split split{found.T, static_cast<int>(min(static_cast<long long>(grid), found.T))};
+  if (j >= split.n) return;
+  const int b = found.b;
+  const int tiles = tiles_of(a, b);
+  const int item = static_cast<int>(found.rem / tiles);
+  const int into = static_cast<int>(found.rem - static_cast<long long>(item) * tiles);
+  if (into == 0) return;  // between two items
+  const long long lo = split.start(j) - into, hi = lo + tiles;
+  int first = j, last = j;  // boundaries inside the item
+  while (first > 1 && split.start(first - 1) > lo) --first;
+  while (last + 1 < split.n && split.start(last + 1) < hi) ++last;
+  const int parts = last - first + 2;
+  const int pr = item % p.pairs, h = item / p.pairs;
+  const bool two = 2 * pr + 1 < p.halves;
+  const int row0 = pr * 2 * kTile;
+  const int rows = min(two ? 2 * kTile : kTile, p.R - row0);
+  const int D = a.c.dim;
+  const int units = rows * (D / 8), blocks = last - first + 1, me = j - first;
+  const int u0 = static_cast<int>(static_cast<long long>(units) * me / blocks);
+  const int u1 = static_cast<int>(static_cast<long long>(units) * (me + 1) / blocks);
+  const size_t tile = slot_floats(DP);
+  const float* scratch = static_cast<const float*>(a.scratch);
+  const int slot0 = 2 * (first - 1) + (split.start(first - 1) < lo ? 1 : 0);
+  const auto part = [&](int i, int row) {
+    const int slot = i == 0 ? slot0 : 2 * (first - 1 + i);
+    return scratch + (static_cast<size_t>(slot) * p.qtiles + (row >> 7)) * tile;
+  };
+  for (int i = u0 + threadIdx.x; i < u1; i += 256) {
+    const int row = i % rows, c = i / rows;
+    float M = -INFINITY;
+    for (int x = 0; x < parts; ++x)
+      M = fmaxf(M, reinterpret_cast<const float2*>(part(x, row) + static_cast<size_t>(kTile) * DP)[row & 127].x);
+    float L = 0.0f, o[8] = {};
+#pragma unroll 4
+    for (int x = 0; x < parts; ++x) {
+      const float* q = part(x, row);
+      const float2 ml = reinterpret_cast<const float2*>(q + static_cast<size_t>(kTile) * DP)[row & 127];
+      const float4 y0 = reinterpret_cast<const float4*>(q)[static_cast<size_t>(2 * c) * kTile + (row & 127)];
+      const float4 y1 = reinterpret_cast<const float4*>(q)[static_cast<size_t>(2 * c + 1) * kTile + (row & 127)];
+      const float f = ml.x == M ? 1.0f : ex2f(ml.x - M);
+      if (ml.y == 0.0f) continue;
+      L = fmaf(ml.y, f, L);
+      if (f == 0.0f) continue;
+      o[0] = fmaf(y0.x, f, o[0]), o[1] = fmaf(y0.y, f, o[1]), o[2] = fmaf(y0.z, f, o[2]), o[3] = fmaf(y0.w, f, o[3]);
+      o[4] = fmaf(y1.x, f, o[4]), o[5] = fmaf(y1.y, f, o[5]), o[6] = fmaf(y1.z, f, o[6]), o[7] = fmaf(y1.w, f, o[7]);
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) o[x] *= inv;
+    const int node = (row0 + row) / a.G, head = h * a.G + (row0 + row) % a.G;
+    const long long out_row = (static_cast<long long>(b) * a.N + node) * a.Hq + head;
+    store8(static_cast<QT*>(a.out) + out_row * D + c * 8, o);
+    if (a.lse && c == 0) a.lse[out_row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+  }
+}
+
+// --------------------------------------------------------------- launching
+
+namespace {
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+  static EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// One of the pool's tensors: (element, place, head, page), the place and head
+// axes ordered by their strides.
+bool pool_map(CUtensorMap* m, const CacheView& c, void* base, int dtype, int box, bool head_first) {
+  const int es = dtype == 3 ? 1 : 2;
+  const CUtensorMapDataType type = dtype == 3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const int dp = c.dim <= 64 ? 64 : 128;
+  cuuint64_t dim[4] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.page_size),
+                       static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.num_pages)};
+  cuuint64_t st[3] = {static_cast<cuuint64_t>(c.token_stride) * es, static_cast<cuuint64_t>(c.head_stride) * es,
+                      static_cast<cuuint64_t>(c.page_stride) * es};
+  // an axis of one entry may have any stride: give it a valid one
+  for (int i = 0; i < 3; ++i)
+    if (dim[i + 1] == 1) st[i] = (i == 0 ? static_cast<cuuint64_t>(dp) * es : st[i - 1]);
+  cuuint32_t bx[4] = {static_cast<cuuint32_t>(dtype == 3 ? dp : 64), static_cast<cuuint32_t>(box), 1, 1};
+  if (head_first) {
+    const cuuint64_t d = dim[1];
+    dim[1] = dim[2], dim[2] = d;
+    const cuuint64_t s = st[0];
+    st[0] = st[1], st[1] = s;
+    bx[2] = bx[1], bx[1] = 1;
+  }
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return encoder()(m, type, 4, base, dim, st, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   dtype == 3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool scale_map(CUtensorMap* m, const CacheView& c, void* base, int box) {
+  const cuuint64_t dim[3] = {static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.heads),
+                             static_cast<cuuint64_t>(c.num_pages)};
+  const cuuint64_t st[2] = {static_cast<cuuint64_t>(c.page_size) * 4, static_cast<cuuint64_t>(c.page_size) * c.heads * 4};
+  const cuuint32_t bx[3] = {static_cast<cuuint32_t>(box), 1, 1}, one[3] = {1, 1, 1};
+  return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dim, st, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename QT, int DP, bool E4>
+cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[4], int grid, cudaStream_t st) {
+  constexpr int kQBytes = kTile * DP * 2;
+  constexpr int kEntry = E4 ? kTile * DP + 2 * 16 * 128 : kTile * DP * 2;
+  constexpr int kLimit = 227 * 1024;
+  const int fixed = p.qtiles * kQBytes + (E4 ? kConvStages * kTile * DP * 2 : 0) + static_cast<int>(sizeof(Control));
+  p.stages = (kLimit - fixed) / kEntry;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  const size_t smem = fixed + static_cast<size_t>(p.stages) * kEntry;
+  const auto kernel = attention_mma_kernel<QT, DP, E4>;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLimit);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev] = true;
+  }
+  e = counted(launch_k(SV_PDL >= 2, kernel, dim3(grid), dim3(E4 ? 448 : 320), smem, st, p, maps[0], maps[1], maps[2],
+                       maps[3]),
+              1);
+  if (e != cudaSuccess || grid < 2) return e;
+  return counted(launch_k(SV_PDL >= 1, attention_join_kernel<QT, DP>, dim3(grid - 1), dim3(256), 0, st, p, grid), 1);
+}
+
+}  // namespace
+
+size_t attention_scratch_bytes(int N, int G, int dim) {
+  const int halves = (N * G + kTile - 1) / kTile;
+  return static_cast<size_t>(2 * kMaxCtas) * (halves > 1 ? 2 : 1) * slot_floats(dim <= 64 ? 64 : 128) * 4;
+}
+
+bool attention_mma_takes(const AttnParams& a, int cache_dtype) {
+  const CacheView& c = a.c;
+  const int es = cache_dtype == 3 ? 1 : 2;
+  const auto on16 = [&](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  if (c.dim > 128 || c.dim * es % 16 || c.dim % 8 || c.page_size % 8 || !encoder()) return false;
+  if (!on16(c.k) || !on16(c.v) || !on16(a.out) || (cache_dtype == 3 && (!on16(c.ks) || !on16(c.vs)))) return false;
+  const auto ok = [&](long long stride, int n) { return n == 1 || (stride > 0 && stride * es % 16 == 0 && stride * es < (1ll << 40)); };
+  return ok(c.token_stride, c.page_size) && ok(c.head_stride, c.heads) && ok(c.page_stride, c.num_pages);
+}
+
+cudaError_t launch_attention_mma(const AttnParams& a, int q_dtype, int cache_dtype, int sms, cudaStream_t st) {
+  MmaParams p{};
+  p.a = a;
+  p.R = a.N * a.G;
+  p.halves = (p.R + kTile - 1) / kTile;
+  p.pairs = (p.halves + 1) / 2;
+  p.qtiles = p.halves > 1 ? 2 : 1;
+  p.box = 8;
+  while (p.box < kTile && a.c.page_size % (2 * p.box) == 0) p.box *= 2;
+  p.head_first = a.c.heads > 1 && a.c.page_size > 1 && a.c.head_stride < a.c.token_stride;
+  p.negate = a.c2 < 0.0f;
+  p.a.c2 = a.c2 < 0.0f ? -a.c2 : a.c2;
+  p.qvec = reinterpret_cast<uintptr_t>(a.q.p) % 16 == 0 && a.q.sb % 8 == 0 && a.q.sn % 8 == 0 && a.q.sh % 8 == 0;
+  CUtensorMap maps[4] = {};
+  bool ok = pool_map(&maps[0], a.c, a.c.k, cache_dtype, p.box, p.head_first) &&
+            pool_map(&maps[1], a.c, a.c.v, cache_dtype, p.box, p.head_first);
+  if (cache_dtype == 3) ok = ok && scale_map(&maps[2], a.c, a.c.ks, p.box) && scale_map(&maps[3], a.c, a.c.vs, p.box);
+  if (!ok) return cudaErrorInvalidValue;
+  // no more blocks than tiles there can be
+  const long long per_seq = (static_cast<long long>(a.c.max_pages) * a.c.page_size + kTile - 1) / kTile;
+  const long long most = static_cast<long long>(a.B) * a.c.heads * p.pairs * per_seq;
+  int grid = sms < kMaxCtas ? sms : kMaxCtas;
+  if (most < grid) grid = static_cast<int>(most);
+  const bool wide = a.c.dim > 64, e4 = cache_dtype == 3;
+  if (q_dtype == 1) {
+    if (e4) return wide ? launch_mma<__nv_bfloat16, 128, true>(p, maps, grid, st) : launch_mma<__nv_bfloat16, 64, true>(p, maps, grid, st);
+    return wide ? launch_mma<__nv_bfloat16, 128, false>(p, maps, grid, st) : launch_mma<__nv_bfloat16, 64, false>(p, maps, grid, st);
+  }
+  if (e4) return wide ? launch_mma<__half, 128, true>(p, maps, grid, st) : launch_mma<__half, 64, true>(p, maps, grid, st);
+  return wide ? launch_mma<__half, 128, false>(p, maps, grid, st) : launch_mma<__half, 64, false>(p, maps, grid, st);
+}
+
+}  // namespace sv

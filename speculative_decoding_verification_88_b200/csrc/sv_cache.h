@@ -98,5 +98,10 @@ cudaError_t launch_cache_commit(const CacheCommitParams& p, int elem_bytes, bool
                                 cudaStream_t st);
 cudaError_t launch_attention_plain(const AttnParams& p, int q_dtype, int cache_dtype,
                                    cudaStream_t st);
+// The tensor-core form: whether it takes this layout, its scratch, its launch.
+bool attention_mma_takes(const AttnParams& p, int cache_dtype);
+size_t attention_scratch_bytes(int N, int G, int dim);
+cudaError_t launch_attention_mma(const AttnParams& p, int q_dtype, int cache_dtype, int sms,
+                                 cudaStream_t st);
 
 }  // namespace sv

@@ -233,7 +233,8 @@ extern "C" size_t spec_verify_tree_attention_scratch_size(int B, int N, int Hq, 
   if (B < 0 || B > 65535 || N < 1 || N > 64 || num_heads < 1 || Hq < 1 || Hq > 1024 || Hq % num_heads ||
       head_dim < 1 || head_dim > 256)
     return 0;
-  return 256;
+  const size_t n = head_dim <= 128 ? attention_scratch_bytes(N, Hq / num_heads, head_dim) : 256;
+  return (n + 255) / 256 * 256;
 }
 
 extern "C" int spec_verify_tree_attention(const sv_rows* q, int q_dtype, const sv_kv_cache* cache,
@@ -260,7 +261,14 @@ extern "C" int spec_verify_tree_attention(const sv_rows* q, int q_dtype, const s
   p.B = B, p.N = N, p.Hq = Hq, p.G = Hq / cache->num_heads;
   p.c2 = static_cast<float>(1.4426950408889634 * scale);
   p.out = out, p.lse = lse, p.ctrl = ctrl_of(workspace), p.scratch = scratch;
-  return launch_attention_plain(p, q_dtype, cache->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? SV_OK
-             : SV_ERR_CUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (attention_mma_takes(p, cache->dtype)) {
+    const int n = sms();
+    if (n <= 0) return SV_ERR_CUDA;
+    e = launch_attention_mma(p, q_dtype, cache->dtype, n, st);
+  } else {
+    e = launch_attention_plain(p, q_dtype, cache->dtype, st);
+  }
+  return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
