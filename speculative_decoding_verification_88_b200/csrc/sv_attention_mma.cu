@@ -29,6 +29,7 @@
 // weights by a power of two that follows the largest scale of V.
 #include <cuda.h>
 
+#include <initializer_list>
 #include <type_traits>
 
 #include "sv_cache_device.cuh"
@@ -66,6 +67,7 @@ struct MmaParams {
   int qtiles;   // Q tiles in shared memory: 1 or 2
   int negate;   // the scale is negative: Q is negated instead
   int qvec;     // query rows start on 16-byte boundaries
+  UDiv div_G;   // / a.G
 };
 
 namespace {
@@ -232,34 +234,22 @@ __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 32 columns of this warp's lanes.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+// 16 columns of this warp's lanes; 16 or 8 back.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // Two weights in the values' 16-bit type.
@@ -275,6 +265,13 @@ template <>
 __device__ __forceinline__ uint32_t pack_weights<__half>(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// Two codes as 16-bit floats (exact).
+__device__ __forceinline__ uint32_t half_pair(uint16_t codes) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(codes));
   return d;
 }
 
@@ -300,10 +297,11 @@ struct Control {
   int stop;              // abort, as the softmax warpgroups agreed on it
   int bad[2];            // a page of the segment is missing (by segment parity)
   unsigned int odd[2];   // tree tokens whose values hold an infinity or a NaN
-  unsigned long long mask[64];
+  int parent[64];
   float qscale[2 * kTile];
   float2 ml[2][kTile];
-  float kscale[kScaleRing][kTile], vscale[kScaleRing][kTile];
+  alignas(16) float kscale[kScaleRing][kTile];
+  alignas(16) float vscale[kScaleRing][kTile];
   float vmax[kScaleRing][4];
   long long sums[256];
   Found found;
@@ -311,8 +309,7 @@ struct Control {
 
 // Bounded wait; once one has run out, every wait of the block returns at once
 // and the roles run to their ends on whatever is there.
-__device__ __forceinline__ void wait(Control* s, uint64_t* bar, uint32_t parity, Ctrl* ctrl) {
-  if (mbar_try_wait(bar, parity)) return;
+__device__ __noinline__ void wait_long(Control* s, uint64_t* bar, uint32_t parity, Ctrl* ctrl) {
   const unsigned long long t0 = global_ns();
   for (unsigned int spin = 1;; ++spin) {
     if (mbar_try_wait(bar, parity)) return;
@@ -326,13 +323,113 @@ __device__ __forceinline__ void wait(Control* s, uint64_t* bar, uint32_t parity,
     }
   }
 }
+__device__ __forceinline__ void wait(Control* s, uint64_t* bar, uint32_t parity, Ctrl* ctrl) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return;
+  wait_long(s, bar, parity, ctrl);
+}
 __device__ __forceinline__ bool gave_up(const Control* s) { return *reinterpret_cast<const volatile int*>(&s->abort) != 0; }
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+// Largest score of a row's tile (times K's scales; -inf where all is masked).
+// Both passes over a tile read 16 columns ahead of the arithmetic.
+template <bool E4, bool MASK>
+__device__ __forceinline__ float tile_max(uint32_t s_addr, const float* ks, const uint32_t (&words)[4]) {
+  float top[2] = {-INFINITY, -INFINITY};
+  uint32_t v[2][16];
+  tmem_ld16(s_addr, v[0]);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    tmem_wait_ld();
+    if (c < 7) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      float f[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) f[z] = __uint_as_float(v[c & 1][i + z]);
+      if (E4) {
+        const float4 k = *reinterpret_cast<const float4*>(ks + c * 16 + i);
+        f[0] *= k.x, f[1] *= k.y, f[2] *= k.z, f[3] *= k.w;
+      }
+      if (MASK) {
+#pragma unroll
+        for (int z = 0; z < 4; ++z) f[z] = words[c >> 1] >> ((c & 1) * 16 + i + z) & 1u ? f[z] : -INFINITY;
+      }
+      top[0] = fmax3(top[0], f[0], f[1]);
+      top[1] = fmax3(top[1], f[2], f[3]);
+    }
+  }
+  return fmaxf(top[0], top[1]);
+}
+
+// Weights 2^(s c2 - shift) of a row's tile into tensor memory over the
+// scores (times V's scales); returns their sum (without the scales).
+template <typename M, bool E4, bool MASK>
+__device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, const float* vs,
+                                              const uint32_t (&words)[4], float c2, float shift) {
+  const unsigned long long c22 = splat2(c2), sh2 = splat2(-shift);
+  unsigned long long sum[2] = {0ull, 0ull};
+  uint32_t v[2][16];
+  tmem_ld16(s_addr, v[0]);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint32_t out[8];
+    tmem_wait_ld();
+    if (c < 7) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const uint32_t* w = &v[c & 1][i];
+      unsigned long long x = pack2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+      unsigned long long y = pack2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+      if (E4) {
+        const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(ks + c * 16 + i);
+        x = mul2(x, k.x);
+        y = mul2(y, k.y);
+      }
+      x = fma2(x, c22, sh2);
+      y = fma2(y, c22, sh2);
+      float f[4];
+      unpack2(x, f[0], f[1]);
+      unpack2(y, f[2], f[3]);
+      bool on[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        on[z] = !MASK || (words[c >> 1] >> ((c & 1) * 16 + i + z) & 1u);
+        f[z] = ex2f(f[z]);
+        if (MASK) f[z] = on[z] ? f[z] : 0.0f;
+      }
+      x = pack2(f[0], f[1]);
+      y = pack2(f[2], f[3]);
+      sum[0] = add2(sum[0], x);
+      sum[1] = add2(sum[1], y);
+      if (E4) {
+        const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(vs + c * 16 + i);
+        unpack2(mul2(x, k.x), f[0], f[1]);
+        unpack2(mul2(y, k.y), f[2], f[3]);
+        if (MASK) {
+#pragma unroll
+          for (int z = 0; z < 4; ++z) f[z] = on[z] ? f[z] : 0.0f;
+        }
+      }
+      out[i >> 1] = pack_weights<M>(f[0], f[1]);
+      out[(i >> 1) + 1] = pack_weights<M>(f[2], f[3]);
+    }
+    tmem_st8(s_addr + c * 8, out);
+  }
+  float a, b, d, e;
+  unpack2(sum[0], a, b);
+  unpack2(sum[1], d, e);
+  return (a + b) + (d + e);
+}
+
+__device__ __forceinline__ int div_rows(int n, const UDiv& d) {
+  return d.m == 0u ? n : static_cast<int>(__umulhi(static_cast<unsigned int>(n), d.m) >> d.shift);
+}
+
 // Ring entries of a segment of T tiles, in the order the MMA warp needs them:
 // alternate tiles (one row tile): K0 K1 V0 K2 V1 ...; two row tiles: K0 V0 K1 V1 ...
-__device__ __forceinline__ int k_entry(bool two, int t) { return two ? 2 * t : t == 0 ? 0 : 2 * t - 1; }
 __device__ __forceinline__ int v_entry(bool two, int t, int T) { return two ? 2 * t + 1 : t == T - 1 ? 2 * T - 1 : 2 * t + 2; }
 
 }  // namespace
@@ -365,6 +462,10 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per_b = a.c.heads * p.pairs;
 
+  if (tid == 288) {
+    for (const CUtensorMap* m : {&kmap, &vmap, &ksmap, &vsmap})
+      asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+  }
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&s->full[i], 1);
@@ -411,7 +512,7 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
     if (warp == 8) {
       // ------------------------------------------------ producer: TMA loads
       const int nbox = kTile / p.box;
-      uint32_t e = 0;  // ring entries filled
+      uint32_t e = 0, slot = 0, phase = 0;  // ring entries filled, the next one's place
       bool stop = false;  // the same in all lanes
       do {
         const bool two = 2 * (w.item % p.pairs) + 1 < p.halves;
@@ -432,7 +533,6 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
         };
         const auto load = [&](bool values, int page, int place) {
           if (stop) return;
-          const uint32_t slot = e % p.stages, phase = (e / p.stages) & 1u;
           wait(s, &s->empty[slot], phase ^ 1u, a.ctrl);
           if (__any_sync(0xffffffffu, gave_up(s))) stop = true;
           if (stop) return;
@@ -457,6 +557,7 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
             }
           }
           ++e;
+          if (++slot == static_cast<uint32_t>(p.stages)) slot = 0, phase ^= 1u;
         };
         int pg0, pl0, pg1, pl1;
         locate(0, pg0, pl0);
@@ -483,54 +584,59 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
     } else if (warp == 9) {
       // ------------------------------------------------ MMA issue (one thread)
       if (lane == 0) {
-        uint32_t base = 0;  // ring entries of earlier segments
-        uint32_t seg = 0, np[2] = {0, 0};
         const uint32_t stages = E4 ? kConvStages : p.stages;
-        const uint32_t tiles = smem_addr(E4 ? conv : ring);
         constexpr uint32_t kStep = E4 ? kConv : kEntry;
-        uint64_t* fullb = E4 ? s->cfull : s->full;
-        uint64_t* emptyb = E4 ? s->cempty : s->empty;
+        uint64_t* const fullb = E4 ? s->cfull : s->full;
+        uint64_t* const emptyb = E4 ? s->cempty : s->empty;
+        // The ring is read in its own order; a tile stays until its last product.
+        uint32_t next = 0, next_phase = 0, kslot = 0, vslot = 0;
+        const auto take = [&](uint32_t& slot) {
+          slot = next;
+          wait(s, &fullb[slot], next_phase, a.ctrl);
+          if (++next == stages) next = 0, next_phase ^= 1u;
+        };
+        const uint64_t q0 = operand(smem_addr(qs), 16, 1024);
+        const uint64_t k0 = operand(smem_addr(E4 ? conv : ring), 16, 1024);
+        const uint64_t v0 = operand(smem_addr(E4 ? conv : ring), kTile * 128, 1024);
+        uint32_t seg = 0, np = 0;  // np: phases of p_ready, one bit a warpgroup
         do {
           const bool two = 2 * (w.item % p.pairs) + 1 < p.halves;
           const int T = w.t1 - w.t0, U = two ? 2 * T : T;
           wait(s, &s->q_full, seg & 1u, a.ctrl);
-          for (int x = 0; x <= U && !gave_up(s); ++x) {
+#pragma unroll 1
+          for (int x = 0; x <= U; ++x) {
+            const uint32_t g = x & 1;
+            const bool shared = two && g == 1;  // the second user of this tile
             if (x < U) {
-              const int g = x & 1, t = two ? x >> 1 : x;
-              const uint32_t e = base + k_entry(two, t), slot = e % stages;
-              wait(s, &fullb[slot], (e / stages) & 1u, a.ctrl);
+              if (!shared) take(kslot);
               tmem_fence_after();
-              if (gave_up(s)) break;
-              const uint64_t qd = operand(smem_addr(qs) + (two && g ? kQBytes : 0), 16, 1024);
-              const uint64_t kd = operand(tiles + slot * kStep, 16, 1024);
+              const uint64_t qd = q0 + (shared ? kQBytes >> 4 : 0);
+              const uint64_t kd = k0 + kslot * (kStep >> 4);
 #pragma unroll
               for (int k = 0; k < DP / 16; ++k) {
                 // 16 elements are 32 bytes of a 128-byte row; 64 are the next block of rows
-                const uint64_t step = static_cast<uint64_t>(k / 4) * (kTile * 128 >> 4) + (k % 4) * 2;
+                const uint32_t step = (k / 4) * (kTile * 128 >> 4) + (k % 4) * 2;
                 mma_ss(tmem + g * kTile, qd + step, kd + step, kShapeS, k > 0);
               }
               mma_commit(&s->s_full[g]);
-              if (!two || g == 1) mma_commit(&emptyb[slot]);
+              if (!two || g == 1) mma_commit(&emptyb[kslot]);
             }
             if (x > 0) {
-              const int v = x - 1, g = v & 1, t = two ? v >> 1 : v;
-              const uint32_t e = base + v_entry(two, t, T), slot = e % stages;
-              wait(s, &fullb[slot], (e / stages) & 1u, a.ctrl);
-              wait(s, &s->p_ready[g], np[g] & 1u, a.ctrl);
-              ++np[g];
+              const uint32_t f = g ^ 1u;  // unit x - 1
+              if (!two || f == 0) take(vslot);
+              wait(s, &s->p_ready[f], np >> f & 1u, a.ctrl);
+              np ^= 1u << f;
               tmem_fence_after();
-              if (gave_up(s)) break;
-              const uint64_t vd = operand(tiles + slot * kStep, kTile * 128, 1024);
-              const uint32_t o = tmem + 2 * kTile + g * DP;
+              const uint64_t vd = v0 + vslot * (kStep >> 4);
+              const uint32_t o = tmem + 2 * kTile + f * DP;
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k)
-                mma_ts(o, tmem + g * kTile + k * 8, vd + static_cast<uint64_t>(k) * (16 * 128 >> 4), kShapeO,
-                       v > 1 || k > 0);
-              if (!two || g == 1) mma_commit(&emptyb[slot]);
+                mma_ts(o, tmem + f * kTile + k * 8, vd + k * (16 * 128 >> 4), kShapeO, x > 2 || k > 0);
+              if (!two || f == 1) mma_commit(&emptyb[vslot]);
             }
+            if (gave_up(s)) break;
           }
           mma_commit(&s->o_done);
-          base += 2 * T;
           ++seg;
         } while (!gave_up(s) && w.next(a));
         if (gave_up(s)) {  // MMAs in flight finish before their memory goes away
@@ -543,12 +649,20 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
       // ------------------------------------------------ 8-bit to 16-bit tiles
       if (E4) {
         const int cw = warp - 10;
-        uint32_t e = 0, tile = 0;
+        uint32_t slot = 0, phase = 0, cslot = 0, cphase = 0, tile = 0;
         bool stop = false;  // the same in all lanes
+        constexpr int kLanes = DP / 16;     // lanes a row, 16 codes each
+        constexpr int kRows = 32 / kLanes;  // rows an iteration
+        constexpr int kIter = 32 / kRows;
+        const int j = lane % kLanes, row0 = cw * 32 + lane / kLanes;
+        // Lanes of the second 64 columns store their halves the other way
+        // round: the two blocks share banks.  (row & 7) is the swizzle.
+        const int first = 2 * (j % 4) + (j >= 4 ? 1 : 0);
+        unsigned char* const line0 = conv + (j / 4) * kTile * 128 + row0 * 128;
         do {
           const bool two = 2 * (w.item % p.pairs) + 1 < p.halves;
           const int T = w.t1 - w.t0;
-          for (int i = 0; i < 2 * T && !stop; ++i, ++e) {
+          for (int i = 0; i < 2 * T && !stop; ++i) {
             bool values;
             int t;
             if (two) {
@@ -558,17 +672,19 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
               values = i == 2 * T - 1 || (i > 0 && (i & 1) == 0);
               t = !values ? (i + 1) / 2 : i == 2 * T - 1 ? T - 1 : i / 2 - 1;
             }
-            const uint32_t slot = e % p.stages, cslot = e % kConvStages;
-            wait(s, &s->full[slot], (e / p.stages) & 1u, a.ctrl);
-            wait(s, &s->cempty[cslot], ((e / kConvStages) & 1u) ^ 1u, a.ctrl);
+            wait(s, &s->full[slot], phase, a.ctrl);
+            wait(s, &s->cempty[cslot], cphase ^ 1u, a.ctrl);
             stop = __any_sync(0xffffffffu, gave_up(s));
             if (stop) break;
             const unsigned char* src = ring + slot * kEntry;
-            unsigned char* dst = conv + cslot * kConv;
             const long long tok0 = static_cast<long long>(w.t0 + t) * kTile;
+            const uint32_t ti = (tile + t) % kScaleRing;
+            uint4 c[kIter];
+#pragma unroll
+            for (int it = 0; it < kIter; ++it)
+              c[it] = *reinterpret_cast<const uint4*>(src + (row0 + it * kRows) * DP + j * 16);
             if (!values) {
               // scales of this warp's 32 tokens; places past the end count as 0
-              const uint32_t ti = (tile + t) % kScaleRing;
               const int x = cw * 32 + lane;
               const int off = x / p.box * max(p.box * 4, 128) + x % p.box * 4;
               const bool in = tok0 + x < w.total;
@@ -579,54 +695,50 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
               const float top = warp_max(fabsf(vs) < INFINITY ? fabsf(vs) : 0.0f);
               if (lane == 0) s->vmax[ti][cw] = top;
             }
-            constexpr int kLanes = DP / 16;          // lanes a row, 16 codes each
-            constexpr int kRows = 32 / kLanes;       // rows an iteration
-            const int j = lane % kLanes;
+            if (tok0 + kTile > w.len) {
 #pragma unroll
-            for (int it = 0; it < 32 / kRows; ++it) {
-              const int row = cw * 32 + it * kRows + lane / kLanes;
-              uint4 c = *reinterpret_cast<const uint4*>(src + row * DP + j * 16);
-              const long long tok = tok0 + row;
-              if (tok >= w.total) c = make_uint4(0u, 0u, 0u, 0u);
-              if (values && tok >= w.len) {
-                // a drafted token's NaN must reach its own descendants only:
-                // it goes by the scale, which multiplies their weights alone
-                const uint32_t words[4] = {c.x, c.y, c.z, c.w};
-                bool odd = false;
+              for (int it = 0; it < kIter; ++it) {
+                const long long tok = tok0 + row0 + it * kRows;
+                if (tok >= w.total) c[it] = make_uint4(0u, 0u, 0u, 0u);
+                if (values && tok >= w.len) {
+                  // a drafted token's NaN must reach its own descendants only:
+                  // it goes by the scale, which multiplies their weights alone
+                  const uint32_t words[4] = {c[it].x, c[it].y, c[it].z, c[it].w};
+                  bool odd = false;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                  for (int q = 0; q < 4; ++q)
 #pragma unroll
-                  for (int z = 0; z < 4; ++z) odd |= (words[q] >> (8 * z) & 0x7fu) == 0x7fu;
-                if (odd) {
-                  c = make_uint4(0u, 0u, 0u, 0u);
-                  s->vscale[(tile + t) % kScaleRing][row] = __int_as_float(0x7fc00000);
+                    for (int z = 0; z < 4; ++z) odd |= (words[q] >> (8 * z) & 0x7fu) == 0x7fu;
+                  if (odd) {
+                    c[it] = make_uint4(0u, 0u, 0u, 0u);
+                    s->vscale[ti][row0 + it * kRows] = __int_as_float(0x7fc00000);
+                  }
                 }
               }
-              uint32_t out[8];
-              const uint32_t words[4] = {c.x, c.y, c.z, c.w};
+            }
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2(
-                    static_cast<__nv_fp8x2_storage_t>(words[q >> 1] >> (16 * (q & 1))), __NV_E4M3);
-                out[q] = static_cast<uint32_t>(v.x) | static_cast<uint32_t>(v.y) << 16;
-              }
-              unsigned char* line = dst + (j / 4) * kTile * 128 + row * 128;
-              const int first = 2 * (j % 4);
+            for (int it = 0; it < kIter; ++it) {
+              const int row = row0 + it * kRows;
+              const uint32_t words[4] = {c[it].x, c[it].y, c[it].z, c[it].w};
+              uint32_t out[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q) out[q] = half_pair(static_cast<uint16_t>(words[q >> 1] >> (16 * (q & 1))));
+              unsigned char* line = line0 + cslot * kConv + it * kRows * 128;
+              const bool swap = j >= 4;
               const uint4 lo = make_uint4(out[0], out[1], out[2], out[3]);
               const uint4 hi = make_uint4(out[4], out[5], out[6], out[7]);
-              // lanes of the second 64 columns store their halves the other
-              // way round: the two blocks share banks
-              const bool swap = j >= 4;
-              *reinterpret_cast<uint4*>(line + (((first + (swap ? 1 : 0)) ^ (row & 7)) * 16)) = swap ? hi : lo;
-              *reinterpret_cast<uint4*>(line + (((first + (swap ? 0 : 1)) ^ (row & 7)) * 16)) = swap ? lo : hi;
+              *reinterpret_cast<uint4*>(line + ((first ^ (row & 7)) * 16)) = swap ? hi : lo;
+              *reinterpret_cast<uint4*>(line + (((first ^ 1) ^ (row & 7)) * 16)) = swap ? lo : hi;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
               mbar_arrive(&s->cfull[cslot]);
               mbar_arrive(&s->empty[slot]);
-              if (!values) mbar_arrive(&s->scale_full[(tile + t) % kScaleRing]);
+              if (!values) mbar_arrive(&s->scale_full[ti]);
             }
+            if (++slot == static_cast<uint32_t>(p.stages)) slot = 0, phase ^= 1u;
+            if (++cslot == kConvStages) cslot = 0, cphase ^= 1u;
           }
           tile += T;
         } while (!stop && w.next(a));
@@ -643,29 +755,8 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
         const int T = w.t1 - w.t0;
         const int row0 = pr * 2 * kTile;
         const int rows = min(two ? 2 * kTile : kTile, p.R - row0);
-        // ---- ancestors, missing pages, queries
-        if (w.new_b && tid < 64) {
-          const int* par = a.parent ? a.parent + static_cast<long long>(w.b) * a.N : nullptr;
-          unsigned long long m = 0ull;
-          if (tid < w.nodes) {
-            if (!par) {
-              m = tid == 63 ? ~0ull : (2ull << tid) - 1ull;
-            } else {
-              m = 1ull << tid;
-              for (int i = tid; i > 0;) {
-                const int up = __ldg(par + i);
-                if (up < 0 || up >= i) {
-                  if (w.t0 == 0) raise_flag(a.ctrl, kFlagInvalidTree);
-                  m = 0ull;
-                  break;
-                }
-                m |= 1ull << up;
-                i = up;
-              }
-            }
-          }
-          s->mask[tid] = m;
-        }
+        // ---- parents, missing pages, queries
+        if (w.new_b && a.parent && tid < a.N) s->parent[tid] = __ldg(a.parent + static_cast<long long>(w.b) * a.N + tid);
         if (tid == 0) {
           if (w.t0 == 0 && w.nodes > 0 && w.len + w.nodes > w.total) raise_flag(a.ctrl, kFlagCapacity);
           s->bad[(seg + 1) & 1] = 0;
@@ -683,48 +774,57 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
           }
         }
         {
-          constexpr int kUnits = DP / 8;  // runs of 8 elements a row
-          const int D = a.c.dim;
-          for (int i0 = 0; i0 < rows * kUnits; i0 += 256) {
-            const int i = i0 + tid;
-            const bool in = i < rows * kUnits;
-            const int rr = in ? i / kUnits : 0, j = i % kUnits;
-            const int node = (row0 + rr) / a.G, head = h * a.G + (row0 + rr) % a.G;
-            const QT* src = static_cast<const QT*>(a.q.p) + w.b * a.q.sb + node * a.q.sn + head * a.q.sh + j * 8;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (in && j * 8 < D) {
-              if (p.qvec) {
-                v = *reinterpret_cast<const uint4*>(src);
-              } else {
-                const uint16_t* x = reinterpret_cast<const uint16_t*>(src);
-                uint32_t y[4];
+          constexpr int kUnits = DP / 8;   // runs of 8 elements a row
+          constexpr int kStride = 256 / kUnits;  // rows a step
+          constexpr int kAhead = 4;
+          const int D = a.c.dim, j = tid % kUnits;
+          for (int r0 = tid / kUnits; r0 - tid / kUnits < rows; r0 += kAhead * kStride) {
+            uint4 q4[kAhead];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) y[q] = x[2 * q] | static_cast<uint32_t>(x[2 * q + 1]) << 16;
-                v = make_uint4(y[0], y[1], y[2], y[3]);
+            for (int z = 0; z < kAhead; ++z) {
+              const int rr = r0 + z * kStride;
+              q4[z] = make_uint4(0u, 0u, 0u, 0u);
+              if (rr < rows && j * 8 < D) {
+                const int nd = div_rows(row0 + rr, p.div_G), head = h * a.G + (row0 + rr - nd * a.G);
+                const QT* src = static_cast<const QT*>(a.q.p) + w.b * a.q.sb + nd * a.q.sn + head * a.q.sh + j * 8;
+                if (p.qvec) {
+                  q4[z] = *reinterpret_cast<const uint4*>(src);
+                } else {
+                  const uint16_t* x = reinterpret_cast<const uint16_t*>(src);
+                  uint32_t y[4];
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) y[q] = x[2 * q] | static_cast<uint32_t>(x[2 * q + 1]) << 16;
+                  q4[z] = make_uint4(y[0], y[1], y[2], y[3]);
+                }
               }
             }
-            if (p.negate) v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
-            if (E4) {
-              // a power of two brings the row's largest element to 2^14..2^15
-              float f[8];
-              load8(reinterpret_cast<const QT*>(&v), f);
-              float top = 0.0f;
 #pragma unroll
-              for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(f[q]));
+            for (int z = 0; z < kAhead; ++z) {
+              const int rr = r0 + z * kStride;
+              uint4 v = q4[z];
+              if (p.negate) v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
+              if (E4) {
+                // a power of two brings the row's largest element to 2^14..2^15
+                float f[8];
+                load8(reinterpret_cast<const QT*>(&v), f);
+                float top = 0.0f;
 #pragma unroll
-              for (int o = 1; o < kUnits; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-              int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-              ex = max(ex, -100);
-              const bool plain = top == 0.0f || !(top < INFINITY);
-              const float up = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(14 - ex + 127) << 23);
-              if (in && j == 0) s->qscale[rr] = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(ex - 14 + 127) << 23);
+                for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(f[q]));
 #pragma unroll
-              for (int q = 0; q < 8; ++q) f[q] *= up;
-              store8(reinterpret_cast<__half*>(&v), f);
+                for (int o = 1; o < kUnits; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int ex = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+                const bool plain = top == 0.0f || !(top < INFINITY);
+                const float up = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(14 - ex + 127) << 23);
+                if (rr < rows && j == 0)
+                  s->qscale[rr] = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(ex - 14 + 127) << 23);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) f[q] *= up;
+                store8(reinterpret_cast<__half*>(&v), f);
+              }
+              if (rr < rows)
+                *reinterpret_cast<uint4*>(qs + (rr >> 7) * kQBytes + (j >> 3) * kTile * 128 + (rr & 127) * 128 +
+                                          (((j & 7) ^ (rr & 7)) * 16)) = v;
             }
-            if (in)
-              *reinterpret_cast<uint4*>(qs + (rr >> 7) * kQBytes + (j >> 3) * kTile * 128 + (rr & 127) * 128 +
-                                        (((j & 7) ^ (rr & 7)) * 16)) = v;
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -735,8 +835,23 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
         const int row = two ? g * kTile + r : r;          // row within the item
         const bool live = row < rows;
         const bool warp_live = (two ? g * kTile : 0) + (warp & 3) * 32 < rows;
-        const int node = live ? (row0 + row) / a.G : 0;
-        const unsigned long long mask = live ? s->mask[node] : 0ull;
+        const int node = live ? div_rows(row0 + row, p.div_G) : 0;
+        // the node's ancestors and itself; nothing at or below an invalid parent
+        unsigned long long mask = live && node < w.nodes ? 1ull << node : 0ull;
+        if (mask && !a.parent) {
+          mask |= mask - 1ull;
+        } else if (mask) {
+          for (int i = node; i > 0;) {
+            const int up = s->parent[i];
+            if (up < 0 || up >= i) {
+              raise_flag(a.ctrl, kFlagInvalidTree);
+              mask = 0ull;
+              break;
+            }
+            mask |= 1ull << up;
+            i = up;
+          }
+        }
         const float c2 = E4 ? a.c2 * (live ? s->qscale[row] : 0.0f) : a.c2;
         const uint32_t o_addr = tmem + lane_base + 2 * kTile + g * DP;
         float M = -INFINITY, l = 0.0f;
@@ -784,20 +899,8 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
                 words[c] = y;
               }
             }
-            float top = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[32];
-              tmem_ld32(s_addr + c * 32, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                float f = __uint_as_float(v[i]);
-                if (E4) f *= s->kscale[ti][c * 32 + i];
-                if (masked) f = words[c] >> i & 1u ? f : -INFINITY;
-                top = fmaxf(top, f);
-              }
-            }
+            float top = masked ? tile_max<E4, true>(s_addr, s->kscale[ti], words)
+                               : tile_max<E4, false>(s_addr, s->kscale[ti], words);
             top = top == -INFINITY ? -INFINITY : top * c2;
             bool raise;
             float Mn = M;
@@ -818,45 +921,20 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
             // the first tile's product overwrites O
             if (x > 1 && __any_sync(0xffffffffu, Mn != M)) {
               const float f = M == -INFINITY ? 0.0f : Mn == M ? 1.0f : ex2f(M - Mn);
-#pragma unroll
-              for (int c = 0; c < DP / 32; ++c) {
-                uint32_t v[32];
-                tmem_ld32(o_addr + c * 32, v);
+#pragma unroll 2
+              for (int c = 0; c < DP / 16; ++c) {
+                uint32_t v[16];
+                tmem_ld16(o_addr + c * 16, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(v[i]) * f);
-                tmem_st32(o_addr + c * 32, v);
+                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(v[i]) * f);
+                tmem_st16(o_addr + c * 16, v);
               }
             }
             M = Mn;
             const float shift = M == -INFINITY ? 0.0f : M;
-            float sum = 0.0f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[32], out[16];
-              tmem_ld32(s_addr + c * 32, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                float pw[2];
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  float f = __uint_as_float(v[i + z]);
-                  if (E4) f *= s->kscale[ti][c * 32 + i + z];
-                  f = ex2f(fmaf(f, c2, -shift));
-                  if (masked) f = words[c] >> (i + z) & 1u ? f : 0.0f;
-                  sum += f;
-                  if (E4) {
-                    f *= s->vscale[ti][c * 32 + i + z];
-                    if (masked) f = words[c] >> (i + z) & 1u ? f : 0.0f;
-                  }
-                  pw[z] = f;
-                }
-                out[i >> 1] = pack_weights<MT>(pw[0], pw[1]);
-              }
-              tmem_st16(s_addr + c * 16, out);
-            }
-            l += sum;
+            l += masked ? tile_weights<MT, E4, true>(s_addr, s->kscale[ti], s->vscale[ti], words, c2, shift)
+                        : tile_weights<MT, E4, false>(s_addr, s->kscale[ti], s->vscale[ti], words, c2, shift);
             tmem_wait_st();
           }
           if (!E4 && tail && (!two || g == 0)) {
@@ -923,23 +1001,23 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
           const bool none = mask == 0ull || l == 0.0f;
           const float inv = none ? 0.0f : whole ? 1.0f / l : 1.0f;
           const int col0 = two ? 0 : g * (DP / 2), ncol = two ? DP : DP / 2;
-          const int D = a.c.dim, head = h * a.G + (row0 + row) % a.G;
+          const int D = a.c.dim, head = h * a.G + (row0 + row - node * a.G);
           const long long out_row = (static_cast<long long>(w.b) * a.N + node) * a.Hq + head;
           const int slot = 2 * cta + (w.first ? 0 : 1);
           float* part = static_cast<float*>(a.scratch) +
                         (static_cast<size_t>(slot) * p.qtiles + (row >> 7)) * slot_floats(DP);
-#pragma unroll 1
-          for (int c = 0; c < ncol; c += 32) {
-            uint32_t v[32], v1[32];
+#pragma unroll 2
+          for (int c = 0; c < ncol; c += 16) {
+            uint32_t v[16], v1[16];
             const uint32_t at = tmem + lane_base + 2 * kTile + col0 + c;
             __syncwarp();
-            tmem_ld32(at + (two ? g * DP : 0), v);
-            if (!two) tmem_ld32(at + DP, v1);
+            tmem_ld16(at + (two ? g * DP : 0), v);
+            if (!two) tmem_ld16(at + DP, v1);
             tmem_wait_ld();
             if (live) {
-              float o[32];
+              float o[16];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
+              for (int i = 0; i < 16; ++i) {
                 float y = f0 == 0.0f ? 0.0f : __uint_as_float(v[i]) * f0;
                 if (!two && f1 != 0.0f) y = fmaf(__uint_as_float(v1[i]), f1, y);
                 o[i] = none ? 0.0f : y * inv;
@@ -953,7 +1031,7 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
                   const QT* x = static_cast<const QT*>(a.c.v) + page * a.c.page_stride + place * a.c.token_stride +
                                 h * a.c.head_stride + col0 + c;
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) {
+                  for (int i = 0; i < 16; ++i) {
                     const float y = col0 + c + i < D ? elem_f32(x[i]) : 0.0f;
                     if (!isfinite(y)) o[i] += y;
                   }
@@ -962,7 +1040,7 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
               if (whole) {
                 QT* dst = static_cast<QT*>(a.out) + out_row * D + col0 + c;
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
+                for (int i = 0; i < 16; i += 8) {
                   if (col0 + c + i < D) {
                     const float y[8] = {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]};
                     store8(dst + i, y);
@@ -971,7 +1049,7 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
               } else {
                 float4* dst = reinterpret_cast<float4*>(part) + static_cast<size_t>((col0 + c) / 4) * kTile + (row & 127);
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) dst[i / 4 * kTile] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                for (int i = 0; i < 16; i += 4) dst[i / 4 * kTile] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
               }
             }
           }
@@ -1067,7 +1145,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const MmaParams p, 
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
     for (int x = 0; x < 8; ++x) o[x] *= inv;
-    const int node = (row0 + row) / a.G, head = h * a.G + (row0 + row) % a.G;
+    const int node = div_rows(row0 + row, p.div_G), head = h * a.G + (row0 + row - node * a.G);
     const long long out_row = (static_cast<long long>(b) * a.N + node) * a.Hq + head;
     store8(static_cast<QT*>(a.out) + out_row * D + c * 8, o);
     if (a.lse && c == 0) a.lse[out_row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
@@ -1178,6 +1256,7 @@ cudaError_t launch_attention_mma(const AttnParams& a, int q_dtype, int cache_dty
   MmaParams p{};
   p.a = a;
   p.R = a.N * a.G;
+  p.div_G = make_udiv(static_cast<unsigned int>(a.G));
   p.halves = (p.R + kTile - 1) / kTile;
   p.pairs = (p.halves + 1) / 2;
   p.qtiles = p.halves > 1 ? 2 : 1;
