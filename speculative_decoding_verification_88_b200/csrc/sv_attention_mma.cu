@@ -64,7 +64,10 @@ struct MmaParams {
   int box;      // tokens a TMA box: the largest power of two up to 128 that divides a page
   int head_first;  // the tensor maps' second axis is the head, not the place
   int stages;   // TMA ring entries
-  int qtiles;   // Q tiles in shared memory: 1 or 2
+  int qtiles;   // row tiles of an item: 1 or 2
+  int qrows;    // rows a Q tile has room for (a multiple of 8; the product reads 128, the rest is never used)
+  int qbufs;    // Q buffers: 2, or 1 where two row tiles leave no room
+  int scale_bytes;  // one scale array of a ring entry (8-bit pools)
   int negate;   // the scale is negative: Q is negated instead
   int qvec;     // query rows start on 16-byte boundaries
   UDiv div_G;   // / a.G
@@ -291,14 +294,14 @@ struct Control {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t cfull[kConvStages], cempty[kConvStages];
   uint64_t scale_full[kScaleRing];
-  uint64_t s_full[2], p_ready[2], o_done, q_full;
+  uint64_t s_full[2], p_ready[2], o_done, q_full[2], q_empty[2];
   uint32_t tmem;
   int abort;
   int stop;              // abort, as the softmax warpgroups agreed on it
-  int bad[2];            // a page of the segment is missing (by segment parity)
+  int bad[2];            // a page of the segment is missing (by Q buffer)
   unsigned int odd[2];   // tree tokens whose values hold an infinity or a NaN
-  int parent[64];
-  float qscale[2 * kTile];
+  int parent[2][64];
+  float qscale[2][2 * kTile];
   float2 ml[2][kTile];
   alignas(16) float kscale[kScaleRing][kTile];
   alignas(16) float vscale[kScaleRing][kTile];
@@ -342,6 +345,11 @@ __device__ __forceinline__ float tile_max(uint32_t s_addr, const float* ks, cons
   tmem_ld16(s_addr, v[0]);
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
+    float4 kc[4];
+    if (E4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kc[i] = *reinterpret_cast<const float4*>(ks + c * 16 + i * 4);
+    }
     tmem_wait_ld();
     if (c < 7) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
 #pragma unroll
@@ -349,10 +357,7 @@ __device__ __forceinline__ float tile_max(uint32_t s_addr, const float* ks, cons
       float f[4];
 #pragma unroll
       for (int z = 0; z < 4; ++z) f[z] = __uint_as_float(v[c & 1][i + z]);
-      if (E4) {
-        const float4 k = *reinterpret_cast<const float4*>(ks + c * 16 + i);
-        f[0] *= k.x, f[1] *= k.y, f[2] *= k.z, f[3] *= k.w;
-      }
+      if (E4) f[0] *= kc[i >> 2].x, f[1] *= kc[i >> 2].y, f[2] *= kc[i >> 2].z, f[3] *= kc[i >> 2].w;
       if (MASK) {
 #pragma unroll
         for (int z = 0; z < 4; ++z) f[z] = words[c >> 1] >> ((c & 1) * 16 + i + z) & 1u ? f[z] : -INFINITY;
@@ -376,6 +381,14 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, 
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     uint32_t out[8];
+    ulonglong2 kc[4], vc[4];
+    if (E4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        kc[i] = *reinterpret_cast<const ulonglong2*>(ks + c * 16 + i * 4);
+        vc[i] = *reinterpret_cast<const ulonglong2*>(vs + c * 16 + i * 4);
+      }
+    }
     tmem_wait_ld();
     if (c < 7) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
 #pragma unroll
@@ -384,9 +397,8 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, 
       unsigned long long x = pack2(__uint_as_float(w[0]), __uint_as_float(w[1]));
       unsigned long long y = pack2(__uint_as_float(w[2]), __uint_as_float(w[3]));
       if (E4) {
-        const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(ks + c * 16 + i);
-        x = mul2(x, k.x);
-        y = mul2(y, k.y);
+        x = mul2(x, kc[i >> 2].x);
+        y = mul2(y, kc[i >> 2].y);
       }
       x = fma2(x, c22, sh2);
       y = fma2(y, c22, sh2);
@@ -405,9 +417,8 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, 
       sum[0] = add2(sum[0], x);
       sum[1] = add2(sum[1], y);
       if (E4) {
-        const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(vs + c * 16 + i);
-        unpack2(mul2(x, k.x), f[0], f[1]);
-        unpack2(mul2(y, k.y), f[2], f[3]);
+        unpack2(mul2(x, vc[i >> 2].x), f[0], f[1]);
+        unpack2(mul2(y, vc[i >> 2].y), f[2], f[3]);
         if (MASK) {
 #pragma unroll
           for (int z = 0; z < 4; ++z) f[z] = on[z] ? f[z] : 0.0f;
@@ -428,6 +439,83 @@ __device__ __forceinline__ int div_rows(int n, const UDiv& d) {
   return d.m == 0u ? n : static_cast<int>(__umulhi(static_cast<unsigned int>(n), d.m) >> d.shift);
 }
 
+// What a segment needs besides its tiles, by N threads: the queries (in the
+// products' layout), the parents, and whether a page is missing.
+template <typename QT, int DP, bool E4, int N>
+__device__ __forceinline__ void load_segment(const MmaParams& p, const Walk& w, Control* s, unsigned char* q_tiles, int buf,
+                                             int tid) {
+  const AttnParams& a = p.a;
+  const int pr = w.item % p.pairs, h = w.item / p.pairs;
+  const int row0 = pr * 2 * kTile;
+  const int rows = min(2 * pr + 1 < p.halves ? 2 * kTile : kTile, p.R - row0);
+  constexpr int kUnits = DP / 8;       // runs of 8 elements a row
+  constexpr int kStride = N / kUnits;  // rows a step
+  constexpr int kAhead = N > 64 ? 4 : 8;
+  const int D = a.c.dim, j = tid % kUnits, first = tid / kUnits;
+  if (a.parent)
+    for (int i = tid; i < a.N; i += N) s->parent[buf][i] = __ldg(a.parent + static_cast<long long>(w.b) * a.N + i);
+  bool miss = false;
+  const long long lo = static_cast<long long>(w.t0) * kTile, hi = min(static_cast<long long>(w.t1) * kTile, w.total);
+  if (lo < hi)
+    for (int pi = page_of(a.c, static_cast<int>(lo)) + tid; pi <= page_of(a.c, static_cast<int>(hi - 1)); pi += N)
+      miss |= static_cast<unsigned int>(__ldg(a.c.table + static_cast<long long>(w.b) * a.c.table_stride + pi)) >=
+              static_cast<unsigned int>(a.c.num_pages);
+#pragma unroll 1
+  for (int r0 = first; r0 - first < rows; r0 += kAhead * kStride) {
+    uint4 q4[kAhead];
+#pragma unroll
+    for (int z = 0; z < kAhead; ++z) {
+      const int rr = r0 + z * kStride;
+      q4[z] = make_uint4(0u, 0u, 0u, 0u);
+      if (rr < rows && j * 8 < D) {
+        const int nd = div_rows(row0 + rr, p.div_G), head = h * a.G + (row0 + rr - nd * a.G);
+        const QT* src = static_cast<const QT*>(a.q.p) + w.b * a.q.sb + nd * a.q.sn + head * a.q.sh + j * 8;
+        if (p.qvec) {
+          q4[z] = *reinterpret_cast<const uint4*>(src);
+        } else {
+          const uint16_t* x = reinterpret_cast<const uint16_t*>(src);
+          uint32_t y[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) y[q] = x[2 * q] | static_cast<uint32_t>(x[2 * q + 1]) << 16;
+          q4[z] = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int z = 0; z < kAhead; ++z) {
+      const int rr = r0 + z * kStride;
+      uint4 v = q4[z];
+      if (p.negate) v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
+      if (E4) {
+        // a power of two brings the row's largest element to 2^14..2^15
+        float f[8];
+        load8(reinterpret_cast<const QT*>(&v), f);
+        float top = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(f[q]));
+#pragma unroll
+        for (int o = 1; o < kUnits; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int ex = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+        const bool plain = top == 0.0f || !(top < INFINITY);
+        const float up = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(14 - ex + 127) << 23);
+        if (rr < rows && j == 0)
+          s->qscale[buf][rr] = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(ex - 14 + 127) << 23);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] *= up;
+        store8(reinterpret_cast<__half*>(&v), f);
+      }
+      if (rr < rows)
+        *reinterpret_cast<uint4*>(q_tiles + (rr >> 7) * kTile * DP * 2 + (j >> 3) * p.qrows * 128 + (rr & 127) * 128 +
+                                  (((j & 7) ^ (rr & 7)) * 16)) = v;
+    }
+  }
+  if (miss) {
+    s->bad[buf] = 1;
+    raise_flag(a.ctrl, kFlagInvalidPage);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // Ring entries of a segment of T tiles, in the order the MMA warp needs them:
 // alternate tiles (one row tile): K0 K1 V0 K2 V1 ...; two row tiles: K0 V0 K1 V1 ...
 __device__ __forceinline__ int v_entry(bool two, int t, int T) { return two ? 2 * t + 1 : t == T - 1 ? 2 * T - 1 : 2 * t + 2; }
@@ -436,16 +524,14 @@ __device__ __forceinline__ int v_entry(bool two, int t, int T) { return two ? 2 
 
 // DP: head_dim rounded up to 64 or 128.  QT: queries and output; E4: 8-bit pool.
 template <typename QT, int DP, bool E4>
-__global__ void __launch_bounds__(E4 ? 448 : 320, 1)
+__global__ void __launch_bounds__(E4 ? 512 : 384, 1)
     attention_mma_kernel(const MmaParams p, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ksmap,
                          const __grid_constant__ CUtensorMap vsmap) {
   using MT = typename std::conditional<E4, __half, QT>::type;  // operands of the products
-  constexpr int kQBytes = kTile * DP * 2;
   constexpr int kRow = E4 ? DP : DP * 2;             // bytes of a token's row in a TMA tile
   constexpr int kData = kTile * kRow;
-  constexpr int kScaleBytes = E4 ? 16 * 128 : 0;     // one array's boxes, 128 bytes apart at least
-  constexpr int kEntry = kData + 2 * kScaleBytes;
+  constexpr int kLoader = E4 ? 14 : 10;              // first of the two warps that load queries ahead
   constexpr int kConv = kTile * DP * 2;
   constexpr int kChunks = DP / 64;
   constexpr bool kBf16 = std::is_same<MT, __nv_bfloat16>::value;
@@ -453,11 +539,13 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
   constexpr uint32_t kShapeO = mma_shape(kBf16, DP, true);
 
   dep_enter();
+  const uint32_t entry = kData + (E4 ? 2 * p.scale_bytes : 0);
+  const uint32_t qbytes = static_cast<uint32_t>(p.qtiles) * p.qrows * DP * 2;
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* qs = smem;
-  unsigned char* conv = qs + p.qtiles * kQBytes;                          // E4 only
+  unsigned char* conv = qs + p.qbufs * qbytes;                            // E4 only
   unsigned char* ring = conv + (E4 ? kConvStages * kConv : 0);
-  Control* s = reinterpret_cast<Control*>(ring + p.stages * kEntry);
+  Control* s = reinterpret_cast<Control*>(ring + p.stages * entry);
   const AttnParams& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per_b = a.c.heads * p.pairs;
@@ -481,9 +569,10 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
       mbar_init(&s->p_ready[i], 4);
       s->bad[i] = 0;
       s->odd[i] = 0u;
+      mbar_init(&s->q_full[i], 2);
+      mbar_init(&s->q_empty[i], 8);
     }
     mbar_init(&s->o_done, 1);
-    mbar_init(&s->q_full, 1);
     s->abort = 0;
     s->stop = 0;
     mbar_fence_init();
@@ -536,7 +625,7 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
           wait(s, &s->empty[slot], phase ^ 1u, a.ctrl);
           if (__any_sync(0xffffffffu, gave_up(s))) stop = true;
           if (stop) return;
-          const uint32_t dst = smem_addr(ring + slot * kEntry);
+          const uint32_t dst = smem_addr(ring + slot * entry);
           if (lane == 0)
             mbar_arrive_expect_tx(&s->full[slot], kData + (E4 && !values ? 2 * kTile * 4 : 0));
           __syncwarp();
@@ -548,7 +637,7 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
               if (!values) {
                 const uint32_t sd = dst + kData + lane * max(p.box * 4, 128);
                 tma_3d(sd, &ksmap, place, h, page, &s->full[slot]);
-                tma_3d(sd + kScaleBytes, &vsmap, place, h, page, &s->full[slot]);
+                tma_3d(sd + p.scale_bytes, &vsmap, place, h, page, &s->full[slot]);
               }
             } else {
 #pragma unroll
@@ -585,7 +674,8 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
       // ------------------------------------------------ MMA issue (one thread)
       if (lane == 0) {
         const uint32_t stages = E4 ? kConvStages : p.stages;
-        constexpr uint32_t kStep = E4 ? kConv : kEntry;
+        const uint32_t step_bytes = E4 ? kConv : entry;
+        const uint32_t chunk = p.qrows * 128 >> 4;  // Q's next 64 columns
         uint64_t* const fullb = E4 ? s->cfull : s->full;
         uint64_t* const emptyb = E4 ? s->cempty : s->empty;
         // The ring is read in its own order; a tile stays until its last product.
@@ -602,7 +692,9 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
         do {
           const bool two = 2 * (w.item % p.pairs) + 1 < p.halves;
           const int T = w.t1 - w.t0, U = two ? 2 * T : T;
-          wait(s, &s->q_full, seg & 1u, a.ctrl);
+          const uint32_t buf = p.qbufs == 2 ? seg & 1u : 0u;
+          wait(s, &s->q_full[buf], (p.qbufs == 2 ? seg >> 1 : seg) & 1u, a.ctrl);
+          const uint64_t q1 = q0 + buf * (qbytes >> 4);
 #pragma unroll 1
           for (int x = 0; x <= U; ++x) {
             const uint32_t g = x & 1;
@@ -610,13 +702,13 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
             if (x < U) {
               if (!shared) take(kslot);
               tmem_fence_after();
-              const uint64_t qd = q0 + (shared ? kQBytes >> 4 : 0);
-              const uint64_t kd = k0 + kslot * (kStep >> 4);
+              const uint64_t qd = q1 + (shared ? kTile * DP * 2 >> 4 : 0);
+              const uint64_t kd = k0 + kslot * (step_bytes >> 4);
 #pragma unroll
               for (int k = 0; k < DP / 16; ++k) {
                 // 16 elements are 32 bytes of a 128-byte row; 64 are the next block of rows
                 const uint32_t step = (k / 4) * (kTile * 128 >> 4) + (k % 4) * 2;
-                mma_ss(tmem + g * kTile, qd + step, kd + step, kShapeS, k > 0);
+                mma_ss(tmem + g * kTile, qd + (k / 4) * chunk + (k % 4) * 2, kd + step, kShapeS, k > 0);
               }
               mma_commit(&s->s_full[g]);
               if (!two || g == 1) mma_commit(&emptyb[kslot]);
@@ -627,7 +719,7 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
               wait(s, &s->p_ready[f], np >> f & 1u, a.ctrl);
               np ^= 1u << f;
               tmem_fence_after();
-              const uint64_t vd = v0 + vslot * (kStep >> 4);
+              const uint64_t vd = v0 + vslot * (step_bytes >> 4);
               const uint32_t o = tmem + 2 * kTile + f * DP;
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k)
@@ -645,6 +737,22 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
         }
       }
       __syncwarp();
+    } else if (warp >= kLoader) {
+      // ------------------------------------------------ the next segment's queries
+      const int lt = tid - kLoader * 32;
+      uint32_t seg = 1;
+      bool stop = false;
+      while (!stop && w.next(a)) {
+        const uint32_t buf = p.qbufs == 2 ? seg & 1u : 0u, use = p.qbufs == 2 ? seg >> 1 : seg;
+        wait(s, &s->q_empty[buf], (use & 1u) ^ 1u, a.ctrl);
+        stop = __any_sync(0xffffffffu, gave_up(s));
+        if (!stop) {
+          load_segment<QT, DP, E4, 64>(p, w, s, qs + buf * qbytes, buf, lt);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s->q_full[buf]);
+        }
+        ++seg;
+      }
     } else if (warp >= 10) {
       // ------------------------------------------------ 8-bit to 16-bit tiles
       if (E4) {
@@ -676,7 +784,7 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
             wait(s, &s->cempty[cslot], cphase ^ 1u, a.ctrl);
             stop = __any_sync(0xffffffffu, gave_up(s));
             if (stop) break;
-            const unsigned char* src = ring + slot * kEntry;
+            const unsigned char* src = ring + slot * entry;
             const long long tok0 = static_cast<long long>(w.t0 + t) * kTile;
             const uint32_t ti = (tile + t) % kScaleRing;
             uint4 c[kIter];
@@ -689,7 +797,7 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
               const int off = x / p.box * max(p.box * 4, 128) + x % p.box * 4;
               const bool in = tok0 + x < w.total;
               const float ks = in ? *reinterpret_cast<const float*>(src + kData + off) : 0.0f;
-              const float vs = in ? *reinterpret_cast<const float*>(src + kData + kScaleBytes + off) : 0.0f;
+              const float vs = in ? *reinterpret_cast<const float*>(src + kData + p.scale_bytes + off) : 0.0f;
               s->kscale[ti][x] = ks;
               s->vscale[ti][x] = vs;
               const float top = warp_max(fabsf(vs) < INFINITY ? fabsf(vs) : 0.0f);
@@ -755,82 +863,19 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
         const int T = w.t1 - w.t0;
         const int row0 = pr * 2 * kTile;
         const int rows = min(two ? 2 * kTile : kTile, p.R - row0);
-        // ---- parents, missing pages, queries
-        if (w.new_b && a.parent && tid < a.N) s->parent[tid] = __ldg(a.parent + static_cast<long long>(w.b) * a.N + tid);
-        if (tid == 0) {
-          if (w.t0 == 0 && w.nodes > 0 && w.len + w.nodes > w.total) raise_flag(a.ctrl, kFlagCapacity);
-          s->bad[(seg + 1) & 1] = 0;
-        }
-        {
-          const long long lo = static_cast<long long>(w.t0) * kTile, hi = min(static_cast<long long>(w.t1) * kTile, w.total);
-          bool miss = false;
-          if (lo < hi)
-            for (int pi = page_of(a.c, static_cast<int>(lo)) + tid; pi <= page_of(a.c, static_cast<int>(hi - 1)); pi += 256)
-              miss |= static_cast<unsigned int>(__ldg(a.c.table + static_cast<long long>(w.b) * a.c.table_stride + pi)) >=
-                      static_cast<unsigned int>(a.c.num_pages);
-          if (miss) {
-            s->bad[seg & 1] = 1;
-            raise_flag(a.ctrl, kFlagInvalidPage);
+        const uint32_t buf = p.qbufs == 2 ? seg & 1u : 0u;
+        if (seg == 0) {
+          load_segment<QT, DP, E4, 256>(p, w, s, qs, 0, tid);
+          softmax_sync();
+          if (tid == 0) {
+            mbar_arrive(&s->q_full[0]);
+            mbar_arrive(&s->q_full[0]);
           }
+        } else {
+          wait(s, &s->q_full[buf], (p.qbufs == 2 ? seg >> 1 : seg) & 1u, a.ctrl);
         }
-        {
-          constexpr int kUnits = DP / 8;   // runs of 8 elements a row
-          constexpr int kStride = 256 / kUnits;  // rows a step
-          constexpr int kAhead = 4;
-          const int D = a.c.dim, j = tid % kUnits;
-          for (int r0 = tid / kUnits; r0 - tid / kUnits < rows; r0 += kAhead * kStride) {
-            uint4 q4[kAhead];
-#pragma unroll
-            for (int z = 0; z < kAhead; ++z) {
-              const int rr = r0 + z * kStride;
-              q4[z] = make_uint4(0u, 0u, 0u, 0u);
-              if (rr < rows && j * 8 < D) {
-                const int nd = div_rows(row0 + rr, p.div_G), head = h * a.G + (row0 + rr - nd * a.G);
-                const QT* src = static_cast<const QT*>(a.q.p) + w.b * a.q.sb + nd * a.q.sn + head * a.q.sh + j * 8;
-                if (p.qvec) {
-                  q4[z] = *reinterpret_cast<const uint4*>(src);
-                } else {
-                  const uint16_t* x = reinterpret_cast<const uint16_t*>(src);
-                  uint32_t y[4];
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) y[q] = x[2 * q] | static_cast<uint32_t>(x[2 * q + 1]) << 16;
-                  q4[z] = make_uint4(y[0], y[1], y[2], y[3]);
-                }
-              }
-            }
-#pragma unroll
-            for (int z = 0; z < kAhead; ++z) {
-              const int rr = r0 + z * kStride;
-              uint4 v = q4[z];
-              if (p.negate) v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
-              if (E4) {
-                // a power of two brings the row's largest element to 2^14..2^15
-                float f[8];
-                load8(reinterpret_cast<const QT*>(&v), f);
-                float top = 0.0f;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(f[q]));
-#pragma unroll
-                for (int o = 1; o < kUnits; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const int ex = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
-                const bool plain = top == 0.0f || !(top < INFINITY);
-                const float up = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(14 - ex + 127) << 23);
-                if (rr < rows && j == 0)
-                  s->qscale[rr] = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(ex - 14 + 127) << 23);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) f[q] *= up;
-                store8(reinterpret_cast<__half*>(&v), f);
-              }
-              if (rr < rows)
-                *reinterpret_cast<uint4*>(qs + (rr >> 7) * kQBytes + (j >> 3) * kTile * 128 + (rr & 127) * 128 +
-                                          (((j & 7) ^ (rr & 7)) * 16)) = v;
-            }
-          }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        softmax_sync();
-        if (tid == 0) mbar_arrive(&s->q_full);
-        const bool missing = *reinterpret_cast<volatile int*>(&s->bad[seg & 1]) != 0;
+        if (tid == 0 && w.t0 == 0 && w.nodes > 0 && w.len + w.nodes > w.total) raise_flag(a.ctrl, kFlagCapacity);
+        const bool missing = *reinterpret_cast<volatile int*>(&s->bad[buf]) != 0;
 
         const int row = two ? g * kTile + r : r;          // row within the item
         const bool live = row < rows;
@@ -842,7 +887,7 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
           mask |= mask - 1ull;
         } else if (mask) {
           for (int i = node; i > 0;) {
-            const int up = s->parent[i];
+            const int up = s->parent[buf][i];
             if (up < 0 || up >= i) {
               raise_flag(a.ctrl, kFlagInvalidTree);
               mask = 0ull;
@@ -852,7 +897,7 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
             i = up;
           }
         }
-        const float c2 = E4 ? a.c2 * (live ? s->qscale[row] : 0.0f) : a.c2;
+        const float c2 = E4 ? a.c2 * (live ? s->qscale[buf][row] : 0.0f) : a.c2;
         const uint32_t o_addr = tmem + lane_base + 2 * kTile + g * DP;
         float M = -INFINITY, l = 0.0f;
         int vexp = -200;  // log2 of the weights' common factor (8-bit pools)
@@ -945,31 +990,30 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
             wait(s, &s->full[slot], (e / p.stages) & 1u, a.ctrl);
             const long long tok = tok0 + r;
             if (tok >= w.len) {
-              unsigned char* line = ring + slot * kEntry + r * 128;
-#pragma unroll 1
-              for (int c = 0; c < kChunks; ++c)
-#pragma unroll 1
-                for (int q = 0; q < 8; ++q) {
-                  uint4* at = reinterpret_cast<uint4*>(line + c * kTile * 128 + q * 16);
-                  if (tok >= w.total) {
-                    *at = make_uint4(0u, 0u, 0u, 0u);
-                  } else {
-                    uint4 v = *at;
-                    uint32_t y[4] = {v.x, v.y, v.z, v.w};
-                    bool odd = false;
+              uint4* line = reinterpret_cast<uint4*>(ring + slot * entry + r * 128);
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) odd |= odd_word<MT>(y[z]);
-                    if (odd) {
+              for (int c = 0; c < kChunks; ++c, line += kTile * 8) {
+                if (tok >= w.total) {
 #pragma unroll
-                      for (int z = 0; z < 4; ++z) {
-                        if (odd_word<MT>(y[z] & 0xffffu)) y[z] &= 0xffff0000u;
-                        if (odd_word<MT>(y[z] & 0xffff0000u)) y[z] &= 0xffffu;
-                      }
-                      *at = make_uint4(y[0], y[1], y[2], y[3]);
-                      atomicOr(&s->odd[(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
+                  for (int q = 0; q < 8; ++q) line[q ^ (r & 7)] = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                  bool odd = false;
+#pragma unroll
+                  for (int q = 0; q < 8; ++q) {
+                    const uint4 v = line[q ^ (r & 7)];
+                    odd |= odd_word<MT>(v.x) | odd_word<MT>(v.y) | odd_word<MT>(v.z) | odd_word<MT>(v.w);
+                  }
+                  if (odd) {
+                    uint32_t* y = reinterpret_cast<uint32_t*>(line);
+#pragma unroll 1
+                    for (int q = 0; q < 32; ++q) {
+                      if (odd_word<MT>(y[q] & 0xffffu)) y[q] &= 0xffff0000u;
+                      if (odd_word<MT>(y[q] & 0xffff0000u)) y[q] &= 0xffffu;
                     }
+                    atomicOr(&s->odd[(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
                   }
                 }
+              }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
@@ -1006,7 +1050,7 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
           const int slot = 2 * cta + (w.first ? 0 : 1);
           float* part = static_cast<float*>(a.scratch) +
                         (static_cast<size_t>(slot) * p.qtiles + (row >> 7)) * slot_floats(DP);
-#pragma unroll 2
+#pragma unroll 1
           for (int c = 0; c < ncol; c += 16) {
             uint32_t v[16], v1[16];
             const uint32_t at = tmem + lane_base + 2 * kTile + col0 + c;
@@ -1064,8 +1108,11 @@ __global__ void __launch_bounds__(E4 ? 448 : 320, 1)
         }
         tmem_fence_before();
         if (tid == 0) s->stop = gave_up(s);
-        softmax_sync();  // O, Q, ml, mask and odd may be overwritten now
+        softmax_sync();  // O, Q, ml and odd may be overwritten now
         if (tid < 2) s->odd[tid] = 0u;
+        if (tid == 2) s->bad[buf] = 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s->q_empty[buf]);
         base += 2 * T;
         tile_base += T;
         ++seg;
@@ -1211,13 +1258,17 @@ bool scale_map(CUtensorMap* m, const CacheView& c, void* base, int box) {
 
 template <typename QT, int DP, bool E4>
 cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[4], int grid, cudaStream_t st) {
-  constexpr int kQBytes = kTile * DP * 2;
-  constexpr int kEntry = E4 ? kTile * DP + 2 * 16 * 128 : kTile * DP * 2;
   constexpr int kLimit = 227 * 1024;
-  const int fixed = p.qtiles * kQBytes + (E4 ? kConvStages * kTile * DP * 2 : 0) + static_cast<int>(sizeof(Control));
-  p.stages = (kLimit - fixed) / kEntry;
+  const int boxes = kTile / p.box;
+  p.scale_bytes = E4 ? boxes * (p.box * 4 > 128 ? p.box * 4 : 128) : 0;
+  const int entry = kTile * DP * (E4 ? 1 : 2) + 2 * p.scale_bytes;
+  p.qrows = p.qtiles == 2 ? kTile : (p.R + 7) / 8 * 8;
+  p.qbufs = p.qtiles == 2 ? 1 : 2;
+  const int fixed = p.qbufs * p.qtiles * p.qrows * DP * 2 + (E4 ? kConvStages * kTile * DP * 2 : 0) +
+                    static_cast<int>(sizeof(Control));
+  p.stages = (kLimit - fixed) / entry;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  const size_t smem = fixed + static_cast<size_t>(p.stages) * kEntry;
+  const size_t smem = fixed + static_cast<size_t>(p.stages) * entry;
   const auto kernel = attention_mma_kernel<QT, DP, E4>;
   static bool done[64] = {};
   int dev = 0;
@@ -1228,7 +1279,7 @@ cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[4], int grid, cud
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev] = true;
   }
-  e = counted(launch_k(SV_PDL >= 2, kernel, dim3(grid), dim3(E4 ? 448 : 320), smem, st, p, maps[0], maps[1], maps[2],
+  e = counted(launch_k(SV_PDL >= 2, kernel, dim3(grid), dim3(E4 ? 512 : 384), smem, st, p, maps[0], maps[1], maps[2],
                        maps[3]),
               1);
   if (e != cudaSuccess || grid < 2) return e;
