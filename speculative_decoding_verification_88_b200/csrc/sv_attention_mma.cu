@@ -42,14 +42,15 @@ constexpr int kMaxCtas = 148;     // scratch is sized for this many blocks
 constexpr int kScaleRing = 4;     // tiles whose scales are held
 constexpr int kMaxStages = 8;
 constexpr int kConvStages = 3;    // widened tiles (8-bit pools)
+constexpr int kJoinThreads = 512;
 constexpr float kLazy = 8.0f;     // log2 of what a weight may exceed 1 by
 
-// Work split shared by the two grids: sequence b has tiles(b) * per_b tiles,
-// block c takes [T c / n, T (c + 1) / n).
+// Work split shared by the two grids: of T tiles block c of n takes
+// [start(c), start(c + 1)), the first T % n blocks one more than the others.
 struct Split {
-  long long T;
-  int n;
-  __device__ __forceinline__ long long start(int c) const { return T * c / n; }
+  long long each;
+  int n, more;
+  __device__ __forceinline__ long long start(int c) const { return each * c + min(c, more); }
 };
 
 __host__ __device__ inline size_t slot_floats(int DP) { return static_cast<size_t>(kTile) * (DP + 2); }
@@ -89,19 +90,18 @@ __device__ __forceinline__ int tiles_of(const AttnParams& a, int b) {
   return t < 1 ? 1 : static_cast<int>(t);
 }
 
-// Total tiles, and the sequence and remainder of tile x(total), by the first
-// 256 threads of a block; all of them take part in the barriers.
+// The split, and where block c's share starts, by the first 256 threads of a
+// block; all of them take part in the barriers.  b < 0: block c has none.
 struct Found {
-  long long T;
-  int b;
-  long long rem;  // tiles into sequence b
+  Split split;
+  int b, h, pr, t0;  // sequence, cache head, pair of row tiles, tile
 };
-template <typename At>
-__device__ __forceinline__ void find_tile(const AttnParams& a, int per_b, long long* sums, Found* f, At at) {
+__device__ __forceinline__ void find_share(const AttnParams& a, int pairs, int blocks, int c, long long* sums, Found* f) {
   const int tid = threadIdx.x;
-  const int per = (a.B + 255) / 256;
+  const int per = (a.B + 255) / 256, per_b = a.c.heads * pairs;
   long long mine = 0;
   if (tid < 256) {
+#pragma unroll 1
     for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) mine += static_cast<long long>(tiles_of(a, b)) * per_b;
     sums[tid] = mine;
   }
@@ -121,20 +121,28 @@ __device__ __forceinline__ void find_tile(const AttnParams& a, int per_b, long l
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) sums[tid * 8 + i] = incl - run + s[i];
-    if (tid == 31) f->T = incl;
+    if (tid == 31) {
+      f->split.n = static_cast<int>(min(static_cast<long long>(blocks), incl));
+      f->split.each = incl / f->split.n;
+      f->split.more = static_cast<int>(incl - f->split.each * f->split.n);
+      f->b = -1;
+    }
   }
   __syncthreads();
-  const long long x = at(f->T);
+  const long long x = c < f->split.n ? f->split.start(c) : -1;
   if (tid < 256 && mine > 0 && x >= sums[tid] && x < sums[tid] + mine) {
     long long rem = x - sums[tid];
-    int b = tid * per;
-    for (;; ++b) {
-      const long long t = static_cast<long long>(tiles_of(a, b)) * per_b;
-      if (rem < t) break;
-      rem -= t;
+    int b = tid * per, t = tiles_of(a, b);
+#pragma unroll 1
+    while (rem >= static_cast<long long>(t) * per_b) {
+      rem -= static_cast<long long>(t) * per_b;
+      t = tiles_of(a, ++b);
     }
+    const int item = static_cast<int>(rem / t);
+    f->t0 = static_cast<int>(rem - static_cast<long long>(item) * t);
+    f->h = item / pairs;
+    f->pr = item - f->h * pairs;
     f->b = b;
-    f->rem = rem;
   }
   __syncthreads();
 }
@@ -142,44 +150,43 @@ __device__ __forceinline__ void find_tile(const AttnParams& a, int per_b, long l
 // A block's segments in order, as every role walks them.
 struct Walk {
   long long left;  // tiles of the share not yet walked
-  int b, item, items;
+  int b, h, pr;    // sequence, cache head, pair of row tiles
   int tiles;       // of an item of b
   int t0, t1;      // this segment's tiles
   int nodes;
   long long len, total;
   bool first;
-  bool new_b;
   __device__ __forceinline__ void load(const AttnParams& a) {
     total = tokens_of(a, b, nodes, len);
     const long long t = (total + kTile - 1) / kTile;
     tiles = t < 1 ? 1 : static_cast<int>(t);
-    new_b = true;
   }
-  __device__ __forceinline__ void begin(const AttnParams& a, int per_b, const Found& f, long long share) {
+  __device__ __forceinline__ void begin(const AttnParams& a, const Found& f, long long share) {
     left = share;
-    items = per_b;
-    b = f.b;
+    b = f.b, h = f.h, pr = f.pr, t0 = f.t0;
     first = true;
     load(a);
-    item = static_cast<int>(f.rem / tiles);
-    t0 = static_cast<int>(f.rem - static_cast<long long>(item) * tiles);
     t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + left));
   }
-  __device__ __forceinline__ bool next(const AttnParams& a) {
+  __device__ __forceinline__ bool next(const AttnParams& a, int pairs) {
     left -= t1 - t0;
     if (left <= 0) return false;
     first = false;
-    new_b = false;
     t0 = 0;
-    if (++item == items) {
-      item = 0;
-      ++b;
-      load(a);
+    if (++pr == pairs) {
+      pr = 0;
+      if (++h == a.c.heads) {
+        h = 0;
+        ++b;
+        load(a);
+      }
     }
     t1 = static_cast<int>(min(static_cast<long long>(tiles), left));
     return true;
   }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+  // Rows of the item, and whether it has two row tiles.
+  __device__ __forceinline__ int row0() const { return pr * 2 * kTile; }
 };
 
 // ------------------------------------------------------------- PTX wrappers
@@ -313,7 +320,11 @@ struct Control {
 // Bounded wait; once one has run out, every wait of the block returns at once
 // and the roles run to their ends on whatever is there.
 __device__ __noinline__ void wait_long(Control* s, uint64_t* bar, uint32_t parity, Ctrl* ctrl) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return;
   const unsigned long long t0 = global_ns();
+#pragma unroll 1
   for (unsigned int spin = 1;; ++spin) {
     if (mbar_try_wait(bar, parity)) return;
     if ((spin & 63u) == 0u) {
@@ -327,19 +338,16 @@ __device__ __noinline__ void wait_long(Control* s, uint64_t* bar, uint32_t parit
   }
 }
 __device__ __forceinline__ void wait(Control* s, uint64_t* bar, uint32_t parity, Ctrl* ctrl) {
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return;
-  wait_long(s, bar, parity, ctrl);
+  if (!mbar_try_wait(bar, parity)) wait_long(s, bar, parity, ctrl);
 }
 __device__ __forceinline__ bool gave_up(const Control* s) { return *reinterpret_cast<const volatile int*>(&s->abort) != 0; }
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// Largest score of a row's tile (times K's scales; -inf where all is masked).
-// Both passes over a tile read 16 columns ahead of the arithmetic.
-template <bool E4, bool MASK>
-__device__ __forceinline__ float tile_max(uint32_t s_addr, const float* ks, const uint32_t (&words)[4]) {
+// Largest score of a row's tile (times K's scales).  Both passes over a tile
+// read 16 columns ahead of the arithmetic.
+template <bool E4>
+__device__ __forceinline__ float tile_max(uint32_t s_addr, const float* ks) {
   float top[2] = {-INFINITY, -INFINITY};
   uint32_t v[2][16];
   tmem_ld16(s_addr, v[0]);
@@ -358,10 +366,6 @@ __device__ __forceinline__ float tile_max(uint32_t s_addr, const float* ks, cons
 #pragma unroll
       for (int z = 0; z < 4; ++z) f[z] = __uint_as_float(v[c & 1][i + z]);
       if (E4) f[0] *= kc[i >> 2].x, f[1] *= kc[i >> 2].y, f[2] *= kc[i >> 2].z, f[3] *= kc[i >> 2].w;
-      if (MASK) {
-#pragma unroll
-        for (int z = 0; z < 4; ++z) f[z] = words[c >> 1] >> ((c & 1) * 16 + i + z) & 1u ? f[z] : -INFINITY;
-      }
       top[0] = fmax3(top[0], f[0], f[1]);
       top[1] = fmax3(top[1], f[2], f[3]);
     }
@@ -371,9 +375,8 @@ __device__ __forceinline__ float tile_max(uint32_t s_addr, const float* ks, cons
 
 // Weights 2^(s c2 - shift) of a row's tile into tensor memory over the
 // scores (times V's scales); returns their sum (without the scales).
-template <typename M, bool E4, bool MASK>
-__device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, const float* vs,
-                                              const uint32_t (&words)[4], float c2, float shift) {
+template <typename M, bool E4>
+__device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, const float* vs, float c2, float shift) {
   const unsigned long long c22 = splat2(c2), sh2 = splat2(-shift);
   unsigned long long sum[2] = {0ull, 0ull};
   uint32_t v[2][16];
@@ -405,13 +408,8 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, 
       float f[4];
       unpack2(x, f[0], f[1]);
       unpack2(y, f[2], f[3]);
-      bool on[4];
 #pragma unroll
-      for (int z = 0; z < 4; ++z) {
-        on[z] = !MASK || (words[c >> 1] >> ((c & 1) * 16 + i + z) & 1u);
-        f[z] = ex2f(f[z]);
-        if (MASK) f[z] = on[z] ? f[z] : 0.0f;
-      }
+      for (int z = 0; z < 4; ++z) f[z] = ex2f(f[z]);
       x = pack2(f[0], f[1]);
       y = pack2(f[2], f[3]);
       sum[0] = add2(sum[0], x);
@@ -419,10 +417,6 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, 
       if (E4) {
         unpack2(mul2(x, vc[i >> 2].x), f[0], f[1]);
         unpack2(mul2(y, vc[i >> 2].y), f[2], f[3]);
-        if (MASK) {
-#pragma unroll
-          for (int z = 0; z < 4; ++z) f[z] = on[z] ? f[z] : 0.0f;
-        }
       }
       out[i >> 1] = pack_weights<M>(f[0], f[1]);
       out[(i >> 1) + 1] = pack_weights<M>(f[2], f[3]);
@@ -435,56 +429,114 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, 
   return (a + b) + (d + e);
 }
 
+// The same two passes where some columns are masked (allowed: bit i of word
+// c is column 32 c + i).  A sequence's last tile or two; kept small.
+template <bool E4>
+__device__ __forceinline__ float tile_max_masked(uint32_t s_addr, const float* ks, const uint4& allowed) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t word = (c < 4 ? (c < 2 ? allowed.x : allowed.y) : (c < 6 ? allowed.z : allowed.w)) >> (c & 1) * 16;
+    uint32_t v[16];
+    tmem_ld16(s_addr + c * 16, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float f = __uint_as_float(v[i]);
+      if (E4) f *= ks[c * 16 + i];
+      if (word >> i & 1u) top = fmaxf(top, f);
+    }
+  }
+  return top;
+}
+template <typename M, bool E4>
+__device__ __forceinline__ float tile_weights_masked(uint32_t s_addr, const float* ks, const float* vs,
+                                                     const uint4& allowed, float c2, float shift) {
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t word = (c < 4 ? (c < 2 ? allowed.x : allowed.y) : (c < 6 ? allowed.z : allowed.w)) >> (c & 1) * 16;
+    uint32_t v[16], out[8];
+    tmem_ld16(s_addr + c * 16, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      float f[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const bool on = word >> (i + z) & 1u;
+        f[z] = __uint_as_float(v[i + z]);
+        if (E4) f[z] *= ks[c * 16 + i + z];
+        f[z] = on ? ex2f(fmaf(f[z], c2, -shift)) : 0.0f;
+        sum += f[z];
+        if (E4 && on) f[z] *= vs[c * 16 + i + z];
+      }
+      out[i >> 1] = pack_weights<M>(f[0], f[1]);
+    }
+    tmem_st8(s_addr + c * 8, out);
+  }
+  return sum;
+}
+
 __device__ __forceinline__ int div_rows(int n, const UDiv& d) {
   return d.m == 0u ? n : static_cast<int>(__umulhi(static_cast<unsigned int>(n), d.m) >> d.shift);
 }
 
-// What a segment needs besides its tiles, by N threads: the queries (in the
-// products' layout), the parents, and whether a page is missing.
-template <typename QT, int DP, bool E4, int N>
+// What a segment needs besides its tiles, by 64 threads: the queries (in the
+// products' layout; all copies in flight at once, since a load's latency is
+// several microseconds behind a full queue of tiles), the parents, and
+// whether a page is missing.
+template <typename QT, int DP, bool E4>
 __device__ __forceinline__ void load_segment(const MmaParams& p, const Walk& w, Control* s, unsigned char* q_tiles, int buf,
                                              int tid) {
   const AttnParams& a = p.a;
-  const int pr = w.item % p.pairs, h = w.item / p.pairs;
-  const int row0 = pr * 2 * kTile;
-  const int rows = min(2 * pr + 1 < p.halves ? 2 * kTile : kTile, p.R - row0);
-  constexpr int kUnits = DP / 8;       // runs of 8 elements a row
-  constexpr int kStride = N / kUnits;  // rows a step
-  constexpr int kAhead = N > 64 ? 4 : 8;
+  const int row0 = w.row0();
+  const int rows = min(2 * w.pr + 1 < p.halves ? 2 * kTile : kTile, p.R - row0);
+  constexpr int kUnits = DP / 8;        // runs of 8 elements a row
+  constexpr int kStride = 64 / kUnits;  // rows a step
   const int D = a.c.dim, j = tid % kUnits, first = tid / kUnits;
-  if (a.parent)
-    for (int i = tid; i < a.N; i += N) s->parent[buf][i] = __ldg(a.parent + static_cast<long long>(w.b) * a.N + i);
+  const QT* const q = static_cast<const QT*>(a.q.p) + w.b * a.q.sb + static_cast<long long>(w.h * a.G) * a.q.sh + j * 8;
+  const auto place = [&](int rr) {
+    return reinterpret_cast<uint4*>(q_tiles + (rr >> 7) * kTile * DP * 2 + (j >> 3) * p.qrows * 128 + (rr & 127) * 128 +
+                                    (((j & 7) ^ (rr & 7)) * 16));
+  };
+#pragma unroll 2
+  for (int rr = first; rr < rows; rr += kStride) {
+    const int nd = div_rows(row0 + rr, p.div_G);
+    const QT* src = q + nd * a.q.sn + (row0 + rr - nd * a.G) * a.q.sh;
+    uint4* dst = place(rr);
+    if (j * 8 >= D) {
+      *dst = make_uint4(0u, 0u, 0u, 0u);
+    } else if (p.qvec) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+    } else {
+      const uint16_t* x = reinterpret_cast<const uint16_t*>(src);
+      uint32_t y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = x[2 * i] | static_cast<uint32_t>(x[2 * i + 1]) << 16;
+      *dst = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+  }
+  if (a.parent && tid < a.N) s->parent[buf][tid] = __ldg(a.parent + static_cast<long long>(w.b) * a.N + tid);
   bool miss = false;
   const long long lo = static_cast<long long>(w.t0) * kTile, hi = min(static_cast<long long>(w.t1) * kTile, w.total);
-  if (lo < hi)
-    for (int pi = page_of(a.c, static_cast<int>(lo)) + tid; pi <= page_of(a.c, static_cast<int>(hi - 1)); pi += N)
-      miss |= static_cast<unsigned int>(__ldg(a.c.table + static_cast<long long>(w.b) * a.c.table_stride + pi)) >=
-              static_cast<unsigned int>(a.c.num_pages);
+  if (lo < hi) {
+    const int* row = a.c.table + static_cast<long long>(w.b) * a.c.table_stride;
+    const int last = page_of(a.c, static_cast<int>(hi - 1));
+#pragma unroll 4
+    for (int pi = page_of(a.c, static_cast<int>(lo)) + tid; pi <= last; pi += 64)
+      miss |= static_cast<unsigned int>(__ldg(row + pi)) >= static_cast<unsigned int>(a.c.num_pages);
+  }
+  if (miss) {
+    s->bad[buf] = 1;
+    raise_flag(a.ctrl, kFlagInvalidPage);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (E4 || p.negate) {
 #pragma unroll 1
-  for (int r0 = first; r0 - first < rows; r0 += kAhead * kStride) {
-    uint4 q4[kAhead];
-#pragma unroll
-    for (int z = 0; z < kAhead; ++z) {
-      const int rr = r0 + z * kStride;
-      q4[z] = make_uint4(0u, 0u, 0u, 0u);
-      if (rr < rows && j * 8 < D) {
-        const int nd = div_rows(row0 + rr, p.div_G), head = h * a.G + (row0 + rr - nd * a.G);
-        const QT* src = static_cast<const QT*>(a.q.p) + w.b * a.q.sb + nd * a.q.sn + head * a.q.sh + j * 8;
-        if (p.qvec) {
-          q4[z] = *reinterpret_cast<const uint4*>(src);
-        } else {
-          const uint16_t* x = reinterpret_cast<const uint16_t*>(src);
-          uint32_t y[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) y[q] = x[2 * q] | static_cast<uint32_t>(x[2 * q + 1]) << 16;
-          q4[z] = make_uint4(y[0], y[1], y[2], y[3]);
-        }
-      }
-    }
-#pragma unroll
-    for (int z = 0; z < kAhead; ++z) {
-      const int rr = r0 + z * kStride;
-      uint4 v = q4[z];
+    for (int r0 = first; r0 - first < rows; r0 += kStride) {  // all lanes take part
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (r0 < rows) v = *place(r0);
       if (p.negate) v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
       if (E4) {
         // a power of two brings the row's largest element to 2^14..2^15
@@ -492,26 +544,20 @@ __device__ __forceinline__ void load_segment(const MmaParams& p, const Walk& w, 
         load8(reinterpret_cast<const QT*>(&v), f);
         float top = 0.0f;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(f[q]));
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
 #pragma unroll
         for (int o = 1; o < kUnits; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const int ex = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
         const bool plain = top == 0.0f || !(top < INFINITY);
         const float up = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(14 - ex + 127) << 23);
-        if (rr < rows && j == 0)
-          s->qscale[buf][rr] = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(ex - 14 + 127) << 23);
+        if (r0 < rows && j == 0)
+          s->qscale[buf][r0] = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(ex - 14 + 127) << 23);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) f[q] *= up;
+        for (int i = 0; i < 8; ++i) f[i] *= up;
         store8(reinterpret_cast<__half*>(&v), f);
       }
-      if (rr < rows)
-        *reinterpret_cast<uint4*>(q_tiles + (rr >> 7) * kTile * DP * 2 + (j >> 3) * p.qrows * 128 + (rr & 127) * 128 +
-                                  (((j & 7) ^ (rr & 7)) * 16)) = v;
+      if (r0 < rows) *place(r0) = v;
     }
-  }
-  if (miss) {
-    s->bad[buf] = 1;
-    raise_flag(a.ctrl, kFlagInvalidPage);
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -525,7 +571,7 @@ __device__ __forceinline__ int v_entry(bool two, int t, int T) { return two ? 2 
 // DP: head_dim rounded up to 64 or 128.  QT: queries and output; E4: 8-bit pool.
 template <typename QT, int DP, bool E4>
 __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
-    attention_mma_kernel(const MmaParams p, const __grid_constant__ CUtensorMap kmap,
+    attention_mma_kernel(const __grid_constant__ MmaParams p, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ksmap,
                          const __grid_constant__ CUtensorMap vsmap) {
   using MT = typename std::conditional<E4, __half, QT>::type;  // operands of the products
@@ -548,7 +594,6 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
   Control* s = reinterpret_cast<Control*>(ring + p.stages * entry);
   const AttnParams& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per_b = a.c.heads * p.pairs;
 
   if (tid == 288) {
     for (const CUtensorMap* m : {&kmap, &vmap, &ksmap, &vsmap})
@@ -585,27 +630,21 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
   }
   __syncthreads();
   tmem_fence_after();
-  const int grid = gridDim.x;
   const int cta = blockIdx.x;
-  find_tile(a, per_b, s->sums, &s->found, [&](long long T) {
-    const Split sp{T, static_cast<int>(min(static_cast<long long>(grid), T))};
-    return cta < sp.n ? sp.start(cta) : -1;
-  });
+  find_share(a, p.pairs, gridDim.x, cta, s->sums, &s->found);
   const uint32_t tmem = s->tmem;
-  const Split split{s->found.T, static_cast<int>(min(static_cast<long long>(grid), s->found.T))};
-  const long long share = cta < split.n ? split.start(cta + 1) - split.start(cta) : 0;
 
-  if (share > 0) {
+  if (s->found.b >= 0) {
     Walk w;
-    w.begin(a, per_b, s->found, share);
+    w.begin(a, s->found, s->found.split.start(cta + 1) - s->found.split.start(cta));
     if (warp == 8) {
       // ------------------------------------------------ producer: TMA loads
       const int nbox = kTile / p.box;
       uint32_t e = 0, slot = 0, phase = 0;  // ring entries filled, the next one's place
       bool stop = false;  // the same in all lanes
       do {
-        const bool two = 2 * (w.item % p.pairs) + 1 < p.halves;
-        const int h = w.item / p.pairs;
+        const bool two = 2 * w.pr + 1 < p.halves;
+        const int h = w.h;
         const int T = w.t1 - w.t0;
         // page (num_pages: none, which TMA fills with zeros) and place of this
         // lane's box in two tiles running
@@ -663,7 +702,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
           pg0 = pg1;
           pl0 = pl1;
         }
-      } while (!stop && w.next(a));
+      } while (!stop && w.next(a, p.pairs));
       if (stop) {  // copies in flight land before the block ends
         const unsigned long long t0 = global_ns();
         const uint32_t n = min(e, static_cast<uint32_t>(p.stages));
@@ -690,7 +729,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
         const uint64_t v0 = operand(smem_addr(E4 ? conv : ring), kTile * 128, 1024);
         uint32_t seg = 0, np = 0;  // np: phases of p_ready, one bit a warpgroup
         do {
-          const bool two = 2 * (w.item % p.pairs) + 1 < p.halves;
+          const bool two = 2 * w.pr + 1 < p.halves;
           const int T = w.t1 - w.t0, U = two ? 2 * T : T;
           const uint32_t buf = p.qbufs == 2 ? seg & 1u : 0u;
           wait(s, &s->q_full[buf], (p.qbufs == 2 ? seg >> 1 : seg) & 1u, a.ctrl);
@@ -730,7 +769,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
           }
           mma_commit(&s->o_done);
           ++seg;
-        } while (!gave_up(s) && w.next(a));
+        } while (!gave_up(s) && w.next(a, p.pairs));
         if (gave_up(s)) {  // MMAs in flight finish before their memory goes away
           const unsigned long long t0 = global_ns();
           while (!mbar_try_wait(&s->o_done, (seg - 1) & 1u) && global_ns() - t0 < kWaitLimitNs) {}
@@ -740,19 +779,19 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
     } else if (warp >= kLoader) {
       // ------------------------------------------------ the next segment's queries
       const int lt = tid - kLoader * 32;
-      uint32_t seg = 1;
+      uint32_t seg = 0;
       bool stop = false;
-      while (!stop && w.next(a)) {
+      do {
         const uint32_t buf = p.qbufs == 2 ? seg & 1u : 0u, use = p.qbufs == 2 ? seg >> 1 : seg;
         wait(s, &s->q_empty[buf], (use & 1u) ^ 1u, a.ctrl);
         stop = __any_sync(0xffffffffu, gave_up(s));
         if (!stop) {
-          load_segment<QT, DP, E4, 64>(p, w, s, qs + buf * qbytes, buf, lt);
+          load_segment<QT, DP, E4>(p, w, s, qs + buf * qbytes, buf, lt);
           __syncwarp();
           if (lane == 0) mbar_arrive(&s->q_full[buf]);
         }
         ++seg;
-      }
+      } while (!stop && w.next(a, p.pairs));
     } else if (warp >= 10) {
       // ------------------------------------------------ 8-bit to 16-bit tiles
       if (E4) {
@@ -766,9 +805,10 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
         // Lanes of the second 64 columns store their halves the other way
         // round: the two blocks share banks.  (row & 7) is the swizzle.
         const int first = 2 * (j % 4) + (j >= 4 ? 1 : 0);
+        const int scale_at = (cw * 32 + lane) / p.box * max(p.box * 4, 128) + (cw * 32 + lane) % p.box * 4;
         unsigned char* const line0 = conv + (j / 4) * kTile * 128 + row0 * 128;
         do {
-          const bool two = 2 * (w.item % p.pairs) + 1 < p.halves;
+          const bool two = 2 * w.pr + 1 < p.halves;
           const int T = w.t1 - w.t0;
           for (int i = 0; i < 2 * T && !stop; ++i) {
             bool values;
@@ -787,47 +827,20 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
             const unsigned char* src = ring + slot * entry;
             const long long tok0 = static_cast<long long>(w.t0 + t) * kTile;
             const uint32_t ti = (tile + t) % kScaleRing;
-            uint4 c[kIter];
-#pragma unroll
-            for (int it = 0; it < kIter; ++it)
-              c[it] = *reinterpret_cast<const uint4*>(src + (row0 + it * kRows) * DP + j * 16);
             if (!values) {
               // scales of this warp's 32 tokens; places past the end count as 0
               const int x = cw * 32 + lane;
-              const int off = x / p.box * max(p.box * 4, 128) + x % p.box * 4;
               const bool in = tok0 + x < w.total;
-              const float ks = in ? *reinterpret_cast<const float*>(src + kData + off) : 0.0f;
-              const float vs = in ? *reinterpret_cast<const float*>(src + kData + p.scale_bytes + off) : 0.0f;
+              const float ks = in ? *reinterpret_cast<const float*>(src + kData + scale_at) : 0.0f;
+              const float vs = in ? *reinterpret_cast<const float*>(src + kData + p.scale_bytes + scale_at) : 0.0f;
               s->kscale[ti][x] = ks;
               s->vscale[ti][x] = vs;
               const float top = warp_max(fabsf(vs) < INFINITY ? fabsf(vs) : 0.0f);
               if (lane == 0) s->vmax[ti][cw] = top;
             }
-            if (tok0 + kTile > w.len) {
-#pragma unroll
-              for (int it = 0; it < kIter; ++it) {
-                const long long tok = tok0 + row0 + it * kRows;
-                if (tok >= w.total) c[it] = make_uint4(0u, 0u, 0u, 0u);
-                if (values && tok >= w.len) {
-                  // a drafted token's NaN must reach its own descendants only:
-                  // it goes by the scale, which multiplies their weights alone
-                  const uint32_t words[4] = {c[it].x, c[it].y, c[it].z, c[it].w};
-                  bool odd = false;
-#pragma unroll
-                  for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) odd |= (words[q] >> (8 * z) & 0x7fu) == 0x7fu;
-                  if (odd) {
-                    c[it] = make_uint4(0u, 0u, 0u, 0u);
-                    s->vscale[ti][row0 + it * kRows] = __int_as_float(0x7fc00000);
-                  }
-                }
-              }
-            }
-#pragma unroll
-            for (int it = 0; it < kIter; ++it) {
-              const int row = row0 + it * kRows;
-              const uint32_t words[4] = {c[it].x, c[it].y, c[it].z, c[it].w};
+            const auto widen = [&](const uint4& c, int it) {
+              const int sw = (row0 + it * kRows) & 7;
+              const uint32_t words[4] = {c.x, c.y, c.z, c.w};
               uint32_t out[8];
 #pragma unroll
               for (int q = 0; q < 8; ++q) out[q] = half_pair(static_cast<uint16_t>(words[q >> 1] >> (16 * (q & 1))));
@@ -835,8 +848,38 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
               const bool swap = j >= 4;
               const uint4 lo = make_uint4(out[0], out[1], out[2], out[3]);
               const uint4 hi = make_uint4(out[4], out[5], out[6], out[7]);
-              *reinterpret_cast<uint4*>(line + ((first ^ (row & 7)) * 16)) = swap ? hi : lo;
-              *reinterpret_cast<uint4*>(line + (((first ^ 1) ^ (row & 7)) * 16)) = swap ? lo : hi;
+              *reinterpret_cast<uint4*>(line + ((first ^ sw) * 16)) = swap ? hi : lo;
+              *reinterpret_cast<uint4*>(line + (((first ^ 1) ^ sw) * 16)) = swap ? lo : hi;
+            };
+            const uint4* codes = reinterpret_cast<const uint4*>(src + row0 * DP + j * 16);
+            if (tok0 + kTile <= w.len) {
+              uint4 c[kIter];
+#pragma unroll
+              for (int it = 0; it < kIter; ++it) c[it] = codes[it * kRows * DP / 16];
+#pragma unroll
+              for (int it = 0; it < kIter; ++it) widen(c[it], it);
+            } else {
+#pragma unroll 1
+              for (int it = 0; it < kIter; ++it) {
+                uint4 c = codes[it * kRows * DP / 16];
+                const long long tok = tok0 + row0 + it * kRows;
+                if (tok >= w.total) c = make_uint4(0u, 0u, 0u, 0u);
+                if (values && tok >= w.len) {
+                  // a drafted token's NaN must reach its own descendants only:
+                  // it goes by the scale, which multiplies their weights alone
+                  const uint32_t words[4] = {c.x, c.y, c.z, c.w};
+                  bool odd = false;
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) odd |= (words[q] >> (8 * z) & 0x7fu) == 0x7fu;
+                  if (odd) {
+                    c = make_uint4(0u, 0u, 0u, 0u);
+                    s->vscale[ti][row0 + it * kRows] = __int_as_float(0x7fc00000);
+                  }
+                }
+                widen(c, it);
+              }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -849,7 +892,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
             if (++cslot == kConvStages) cslot = 0, cphase ^= 1u;
           }
           tile += T;
-        } while (!stop && w.next(a));
+        } while (!stop && w.next(a, p.pairs));
       }
     } else {
       // ------------------------------------------------ softmax warpgroups
@@ -858,22 +901,13 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
       const uint32_t s_addr = tmem + lane_base + g * kTile;
       uint32_t base = 0, tile_base = 0, ns = 0, seg = 0;
       do {
-        const int pr = w.item % p.pairs, h = w.item / p.pairs;
-        const bool two = 2 * pr + 1 < p.halves;
+        const int h = w.h;
+        const bool two = 2 * w.pr + 1 < p.halves;
         const int T = w.t1 - w.t0;
-        const int row0 = pr * 2 * kTile;
+        const int row0 = w.row0();
         const int rows = min(two ? 2 * kTile : kTile, p.R - row0);
         const uint32_t buf = p.qbufs == 2 ? seg & 1u : 0u;
-        if (seg == 0) {
-          load_segment<QT, DP, E4, 256>(p, w, s, qs, 0, tid);
-          softmax_sync();
-          if (tid == 0) {
-            mbar_arrive(&s->q_full[0]);
-            mbar_arrive(&s->q_full[0]);
-          }
-        } else {
-          wait(s, &s->q_full[buf], (p.qbufs == 2 ? seg >> 1 : seg) & 1u, a.ctrl);
-        }
+        wait(s, &s->q_full[buf], (p.qbufs == 2 ? seg >> 1 : seg) & 1u, a.ctrl);
         if (tid == 0 && w.t0 == 0 && w.nodes > 0 && w.len + w.nodes > w.total) raise_flag(a.ctrl, kFlagCapacity);
         const bool missing = *reinterpret_cast<volatile int*>(&s->bad[buf]) != 0;
 
@@ -921,9 +955,10 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
           __syncwarp();
           tmem_fence_after();
           if (warp_live) {
-            uint32_t words[4] = {~0u, ~0u, ~0u, ~0u};
+            uint4 allowed;
             if (masked) {
-#pragma unroll
+              uint32_t words[4];
+#pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 const long long off = tok0 + 32 * c - w.len, lim = w.total - (tok0 + 32 * c);
                 uint32_t y = ~0u;
@@ -941,11 +976,15 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
                   }
                   y &= __ballot_sync(0xffffffffu, in);
                 }
-                words[c] = y;
+                words[0] = c == 0 ? y : words[0];
+                words[1] = c == 1 ? y : words[1];
+                words[2] = c == 2 ? y : words[2];
+                words[3] = c == 3 ? y : words[3];
               }
+              allowed = make_uint4(words[0], words[1], words[2], words[3]);
             }
-            float top = masked ? tile_max<E4, true>(s_addr, s->kscale[ti], words)
-                               : tile_max<E4, false>(s_addr, s->kscale[ti], words);
+            float top = masked ? tile_max_masked<E4>(s_addr, s->kscale[ti], allowed)
+                               : tile_max<E4>(s_addr, s->kscale[ti]);
             top = top == -INFINITY ? -INFINITY : top * c2;
             bool raise;
             float Mn = M;
@@ -966,7 +1005,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
             // the first tile's product overwrites O
             if (x > 1 && __any_sync(0xffffffffu, Mn != M)) {
               const float f = M == -INFINITY ? 0.0f : Mn == M ? 1.0f : ex2f(M - Mn);
-#pragma unroll 2
+#pragma unroll 1
               for (int c = 0; c < DP / 16; ++c) {
                 uint32_t v[16];
                 tmem_ld16(o_addr + c * 16, v);
@@ -978,8 +1017,8 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
             }
             M = Mn;
             const float shift = M == -INFINITY ? 0.0f : M;
-            l += masked ? tile_weights<MT, E4, true>(s_addr, s->kscale[ti], s->vscale[ti], words, c2, shift)
-                        : tile_weights<MT, E4, false>(s_addr, s->kscale[ti], s->vscale[ti], words, c2, shift);
+            l += masked ? tile_weights_masked<MT, E4>(s_addr, s->kscale[ti], s->vscale[ti], allowed, c2, shift)
+                        : tile_weights<MT, E4>(s_addr, s->kscale[ti], s->vscale[ti], c2, shift);
             tmem_wait_st();
           }
           if (!E4 && tail && (!two || g == 0)) {
@@ -991,7 +1030,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
             const long long tok = tok0 + r;
             if (tok >= w.len) {
               uint4* line = reinterpret_cast<uint4*>(ring + slot * entry + r * 128);
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < kChunks; ++c, line += kTile * 8) {
                 if (tok >= w.total) {
 #pragma unroll
@@ -1116,7 +1155,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
         base += 2 * T;
         tile_base += T;
         ++seg;
-      } while (!*reinterpret_cast<volatile int*>(&s->stop) && w.next(a));
+      } while (!*reinterpret_cast<volatile int*>(&s->stop) && w.next(a, p.pairs));
     }
   }
   __syncthreads();
@@ -1132,37 +1171,26 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
 // boundaries cut one item share its rows' columns (runs of 8), so that each
 // reads about as much as one share wrote.
 template <typename QT, int DP>
-__global__ void __launch_bounds__(256) attention_join_kernel(const MmaParams p, int grid) {
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __grid_constant__ MmaParams p, int grid) {
   griddep_wait();
   __shared__ long long sums[256];
   __shared__ Found found;
   const AttnParams& a = p.a;
-  const int per_b = a.c.heads * p.pairs;
   const int j = blockIdx.x + 1;
-  find_tile(a, per_b, sums, &found, [&](long long T) {
-    const Split sp{T, static_cast<int>(min(static_cast<long long>(grid), T))};
-    return j < sp.n ? sp.start(j) : -1;
-  });
-  const Split split{found.T, static_cast<int>(min(static_cast<long long>(grid), found.T))};
-  if (j >= split.n) return;
-  const int b = found.b;
-  const int tiles = tiles_of(a, b);
-  const int item = static_cast<int>(found.rem / tiles);
-  const int into = static_cast<int>(found.rem - static_cast<long long>(item) * tiles);
-  if (into == 0) return;  // between two items
-  const long long lo = split.start(j) - into, hi = lo + tiles;
+  find_share(a, p.pairs, grid, j, sums, &found);
+  const Split split = found.split;
+  const int b = found.b, h = found.h;
+  if (b < 0 || found.t0 == 0) return;  // no such share, or one that starts with an item
+  const long long lo = split.start(j) - found.t0, hi = lo + tiles_of(a, b);
   int first = j, last = j;  // boundaries inside the item
   while (first > 1 && split.start(first - 1) > lo) --first;
   while (last + 1 < split.n && split.start(last + 1) < hi) ++last;
   const int parts = last - first + 2;
-  const int pr = item % p.pairs, h = item / p.pairs;
-  const bool two = 2 * pr + 1 < p.halves;
-  const int row0 = pr * 2 * kTile;
+  const bool two = 2 * found.pr + 1 < p.halves;
+  const int row0 = found.pr * 2 * kTile;
   const int rows = min(two ? 2 * kTile : kTile, p.R - row0);
   const int D = a.c.dim;
   const int units = rows * (D / 8), blocks = last - first + 1, me = j - first;
-  const int u0 = static_cast<int>(static_cast<long long>(units) * me / blocks);
-  const int u1 = static_cast<int>(static_cast<long long>(units) * (me + 1) / blocks);
   const size_t tile = slot_floats(DP);
   const float* scratch = static_cast<const float*>(a.scratch);
   const int slot0 = 2 * (first - 1) + (split.start(first - 1) < lo ? 1 : 0);
@@ -1170,32 +1198,73 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const MmaParams p, 
     const int slot = i == 0 ? slot0 : 2 * (first - 1 + i);
     return scratch + (static_cast<size_t>(slot) * p.qtiles + (row >> 7)) * tile;
   };
-  for (int i = u0 + threadIdx.x; i < u1; i += 256) {
-    const int row = i % rows, c = i / rows;
-    float M = -INFINITY;
+  // A row's factors, for the rows this block has columns of: 2^(m - M) / l of
+  // each part; a block whose boundaries cut one item has at most kMaxCtas
+  // parts, of which kParts are kept here at a time.
+  constexpr int kParts = 8;
+  __shared__ float factor[kParts][2 * kTile];
+  __shared__ float top[2 * kTile], inv[2 * kTile];
+  for (int row = threadIdx.x; row < rows; row += kJoinThreads) {
+    float M = -INFINITY, L = 0.0f;
+#pragma unroll 4
     for (int x = 0; x < parts; ++x)
       M = fmaxf(M, reinterpret_cast<const float2*>(part(x, row) + static_cast<size_t>(kTile) * DP)[row & 127].x);
-    float L = 0.0f, o[8] = {};
 #pragma unroll 4
     for (int x = 0; x < parts; ++x) {
-      const float* q = part(x, row);
-      const float2 ml = reinterpret_cast<const float2*>(q + static_cast<size_t>(kTile) * DP)[row & 127];
-      const float4 y0 = reinterpret_cast<const float4*>(q)[static_cast<size_t>(2 * c) * kTile + (row & 127)];
-      const float4 y1 = reinterpret_cast<const float4*>(q)[static_cast<size_t>(2 * c + 1) * kTile + (row & 127)];
+      const float2 ml = reinterpret_cast<const float2*>(part(x, row) + static_cast<size_t>(kTile) * DP)[row & 127];
       const float f = ml.x == M ? 1.0f : ex2f(ml.x - M);
-      if (ml.y == 0.0f) continue;
-      L = fmaf(ml.y, f, L);
-      if (f == 0.0f) continue;
-      o[0] = fmaf(y0.x, f, o[0]), o[1] = fmaf(y0.y, f, o[1]), o[2] = fmaf(y0.z, f, o[2]), o[3] = fmaf(y0.w, f, o[3]);
-      o[4] = fmaf(y1.x, f, o[4]), o[5] = fmaf(y1.y, f, o[5]), o[6] = fmaf(y1.z, f, o[6]), o[7] = fmaf(y1.w, f, o[7]);
+      if (ml.y != 0.0f) L = fmaf(ml.y, f, L);
     }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    top[row] = M;
+    inv[row] = L == 0.0f ? 0.0f : 1.0f / L;
+    if (a.lse && me == 0) {
+      const int node = div_rows(row0 + row, p.div_G), head = h * a.G + (row0 + row - node * a.G);
+      a.lse[(static_cast<long long>(b) * a.N + node) * a.Hq + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+    }
+  }
+  const int u0 = static_cast<int>(static_cast<long long>(units) * me / blocks);
+  const int u1 = static_cast<int>(static_cast<long long>(units) * (me + 1) / blocks);
+  for (int i0 = u0; i0 < u1; i0 += kJoinThreads) {
+    const int i = i0 + threadIdx.x;
+    const bool in = i < u1;
+    const int row = in ? i % rows : 0, c = in ? i / rows : 0;
+    float o[8] = {};
+    for (int x0 = 0; x0 < parts; x0 += kParts) {
+      const int n = min(kParts, parts - x0);
+      float4 y[2][4];
+      __syncthreads();  // top and inv are there; the last factors have been used
+      if (i0 == u0 || parts > kParts)
+        for (int z = threadIdx.x; z < n * rows; z += kJoinThreads) {
+          const int x = z / rows, r = z % rows;
+          const float2 ml = reinterpret_cast<const float2*>(part(x0 + x, r) + static_cast<size_t>(kTile) * DP)[r & 127];
+          const float f = ml.x == top[r] ? 1.0f : ex2f(ml.x - top[r]);
+          factor[x][r] = ml.y == 0.0f ? 0.0f : f * inv[r];
+        }
+      __syncthreads();
+      for (int x = 0; x < n; x += 4) {
 #pragma unroll
-    for (int x = 0; x < 8; ++x) o[x] *= inv;
-    const int node = div_rows(row0 + row, p.div_G), head = h * a.G + (row0 + row - node * a.G);
-    const long long out_row = (static_cast<long long>(b) * a.N + node) * a.Hq + head;
-    store8(static_cast<QT*>(a.out) + out_row * D + c * 8, o);
-    if (a.lse && c == 0) a.lse[out_row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
+        for (int z = 0; z < 4; ++z)
+          if (x + z < n) {
+            const float4* q = reinterpret_cast<const float4*>(part(x0 + x + z, row));
+            y[0][z] = q[static_cast<size_t>(2 * c) * kTile + (row & 127)];
+            y[1][z] = q[static_cast<size_t>(2 * c + 1) * kTile + (row & 127)];
+          }
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          if (x + z < n) {
+            const float f = factor[x + z][row];
+            if (f == 0.0f) continue;
+            o[0] = fmaf(y[0][z].x, f, o[0]), o[1] = fmaf(y[0][z].y, f, o[1]), o[2] = fmaf(y[0][z].z, f, o[2]);
+            o[3] = fmaf(y[0][z].w, f, o[3]), o[4] = fmaf(y[1][z].x, f, o[4]), o[5] = fmaf(y[1][z].y, f, o[5]);
+            o[6] = fmaf(y[1][z].z, f, o[6]), o[7] = fmaf(y[1][z].w, f, o[7]);
+          }
+      }
+    }
+    if (in) {
+      const int node = div_rows(row0 + row, p.div_G), head = h * a.G + (row0 + row - node * a.G);
+      const long long out_row = (static_cast<long long>(b) * a.N + node) * a.Hq + head;
+      store8(static_cast<QT*>(a.out) + out_row * D + c * 8, o);
+    }
   }
 }
 
@@ -1283,7 +1352,7 @@ cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[4], int grid, cud
                        maps[3]),
               1);
   if (e != cudaSuccess || grid < 2) return e;
-  return counted(launch_k(SV_PDL >= 1, attention_join_kernel<QT, DP>, dim3(grid - 1), dim3(256), 0, st, p, grid), 1);
+  return counted(launch_k(SV_PDL >= 1, attention_join_kernel<QT, DP>, dim3(grid - 1), dim3(kJoinThreads), 0, st, p, grid), 1);
 }
 
 }  // namespace
