@@ -70,6 +70,7 @@ struct MmaParams {
   int qbufs;    // Q buffers: 2, or 1 where two row tiles leave no room
   int scale_bytes;  // one scale array of a ring entry (8-bit pools)
   int negate;   // the scale is negative: Q is negated instead
+  int zero;     // the scale is zero: Q is zero and the scale 1
   int qvec;     // query rows start on 16-byte boundaries
   UDiv div_G;   // / a.G
 };
@@ -234,6 +235,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
       : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
 // Arrives on `bar` once every MMA this thread has issued is complete.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
@@ -301,15 +309,17 @@ struct Control {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t cfull[kConvStages], cempty[kConvStages];
   uint64_t scale_full[kScaleRing];
-  uint64_t s_full[2], p_ready[2], o_done, q_full[2], q_empty[2];
+  uint64_t s_full[2], p_ready[2], o_done, q_full[2], q_empty[2], drained;
   uint32_t tmem;
   int abort;
   int stop;              // abort, as the softmax warpgroups agreed on it
   int bad[2];            // a page of the segment is missing (by Q buffer)
-  unsigned int odd[2];   // tree tokens whose values hold an infinity or a NaN
+  unsigned int odd[4][2];  // drafted tokens whose values hold an infinity or a NaN (by segment: the
+                           // converters may be two segments ahead)
   int parent[2][64];
   float qscale[2][2 * kTile];
   float2 ml[2][kTile];
+  alignas(16) float ones[kTile];
   alignas(16) float kscale[kScaleRing][kTile];
   alignas(16) float vscale[kScaleRing][kTile];
   float vmax[kScaleRing][4];
@@ -351,12 +361,21 @@ __device__ __forceinline__ float tile_max(uint32_t s_addr, const float* ks) {
   float top[2] = {-INFINITY, -INFINITY};
   uint32_t v[2][16];
   tmem_ld16(s_addr, v[0]);
+  float4 kn[4];
+  if (E4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) kn[i] = *reinterpret_cast<const float4*>(ks + i * 4);
+  }
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     float4 kc[4];
     if (E4) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) kc[i] = *reinterpret_cast<const float4*>(ks + c * 16 + i * 4);
+      for (int i = 0; i < 4; ++i) kc[i] = kn[i];
+      if (c < 7) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kn[i] = *reinterpret_cast<const float4*>(ks + (c + 1) * 16 + i * 4);
+      }
     }
     tmem_wait_ld();
     if (c < 7) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
@@ -381,6 +400,14 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, 
   unsigned long long sum[2] = {0ull, 0ull};
   uint32_t v[2][16];
   tmem_ld16(s_addr, v[0]);
+  ulonglong2 kn[4], vn[4];
+  if (E4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      kn[i] = *reinterpret_cast<const ulonglong2*>(ks + i * 4);
+      vn[i] = *reinterpret_cast<const ulonglong2*>(vs + i * 4);
+    }
+  }
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     uint32_t out[8];
@@ -388,8 +415,15 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, 
     if (E4) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        kc[i] = *reinterpret_cast<const ulonglong2*>(ks + c * 16 + i * 4);
-        vc[i] = *reinterpret_cast<const ulonglong2*>(vs + c * 16 + i * 4);
+        kc[i] = kn[i];
+        vc[i] = vn[i];
+      }
+      if (c < 7) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          kn[i] = *reinterpret_cast<const ulonglong2*>(ks + (c + 1) * 16 + i * 4);
+          vn[i] = *reinterpret_cast<const ulonglong2*>(vs + (c + 1) * 16 + i * 4);
+        }
       }
     }
     tmem_wait_ld();
@@ -429,53 +463,29 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, 
   return (a + b) + (d + e);
 }
 
-// The same two passes where some columns are masked (allowed: bit i of word
-// c is column 32 c + i).  A sequence's last tile or two; kept small.
+// Puts -inf where a column is masked (bit i of word c allows column 32 c + i),
+// before the two passes.  8-bit pools: K's scales enter here, so that a scale
+// of a masked column does not matter, and the passes take ones.
 template <bool E4>
-__device__ __forceinline__ float tile_max_masked(uint32_t s_addr, const float* ks, const uint4& allowed) {
-  float top = -INFINITY;
+__device__ __forceinline__ void mask_tile(uint32_t s_addr, const float* ks, const uint32_t (&words)[4]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t word = words[c];
+    if (!E4 && __all_sync(0xffffffffu, word == ~0u)) continue;
 #pragma unroll 1
-  for (int c = 0; c < 8; ++c) {
-    const uint32_t word = (c < 4 ? (c < 2 ? allowed.x : allowed.y) : (c < 6 ? allowed.z : allowed.w)) >> (c & 1) * 16;
-    uint32_t v[16];
-    tmem_ld16(s_addr + c * 16, v);
-    tmem_wait_ld();
+    for (int z = 0; z < 2; ++z) {
+      uint32_t v[16];
+      tmem_ld16(s_addr + c * 32 + z * 16, v);
+      tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float f = __uint_as_float(v[i]);
-      if (E4) f *= ks[c * 16 + i];
-      if (word >> i & 1u) top = fmaxf(top, f);
-    }
-  }
-  return top;
-}
-template <typename M, bool E4>
-__device__ __forceinline__ float tile_weights_masked(uint32_t s_addr, const float* ks, const float* vs,
-                                                     const uint4& allowed, float c2, float shift) {
-  float sum = 0.0f;
-#pragma unroll 1
-  for (int c = 0; c < 8; ++c) {
-    const uint32_t word = (c < 4 ? (c < 2 ? allowed.x : allowed.y) : (c < 6 ? allowed.z : allowed.w)) >> (c & 1) * 16;
-    uint32_t v[16], out[8];
-    tmem_ld16(s_addr + c * 16, v);
-    tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      float f[2];
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const bool on = word >> (i + z) & 1u;
-        f[z] = __uint_as_float(v[i + z]);
-        if (E4) f[z] *= ks[c * 16 + i + z];
-        f[z] = on ? ex2f(fmaf(f[z], c2, -shift)) : 0.0f;
-        sum += f[z];
-        if (E4 && on) f[z] *= vs[c * 16 + i + z];
+      for (int i = 0; i < 16; ++i) {
+        if (E4) v[i] = __float_as_uint(__uint_as_float(v[i]) * ks[c * 32 + z * 16 + i]);
+        v[i] = word >> (z * 16 + i) & 1u ? v[i] : 0xff800000u;
       }
-      out[i >> 1] = pack_weights<M>(f[0], f[1]);
+      tmem_st16(s_addr + c * 32 + z * 16, v);
     }
-    tmem_st8(s_addr + c * 8, out);
   }
-  return sum;
+  tmem_wait_st();
 }
 
 __device__ __forceinline__ int div_rows(int n, const UDiv& d) {
@@ -500,21 +510,31 @@ __device__ __forceinline__ void load_segment(const MmaParams& p, const Walk& w, 
     return reinterpret_cast<uint4*>(q_tiles + (rr >> 7) * kTile * DP * 2 + (j >> 3) * p.qrows * 128 + (rr & 127) * 128 +
                                     (((j & 7) ^ (rr & 7)) * 16));
   };
-#pragma unroll 2
-  for (int rr = first; rr < rows; rr += kStride) {
-    const int nd = div_rows(row0 + rr, p.div_G);
-    const QT* src = q + nd * a.q.sn + (row0 + rr - nd * a.G) * a.q.sh;
-    uint4* dst = place(rr);
-    if (j * 8 >= D) {
-      *dst = make_uint4(0u, 0u, 0u, 0u);
-    } else if (p.qvec) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-    } else {
-      const uint16_t* x = reinterpret_cast<const uint16_t*>(src);
-      uint32_t y[4];
+  {
+    // (node, head of the group) and the source advance with the row
+    int nd = div_rows(row0 + first, p.div_G), g = row0 + first - nd * a.G;
+    const QT* src = q + nd * a.q.sn + g * a.q.sh;
+    const long long step = kStride * a.q.sh, wrap = a.q.sn - a.G * a.q.sh;
+#pragma unroll 1
+    for (int rr = first; rr < rows; rr += kStride) {
+      uint4* dst = place(rr);
+      if (j * 8 >= D) {
+        *dst = make_uint4(0u, 0u, 0u, 0u);
+      } else if (p.qvec) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+      } else {
+        const uint16_t* x = reinterpret_cast<const uint16_t*>(src);
+        uint32_t y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = x[2 * i] | static_cast<uint32_t>(x[2 * i + 1]) << 16;
-      *dst = make_uint4(y[0], y[1], y[2], y[3]);
+        for (int i = 0; i < 4; ++i) y[i] = x[2 * i] | static_cast<uint32_t>(x[2 * i + 1]) << 16;
+        *dst = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+      g += kStride;
+      src += step;
+      while (g >= a.G) {
+        g -= a.G;
+        src += wrap;
+      }
     }
   }
   if (a.parent && tid < a.N) s->parent[buf][tid] = __ldg(a.parent + static_cast<long long>(w.b) * a.N + tid);
@@ -532,11 +552,12 @@ __device__ __forceinline__ void load_segment(const MmaParams& p, const Walk& w, 
     raise_flag(a.ctrl, kFlagInvalidPage);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  if (E4 || p.negate) {
+  if (E4 || p.negate || p.zero) {
 #pragma unroll 1
     for (int r0 = first; r0 - first < rows; r0 += kStride) {  // all lanes take part
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
       if (r0 < rows) v = *place(r0);
+      if (p.zero) v = make_uint4(0u, 0u, 0u, 0u);
       if (p.negate) v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
       if (E4) {
         // a power of two brings the row's largest element to 2^14..2^15
@@ -613,13 +634,17 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
       mbar_init(&s->s_full[i], 1);
       mbar_init(&s->p_ready[i], 4);
       s->bad[i] = 0;
-      s->odd[i] = 0u;
+      for (int z = 0; z < 4; ++z) s->odd[z][i] = 0u;
       mbar_init(&s->q_full[i], 2);
       mbar_init(&s->q_empty[i], 8);
     }
     mbar_init(&s->o_done, 1);
+    mbar_init(&s->drained, 1);
     s->abort = 0;
     s->stop = 0;
+  }
+  if (tid < kTile) s->ones[tid] = 1.0f;
+  if (tid == 0) {
     mbar_fence_init();
   }
   if (warp == 9) {
@@ -710,70 +735,82 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
           while (!mbar_try_wait(&s->full[i % p.stages], (i / p.stages) & 1u) && global_ns() - t0 < kWaitLimitNs) {}
       }
     } else if (warp == 9) {
-      // ------------------------------------------------ MMA issue (one thread)
-      if (lane == 0) {
-        const uint32_t stages = E4 ? kConvStages : p.stages;
-        const uint32_t step_bytes = E4 ? kConv : entry;
-        const uint32_t chunk = p.qrows * 128 >> 4;  // Q's next 64 columns
-        uint64_t* const fullb = E4 ? s->cfull : s->full;
-        uint64_t* const emptyb = E4 ? s->cempty : s->empty;
-        // The ring is read in its own order; a tile stays until its last product.
-        uint32_t next = 0, next_phase = 0, kslot = 0, vslot = 0;
-        const auto take = [&](uint32_t& slot) {
-          slot = next;
-          wait(s, &fullb[slot], next_phase, a.ctrl);
-          if (++next == stages) next = 0, next_phase ^= 1u;
-        };
-        const uint64_t q0 = operand(smem_addr(qs), 16, 1024);
-        const uint64_t k0 = operand(smem_addr(E4 ? conv : ring), 16, 1024);
-        const uint64_t v0 = operand(smem_addr(E4 ? conv : ring), kTile * 128, 1024);
-        uint32_t seg = 0, np = 0;  // np: phases of p_ready, one bit a warpgroup
-        do {
-          const bool two = 2 * w.pr + 1 < p.halves;
-          const int T = w.t1 - w.t0, U = two ? 2 * T : T;
-          const uint32_t buf = p.qbufs == 2 ? seg & 1u : 0u;
-          wait(s, &s->q_full[buf], (p.qbufs == 2 ? seg >> 1 : seg) & 1u, a.ctrl);
-          const uint64_t q1 = q0 + buf * (qbytes >> 4);
+      // ------------------------------------------------ MMA issue
+      // The whole warp walks the loop, so that addresses and descriptors stay
+      // in uniform registers; one elected thread issues.
+      const uint32_t stages = E4 ? kConvStages : p.stages;
+      const uint32_t step_bytes = E4 ? kConv : entry;
+      const uint32_t chunk = p.qrows * 128 >> 4;  // Q's next 64 columns
+      uint64_t* const fullb = E4 ? s->cfull : s->full;
+      uint64_t* const emptyb = E4 ? s->cempty : s->empty;
+      // The ring is read in its own order; a tile stays until its last product.
+      uint32_t next = 0, next_phase = 0, kslot = 0, vslot = 0;
+      const auto take = [&](uint32_t& slot) {
+        slot = next;
+        wait(s, &fullb[slot], next_phase, a.ctrl);
+        if (++next == stages) next = 0, next_phase ^= 1u;
+      };
+      const uint32_t acc = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t q0 = operand(smem_addr(qs), 16, 1024);
+      const uint64_t k0 = operand(smem_addr(E4 ? conv : ring), 16, 1024);
+      const uint64_t v0 = operand(smem_addr(E4 ? conv : ring), kTile * 128, 1024);
+      uint32_t seg = 0, np = 0;  // np: phases of p_ready, one bit a warpgroup
+      bool stop = false;
+      do {
+        const bool two = __shfl_sync(0xffffffffu, 2 * w.pr + 1 < p.halves, 0);
+        const int T = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0), U = two ? 2 * T : T;
+        const uint32_t buf = p.qbufs == 2 ? seg & 1u : 0u;
+        wait(s, &s->q_full[buf], (p.qbufs == 2 ? seg >> 1 : seg) & 1u, a.ctrl);
+        const uint64_t q1 = q0 + buf * (qbytes >> 4);
 #pragma unroll 1
-          for (int x = 0; x <= U; ++x) {
-            const uint32_t g = x & 1;
-            const bool shared = two && g == 1;  // the second user of this tile
-            if (x < U) {
-              if (!shared) take(kslot);
-              tmem_fence_after();
-              const uint64_t qd = q1 + (shared ? kTile * DP * 2 >> 4 : 0);
-              const uint64_t kd = k0 + kslot * (step_bytes >> 4);
+        for (int x = 0; x <= U; ++x) {
+          const uint32_t g = x & 1;
+          const bool shared = two && g == 1;  // the second user of this tile
+          if (x < U) {
+            if (!shared) take(kslot);
+            tmem_fence_after();
+            const uint64_t qd = q1 + (shared ? kTile * DP * 2 >> 4 : 0);
+            const uint64_t kd = k0 + kslot * (step_bytes >> 4);
+            if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < DP / 16; ++k) {
                 // 16 elements are 32 bytes of a 128-byte row; 64 are the next block of rows
-                const uint32_t step = (k / 4) * (kTile * 128 >> 4) + (k % 4) * 2;
-                mma_ss(tmem + g * kTile, qd + (k / 4) * chunk + (k % 4) * 2, kd + step, kShapeS, k > 0);
+                mma_ss(acc + g * kTile, qd + (k / 4) * chunk + (k % 4) * 2,
+                       kd + (k / 4) * (kTile * 128 >> 4) + (k % 4) * 2, kShapeS, k > 0);
               }
               mma_commit(&s->s_full[g]);
               if (!two || g == 1) mma_commit(&emptyb[kslot]);
             }
-            if (x > 0) {
-              const uint32_t f = g ^ 1u;  // unit x - 1
-              if (!two || f == 0) take(vslot);
-              wait(s, &s->p_ready[f], np >> f & 1u, a.ctrl);
-              np ^= 1u << f;
-              tmem_fence_after();
-              const uint64_t vd = v0 + vslot * (step_bytes >> 4);
-              const uint32_t o = tmem + 2 * kTile + f * DP;
+            __syncwarp();
+          }
+          if (x > 0) {
+            const uint32_t f = g ^ 1u;  // unit x - 1
+            if (!two || f == 0) take(vslot);
+            wait(s, &s->p_ready[f], np >> f & 1u, a.ctrl);
+            np ^= 1u << f;
+            tmem_fence_after();
+            const uint64_t vd = v0 + vslot * (step_bytes >> 4);
+            const uint32_t o = acc + 2 * kTile + f * DP, pw = acc + f * kTile;
+            const bool add = x > 2;
+            if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k)
-                mma_ts(o, tmem + f * kTile + k * 8, vd + k * (16 * 128 >> 4), kShapeO, x > 2 || k > 0);
+                mma_ts(o, pw + k * 8, vd + k * (16 * 128 >> 4), kShapeO, add || k > 0);
               if (!two || f == 1) mma_commit(&emptyb[vslot]);
+              if (x == U) mma_commit(&s->o_done);
             }
-            if (gave_up(s)) break;
+            __syncwarp();
           }
-          mma_commit(&s->o_done);
-          ++seg;
-        } while (!gave_up(s) && w.next(a, p.pairs));
-        if (gave_up(s)) {  // MMAs in flight finish before their memory goes away
-          const unsigned long long t0 = global_ns();
-          while (!mbar_try_wait(&s->o_done, (seg - 1) & 1u) && global_ns() - t0 < kWaitLimitNs) {}
+          stop = __any_sync(0xffffffffu, gave_up(s));
+          if (stop) break;
         }
+        ++seg;
+      } while (!stop && w.next(a, p.pairs));
+      if (stop) {  // MMAs in flight finish before their memory goes away
+        if (elect_one()) mma_commit(&s->drained);
+        __syncwarp();
+        const unsigned long long t0 = global_ns();
+        while (!mbar_try_wait(&s->drained, 0) && global_ns() - t0 < kWaitLimitNs) {}
       }
       __syncwarp();
     } else if (warp >= kLoader) {
@@ -796,7 +833,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
       // ------------------------------------------------ 8-bit to 16-bit tiles
       if (E4) {
         const int cw = warp - 10;
-        uint32_t slot = 0, phase = 0, cslot = 0, cphase = 0, tile = 0;
+        uint32_t slot = 0, phase = 0, cslot = 0, cphase = 0, tile = 0, seg = 0;
         bool stop = false;  // the same in all lanes
         constexpr int kLanes = DP / 16;     // lanes a row, 16 codes each
         constexpr int kRows = 32 / kLanes;  // rows an iteration
@@ -832,7 +869,11 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
               const int x = cw * 32 + lane;
               const bool in = tok0 + x < w.total;
               const float ks = in ? *reinterpret_cast<const float*>(src + kData + scale_at) : 0.0f;
-              const float vs = in ? *reinterpret_cast<const float*>(src + kData + p.scale_bytes + scale_at) : 0.0f;
+              float vs = in ? *reinterpret_cast<const float*>(src + kData + p.scale_bytes + scale_at) : 0.0f;
+              if (in && tok0 + x >= w.len && !(fabsf(vs) < INFINITY)) {
+                atomicOr(&s->odd[seg & 3][(tok0 + x - w.len) >> 5], 1u << ((tok0 + x - w.len) & 31));
+                vs = 0.0f;
+              }
               s->kscale[ti][x] = ks;
               s->vscale[ti][x] = vs;
               const float top = warp_max(fabsf(vs) < INFINITY ? fabsf(vs) : 0.0f);
@@ -864,9 +905,9 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
                 uint4 c = codes[it * kRows * DP / 16];
                 const long long tok = tok0 + row0 + it * kRows;
                 if (tok >= w.total) c = make_uint4(0u, 0u, 0u, 0u);
-                if (values && tok >= w.len) {
+                if (values && tok >= w.len && tok < w.total) {
                   // a drafted token's NaN must reach its own descendants only:
-                  // it goes by the scale, which multiplies their weights alone
+                  // it counts as zero here, and its row is listed
                   const uint32_t words[4] = {c.x, c.y, c.z, c.w};
                   bool odd = false;
 #pragma unroll
@@ -875,7 +916,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
                     for (int z = 0; z < 4; ++z) odd |= (words[q] >> (8 * z) & 0x7fu) == 0x7fu;
                   if (odd) {
                     c = make_uint4(0u, 0u, 0u, 0u);
-                    s->vscale[ti][row0 + it * kRows] = __int_as_float(0x7fc00000);
+                    atomicOr(&s->odd[seg & 3][(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
                   }
                 }
                 widen(c, it);
@@ -892,6 +933,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
             if (++cslot == kConvStages) cslot = 0, cphase ^= 1u;
           }
           tile += T;
+          ++seg;
         } while (!stop && w.next(a, p.pairs));
       }
     } else {
@@ -947,18 +989,14 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
           ++ns;
           if (E4) {
             wait(s, &s->scale_full[ti], ((tile_base + t) / kScaleRing) & 1u, a.ctrl);
-            if (tail) {  // the widening of drafted tokens' values may still mark a scale
-              const uint32_t e = base + v_entry(two, t, T);
-              wait(s, &s->cfull[e % kConvStages], (e / kConvStages) & 1u, a.ctrl);
-            }
           }
           __syncwarp();
           tmem_fence_after();
           if (warp_live) {
-            uint4 allowed;
+            const float* ks = s->kscale[ti];
             if (masked) {
               uint32_t words[4];
-#pragma unroll 1
+#pragma unroll
               for (int c = 0; c < 4; ++c) {
                 const long long off = tok0 + 32 * c - w.len, lim = w.total - (tok0 + 32 * c);
                 uint32_t y = ~0u;
@@ -976,15 +1014,12 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
                   }
                   y &= __ballot_sync(0xffffffffu, in);
                 }
-                words[0] = c == 0 ? y : words[0];
-                words[1] = c == 1 ? y : words[1];
-                words[2] = c == 2 ? y : words[2];
-                words[3] = c == 3 ? y : words[3];
+                words[c] = y;
               }
-              allowed = make_uint4(words[0], words[1], words[2], words[3]);
+              mask_tile<E4>(s_addr, ks, words);
+              ks = s->ones;
             }
-            float top = masked ? tile_max_masked<E4>(s_addr, s->kscale[ti], allowed)
-                               : tile_max<E4>(s_addr, s->kscale[ti]);
+            float top = tile_max<E4>(s_addr, ks);
             top = top == -INFINITY ? -INFINITY : top * c2;
             bool raise;
             float Mn = M;
@@ -1017,8 +1052,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
             }
             M = Mn;
             const float shift = M == -INFINITY ? 0.0f : M;
-            l += masked ? tile_weights_masked<MT, E4>(s_addr, s->kscale[ti], s->vscale[ti], allowed, c2, shift)
-                        : tile_weights<MT, E4>(s_addr, s->kscale[ti], s->vscale[ti], c2, shift);
+            l += tile_weights<MT, E4>(s_addr, ks, s->vscale[ti], c2, shift);
             tmem_wait_st();
           }
           if (!E4 && tail && (!two || g == 0)) {
@@ -1049,7 +1083,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
                       if (odd_word<MT>(y[q] & 0xffffu)) y[q] &= 0xffff0000u;
                       if (odd_word<MT>(y[q] & 0xffff0000u)) y[q] &= 0xffffu;
                     }
-                    atomicOr(&s->odd[(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
+                    atomicOr(&s->odd[seg & 3][(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
                   }
                 }
               }
@@ -1068,7 +1102,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
         if (mask == 0ull) M = -INFINITY, l = 0.0f;
         s->ml[g][r] = make_float2(M, l);
         softmax_sync();
-        const unsigned int odd0 = E4 ? 0u : s->odd[0], odd1 = E4 ? 0u : s->odd[1];
+        const unsigned int odd0 = s->odd[seg & 3][0], odd1 = s->odd[seg & 3][1];
         if (warp_live) {
           float f0 = 1.0f, f1 = 0.0f;
           if (!two) {
@@ -1083,6 +1117,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
           const bool whole = w.whole();
           const bool none = mask == 0ull || l == 0.0f;
           const float inv = none ? 0.0f : whole ? 1.0f / l : 1.0f;
+          unsigned char* const staged = qs + buf * qbytes;
           const int col0 = two ? 0 : g * (DP / 2), ncol = two ? DP : DP / 2;
           const int D = a.c.dim, head = h * a.G + (row0 + row - node * a.G);
           const long long out_row = (static_cast<long long>(w.b) * a.N + node) * a.Hq + head;
@@ -1105,9 +1140,15 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
                 if (!two && f1 != 0.0f) y = fmaf(__uint_as_float(v1[i]), f1, y);
                 o[i] = none ? 0.0f : y * inv;
               }
-              if (!E4 && (odd0 | odd1) && !none) {
+              const unsigned long long seen = mask & (static_cast<unsigned long long>(odd1) << 32 | odd0);
+              if (E4 && seen && !none) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __int_as_float(0x7fc00000);
+              }
+              if (!E4 && seen && !none) {
                 // weight times an infinity or a NaN: itself, whatever the weight
-                for (unsigned long long m = mask & (static_cast<unsigned long long>(odd1) << 32 | odd0); m; m &= m - 1) {
+#pragma unroll 1
+                for (unsigned long long m = seen; m; m &= m - 1) {
                   const long long tok = w.len + __ffsll(static_cast<long long>(m)) - 1;
                   int page, place;
                   if (tok >= w.total || !find_place(a.c, w.b, tok, page, place, nullptr)) continue;
@@ -1121,14 +1162,13 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
                 }
               }
               if (whole) {
-                QT* dst = static_cast<QT*>(a.out) + out_row * D + col0 + c;
-#pragma unroll
-                for (int i = 0; i < 16; i += 8) {
-                  if (col0 + c + i < D) {
-                    const float y[8] = {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]};
-                    store8(dst + i, y);
-                  }
-                }
+                // into the row's place among the queries, which are done with
+                uint4* dst = reinterpret_cast<uint4*>(staged + (row >> 7) * kTile * DP * 2) + (row & 127) * (DP / 8);
+                const float y0[8] = {o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]};
+                const float y1[8] = {o[8], o[9], o[10], o[11], o[12], o[13], o[14], o[15]};
+                const int unit = (col0 + c) / 8;
+                store8(reinterpret_cast<QT*>(dst + (unit ^ (row & 7))), y0);
+                store8(reinterpret_cast<QT*>(dst + ((unit + 1) ^ (row & 7))), y1);
               } else {
                 float4* dst = reinterpret_cast<float4*>(part) + static_cast<size_t>((col0 + c) / 4) * kTile + (row & 127);
 #pragma unroll
@@ -1147,8 +1187,25 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
         }
         tmem_fence_before();
         if (tid == 0) s->stop = gave_up(s);
-        softmax_sync();  // O, Q, ml and odd may be overwritten now
-        if (tid < 2) s->odd[tid] = 0u;
+        softmax_sync();  // O, ml and odd may be overwritten now
+        if (w.whole()) {
+          // 16-byte runs of neighbouring lanes lie next to each other in the output
+          const int D = a.c.dim, units = D / 8;
+          const unsigned char* staged = qs + buf * qbytes;
+#pragma unroll 1
+          for (int i = tid; i < rows * (DP / 8); i += 256) {
+            const int rr = i / (DP / 8), unit = i % (DP / 8);
+            if (unit >= units) continue;
+            const uint4 v = reinterpret_cast<const uint4*>(staged + (rr >> 7) * kTile * DP * 2)[(rr & 127) * (DP / 8) +
+                                                                                               (unit ^ (rr & 7))];
+            const int nd = div_rows(row0 + rr, p.div_G), hd = h * a.G + (row0 + rr - nd * a.G);
+            *reinterpret_cast<uint4*>(static_cast<QT*>(a.out) +
+                                      ((static_cast<long long>(w.b) * a.N + nd) * a.Hq + hd) * D + unit * 8) = v;
+          }
+          // the next queries come by another proxy's writes
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if (tid < 2) s->odd[seg & 3][tid] = 0u;
         if (tid == 2) s->bad[buf] = 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&s->q_empty[buf]);
@@ -1384,7 +1441,8 @@ cudaError_t launch_attention_mma(const AttnParams& a, int q_dtype, int cache_dty
   while (p.box < kTile && a.c.page_size % (2 * p.box) == 0) p.box *= 2;
   p.head_first = a.c.heads > 1 && a.c.page_size > 1 && a.c.head_stride < a.c.token_stride;
   p.negate = a.c2 < 0.0f;
-  p.a.c2 = a.c2 < 0.0f ? -a.c2 : a.c2;
+  p.zero = a.c2 == 0.0f;
+  p.a.c2 = p.zero ? 1.0f : a.c2 < 0.0f ? -a.c2 : a.c2;
   p.qvec = reinterpret_cast<uintptr_t>(a.q.p) % 16 == 0 && a.q.sb % 8 == 0 && a.q.sn % 8 == 0 && a.q.sh % 8 == 0;
   CUtensorMap maps[4] = {};
   bool ok = pool_map(&maps[0], a.c, a.c.k, cache_dtype, p.box, p.head_first) &&
