@@ -71,7 +71,8 @@ struct MmaParams {
   int scale_bytes;  // one scale array of a ring entry (8-bit pools)
   int negate;   // the scale is negative: Q is negated instead
   int zero;     // the scale is zero: Q is zero and the scale 1
-  int qvec;     // query rows start on 16-byte boundaries
+  int qbox;     // nodes of a query box (the tensor map's); 0: plain loads
+  int split;    // copies of the rows in the 128 lanes, each with a share of a tile's columns
   UDiv div_G;   // / a.G
 };
 
@@ -309,7 +310,7 @@ struct Control {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t cfull[kConvStages], cempty[kConvStages];
   uint64_t scale_full[kScaleRing];
-  uint64_t s_full[2], p_ready[2], o_done, q_full[2], q_empty[2], drained;
+  uint64_t s_full[2], p_ready[2], o_done, q_full[2], q_empty[2], q_tma, drained;
   uint32_t tmem;
   int abort;
   int stop;              // abort, as the softmax warpgroups agreed on it
@@ -356,7 +357,8 @@ __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;"
 
 // Largest score of a row's tile (times K's scales).  Both passes over a tile
 // read 16 columns ahead of the arithmetic.
-template <bool E4>
+// NC: chunks of 16 columns.
+template <bool E4, int NC>
 __device__ __forceinline__ float tile_max(uint32_t s_addr, const float* ks) {
   float top[2] = {-INFINITY, -INFINITY};
   uint32_t v[2][16];
@@ -367,18 +369,18 @@ __device__ __forceinline__ float tile_max(uint32_t s_addr, const float* ks) {
     for (int i = 0; i < 4; ++i) kn[i] = *reinterpret_cast<const float4*>(ks + i * 4);
   }
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < NC; ++c) {
     float4 kc[4];
     if (E4) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) kc[i] = kn[i];
-      if (c < 7) {
+      if (c < NC - 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) kn[i] = *reinterpret_cast<const float4*>(ks + (c + 1) * 16 + i * 4);
       }
     }
     tmem_wait_ld();
-    if (c < 7) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
+    if (c < NC - 1) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       float f[4];
@@ -394,8 +396,9 @@ __device__ __forceinline__ float tile_max(uint32_t s_addr, const float* ks) {
 
 // Weights 2^(s c2 - shift) of a row's tile into tensor memory over the
 // scores (times V's scales); returns their sum (without the scales).
-template <typename M, bool E4>
-__device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, const float* vs, float c2, float shift) {
+template <typename M, bool E4, int NC>
+__device__ __forceinline__ float tile_weights(uint32_t s_addr, uint32_t p_addr, const float* ks, const float* vs, float c2,
+                                              float shift) {
   const unsigned long long c22 = splat2(c2), sh2 = splat2(-shift);
   unsigned long long sum[2] = {0ull, 0ull};
   uint32_t v[2][16];
@@ -409,7 +412,7 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, 
     }
   }
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < NC; ++c) {
     uint32_t out[8];
     ulonglong2 kc[4], vc[4];
     if (E4) {
@@ -418,7 +421,7 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, 
         kc[i] = kn[i];
         vc[i] = vn[i];
       }
-      if (c < 7) {
+      if (c < NC - 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           kn[i] = *reinterpret_cast<const ulonglong2*>(ks + (c + 1) * 16 + i * 4);
@@ -427,7 +430,7 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, 
       }
     }
     tmem_wait_ld();
-    if (c < 7) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
+    if (c < NC - 1) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       const uint32_t* w = &v[c & 1][i];
@@ -455,7 +458,7 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, 
       out[i >> 1] = pack_weights<M>(f[0], f[1]);
       out[(i >> 1) + 1] = pack_weights<M>(f[2], f[3]);
     }
-    tmem_st8(s_addr + c * 8, out);
+    tmem_st8(p_addr + c * 8, out);
   }
   float a, b, d, e;
   unpack2(sum[0], a, b);
@@ -467,10 +470,11 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float* ks, 
 // before the two passes.  8-bit pools: K's scales enter here, so that a scale
 // of a masked column does not matter, and the passes take ones.
 template <bool E4>
-__device__ __forceinline__ void mask_tile(uint32_t s_addr, const float* ks, const uint32_t (&words)[4]) {
+__device__ __forceinline__ void mask_tile(uint32_t s_addr, const float* ks, const uint32_t (&words)[4], int lo, int hi) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const uint32_t word = words[c];
+    if (c < lo || c >= hi) continue;
     if (!E4 && __all_sync(0xffffffffu, word == ~0u)) continue;
 #pragma unroll 1
     for (int z = 0; z < 2; ++z) {
@@ -492,49 +496,49 @@ __device__ __forceinline__ int div_rows(int n, const UDiv& d) {
   return d.m == 0u ? n : static_cast<int>(__umulhi(static_cast<unsigned int>(n), d.m) >> d.shift);
 }
 
-// What a segment needs besides its tiles, by 64 threads: the queries (in the
-// products' layout; all copies in flight at once, since a load's latency is
-// several microseconds behind a full queue of tiles), the parents, and
-// whether a page is missing.
-template <typename QT, int DP, bool E4>
-__device__ __forceinline__ void load_segment(const MmaParams& p, const Walk& w, Control* s, unsigned char* q_tiles, int buf,
-                                             int tid) {
+// What a segment needs besides its tiles, by 64 threads: the queries in the
+// products' layout, the parents, and whether a page is missing.  Plain loads
+// take microseconds each behind a full queue of tiles, so the queries come by
+// one TMA box for 64 columns where rows of whole nodes fill a row tile.
+template <typename QT, int DP, bool E4, int SPLIT>
+__device__ __forceinline__ void load_segment(const MmaParams& p, const CUtensorMap* qmap, const Walk& w, Control* s,
+                                             unsigned char* q_tiles, int buf, uint32_t phase, int tid) {
   const AttnParams& a = p.a;
   const int row0 = w.row0();
   const int rows = min(2 * w.pr + 1 < p.halves ? 2 * kTile : kTile, p.R - row0);
   constexpr int kUnits = DP / 8;        // runs of 8 elements a row
   constexpr int kStride = 64 / kUnits;  // rows a step
   const int D = a.c.dim, j = tid % kUnits, first = tid / kUnits;
-  const QT* const q = static_cast<const QT*>(a.q.p) + w.b * a.q.sb + static_cast<long long>(w.h * a.G) * a.q.sh + j * 8;
   const auto place = [&](int rr) {
     return reinterpret_cast<uint4*>(q_tiles + (rr >> 7) * kTile * DP * 2 + (j >> 3) * p.qrows * 128 + (rr & 127) * 128 +
                                     (((j & 7) ^ (rr & 7)) * 16));
   };
-  {
-    // (node, head of the group) and the source advance with the row
-    int nd = div_rows(row0 + first, p.div_G), g = row0 + first - nd * a.G;
-    const QT* src = q + nd * a.q.sn + g * a.q.sh;
-    const long long step = kStride * a.q.sh, wrap = a.q.sn - a.G * a.q.sh;
+  if (p.qbox) {
+    if (tid == 0) {
+      // boxes of qbox nodes: one for each row tile, or one for each copy
+      const bool one = E4 || p.negate || p.zero;  // the copies are written below
+      const int boxes = SPLIT > 1 ? (one ? 1 : SPLIT) : rows > kTile ? 2 : 1;
+      mbar_arrive_expect_tx(&s->q_tma, boxes * p.qbox * a.G * DP * 2);
+      for (int i = 0; i < boxes; ++i) {
+        const int node = SPLIT > 1 ? 0 : (row0 + i * kTile) / a.G;
+#pragma unroll
+        for (int c = 0; c < DP / 64; ++c)
+          tma_4d(smem_addr(q_tiles) + (SPLIT > 1 ? i * (kTile / SPLIT) * 128 : i * kTile * DP * 2) + c * p.qrows * 128,
+                 qmap, c * 64, w.h * a.G, node, w.b, &s->q_tma);
+      }
+    }
+  } else {
+    const QT* const q = static_cast<const QT*>(a.q.p) + w.b * a.q.sb + static_cast<long long>(w.h * a.G) * a.q.sh + j * 8;
 #pragma unroll 1
     for (int rr = first; rr < rows; rr += kStride) {
-      uint4* dst = place(rr);
-      if (j * 8 >= D) {
-        *dst = make_uint4(0u, 0u, 0u, 0u);
-      } else if (p.qvec) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-      } else {
-        const uint16_t* x = reinterpret_cast<const uint16_t*>(src);
-        uint32_t y[4];
+      const int nd = div_rows(row0 + rr, p.div_G);
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(q + nd * a.q.sn + (row0 + rr - nd * a.G) * a.q.sh);
+      uint32_t y[4] = {0u, 0u, 0u, 0u};
+      if (j * 8 < D) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = x[2 * i] | static_cast<uint32_t>(x[2 * i + 1]) << 16;
-        *dst = make_uint4(y[0], y[1], y[2], y[3]);
+        for (int i = 0; i < 4; ++i) y[i] = src[2 * i] | static_cast<uint32_t>(src[2 * i + 1]) << 16;
       }
-      g += kStride;
-      src += step;
-      while (g >= a.G) {
-        g -= a.G;
-        src += wrap;
-      }
+      for (int i = 0; i < SPLIT; ++i) *place(rr + i * (kTile / SPLIT)) = make_uint4(y[0], y[1], y[2], y[3]);
     }
   }
   if (a.parent && tid < a.N) s->parent[buf][tid] = __ldg(a.parent + static_cast<long long>(w.b) * a.N + tid);
@@ -551,12 +555,14 @@ __device__ __forceinline__ void load_segment(const MmaParams& p, const Walk& w, 
     s->bad[buf] = 1;
     raise_flag(a.ctrl, kFlagInvalidPage);
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (p.qbox) wait(s, &s->q_tma, phase, a.ctrl);
   if (E4 || p.negate || p.zero) {
-#pragma unroll 1
+    // (a row's copies are written from the first)
+#pragma unroll 2
     for (int r0 = first; r0 - first < rows; r0 += kStride) {  // all lanes take part
+      const bool in = r0 < rows;
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (r0 < rows) v = *place(r0);
+      if (in) v = *place(r0);
       if (p.zero) v = make_uint4(0u, 0u, 0u, 0u);
       if (p.negate) v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
       if (E4) {
@@ -571,16 +577,59 @@ __device__ __forceinline__ void load_segment(const MmaParams& p, const Walk& w, 
         const int ex = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
         const bool plain = top == 0.0f || !(top < INFINITY);
         const float up = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(14 - ex + 127) << 23);
-        if (r0 < rows && j == 0)
+        if (in && j == 0)
           s->qscale[buf][r0] = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(ex - 14 + 127) << 23);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] *= up;
         store8(reinterpret_cast<__half*>(&v), f);
       }
-      if (r0 < rows) *place(r0) = v;
+      if (in) {
+#pragma unroll
+        for (int i = 0; i < SPLIT; ++i) *place(r0 + i * (kTile / SPLIT)) = v;
+      }
     }
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// What the infinities and NaN of the drafted tokens in `seen` add to one
+// element of a row that sees them: weight times an infinity or a NaN is
+// itself, whatever the weight.  (8-bit pools: such a token makes the row NaN.)
+template <typename QT, bool E4>
+__device__ __noinline__ float odd_sum(const AttnParams& a, int b, long long len, long long total, unsigned long long seen, int h,
+                                      int col) {
+  float sum = E4 ? __int_as_float(0x7fc00000) : 0.0f;
+  if (E4 || col >= a.c.dim) return sum;
+#pragma unroll 1
+  for (; seen; seen &= seen - 1) {
+    const long long tok = len + __ffsll(static_cast<long long>(seen)) - 1;
+    int page, place;
+    if (tok >= total || !find_place(a.c, b, tok, page, place, nullptr)) continue;
+    const float y = elem_f32(static_cast<const QT*>(a.c.v)[page * a.c.page_stride + place * a.c.token_stride +
+                                                           h * a.c.head_stride + col]);
+    if (!isfinite(y)) sum += y;
+  }
+  return sum;
+}
+
+// A finished segment's rows, staged one after the other, to the output: a
+// node's heads lie next to each other there, so each node is one bulk copy.
+template <typename QT>
+__device__ __forceinline__ void store_segment(const MmaParams& p, const Walk& w, const unsigned char* staged, int tid) {
+  const AttnParams& a = p.a;
+  const int row0 = w.row0();
+  const int rows = min(2 * w.pr + 1 < p.halves ? 2 * kTile : kTile, p.R - row0);
+  const int n0 = div_rows(row0, p.div_G), n1 = div_rows(row0 + rows - 1, p.div_G);
+  for (int nd = n0 + tid; nd <= n1; nd += 64) {
+    const int r0 = max(nd * a.G, row0), r1 = min((nd + 1) * a.G, row0 + rows);
+    QT* dst = static_cast<QT*>(a.out) +
+              ((static_cast<long long>(w.b) * a.N + nd) * a.Hq + w.h * a.G + (r0 - nd * a.G)) * a.c.dim;
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                 "r"(smem_addr(staged) + (r0 - row0) * a.c.dim * 2), "r"((r1 - r0) * a.c.dim * 2)
+                 : "memory");
+  }
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // Ring entries of a segment of T tiles, in the order the MMA warp needs them:
@@ -589,12 +638,15 @@ __device__ __forceinline__ int v_entry(bool two, int t, int T) { return two ? 2 
 
 }  // namespace
 
-// DP: head_dim rounded up to 64 or 128.  QT: queries and output; E4: 8-bit pool.
-template <typename QT, int DP, bool E4>
+// DP: head_dim rounded up to 64 or 128.  QT: queries and output; E4: 8-bit
+// pool.  SPLIT: with few rows, copies of them that fill the 128 lanes; each
+// takes a share of a tile's columns, as a sequence of its own that is joined
+// at the segment's end.
+template <typename QT, int DP, bool E4, int SPLIT>
 __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
     attention_mma_kernel(const __grid_constant__ MmaParams p, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ksmap,
-                         const __grid_constant__ CUtensorMap vsmap) {
+                         const __grid_constant__ CUtensorMap vsmap, const __grid_constant__ CUtensorMap qmap) {
   using MT = typename std::conditional<E4, __half, QT>::type;  // operands of the products
   constexpr int kRow = E4 ? DP : DP * 2;             // bytes of a token's row in a TMA tile
   constexpr int kData = kTile * kRow;
@@ -617,7 +669,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 288) {
-    for (const CUtensorMap* m : {&kmap, &vmap, &ksmap, &vsmap})
+    for (const CUtensorMap* m : {&kmap, &vmap, &ksmap, &vsmap, &qmap})
       asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
   }
   if (tid == 0) {
@@ -640,6 +692,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
     }
     mbar_init(&s->o_done, 1);
     mbar_init(&s->drained, 1);
+    mbar_init(&s->q_tma, 1);
     s->abort = 0;
     s->stop = 0;
   }
@@ -814,21 +867,42 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
       }
       __syncwarp();
     } else if (warp >= kLoader) {
-      // ------------------------------------------------ the next segment's queries
+      // -------------------------- the next segment's queries, the last one's result
       const int lt = tid - kLoader * 32;
-      uint32_t seg = 0;
-      bool stop = false;
-      do {
-        const uint32_t buf = p.qbufs == 2 ? seg & 1u : 0u, use = p.qbufs == 2 ? seg >> 1 : seg;
-        wait(s, &s->q_empty[buf], (use & 1u) ^ 1u, a.ctrl);
-        stop = __any_sync(0xffffffffu, gave_up(s));
-        if (!stop) {
-          load_segment<QT, DP, E4>(p, w, s, qs + buf * qbytes, buf, lt);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s->q_full[buf]);
-        }
+      Walk done = w;  // the oldest segment whose buffer has not been emptied
+      uint32_t seg = 0, oldest = 0;
+      bool stop = false, more = true;
+      const auto buffer = [&](uint32_t x) { return p.qbufs == 2 ? x & 1u : 0u; };
+      const auto turn = [&](uint32_t x) { return (p.qbufs == 2 ? x >> 1 : x) & 1u; };
+      const auto empty = [&] {
+        const uint32_t buf = buffer(oldest);
+        wait(s, &s->q_empty[buf], turn(oldest), a.ctrl);
+        const bool lost = gave_up(s);
+        if (!lost && done.whole()) store_segment<QT>(p, done, qs + buf * qbytes, lt);
+        ++oldest;
+        done.next(a, p.pairs);
+        // Both warps' copies have been read before either loads over them, and
+        // both stop together.
+        uint32_t any;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+            "bar.red.or.pred p, 2, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(any)
+            : "r"(static_cast<uint32_t>(lost))
+            : "memory");
+        stop = any != 0;
+      };
+      while (!stop && more) {
+        if (seg >= static_cast<uint32_t>(p.qbufs)) empty();
+        if (stop) break;
+        const uint32_t buf = buffer(seg);
+        load_segment<QT, DP, E4, SPLIT>(p, &qmap, w, s, qs + buf * qbytes, buf, seg & 1u, lt);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s->q_full[buf]);
         ++seg;
-      } while (!stop && w.next(a, p.pairs));
+        more = w.next(a, p.pairs);
+      }
+      while (!stop && oldest < seg) empty();
     } else if (warp >= 10) {
       // ------------------------------------------------ 8-bit to 16-bit tiles
       if (E4) {
@@ -897,6 +971,8 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
               uint4 c[kIter];
 #pragma unroll
               for (int it = 0; it < kIter; ++it) c[it] = codes[it * kRows * DP / 16];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&s->empty[slot]);  // the tile is in registers
 #pragma unroll
               for (int it = 0; it < kIter; ++it) widen(c[it], it);
             } else {
@@ -921,12 +997,13 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
                 }
                 widen(c, it);
               }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&s->empty[slot]);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
               mbar_arrive(&s->cfull[cslot]);
-              mbar_arrive(&s->empty[slot]);
               if (!values) mbar_arrive(&s->scale_full[ti]);
             }
             if (++slot == static_cast<uint32_t>(p.stages)) slot = 0, phase ^= 1u;
@@ -953,9 +1030,11 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
         if (tid == 0 && w.t0 == 0 && w.nodes > 0 && w.len + w.nodes > w.total) raise_flag(a.ctrl, kFlagCapacity);
         const bool missing = *reinterpret_cast<volatile int*>(&s->bad[buf]) != 0;
 
-        const int row = two ? g * kTile + r : r;          // row within the item
+        constexpr int lanes = kTile / SPLIT;
+        const int copy = r / lanes;
+        const int row = two ? g * kTile + r : r - copy * lanes;  // row within the item
         const bool live = row < rows;
-        const bool warp_live = (two ? g * kTile : 0) + (warp & 3) * 32 < rows;
+        const bool warp_live = two ? g * kTile + (warp & 3) * 32 < rows : ((warp & 3) * 32) % lanes < rows;
         const int node = live ? div_rows(row0 + row, p.div_G) : 0;
         // the node's ancestors and itself; nothing at or below an invalid parent
         unsigned long long mask = live && node < w.nodes ? 1ull << node : 0ull;
@@ -1016,10 +1095,11 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
                 }
                 words[c] = y;
               }
-              mask_tile<E4>(s_addr, ks, words);
+              mask_tile<E4>(s_addr, ks, words, copy * 4 / SPLIT, (copy * 4 + 4) / SPLIT);
               ks = s->ones;
             }
-            float top = tile_max<E4>(s_addr, ks);
+            const int c0 = copy * (8 / SPLIT);
+            float top = tile_max<E4, 8 / SPLIT>(s_addr + c0 * 16, ks + c0 * 16);
             top = top == -INFINITY ? -INFINITY : top * c2;
             bool raise;
             float Mn = M;
@@ -1052,7 +1132,16 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
             }
             M = Mn;
             const float shift = M == -INFINITY ? 0.0f : M;
-            l += tile_weights<MT, E4>(s_addr, ks, s->vscale[ti], c2, shift);
+            const float* vs = s->vscale[ti];
+            l += tile_weights<MT, E4, 8 / SPLIT>(s_addr + c0 * 16, s_addr + c0 * 8, ks + c0 * 16, vs + c0 * 16, c2, shift);
+            if (SPLIT > 1) {
+              // the other copies' columns count as zero here
+              const uint32_t none[16] = {};
+              const int mine = copy * (4 / SPLIT) ;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (c < mine || c >= mine + 4 / SPLIT) tmem_st16(s_addr + c * 16, none);
+            }
             tmem_wait_st();
           }
           if (!E4 && tail && (!two || g == 0)) {
@@ -1103,108 +1192,107 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
         s->ml[g][r] = make_float2(M, l);
         softmax_sync();
         const unsigned int odd0 = s->odd[seg & 3][0], odd1 = s->odd[seg & 3][1];
-        if (warp_live) {
-          float f0 = 1.0f, f1 = 0.0f;
-          if (!two) {
-            const float2 x0 = s->ml[0][r], x1 = s->ml[1][r];
-            M = fmaxf(x0.x, x1.x);
-            // a NaN sum comes with a maximum of -inf when every score was NaN
-            f0 = x0.x == M ? 1.0f : ex2f(x0.x - M);
-            f1 = x1.x == M ? 1.0f : ex2f(x1.x - M);
-            if (T < 2) f1 = 0.0f;
-            l = x0.y * f0 + (T < 2 ? 0.0f : x1.y * f1);
+        float f0 = 1.0f, f1 = 0.0f;
+        if (!two) {
+          // all copies of the row in both groups; a group without a tile has
+          // sum 0, and a NaN sum comes with a maximum of -inf
+          float top = -INFINITY, sum = 0.0f;
+          float2 x[2 * SPLIT];
+#pragma unroll
+          for (int z = 0; z < 2 * SPLIT; ++z) {
+            x[z] = s->ml[z & 1][row + (z >> 1) * lanes];
+            top = fmaxf(top, x[z].x);
           }
-          const bool whole = w.whole();
-          const bool none = mask == 0ull || l == 0.0f;
-          const float inv = none ? 0.0f : whole ? 1.0f / l : 1.0f;
-          unsigned char* const staged = qs + buf * qbytes;
-          const int col0 = two ? 0 : g * (DP / 2), ncol = two ? DP : DP / 2;
-          const int D = a.c.dim, head = h * a.G + (row0 + row - node * a.G);
-          const long long out_row = (static_cast<long long>(w.b) * a.N + node) * a.Hq + head;
-          const int slot = 2 * cta + (w.first ? 0 : 1);
-          float* part = static_cast<float*>(a.scratch) +
-                        (static_cast<size_t>(slot) * p.qtiles + (row >> 7)) * slot_floats(DP);
+#pragma unroll
+          for (int z = 0; z < 2 * SPLIT; ++z)
+            if (x[z].y != 0.0f) sum += x[z].y * (x[z].x == top ? 1.0f : ex2f(x[z].x - top));
+          const float2 x0 = s->ml[0][r], x1 = s->ml[1][r];
+          f0 = x0.y == 0.0f ? 0.0f : x0.x == top ? 1.0f : ex2f(x0.x - top);
+          f1 = x1.y == 0.0f ? 0.0f : x1.x == top ? 1.0f : ex2f(x1.x - top);
+          M = top;
+          l = sum;
+        }
+        const bool whole = w.whole();
+        const bool none = mask == 0ull || l == 0.0f;
+        const float inv = none ? 0.0f : whole ? 1.0f / l : 1.0f;
+        const unsigned long long seen = mask & (static_cast<unsigned long long>(odd1) << 32 | odd0);
+        const int col0 = two ? 0 : g * (DP / 2), ncol = two ? DP : DP / 2;
+        const int D = a.c.dim, head = h * a.G + (row0 + row - node * a.G);
+        const int slot = 2 * cta + (w.first ? 0 : 1);
+        float* part = static_cast<float*>(a.scratch) + (static_cast<size_t>(slot) * p.qtiles + (row >> 7)) * slot_floats(DP);
+        // The queries are done with: their buffer takes the result's rows, one
+        // after the other, and behind them what the copies hand over.
+        unsigned char* const staged = qs + buf * qbytes;
+        float4* const handed =
+            reinterpret_cast<float4*>(staged + lanes * DP * 2) + g * (SPLIT - 1) * 4 * lanes;
 #pragma unroll 1
-          for (int c = 0; c < ncol; c += 16) {
+        for (int c = 0; c < ncol; c += 16) {
+          float o[16];
+          if (warp_live) {
             uint32_t v[16], v1[16];
             const uint32_t at = tmem + lane_base + 2 * kTile + col0 + c;
             __syncwarp();
             tmem_ld16(at + (two ? g * DP : 0), v);
             if (!two) tmem_ld16(at + DP, v1);
             tmem_wait_ld();
-            if (live) {
-              float o[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float y = f0 == 0.0f ? 0.0f : __uint_as_float(v[i]) * f0;
-                if (!two && f1 != 0.0f) y = fmaf(__uint_as_float(v1[i]), f1, y);
-                o[i] = none ? 0.0f : y * inv;
-              }
-              const unsigned long long seen = mask & (static_cast<unsigned long long>(odd1) << 32 | odd0);
-              if (E4 && seen && !none) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __int_as_float(0x7fc00000);
-              }
-              if (!E4 && seen && !none) {
-                // weight times an infinity or a NaN: itself, whatever the weight
-#pragma unroll 1
-                for (unsigned long long m = seen; m; m &= m - 1) {
-                  const long long tok = w.len + __ffsll(static_cast<long long>(m)) - 1;
-                  int page, place;
-                  if (tok >= w.total || !find_place(a.c, w.b, tok, page, place, nullptr)) continue;
-                  const QT* x = static_cast<const QT*>(a.c.v) + page * a.c.page_stride + place * a.c.token_stride +
-                                h * a.c.head_stride + col0 + c;
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) {
-                    const float y = col0 + c + i < D ? elem_f32(x[i]) : 0.0f;
-                    if (!isfinite(y)) o[i] += y;
-                  }
-                }
-              }
-              if (whole) {
-                // into the row's place among the queries, which are done with
-                uint4* dst = reinterpret_cast<uint4*>(staged + (row >> 7) * kTile * DP * 2) + (row & 127) * (DP / 8);
-                const float y0[8] = {o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]};
-                const float y1[8] = {o[8], o[9], o[10], o[11], o[12], o[13], o[14], o[15]};
-                const int unit = (col0 + c) / 8;
-                store8(reinterpret_cast<QT*>(dst + (unit ^ (row & 7))), y0);
-                store8(reinterpret_cast<QT*>(dst + ((unit + 1) ^ (row & 7))), y1);
-              } else {
-                float4* dst = reinterpret_cast<float4*>(part) + static_cast<size_t>((col0 + c) / 4) * kTile + (row & 127);
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) dst[i / 4 * kTile] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-              }
+            for (int i = 0; i < 16; ++i) {
+              float y = f0 == 0.0f ? 0.0f : __uint_as_float(v[i]) * f0;
+              if (!two && f1 != 0.0f) y = fmaf(__uint_as_float(v1[i]), f1, y);
+              o[i] = none ? 0.0f : y * inv;
             }
           }
-          if (live && (two || g == 0)) {
+          if (SPLIT > 1) {
+            if (live && copy > 0) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                handed[((copy - 1) * 4 + i / 4) * lanes + row] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            }
+            softmax_sync();
+            if (live && copy == 0) {
+              for (int z = 1; z < SPLIT; ++z)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                  const float4 y = handed[((z - 1) * 4 + i / 4) * lanes + row];
+                  o[i] += y.x, o[i + 1] += y.y, o[i + 2] += y.z, o[i + 3] += y.w;
+                }
+            }
+            softmax_sync();
+          }
+          if (live && copy == 0) {
+            if (seen && !none) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] += odd_sum<QT, E4>(a, w.b, w.len, w.total, seen, h, col0 + c + i);
+            }
             if (whole) {
-              if (a.lse) a.lse[out_row] = none ? -INFINITY : (M + log2f(l)) * kLn2;
+              QT* dst = reinterpret_cast<QT*>(staged) + row * D + col0 + c;
+#pragma unroll
+              for (int i = 0; i < 16; i += 8) {
+                if (col0 + c + i < D) {
+                  const float y[8] = {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]};
+                  store8(dst + i, y);
+                }
+              }
             } else {
-              float2* ml = reinterpret_cast<float2*>(part + static_cast<size_t>(kTile) * DP);
-              ml[row & 127] = make_float2(none ? -INFINITY : M, none ? 0.0f : l);
+              float4* dst = reinterpret_cast<float4*>(part) + static_cast<size_t>((col0 + c) / 4) * kTile + (row & 127);
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) dst[i / 4 * kTile] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             }
           }
         }
+        if (live && copy == 0 && (two || g == 0)) {
+          if (whole) {
+            if (a.lse)
+              a.lse[(static_cast<long long>(w.b) * a.N + node) * a.Hq + head] = none ? -INFINITY : (M + log2f(l)) * kLn2;
+          } else {
+            float2* ml = reinterpret_cast<float2*>(part + static_cast<size_t>(kTile) * DP);
+            ml[row & 127] = make_float2(none ? -INFINITY : M, none ? 0.0f : l);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the staged rows
         tmem_fence_before();
         if (tid == 0) s->stop = gave_up(s);
         softmax_sync();  // O, ml and odd may be overwritten now
-        if (w.whole()) {
-          // 16-byte runs of neighbouring lanes lie next to each other in the output
-          const int D = a.c.dim, units = D / 8;
-          const unsigned char* staged = qs + buf * qbytes;
-#pragma unroll 1
-          for (int i = tid; i < rows * (DP / 8); i += 256) {
-            const int rr = i / (DP / 8), unit = i % (DP / 8);
-            if (unit >= units) continue;
-            const uint4 v = reinterpret_cast<const uint4*>(staged + (rr >> 7) * kTile * DP * 2)[(rr & 127) * (DP / 8) +
-                                                                                               (unit ^ (rr & 7))];
-            const int nd = div_rows(row0 + rr, p.div_G), hd = h * a.G + (row0 + rr - nd * a.G);
-            *reinterpret_cast<uint4*>(static_cast<QT*>(a.out) +
-                                      ((static_cast<long long>(w.b) * a.N + nd) * a.Hq + hd) * D + unit * 8) = v;
-          }
-          // the next queries come by another proxy's writes
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
         if (tid < 2) s->odd[seg & 3][tid] = 0u;
         if (tid == 2) s->bad[buf] = 0;
         __syncwarp();
@@ -1382,20 +1470,39 @@ bool scale_map(CUtensorMap* m, const CacheView& c, void* base, int box) {
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename QT, int DP, bool E4>
-cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[4], int grid, cudaStream_t st) {
+// The queries: (element, head, node, sequence), boxes of one group of heads.
+bool query_map(CUtensorMap* m, const AttnParams& a, int q_dtype, int nodes) {
+  const cuuint64_t dim[4] = {static_cast<cuuint64_t>(a.c.dim), static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.N),
+                             static_cast<cuuint64_t>(a.B)};
+  long long st[3] = {a.q.sh, a.q.sn, a.q.sb};
+  for (int i = 0; i < 3; ++i) {
+    if (dim[i + 1] == 1) st[i] = i == 0 ? (a.c.dim + 7) / 8 * 8 : st[i - 1];  // any valid one will do
+    if (st[i] <= 0 || st[i] % 8 || st[i] >= (1ll << 38)) return false;
+  }
+  if (reinterpret_cast<uintptr_t>(a.q.p) % 16 || a.G > 256) return false;
+  const cuuint64_t bytes[3] = {static_cast<cuuint64_t>(st[0]) * 2, static_cast<cuuint64_t>(st[1]) * 2,
+                               static_cast<cuuint64_t>(st[2]) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(nodes), 1}, one[4] = {1, 1, 1, 1};
+  return encoder()(m, q_dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                   const_cast<void*>(a.q.p), dim, bytes, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename QT, int DP, bool E4, int SPLIT>
+cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[5], int grid, cudaStream_t st) {
   constexpr int kLimit = 227 * 1024;
   const int boxes = kTile / p.box;
   p.scale_bytes = E4 ? boxes * (p.box * 4 > 128 ? p.box * 4 : 128) : 0;
   const int entry = kTile * DP * (E4 ? 1 : 2) + 2 * p.scale_bytes;
-  p.qrows = p.qtiles == 2 ? kTile : (p.R + 7) / 8 * 8;
+  p.qrows = p.qtiles == 2 || p.split > 1 ? kTile : (p.R + 7) / 8 * 8;
   p.qbufs = p.qtiles == 2 ? 1 : 2;
   const int fixed = p.qbufs * p.qtiles * p.qrows * DP * 2 + (E4 ? kConvStages * kTile * DP * 2 : 0) +
                     static_cast<int>(sizeof(Control));
   p.stages = (kLimit - fixed) / entry;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   const size_t smem = fixed + static_cast<size_t>(p.stages) * entry;
-  const auto kernel = attention_mma_kernel<QT, DP, E4>;
+  const auto kernel = attention_mma_kernel<QT, DP, E4, SPLIT>;
   static bool done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1406,10 +1513,18 @@ cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[4], int grid, cud
     if (dev >= 0 && dev < 64) done[dev] = true;
   }
   e = counted(launch_k(SV_PDL >= 2, kernel, dim3(grid), dim3(E4 ? 512 : 384), smem, st, p, maps[0], maps[1], maps[2],
-                       maps[3]),
+                       maps[3], maps[4]),
               1);
   if (e != cudaSuccess || grid < 2) return e;
   return counted(launch_k(SV_PDL >= 1, attention_join_kernel<QT, DP>, dim3(grid - 1), dim3(kJoinThreads), 0, st, p, grid), 1);
+}
+
+template <typename QT, bool E4>
+cudaError_t launch_split(MmaParams& p, const CUtensorMap (&maps)[5], int grid, cudaStream_t st) {
+  const bool wide = p.a.c.dim > 64;
+  if (p.split == 4) return wide ? launch_mma<QT, 128, E4, 4>(p, maps, grid, st) : launch_mma<QT, 64, E4, 4>(p, maps, grid, st);
+  if (p.split == 2) return wide ? launch_mma<QT, 128, E4, 2>(p, maps, grid, st) : launch_mma<QT, 64, E4, 2>(p, maps, grid, st);
+  return wide ? launch_mma<QT, 128, E4, 1>(p, maps, grid, st) : launch_mma<QT, 64, E4, 1>(p, maps, grid, st);
 }
 
 }  // namespace
@@ -1443,24 +1558,24 @@ cudaError_t launch_attention_mma(const AttnParams& a, int q_dtype, int cache_dty
   p.negate = a.c2 < 0.0f;
   p.zero = a.c2 == 0.0f;
   p.a.c2 = p.zero ? 1.0f : a.c2 < 0.0f ? -a.c2 : a.c2;
-  p.qvec = reinterpret_cast<uintptr_t>(a.q.p) % 16 == 0 && a.q.sb % 8 == 0 && a.q.sn % 8 == 0 && a.q.sh % 8 == 0;
-  CUtensorMap maps[4] = {};
+  p.split = p.R <= 32 ? 4 : p.R <= 64 ? 2 : 1;
+  CUtensorMap maps[5] = {};
   bool ok = pool_map(&maps[0], a.c, a.c.k, cache_dtype, p.box, p.head_first) &&
             pool_map(&maps[1], a.c, a.c.v, cache_dtype, p.box, p.head_first);
   if (cache_dtype == 3) ok = ok && scale_map(&maps[2], a.c, a.c.ks, p.box) && scale_map(&maps[3], a.c, a.c.vs, p.box);
   if (!ok) return cudaErrorInvalidValue;
+  // rows of whole nodes that fill a row tile, or all rows at once
+  const int box = p.R <= kTile ? a.N : kTile % a.G == 0 ? kTile / a.G : 0;
+  p.qbox = box > 0 && query_map(&maps[4], a, q_dtype, box) ? box : 0;
   // no more blocks than tiles there can be
   const long long per_seq = (static_cast<long long>(a.c.max_pages) * a.c.page_size + kTile - 1) / kTile;
   const long long most = static_cast<long long>(a.B) * a.c.heads * p.pairs * per_seq;
   int grid = sms < kMaxCtas ? sms : kMaxCtas;
   if (most < grid) grid = static_cast<int>(most);
-  const bool wide = a.c.dim > 64, e4 = cache_dtype == 3;
-  if (q_dtype == 1) {
-    if (e4) return wide ? launch_mma<__nv_bfloat16, 128, true>(p, maps, grid, st) : launch_mma<__nv_bfloat16, 64, true>(p, maps, grid, st);
-    return wide ? launch_mma<__nv_bfloat16, 128, false>(p, maps, grid, st) : launch_mma<__nv_bfloat16, 64, false>(p, maps, grid, st);
-  }
-  if (e4) return wide ? launch_mma<__half, 128, true>(p, maps, grid, st) : launch_mma<__half, 64, true>(p, maps, grid, st);
-  return wide ? launch_mma<__half, 128, false>(p, maps, grid, st) : launch_mma<__half, 64, false>(p, maps, grid, st);
+  const bool e4 = cache_dtype == 3;
+  if (q_dtype == 1)
+    return e4 ? launch_split<__nv_bfloat16, true>(p, maps, grid, st) : launch_split<__nv_bfloat16, false>(p, maps, grid, st);
+  return e4 ? launch_split<__half, true>(p, maps, grid, st) : launch_split<__half, false>(p, maps, grid, st);
 }
 
 }  // namespace sv
