@@ -1317,7 +1317,6 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
 // reads about as much as one share wrote.
 template <typename QT, int DP>
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __grid_constant__ MmaParams p, int grid) {
-  griddep_wait();
   __shared__ long long sums[256];
   __shared__ Found found;
   const AttnParams& a = p.a;
@@ -1325,6 +1324,9 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
   find_share(a, p.pairs, grid, j, sums, &found);
   const Split split = found.split;
   const int b = found.b, h = found.h;
+  // The split depends on nothing that the first grid writes: only here is its
+  // end waited for (which all blocks do, so that a later grid may rely on it).
+  griddep_wait();
   if (b < 0 || found.t0 == 0) return;  // no such share, or one that starts with an item
   const long long lo = split.start(j) - found.t0, hi = lo + tiles_of(a, b);
   int first = j, last = j;  // boundaries inside the item
