@@ -310,7 +310,7 @@ struct Control {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t cfull[kConvStages], cempty[kConvStages];
   uint64_t scale_full[kScaleRing];
-  uint64_t s_full[2], p_ready[2], o_done, q_full[2], q_empty[2], q_tma, drained;
+  uint64_t s_full[2], p_ready[2][2], o_done, q_full[2], q_empty[2], q_tma, drained;
   uint32_t tmem;
   int abort;
   int stop;              // abort, as the softmax warpgroups agreed on it
@@ -323,7 +323,7 @@ struct Control {
   alignas(16) float ones[kTile];
   alignas(16) float kscale[kScaleRing][kTile];
   alignas(16) float vscale[kScaleRing][kTile];
-  float vmax[kScaleRing][4];
+  float vmax[kScaleRing][2];
   long long sums[256];
   Found found;
 };
@@ -396,9 +396,10 @@ __device__ __forceinline__ float tile_max(uint32_t s_addr, const float* ks) {
 
 // Weights 2^(s c2 - shift) of a row's tile into tensor memory over the
 // scores (times V's scales); returns their sum (without the scales).
+// `half` (nullable) is told when the first half of the columns is there.
 template <typename M, bool E4, int NC>
 __device__ __forceinline__ float tile_weights(uint32_t s_addr, uint32_t p_addr, const float* ks, const float* vs, float c2,
-                                              float shift) {
+                                              float shift, uint64_t* half) {
   const unsigned long long c22 = splat2(c2), sh2 = splat2(-shift);
   unsigned long long sum[2] = {0ull, 0ull};
   uint32_t v[2][16];
@@ -445,10 +446,21 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, uint32_t p_addr, 
       float f[4];
       unpack2(x, f[0], f[1]);
       unpack2(y, f[2], f[3]);
-#pragma unroll
-      for (int z = 0; z < 4; ++z) f[z] = ex2f(f[z]);
+      f[0] = ex2f(f[0]);
+      f[1] = ex2f(f[1]);
       x = pack2(f[0], f[1]);
-      y = pack2(f[2], f[3]);
+      if (!E4 && (i & 4)) {
+        // a quarter of them on the FMA pipe, whose polynomial knows no NaN
+        float p2, p3;
+        unpack2(ex2_poly_x2(f[2], f[3]), p2, p3);
+        f[2] = f[2] == f[2] ? p2 : f[2];
+        f[3] = f[3] == f[3] ? p3 : f[3];
+        y = pack2(f[2], f[3]);
+      } else {
+        f[2] = ex2f(f[2]);
+        f[3] = ex2f(f[3]);
+        y = pack2(f[2], f[3]);
+      }
       sum[0] = add2(sum[0], x);
       sum[1] = add2(sum[1], y);
       if (E4) {
@@ -459,6 +471,12 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, uint32_t p_addr, 
       out[(i >> 1) + 1] = pack_weights<M>(f[2], f[3]);
     }
     tmem_st8(p_addr + c * 8, out);
+    if (NC == 8 && c == 3) {
+      tmem_wait_st();
+      tmem_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(half);
+    }
   }
   float a, b, d, e;
   unpack2(sum[0], a, b);
@@ -675,16 +693,16 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&s->full[i], 1);
-      mbar_init(&s->empty[i], E4 ? 4 : 1);
+      mbar_init(&s->empty[i], E4 ? 2 : 1);
     }
     for (int i = 0; i < kConvStages; ++i) {
-      mbar_init(&s->cfull[i], 4);
+      mbar_init(&s->cfull[i], 2);
       mbar_init(&s->cempty[i], 1);
     }
-    for (int i = 0; i < kScaleRing; ++i) mbar_init(&s->scale_full[i], 4);
+    for (int i = 0; i < kScaleRing; ++i) mbar_init(&s->scale_full[i], 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s->s_full[i], 1);
-      mbar_init(&s->p_ready[i], 4);
+      for (int z = 0; z < 2; ++z) mbar_init(&s->p_ready[i][z], 4);
       s->bad[i] = 0;
       for (int z = 0; z < 4; ++z) s->odd[z][i] = 0u;
       mbar_init(&s->q_full[i], 2);
@@ -839,25 +857,32 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
           if (x > 0) {
             const uint32_t f = g ^ 1u;  // unit x - 1
             if (!two || f == 0) take(vslot);
-            wait(s, &s->p_ready[f], np >> f & 1u, a.ctrl);
-            np ^= 1u << f;
-            tmem_fence_after();
             const uint64_t vd = v0 + vslot * (step_bytes >> 4);
             const uint32_t o = acc + 2 * kTile + f * DP, pw = acc + f * kTile;
             const bool add = x > 2;
+            wait(s, &s->p_ready[f][0], np >> f & 1u, a.ctrl);
+            tmem_fence_after();
             if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < kTile / 16; ++k)
+              for (int k = 0; k < kTile / 32; ++k)
                 mma_ts(o, pw + k * 8, vd + k * (16 * 128 >> 4), kShapeO, add || k > 0);
+            }
+            __syncwarp();
+            wait(s, &s->p_ready[f][1], np >> f & 1u, a.ctrl);
+            np ^= 1u << f;
+            tmem_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = kTile / 32; k < kTile / 16; ++k)
+                mma_ts(o, pw + k * 8, vd + k * (16 * 128 >> 4), kShapeO, true);
               if (!two || f == 1) mma_commit(&emptyb[vslot]);
               if (x == U) mma_commit(&s->o_done);
             }
             __syncwarp();
           }
-          stop = __any_sync(0xffffffffu, gave_up(s));
-          if (stop) break;
         }
         ++seg;
+        stop = __any_sync(0xffffffffu, gave_up(s));  // (after a wait ran out, none waits any more)
       } while (!stop && w.next(a, p.pairs));
       if (stop) {  // MMAs in flight finish before their memory goes away
         if (elect_one()) mma_commit(&s->drained);
@@ -906,111 +931,118 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
     } else if (warp >= 10) {
       // ------------------------------------------------ 8-bit to 16-bit tiles
       if (E4) {
-        const int cw = warp - 10;
-        uint32_t slot = 0, phase = 0, cslot = 0, cphase = 0, tile = 0, seg = 0;
+        // Two teams of two warps take alternate ring entries, so that one's
+        // waits and latencies overlap the other's conversions.
+        const int team = (warp - 10) >> 1, cw = (warp - 10) & 1;
+        uint32_t slot = 0, phase = 0, cslot = 0, cphase = 0, tile = 0, seg = 0, e = 0;
         bool stop = false;  // the same in all lanes
-        constexpr int kLanes = DP / 16;     // lanes a row, 16 codes each
-        constexpr int kRows = 32 / kLanes;  // rows an iteration
-        constexpr int kIter = 32 / kRows;
-        const int j = lane % kLanes, row0 = cw * 32 + lane / kLanes;
-        // Lanes of the second 64 columns store their halves the other way
-        // round: the two blocks share banks.  (row & 7) is the swizzle.
-        const int first = 2 * (j % 4) + (j >= 4 ? 1 : 0);
-        const int scale_at = (cw * 32 + lane) / p.box * max(p.box * 4, 128) + (cw * 32 + lane) % p.box * 4;
-        unsigned char* const line0 = conv + (j / 4) * kTile * 128 + row0 * 128;
+        constexpr int kLanes = DP / 8;        // lanes a row, 8 codes each
+        constexpr int kRows = 32 / kLanes;    // rows a step
+        constexpr int kSteps = 64 / kRows;    // steps of this warp's 64 rows
+        constexpr int kPeriod = 8 / kRows;    // steps after which the swizzle (row & 7) repeats
+        constexpr int kBatch = 16;            // steps whose codes are held at once
+        const int row0 = cw * 64 + lane / kLanes;
+        uint32_t line[kPeriod];               // where this lane's 16 bytes of a row go
+#pragma unroll
+        for (int k = 0; k < kPeriod; ++k) {
+          const int row = row0 + k * kRows, unit = lane % kLanes;
+          line[k] = (unit >> 3) * kTile * 128 + row * 128 + (((unit & 7) ^ (row & 7)) * 16);
+        }
+        const int box_bytes = max(p.box * 4, 128);
         do {
           const bool two = 2 * w.pr + 1 < p.halves;
           const int T = w.t1 - w.t0;
-          for (int i = 0; i < 2 * T && !stop; ++i) {
-            bool values;
-            int t;
-            if (two) {
-              values = i & 1;
-              t = i >> 1;
-            } else {
-              values = i == 2 * T - 1 || (i > 0 && (i & 1) == 0);
-              t = !values ? (i + 1) / 2 : i == 2 * T - 1 ? T - 1 : i / 2 - 1;
-            }
-            wait(s, &s->full[slot], phase, a.ctrl);
-            wait(s, &s->cempty[cslot], cphase ^ 1u, a.ctrl);
-            stop = __any_sync(0xffffffffu, gave_up(s));
-            if (stop) break;
-            const unsigned char* src = ring + slot * entry;
-            const long long tok0 = static_cast<long long>(w.t0 + t) * kTile;
-            const uint32_t ti = (tile + t) % kScaleRing;
-            if (!values) {
-              // scales of this warp's 32 tokens; places past the end count as 0
-              const int x = cw * 32 + lane;
-              const bool in = tok0 + x < w.total;
-              const float ks = in ? *reinterpret_cast<const float*>(src + kData + scale_at) : 0.0f;
-              float vs = in ? *reinterpret_cast<const float*>(src + kData + p.scale_bytes + scale_at) : 0.0f;
-              if (in && tok0 + x >= w.len && !(fabsf(vs) < INFINITY)) {
-                atomicOr(&s->odd[seg & 3][(tok0 + x - w.len) >> 5], 1u << ((tok0 + x - w.len) & 31));
-                vs = 0.0f;
-              }
-              s->kscale[ti][x] = ks;
-              s->vscale[ti][x] = vs;
-              const float top = warp_max(fabsf(vs) < INFINITY ? fabsf(vs) : 0.0f);
-              if (lane == 0) s->vmax[ti][cw] = top;
-            }
-            const auto widen = [&](const uint4& c, int it) {
-              const int sw = (row0 + it * kRows) & 7;
-              const uint32_t words[4] = {c.x, c.y, c.z, c.w};
-              uint32_t out[8];
-#pragma unroll
-              for (int q = 0; q < 8; ++q) out[q] = half_pair(static_cast<uint16_t>(words[q >> 1] >> (16 * (q & 1))));
-              unsigned char* line = line0 + cslot * kConv + it * kRows * 128;
-              const bool swap = j >= 4;
-              const uint4 lo = make_uint4(out[0], out[1], out[2], out[3]);
-              const uint4 hi = make_uint4(out[4], out[5], out[6], out[7]);
-              *reinterpret_cast<uint4*>(line + ((first ^ sw) * 16)) = swap ? hi : lo;
-              *reinterpret_cast<uint4*>(line + (((first ^ 1) ^ sw) * 16)) = swap ? lo : hi;
-            };
-            const uint4* codes = reinterpret_cast<const uint4*>(src + row0 * DP + j * 16);
-            if (tok0 + kTile <= w.len) {
-              uint4 c[kIter];
-#pragma unroll
-              for (int it = 0; it < kIter; ++it) c[it] = codes[it * kRows * DP / 16];
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&s->empty[slot]);  // the tile is in registers
-#pragma unroll
-              for (int it = 0; it < kIter; ++it) widen(c[it], it);
-            } else {
 #pragma unroll 1
-              for (int it = 0; it < kIter; ++it) {
-                uint4 c = codes[it * kRows * DP / 16];
-                const long long tok = tok0 + row0 + it * kRows;
-                if (tok >= w.total) c = make_uint4(0u, 0u, 0u, 0u);
-                if (values && tok >= w.len && tok < w.total) {
-                  // a drafted token's NaN must reach its own descendants only:
-                  // it counts as zero here, and its row is listed
-                  const uint32_t words[4] = {c.x, c.y, c.z, c.w};
-                  bool odd = false;
+          for (int i = 0; i < 2 * T; ++i, ++e) {
+            if ((e & 1u) == static_cast<uint32_t>(team)) {
+              const bool values = two ? i & 1 : i == 2 * T - 1 || (i > 0 && (i & 1) == 0);
+              const int t = two ? i >> 1 : !values ? (i + 1) >> 1 : i == 2 * T - 1 ? T - 1 : (i >> 1) - 1;
+              const unsigned char* src = ring + slot * entry;
+              const long long tok0 = static_cast<long long>(w.t0 + t) * kTile;
+              const uint32_t ti = (tile + t) % kScaleRing;
+              unsigned char* const dst = conv + cslot * kConv;
+              const auto widen = [&](const uint2& c, int it) {
+                *reinterpret_cast<uint4*>(dst + line[it % kPeriod] + it / kPeriod * 1024) =
+                    make_uint4(half_pair(static_cast<uint16_t>(c.x)), half_pair(static_cast<uint16_t>(c.x >> 16)),
+                               half_pair(static_cast<uint16_t>(c.y)), half_pair(static_cast<uint16_t>(c.y >> 16)));
+              };
+              const uint2* codes = reinterpret_cast<const uint2*>(src + row0 * DP + lane % kLanes * 8);
+              wait(s, &s->full[slot], phase, a.ctrl);
+              if (!values) {
+                // scales of this warp's 64 tokens; places past the end count as 0
+                float top = 0.0f;
 #pragma unroll
-                  for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) odd |= (words[q] >> (8 * z) & 0x7fu) == 0x7fu;
-                  if (odd) {
-                    c = make_uint4(0u, 0u, 0u, 0u);
-                    atomicOr(&s->odd[seg & 3][(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
+                for (int z = 0; z < 2; ++z) {
+                  const int x = cw * 64 + z * 32 + lane;
+                  const unsigned char* at = src + kData + x / p.box * box_bytes + x % p.box * 4;
+                  const bool in = tok0 + x < w.total;
+                  const float ks = in ? *reinterpret_cast<const float*>(at) : 0.0f;
+                  float vs = in ? *reinterpret_cast<const float*>(at + p.scale_bytes) : 0.0f;
+                  if (in && tok0 + x >= w.len && !(fabsf(vs) < INFINITY)) {
+                    atomicOr(&s->odd[seg & 3][(tok0 + x - w.len) >> 5], 1u << ((tok0 + x - w.len) & 31));
+                    vs = 0.0f;
                   }
+                  s->kscale[ti][x] = ks;
+                  s->vscale[ti][x] = vs;
+                  top = fmaxf(top, fabsf(vs) < INFINITY ? fabsf(vs) : 0.0f);
                 }
-                widen(c, it);
+                top = warp_max(top);
+                if (lane == 0) s->vmax[ti][cw] = top;
               }
+              if (tok0 + kTile <= w.len) {
+#pragma unroll
+                for (int h = 0; h < kSteps; h += kBatch) {
+                  uint2 c[kBatch];
+#pragma unroll
+                  for (int it = 0; it < kBatch; ++it) c[it] = codes[(h + it) * kRows * DP / 8];
+                  if (h == 0) wait(s, &s->cempty[cslot], cphase ^ 1u, a.ctrl);
+                  if (h + kBatch >= kSteps) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s->empty[slot]);  // the rest of the tile is in registers
+                  }
+#pragma unroll
+                  for (int it = 0; it < kBatch; ++it) widen(c[it], h + it);
+                }
+              } else {
+                wait(s, &s->cempty[cslot], cphase ^ 1u, a.ctrl);
+#pragma unroll 1
+                for (int i1 = 0; i1 < kSteps; i1 += kPeriod)
+#pragma unroll
+                  for (int k = 0; k < kPeriod; ++k) {
+                    const int it = i1 + k;
+                    uint2 c = codes[it * kRows * DP / 8];
+                    const long long tok = tok0 + row0 + it * kRows;
+                    if (tok >= w.total) c = make_uint2(0u, 0u);
+                    if (values && tok >= w.len && tok < w.total) {
+                      // a drafted token's NaN must reach its own descendants only:
+                      // it counts as zero here, and its row is listed
+                      const uint32_t any = (((c.x & 0x7f7f7f7fu) + 0x01010101u) | ((c.y & 0x7f7f7f7fu) + 0x01010101u)) &
+                                           0x80808080u;
+                      if (any) {
+                        c = make_uint2(0u, 0u);
+                        atomicOr(&s->odd[seg & 3][(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
+                      }
+                    }
+                    *reinterpret_cast<uint4*>(dst + line[k] + i1 / kPeriod * 1024) =
+                        make_uint4(half_pair(static_cast<uint16_t>(c.x)), half_pair(static_cast<uint16_t>(c.x >> 16)),
+                                   half_pair(static_cast<uint16_t>(c.y)), half_pair(static_cast<uint16_t>(c.y >> 16)));
+                  }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s->empty[slot]);
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
               __syncwarp();
-              if (lane == 0) mbar_arrive(&s->empty[slot]);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&s->cfull[cslot]);
-              if (!values) mbar_arrive(&s->scale_full[ti]);
+              if (lane == 0) {
+                mbar_arrive(&s->cfull[cslot]);
+                if (!values) mbar_arrive(&s->scale_full[ti]);
+              }
             }
             if (++slot == static_cast<uint32_t>(p.stages)) slot = 0, phase ^= 1u;
             if (++cslot == kConvStages) cslot = 0, cphase ^= 1u;
           }
           tile += T;
           ++seg;
+          stop = __any_sync(0xffffffffu, gave_up(s));
         } while (!stop && w.next(a, p.pairs));
       }
     } else {
@@ -1071,79 +1103,6 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
           }
           __syncwarp();
           tmem_fence_after();
-          if (warp_live) {
-            const float* ks = s->kscale[ti];
-            if (masked) {
-              uint32_t words[4];
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const long long off = tok0 + 32 * c - w.len, lim = w.total - (tok0 + 32 * c);
-                uint32_t y = ~0u;
-                if (off >= 64) y = 0u;
-                else if (off >= 0) y = static_cast<uint32_t>(mask >> off);
-                else if (off > -32) y = static_cast<uint32_t>(mask << -off) | ((1u << -off) - 1u);
-                if (lim <= 0) y = 0u;
-                else if (lim < 32) y &= (1u << lim) - 1u;
-                if (missing) {
-                  bool in = false;
-                  if (lane < lim) {
-                    const int pi = page_of(a.c, static_cast<int>(tok0 + 32 * c + lane));
-                    in = static_cast<unsigned int>(__ldg(a.c.table + static_cast<long long>(w.b) * a.c.table_stride + pi)) <
-                         static_cast<unsigned int>(a.c.num_pages);
-                  }
-                  y &= __ballot_sync(0xffffffffu, in);
-                }
-                words[c] = y;
-              }
-              mask_tile<E4>(s_addr, ks, words, copy * 4 / SPLIT, (copy * 4 + 4) / SPLIT);
-              ks = s->ones;
-            }
-            const int c0 = copy * (8 / SPLIT);
-            float top = tile_max<E4, 8 / SPLIT>(s_addr + c0 * 16, ks + c0 * 16);
-            top = top == -INFINITY ? -INFINITY : top * c2;
-            bool raise;
-            float Mn = M;
-            if (E4) {
-              const float vm = fmaxf(fmaxf(s->vmax[ti][0], s->vmax[ti][1]), fmaxf(s->vmax[ti][2], s->vmax[ti][3]));
-              const int ve = max(vexp, min(max(static_cast<int>(__float_as_uint(vm) >> 23) - 126, -60), 100));  // vm <= 2^ve
-              raise = top > M - vexp + kLazy || ve > vexp;
-              if (__any_sync(0xffffffffu, raise)) Mn = fmaxf(M - vexp, top) + ve;
-              vexp = ve;
-            } else {
-              raise = top > M + kLazy;
-              if (__any_sync(0xffffffffu, raise)) Mn = fmaxf(M, top);
-            }
-            if (Mn != M) {
-              const float f = M == -INFINITY ? 0.0f : ex2f(M - Mn);
-              l *= f;
-            }
-            // the first tile's product overwrites O
-            if (x > 1 && __any_sync(0xffffffffu, Mn != M)) {
-              const float f = M == -INFINITY ? 0.0f : Mn == M ? 1.0f : ex2f(M - Mn);
-#pragma unroll 1
-              for (int c = 0; c < DP / 16; ++c) {
-                uint32_t v[16];
-                tmem_ld16(o_addr + c * 16, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(v[i]) * f);
-                tmem_st16(o_addr + c * 16, v);
-              }
-            }
-            M = Mn;
-            const float shift = M == -INFINITY ? 0.0f : M;
-            const float* vs = s->vscale[ti];
-            l += tile_weights<MT, E4, 8 / SPLIT>(s_addr + c0 * 16, s_addr + c0 * 8, ks + c0 * 16, vs + c0 * 16, c2, shift);
-            if (SPLIT > 1) {
-              // the other copies' columns count as zero here
-              const uint32_t none[16] = {};
-              const int mine = copy * (4 / SPLIT) ;
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                if (c < mine || c >= mine + 4 / SPLIT) tmem_st16(s_addr + c * 16, none);
-            }
-            tmem_wait_st();
-          }
           if (!E4 && tail && (!two || g == 0)) {
             // Values of places past the end may be anything: zeros, so that a
             // zero weight stays zero.  A drafted token's infinities and NaN
@@ -1179,9 +1138,87 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
+          __syncwarp();
+          if (warp_live) {
+            const float* ks = s->kscale[ti];
+            if (masked) {
+              uint32_t words[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const long long off = tok0 + 32 * c - w.len, lim = w.total - (tok0 + 32 * c);
+                uint32_t y = ~0u;
+                if (off >= 64) y = 0u;
+                else if (off >= 0) y = static_cast<uint32_t>(mask >> off);
+                else if (off > -32) y = static_cast<uint32_t>(mask << -off) | ((1u << -off) - 1u);
+                if (lim <= 0) y = 0u;
+                else if (lim < 32) y &= (1u << lim) - 1u;
+                if (missing) {
+                  bool in = false;
+                  if (lane < lim) {
+                    const int pi = page_of(a.c, static_cast<int>(tok0 + 32 * c + lane));
+                    in = static_cast<unsigned int>(__ldg(a.c.table + static_cast<long long>(w.b) * a.c.table_stride + pi)) <
+                         static_cast<unsigned int>(a.c.num_pages);
+                  }
+                  y &= __ballot_sync(0xffffffffu, in);
+                }
+                words[c] = y;
+              }
+              mask_tile<E4>(s_addr, ks, words, copy * 4 / SPLIT, (copy * 4 + 4) / SPLIT);
+              ks = s->ones;
+            }
+            const int c0 = copy * (8 / SPLIT);
+            float top = tile_max<E4, 8 / SPLIT>(s_addr + c0 * 16, ks + c0 * 16);
+            top = top == -INFINITY ? -INFINITY : top * c2;
+            bool raise;
+            float Mn = M;
+            if (E4) {
+              const float vm = fmaxf(s->vmax[ti][0], s->vmax[ti][1]);
+              const int ve = max(vexp, min(max(static_cast<int>(__float_as_uint(vm) >> 23) - 126, -60), 100));  // vm <= 2^ve
+              raise = top > M - vexp + kLazy || ve > vexp;
+              if (__any_sync(0xffffffffu, raise)) Mn = fmaxf(M - vexp, top) + ve;
+              vexp = ve;
+            } else {
+              raise = top > M + kLazy;
+              if (__any_sync(0xffffffffu, raise)) Mn = fmaxf(M, top);
+            }
+            if (Mn != M) {
+              const float f = M == -INFINITY ? 0.0f : ex2f(M - Mn);
+              l *= f;
+            }
+            // the first tile's product overwrites O
+            if (x > 1 && __any_sync(0xffffffffu, Mn != M)) {
+              const float f = M == -INFINITY ? 0.0f : Mn == M ? 1.0f : ex2f(M - Mn);
+#pragma unroll 1
+              for (int c = 0; c < DP / 16; ++c) {
+                uint32_t v[16];
+                tmem_ld16(o_addr + c * 16, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(v[i]) * f);
+                tmem_st16(o_addr + c * 16, v);
+              }
+            }
+            M = Mn;
+            const float shift = M == -INFINITY ? 0.0f : M;
+            const float* vs = s->vscale[ti];
+            l += tile_weights<MT, E4, 8 / SPLIT>(s_addr + c0 * 16, s_addr + c0 * 8, ks + c0 * 16, vs + c0 * 16, c2, shift,
+                                                    &s->p_ready[g][0]);
+            if (SPLIT > 1) {
+              // the other copies' columns count as zero here
+              const uint32_t none[16] = {};
+              const int mine = copy * (4 / SPLIT) ;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (c < mine || c >= mine + 4 / SPLIT) tmem_st16(s_addr + c * 16, none);
+            }
+            tmem_wait_st();
+          }
           tmem_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s->p_ready[g]);
+          if (lane == 0) {
+            if (SPLIT > 1 || !warp_live) mbar_arrive(&s->p_ready[g][0]);
+            mbar_arrive(&s->p_ready[g][1]);
+          }
         }
 
         // ---- the segment's end: join the two groups, write
