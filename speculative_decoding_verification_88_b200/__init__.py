@@ -14,6 +14,7 @@ missing.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -79,6 +80,8 @@ def load_library(path: str | None = None):
     another build of the same library (the bounds-checked one) and returns it
     without making it the default."""
     global _lib
+    if path is None and _lib is not None:
+        return _lib
     with _lock:
         if path is None and _lib is not None:
             return _lib
@@ -558,10 +561,24 @@ _TYPES = {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float16: SV_F16,
 _ROPE = {"none": 0, "linear": 1, "bands": 2, "yarn": 3}
 
 
-def _on(device, stream):
-    """A guard that makes the device current, and the pointer of the stream to
-    launch on."""
-    return torch.cuda.device(device), _stream_ptr(stream, device)
+# The calls below may run many times a step for a few microseconds of work, so
+# their checks are kept to plain attribute tests, and the stream and device are
+# looked up without making objects.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = torch.cuda.current_device
+
+
+def _launch(fn, what, device, stream, args):
+    """Call an entry point, whose last argument is the stream, with `device` current."""
+    st = _raw_stream(device.index) if stream is None else stream.cuda_stream
+    if _current_device() == device.index:
+        code = fn(*args, st)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, st)
+    if code != 0:
+        _check(code, what)
 
 
 def _keep(t, stream):
@@ -572,8 +589,8 @@ def _keep(t, stream):
 
 
 def _ints(t, shape, device, name):
-    if (not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.int32 or
-            tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.shape != shape or
+            t.device != device or not t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on {device}")
     return t.data_ptr()
 
@@ -584,18 +601,20 @@ def _optional_ints(t, shape, device, name):
 
 def _rows(t, heads, dim, name, like=None):
     """Code and descriptor of a [B, N, heads, dim] tensor (`like`: another one)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _TYPES:
+    code = _TYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor of a floating type")
-    if t.dim() != 4 or (heads is not None and t.shape[2] != heads) or t.shape[3] != dim:
+    shape = t.shape
+    if len(shape) != 4 or (heads is not None and shape[2] != heads) or shape[3] != dim:
         raise ValueError(f"{name} must be [B, N, {'H' if heads is None else heads}, {dim}], "
-                         f"got {tuple(t.shape)}")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device or
-                             t.shape[:2] != like.shape[:2]):
+                         f"got {tuple(shape)}")
+    if like is not None and (t.dtype is not like.dtype or shape[0] != like.shape[0] or
+                             shape[1] != like.shape[1] or t.device != like.device):
         raise ValueError(f"{name} must match k's type, device, B and N")
     sb, sn, sh, sd = t.stride()
-    if sd != 1 and t.numel() > 0 and dim > 1:
+    if sd != 1 and dim > 1 and t.numel() > 0:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    return _TYPES[t.dtype], _Rows(t.data_ptr(), sb, sn, sh)
+    return code, _Rows(t.data_ptr(), sb, sn, sh)
 
 
 class KVCache:
@@ -727,26 +746,27 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, rope: Rotary, *, inverse: b
         if t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1 and s[0] != t.shape[1] * s[1]:
             raise ValueError(f"{name}: tokens must be evenly spaced over B and N")
         strides.append((s[1] if t.dim() == 4 and t.shape[1] > 1 else s[0], s[-2]))
-    guard, st = _on(dev, stream)
-    with guard:
-        code = lib.spec_verify_rotary(
-            x.data_ptr(), _TYPES[x.dtype], *strides[0], pos, rope._c, int(inverse),
-            x.numel() // (H * D), H, D, out.data_ptr(), *strides[1], st)
-    _check(code, "spec_verify_rotary")
+    _launch(lib.spec_verify_rotary, "spec_verify_rotary", dev, stream,
+            (x.data_ptr(), _TYPES[x.dtype], *strides[0], pos, rope._c, int(inverse),
+             x.numel() // (H * D), H, D, out.data_ptr(), *strides[1]))
     return out
 
 
 def _table(page_table, B, device):
-    if (not isinstance(page_table, torch.Tensor) or page_table.dtype != torch.int32 or
-            page_table.device != device or page_table.dim() != 2 or page_table.shape[0] != B or
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+    t = page_table
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 2 or
+            t.shape[0] != B or t.device != device or (t.shape[1] > 1 and t.stride(1) != 1)):
         raise TypeError(f"page_table must be int32 [{B}, max_pages] on {device}, rows contiguous")
-    return page_table.data_ptr(), page_table.stride(0), page_table.shape[1]
+    return t.data_ptr(), t.stride(0), t.shape[1]
 
 
 def _status(workspace, device, stream):
-    ws = workspace or default_workspace(device)
-    ws.ensure(256, stream)
+    """Where a call reports its flags: the workspace's status word."""
+    ws = workspace
+    if ws is None:
+        ws = _default_ws.get((device, _raw_stream(device.index))) or default_workspace(device)
+    if ws.buf is None:
+        ws.ensure(256, stream)
     return ws.buf.data_ptr()
 
 
@@ -788,12 +808,9 @@ def cache_write(cache: KVCache, page_table: torch.Tensor, cache_len: torch.Tenso
               not q_out.is_contiguous()):
             raise ValueError("q_out must be a contiguous tensor like q")
         qo = q_out.data_ptr()
-    guard, st = _on(dev, stream)
-    with guard:
-        code = lib.spec_verify_cache_write(
-            cache._c, table, tstride, pages, lens, par, cnt, kr, vr, code_t, B, N,
-            None if rope is None else rope._c, qr, Hq, qo, _status(workspace, dev, stream), st)
-    _check(code, "spec_verify_cache_write")
+    _launch(lib.spec_verify_cache_write, "spec_verify_cache_write", dev, stream,
+            (cache._c, table, tstride, pages, lens, par, cnt, kr, vr, code_t, B, N,
+             None if rope is None else rope._c, qr, Hq, qo, _status(workspace, dev, stream)))
     return q_out
 
 
@@ -816,13 +833,15 @@ def cache_read(cache: KVCache, page_table: torch.Tensor, offsets: torch.Tensor, 
     res = {x: _keep(_out(out, x, shape, dtype, dev), stream) for x in ("k", "v")}
     if total == 0:
         return res
-    guard, st = _on(dev, stream)
-    with guard:
-        code = lib.spec_verify_cache_read(
-            cache._c, table, tstride, pages, offs, st0, B, int(total), res["k"].data_ptr(),
-            res["v"].data_ptr(), _TYPES[dtype], _status(workspace, dev, stream), st)
-    _check(code, "spec_verify_cache_read")
+    _launch(lib.spec_verify_cache_read, "spec_verify_cache_read", dev, stream,
+            (cache._c, table, tstride, pages, offs, st0, B, int(total), res["k"].data_ptr(),
+             res["v"].data_ptr(), _TYPES[dtype], _status(workspace, dev, stream)))
     return res
+
+
+@functools.lru_cache(maxsize=256)
+def _scratch_bytes(*sizes):
+    return load_library().spec_verify_tree_attention_scratch_size(*sizes)
 
 
 def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
@@ -845,20 +864,20 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     par = _optional_ints(parent, (B, N), dev, "parent")
     cnt = _optional_ints(count, (B,), dev, "count")
     table, tstride, pages = _table(page_table, B, dev)
-    res = {"out": _keep(_out(out, "out", (B, N, Hq, D), q.dtype, dev), stream)}
+    if out is None:
+        res = {"out": _keep(torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev), stream)}
+    else:
+        res = {"out": _out(out, "out", (B, N, Hq, D), q.dtype, dev)}
     if lse:
         res["lse"] = _keep(_out(out, "lse", (B, N, Hq), torch.float32, dev), stream)
     if scale is None:
         scale = D ** -0.5
-    need = lib.spec_verify_tree_attention_scratch_size(B, N, Hq, cache.num_heads, D)
+    need = _scratch_bytes(B, N, Hq, cache.num_heads, D)
     scratch = _keep(torch.empty(max(need, 16), dtype=torch.uint8, device=dev), stream)
-    guard, st = _on(dev, stream)
-    with guard:
-        code = lib.spec_verify_tree_attention(
-            qr, code_t, cache._c, table, tstride, pages, lens, par, cnt, B, N, Hq, float(scale),
-            res["out"].data_ptr(), res["lse"].data_ptr() if lse else None,
-            _status(workspace, dev, stream), scratch.data_ptr(), scratch.numel(), st)
-    _check(code, "spec_verify_tree_attention")
+    _launch(lib.spec_verify_tree_attention, "spec_verify_tree_attention", dev, stream,
+            (qr, code_t, cache._c, table, tstride, pages, lens, par, cnt, B, N, Hq, float(scale),
+             res["out"].data_ptr(), res["lse"].data_ptr() if lse else None,
+             _status(workspace, dev, stream), scratch.data_ptr(), scratch.shape[0]))
     return res
 
 
@@ -884,10 +903,7 @@ def cache_commit(cache: KVCache, page_table: torch.Tensor, cache_len: torch.Tens
     table, tstride, pages = _table(page_table, B, dev)
     if new_len is None:
         new_len = _keep(torch.empty(B, dtype=torch.int32, device=dev), stream)
-    guard, st = _on(dev, stream)
-    with guard:
-        code = lib.spec_verify_cache_commit(
-            cache._c, table, tstride, pages, lens, accepted, path, B, N,
-            _ints(new_len, (B,), dev, "new_len"), _status(workspace, dev, stream), st)
-    _check(code, "spec_verify_cache_commit")
+    _launch(lib.spec_verify_cache_commit, "spec_verify_cache_commit", dev, stream,
+            (cache._c, table, tstride, pages, lens, accepted, path, B, N,
+             _ints(new_len, (B,), dev, "new_len"), _status(workspace, dev, stream)))
     return new_len

@@ -8,17 +8,21 @@ namespace sv {
 
 // ------------------------------------------------- rotary and cache write
 //
-// One block takes one token at a time: its threads first turn position * f
-// into (cos, sin) pairs in shared memory, once for all heads, then each
-// group of UP lanes takes one row (a head of q, k or v) and each lane of it
-// one unit of 16 elements: 8 whole pairs, or 16 neighbours past rotary_dim.
-// The angle is reduced as turns in 64 bits (position * f / 2 pi, minus the
-// nearest integer), so it is exact to 1e-10 turns at any 32-bit position;
-// cos and sin then work on a half turn at most.
+// A unit is 16 elements of a row (a head of q, k or v): 8 whole pairs, or 16
+// neighbours past rotary_dim.  A block takes a few tokens at a time: each of
+// its threads first has the loads of its (up to four) units in flight, then
+// the block turns position * f into (cos, sin) pairs in shared memory, once
+// for all heads, and then the units are turned and stored.  The angle is
+// reduced as turns in 64 bits (position * f / 2 pi, minus the nearest
+// integer), so it is exact to 1e-10 turns at any 32-bit position; cos and sin
+// then work on a half turn at most.
 //
-// K rows bound for 8 bits are turned in 64 bits, so that their codes are the
-// exact rotation's, rounded once; a row's scale needs the largest magnitude
-// over the row, one shuffle reduction over its lanes.
+// 8-bit rows: the codes are those of exact arithmetic, rounded once.  32-bit
+// arithmetic decides nearly all of them: a code is taken when the values an
+// error bound below and above give the same one, and only the others (about
+// one in 10^5) are computed again in 64 bits.  The scale needs the row's
+// exact largest magnitude: the elements within the bound of the 32-bit
+// maximum, one or two a row, are computed in 64 bits.
 
 constexpr int kRotThreads = 256;
 
@@ -47,31 +51,47 @@ __device__ __forceinline__ Unit unit_at(int u, bool turn, int rd, int D, bool in
   return x;
 }
 
-// f: first members (or the first 8 elements), g: second members (the next 8).
+// A unit's elements as they are in memory.
+template <typename T>
+struct Raw {
+  alignas(16) T a[8];  // first members (or the first 8 elements)
+  alignas(16) T b[8];  // second members (the next 8)
+};
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_unit(const T* row, const Unit& u, float (&f)[8], float (&g)[8]) {
+__device__ __forceinline__ void load_raw(const T* row, const Unit& u, Raw<T>& r) {
   if (VEC) {
     if (u.na == 0) return;
-    if (u.pair && u.inter) {
-      float x[8], y[8];
-      load8(row + u.a, x);
-      load8(row + u.a + 8, y);
+    constexpr int kWords = sizeof(T) * 8 / 16;
+    const int second = u.pair && u.inter ? u.a + 8 : u.b;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[i] = x[2 * i], g[i] = x[2 * i + 1];
-        f[4 + i] = y[2 * i], g[4 + i] = y[2 * i + 1];
-      }
-    } else {
-      load8(row + u.a, f);
-      load8(row + u.b, g);
+    for (int i = 0; i < kWords; ++i) {
+      reinterpret_cast<uint4*>(r.a)[i] = reinterpret_cast<const uint4*>(row + u.a)[i];
+      reinterpret_cast<uint4*>(r.b)[i] = reinterpret_cast<const uint4*>(row + second)[i];
     }
   } else {
     const int step = u.pair && u.inter ? 2 : 1;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (i < u.na) f[i] = elem_f32(row[u.a + i * step]);
-      if (i < u.nb) g[i] = elem_f32(row[u.b + i * step]);
+      if (i < u.na) r.a[i] = row[u.a + i * step];
+      if (i < u.nb) r.b[i] = row[u.b + i * step];
     }
+  }
+}
+// f: first members (or the first 8 elements), g: second members (the next 8).
+template <typename T, bool VEC>
+__device__ __forceinline__ void unpack_raw(const Raw<T>& r, const Unit& u, float (&f)[8], float (&g)[8]) {
+  float x[8], y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = elem_f32(r.a[i]), y[i] = elem_f32(r.b[i]);
+  if (VEC && u.pair && u.inter) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = x[2 * i], g[i] = x[2 * i + 1];
+      f[4 + i] = y[2 * i], g[4 + i] = y[2 * i + 1];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = VEC || i < u.na ? x[i] : 0.0f, g[i] = VEC || i < u.nb ? y[i] : 0.0f;
   }
 }
 
@@ -103,174 +123,250 @@ __device__ __forceinline__ void store_unit(T* row, const Unit& u, const float (&
   }
 }
 
+// f, g: codes of the first and second members.
 template <bool VEC>
-__device__ __forceinline__ void store_codes(uint8_t* row, const Unit& u, const float (&f)[8],
-                                            const float (&g)[8]) {
-  uint32_t lo[4], hi[4];  // two codes each
-  if (u.pair && u.inter) {
+__device__ __forceinline__ void store_codes(uint8_t* row, const Unit& u, const uint8_t (&f)[8], const uint8_t (&g)[8]) {
+  uint8_t lo[8], hi[8];
+  const bool weave = u.pair && u.inter;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      lo[i] = e4m3_pair(f[i], g[i]);
-      hi[i] = e4m3_pair(f[4 + i], g[4 + i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      lo[i] = e4m3_pair(f[2 * i], f[2 * i + 1]);
-      hi[i] = e4m3_pair(g[2 * i], g[2 * i + 1]);
-    }
+  for (int i = 0; i < 4; ++i) {
+    lo[2 * i] = weave ? f[i] : f[2 * i];
+    lo[2 * i + 1] = weave ? g[i] : f[2 * i + 1];
+    hi[2 * i] = weave ? f[4 + i] : g[2 * i];
+    hi[2 * i + 1] = weave ? g[4 + i] : g[2 * i + 1];
   }
-  const int second = u.pair && u.inter ? u.a + 8 : u.b;
+  const int second = weave ? u.a + 8 : u.b;
   if (VEC) {
     if (u.na == 0) return;
-    *reinterpret_cast<uint2*>(row + u.a) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-    *reinterpret_cast<uint2*>(row + second) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[i] = lo[4 * i] | lo[4 * i + 1] << 8 | lo[4 * i + 2] << 16 | static_cast<uint32_t>(lo[4 * i + 3]) << 24;
+      w[2 + i] = hi[4 * i] | hi[4 * i + 1] << 8 | hi[4 * i + 2] << 16 | static_cast<uint32_t>(hi[4 * i + 3]) << 24;
+    }
+    *reinterpret_cast<uint2*>(row + u.a) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(row + second) = make_uint2(w[2], w[3]);
   } else {
     // counts in elements of each run of 8 neighbours
-    const int n0 = u.pair && u.inter ? min(8, 2 * u.na) : u.na;
-    const int n1 = u.pair && u.inter ? max(0, 2 * u.na - 8) : u.nb;
+    const int n0 = weave ? min(8, 2 * u.na) : u.na;
+    const int n1 = weave ? max(0, 2 * u.na - 8) : u.nb;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (i < n0) row[u.a + i] = static_cast<uint8_t>(lo[i >> 1] >> (8 * (i & 1)));
-      if (i < n1) row[second + i] = static_cast<uint8_t>(hi[i >> 1] >> (8 * (i & 1)));
+      if (i < n0) row[u.a + i] = lo[i];
+      if (i < n1) row[second + i] = hi[i];
     }
   }
 }
 
-// E4: the pool holds codes and scales.  UP: lanes of a row (a power of two).
+// An element of a row bound for 8 bits, exactly: x c - y s with 64-bit (c, s).
+__device__ __noinline__ double exact_elem(float x, float y, double c, double s) {
+  return fma(static_cast<double>(x), c, -(static_cast<double>(y) * s));
+}
+__device__ __noinline__ uint8_t exact_code(double x, float scale) {
+  const double s = scale;
+  return static_cast<uint8_t>(e4m3_pair(quotient_odd(x, s, 1.0 / s), 0.0f));
+}
+
+struct RotatePlan {
+  int UP;         // lanes of a row (8-bit pools: a power of two, for the row's reduction)
+  int group;      // tokens a block takes at a time
+  int per_token;  // units of a token: rows * UP
+  UDiv div_token, div_up, div_N, div_half;  // / per_token, / UP, / N, / (rd / 2)
+};
+__device__ __forceinline__ int quotient(int n, const UDiv& d) {
+  return d.m == 0u ? n : static_cast<int>(__umulhi(static_cast<unsigned int>(n), d.m) >> d.shift);
+}
+
+constexpr int kRotGroup = 16;    // most tokens a block takes at a time
+constexpr int kRotAngles = 1024; // most (cos, sin) pairs of a group
+
+// E4: the pool holds codes and scales.
 template <typename T, bool E4, bool VEC>
-__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotateParams p, int UP) {
+__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_constant__ RotateParams p,
+                                                             const __grid_constant__ RotatePlan n) {
   dep_enter();
-  __shared__ float2 cs[2][256];
-  __shared__ double2 csd[E4 ? 2 : 1][E4 ? 128 : 1];  // cache heads have at most 256 elements
-  __shared__ int par[2][64];
+  constexpr int kUnits = sizeof(T) == 4 ? 2 : 4;  // units a thread has in flight
+  __shared__ float2 cs[kRotAngles];
+  __shared__ double2 csd[E4 ? kRotAngles : 1];
+  __shared__ long long dst[kRotGroup];  // element offset of the token's place; -1: none, -2: padding
+  __shared__ long long sdst[kRotGroup]; // its scales
+  __shared__ int depth_of[kRotGroup];
   const int tid = threadIdx.x;
-  const int lane = tid & (UP - 1);
-  const int rows = p.Hq + (p.write ? 2 * p.c.heads : 0);
-  const int per_pass = kRotThreads / UP;
   const bool turn = p.inv_freq != nullptr;
-  int buf = 0;
-  for (long long t = blockIdx.x; t < p.tokens; t += gridDim.x, buf ^= 1) {
-    const int b = static_cast<int>(t / p.N);
-    const int j = static_cast<int>(t - static_cast<long long>(b) * p.N);
-    if (p.count && j >= __ldg(p.count + b)) {
-      __syncthreads();
-      continue;
-    }
-    long long len = 0, pos = 0;
-    if (p.positions) {
-      pos = __ldg(p.positions + t);
-    } else {
-      len = max(0, __ldg(p.cache_len + b));
-      pos = len + j;
-      if (p.parent) {
-        if (tid < p.N) par[buf][tid] = __ldg(p.parent + static_cast<long long>(b) * p.N + tid);
-        __syncthreads();
-        int depth = 0;
-        for (int x = j; x > 0; ++depth) {  // parents decrease, so this ends
-          const int up = par[buf][x];
-          if (up < 0 || up >= x) {
-            if (tid == 0) raise_flag(p.ctrl, kFlagInvalidTree);
-            break;
-          }
-          x = up;
-        }
-        pos = len + depth;
-      }
-    }
-    if (turn) {
-      for (int i = tid; i < p.rd / 2; i += kRotThreads) {
-        const double turns = static_cast<double>(pos) * __ldg(p.inv_freq + i) * 0.15915494309189533577;
-        const double half = 2.0 * (turns - rint(turns));
-        float s, c;
-        sincospif(static_cast<float>(half), &s, &c);
-        s = p.inverse ? -s : s;
-        cs[buf][i] = make_float2(c * p.magnitude, s * p.magnitude);
-        if (E4) {
-          double sd, cd;
-          sincospi(half, &sd, &cd);
-          csd[buf][i] = make_double2(cd * p.magnitude, sd * p.magnitude);
-        }
-      }
-    }
-    int page = 0, place = 0;
-    const bool placed = p.write && find_place(p.c, b, len + j, page, place, tid == 0 ? p.ctrl : nullptr);
-    __syncthreads();
-    for (int r0 = 0; r0 < rows; r0 += per_pass) {
-      const int r = r0 + tid / UP;
-      const int kind = r < p.Hq ? 0 : r < p.Hq + p.c.heads ? 1 : 2;
-      const bool live = r < rows && (kind == 0 || placed);
-      const int h = kind == 0 ? r : kind == 1 ? r - p.Hq : r - p.Hq - p.c.heads;
-      const bool turned = turn && kind < 2;
-      const Unit u = unit_at(lane, turned, p.rd, p.D, p.interleaved != 0);
-      float f[8] = {}, g[8] = {};
-      if (live) {
+  const int half_rd = p.rd / 2;
+  const int units = n.group * n.per_token;
+  for (long long t0 = static_cast<long long>(blockIdx.x) * n.group; t0 < p.tokens;
+       t0 += static_cast<long long>(gridDim.x) * n.group) {
+    const int group = static_cast<int>(min(static_cast<long long>(n.group), p.tokens - t0));
+    for (int base = 0; base < units; base += kRotThreads * kUnits) {
+      Raw<T> raw[kUnits];
+      // ---- loads
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int id = base + tid + kRotThreads * i;
+        const int k = quotient(id, n.div_token), rem = id - k * n.per_token;
+        const int r = quotient(rem, n.div_up), lane = rem - r * n.UP;
+        if (k >= group) continue;
+        const int t = static_cast<int>(t0) + k;
+        const int b = quotient(t, n.div_N), j = t - b * p.N;
+        const int kind = r < p.Hq ? 0 : r < p.Hq + p.c.heads ? 1 : 2;
+        const int h = kind == 0 ? r : kind == 1 ? r - p.Hq : r - p.Hq - p.c.heads;
+        const Unit u = unit_at(lane, turn && kind < 2, p.rd, p.D, p.interleaved != 0);
         const RowsView& src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-        load_unit<T, VEC>(static_cast<const T*>(src.p) + b * src.sb + j * src.sn + h * src.sh, u, f, g);
+        load_raw<T, VEC>(static_cast<const T*>(src.p) + b * src.sb + j * src.sn + h * src.sh, u, raw[i]);
       }
-      if (!E4 || kind == 0) {
-        if (u.pair && turned) {
-          const int first = 8 * lane;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (VEC || i < u.na) {
-              const float2 w = cs[buf][first + i];
-              const float x = f[i], y = g[i];
-              f[i] = fmaf(x, w.x, -y * w.y);
-              g[i] = fmaf(y, w.x, x * w.y);
+      // ---- places and angles
+      if (base == 0) {
+        if (tid < group) {
+          const int t = static_cast<int>(t0) + tid;
+          const int b = quotient(t, n.div_N), j = t - b * p.N;
+          long long at = -1, sat = 0;
+          int depth = j;
+          if (p.count && j >= __ldg(p.count + b)) {
+            at = -2;
+          } else if (!p.positions) {
+            if (p.parent) {
+              const int* par = p.parent + static_cast<long long>(b) * p.N;
+              depth = 0;
+              for (int x = j; x > 0; ++depth) {  // parents decrease, so this ends
+                const int up = __ldg(par + x);
+                if (up < 0 || up >= x) {
+                  raise_flag(p.ctrl, kFlagInvalidTree);
+                  break;
+                }
+                x = up;
+              }
+            }
+            int page, place;
+            if (p.write && find_place(p.c, b, max(0, __ldg(p.cache_len + b)) + static_cast<long long>(j), page, place,
+                                      p.ctrl)) {
+              at = page * p.c.page_stride + place * p.c.token_stride;
+              sat = static_cast<long long>(page) * p.c.heads * p.c.page_size + place;
             }
           }
+          dst[tid] = at;
+          sdst[tid] = sat;
+          depth_of[tid] = depth;
         }
-        if (live) {
-          T* dst;
-          if (kind == 0)
-            dst = static_cast<T*>(p.q_out) + t * p.qo_st + h * p.qo_sh;
-          else
-            dst = static_cast<T*>(kind == 1 ? p.c.k : p.c.v) + page * p.c.page_stride +
-                  place * p.c.token_stride + h * p.c.head_stride;
-          store_unit<T, VEC>(dst, u, f, g);
+        __syncthreads();
+        if (turn) {
+          for (int i = tid; i < group * half_rd; i += kRotThreads) {
+            const int k = quotient(i, n.div_half), f = i - k * half_rd;
+            const int t = static_cast<int>(t0) + k;
+            const long long pos = p.positions ? __ldg(p.positions + t)
+                                              : max(0, __ldg(p.cache_len + quotient(t, n.div_N))) +
+                                                    static_cast<long long>(depth_of[k]);
+            const double turns = static_cast<double>(pos) * __ldg(p.inv_freq + f) * 0.15915494309189533577;
+            const double half = 2.0 * (turns - rint(turns));
+            float s, c;
+            sincospif(static_cast<float>(half), &s, &c);
+            s = p.inverse ? -s : s;
+            cs[i] = make_float2(c * p.magnitude, s * p.magnitude);
+            if (E4) {
+              double sd, cd;
+              sincospi(half, &sd, &cd);
+              csd[i] = make_double2(cd * p.magnitude, sd * p.magnitude);
+            }
+          }
+          __syncthreads();
         }
       }
-      if (E4) {
-        // Every lane takes part in the row's reduction.
-        double x[8], y[8];
-        double top = 0.0;
-        bool odd = false;  // an infinity or a NaN
-        if (kind != 0) {
+      // ---- turn and store
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] = f[i], y[i] = g[i];
-            odd |= !isfinite(f[i]) || !isfinite(g[i]);
-            if (u.pair && turned && (VEC || i < u.na)) {
-              const double2 w = csd[buf][8 * lane + i];
-              const double a = x[i], d = y[i];
-              x[i] = fma(a, w.x, -d * w.y);
-              y[i] = fma(d, w.x, a * w.y);
+      for (int i = 0; i < kUnits; ++i) {
+        const int id = base + tid + kRotThreads * i;
+        if (!E4 && id >= units) continue;
+        const int k = quotient(id, n.div_token), rem = id - k * n.per_token;
+        const int r = quotient(rem, n.div_up), lane = rem - r * n.UP;
+        const int kind = r < p.Hq ? 0 : r < p.Hq + p.c.heads ? 1 : 2;
+        const int h = kind == 0 ? r : kind == 1 ? r - p.Hq : r - p.Hq - p.c.heads;
+        const long long at = k < group ? dst[k] : -2;
+        const bool live = k < group && (kind == 0 ? at != -2 : at >= 0);
+        const bool turned = turn && kind < 2;
+        const Unit u = unit_at(lane, turned, p.rd, p.D, p.interleaved != 0);
+        const int first = k * half_rd + 8 * lane;  // this unit's angles
+        float f[8] = {}, g[8] = {};
+        if (live && u.na > 0) unpack_raw<T, VEC>(raw[i], u, f, g);
+        const bool pair = u.pair && turned;
+        if ((!E4 || kind == 0) && live) {
+          if (pair) {
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+              if (VEC || z < u.na) {
+                const float2 w = cs[first + z];
+                const float x = f[z], y = g[z];
+                f[z] = fmaf(x, w.x, -y * w.y);
+                g[z] = fmaf(y, w.x, x * w.y);
+              }
             }
-            top = fmax(top, fmax(fabs(x[i]), fabs(y[i])));
           }
+          T* out = kind == 0 ? static_cast<T*>(p.q_out) + (t0 + k) * p.qo_st + h * p.qo_sh
+                             : static_cast<T*>(kind == 1 ? p.c.k : p.c.v) + at + h * p.c.head_stride;
+          store_unit<T, VEC>(out, u, f, g);
         }
-        for (int o = UP >> 1; o > 0; o >>= 1) {
-          top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o, 32));
-          odd |= __shfl_xor_sync(0xffffffffu, static_cast<int>(odd), o, 32) != 0;
-        }
-        if (live && kind != 0) {
-          float scale = static_cast<float>(top / 448.0);
-          const double s = scale, inv = scale > 0.0f ? 1.0 / s : 0.0;
-          if (odd || !isfinite(scale)) scale = __int_as_float(0x7fc00000);
+        if (E4 && __any_sync(0xffffffffu, live && kind != 0)) {
+          // Every lane takes part in the row's reductions.  e: a bound of the
+          // 32-bit error of both members of a pair (angle and functions, two
+          // products, a sum: under 8 roundings of each term).
+          float x[8], y[8], e[8];
+          float top = 0.0f, slack = 0.0f;
+          bool odd = false;  // an infinity or a NaN
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            f[i] = quotient_odd(x[i], s, inv);
-            g[i] = quotient_odd(y[i], s, inv);
+          for (int z = 0; z < 8; ++z) {
+            x[z] = f[z], y[z] = g[z], e[z] = 0.0f;
+            odd |= !isfinite(f[z]) || !isfinite(g[z]);
+            if (pair && (VEC || z < u.na)) {
+              const float2 w = cs[first + z];
+              x[z] = fmaf(f[z], w.x, -g[z] * w.y);
+              y[z] = fmaf(g[z], w.x, f[z] * w.y);
+              e[z] = (fabsf(f[z]) + fabsf(g[z])) * (fabsf(p.magnitude) * 0x1p-20f);
+            }
+            top = fmaxf(top, fmaxf(fabsf(x[z]), fabsf(y[z])));
+            slack = fmaxf(slack, e[z]);
           }
-          const long long at = page * p.c.page_stride + place * p.c.token_stride + h * p.c.head_stride;
-          store_codes<VEC>(static_cast<uint8_t*>(kind == 1 ? p.c.k : p.c.v) + at, u, f, g);
-          if (lane == 0)
-            (kind == 1 ? p.c.ks : p.c.vs)[(static_cast<long long>(page) * p.c.heads + h) * p.c.page_size +
-                                          place] = scale;
+          if (kind == 0) top = 0.0f, slack = 0.0f, odd = false;
+          for (int o = n.UP >> 1; o > 0; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            slack = fmaxf(slack, __shfl_xor_sync(0xffffffffu, slack, o));
+            odd |= __shfl_xor_sync(0xffffffffu, static_cast<int>(odd), o) != 0;
+          }
+          double most = 0.0;
+          const float near = top - 2.0f * slack;
+#pragma unroll
+          for (int z = 0; z < 8; ++z) {
+            const double2 w = pair && (VEC || z < u.na) ? csd[E4 ? first + z : 0] : make_double2(1.0, 0.0);
+            if (fabsf(x[z]) >= near) most = fmax(most, fabs(exact_elem(f[z], g[z], w.x, w.y)));
+            if (fabsf(y[z]) >= near) most = fmax(most, fabs(exact_elem(g[z], f[z], w.x, -w.y)));
+          }
+          for (int o = n.UP >> 1; o > 0; o >>= 1) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, o));
+          if (live && kind != 0) {
+            float scale = static_cast<float>(most / 448.0);
+            if (odd || !isfinite(scale)) scale = __int_as_float(0x7fc00000);
+            // tiny scales have no 32-bit reciprocal: all such codes are exact ones
+            const bool fine = scale > 0x1p-100f;
+            const float inv = fine ? 1.0f / scale : 0.0f;
+            uint8_t cx[8], cy[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+              const float qx = x[z] * inv, qy = y[z] * inv;
+              const float dx = fmaf(fabsf(qx), 0x1p-21f, e[z] * inv), dy = fmaf(fabsf(qy), 0x1p-21f, e[z] * inv);
+              const uint32_t wx = e4m3_pair(qx - dx, qx + dx), wy = e4m3_pair(qy - dy, qy + dy);
+              cx[z] = static_cast<uint8_t>(wx), cy[z] = static_cast<uint8_t>(wy);
+              const bool sure_x = fine && (wx & 0xffu) == (wx >> 8), sure_y = fine && (wy & 0xffu) == (wy >> 8);
+              if (!(sure_x && sure_y)) {
+                const double2 w = pair && (VEC || z < u.na) ? csd[E4 ? first + z : 0] : make_double2(1.0, 0.0);
+                if (!sure_x) cx[z] = scale == 0.0f ? 0 : exact_code(exact_elem(f[z], g[z], w.x, w.y), scale);
+                if (!sure_y) cy[z] = scale == 0.0f ? 0 : exact_code(exact_elem(g[z], f[z], w.x, -w.y), scale);
+              }
+            }
+            store_codes<VEC>(static_cast<uint8_t*>(kind == 1 ? p.c.k : p.c.v) + at + h * p.c.head_stride, u, cx, cy);
+            if (lane == 0)
+              (kind == 1 ? p.c.ks : p.c.vs)[sdst[k] + static_cast<long long>(h) * p.c.page_size] = scale;
+          }
         }
       }
     }
+    __syncthreads();  // the angles and places may be overwritten now
   }
 }
 
@@ -279,13 +375,32 @@ static cudaError_t launch_rotate_t(const RotateParams& p, bool e4, bool vec, int
   const int np = p.inv_freq ? (p.rd / 2 + 7) / 8 + (p.D - p.rd + 15) / 16 : 0;
   int units = p.write || !p.inv_freq ? (p.D + 15) / 16 : 0;
   if (np > units) units = np;
-  int up = 1;
-  while (up < units) up <<= 1;
-  const long long most = static_cast<long long>(sms) * (2048 / kRotThreads);
-  const dim3 grid(static_cast<unsigned int>(p.tokens < most ? p.tokens : most));
-  void (*k)(const RotateParams, int) = e4 ? (vec ? rotate_kernel<T, true, true> : rotate_kernel<T, true, false>)
-                                          : (vec ? rotate_kernel<T, false, true> : rotate_kernel<T, false, false>);
-  return counted(launch_k(SV_PDL >= 2, k, grid, dim3(kRotThreads), 0, st, p, up), 1);
+  RotatePlan n{};
+  n.UP = units;
+  if (e4)
+    for (n.UP = 1; n.UP < units;) n.UP <<= 1;
+  const int rows = p.Hq + (p.write ? 2 * p.c.heads : 0);
+  n.per_token = rows * n.UP;
+  // Tokens together until every thread has its units (more would only delay
+  // the first stores), unless that leaves SMs without a block.
+  const int most = kRotThreads * (sizeof(T) == 4 ? 2 : 4);
+  n.group = most / n.per_token;
+  if (p.rd > 0 && n.group > kRotAngles / (p.rd / 2)) n.group = kRotAngles / (p.rd / 2);
+  if (n.group > kRotGroup) n.group = kRotGroup;
+  while (n.group > 1 && (p.tokens + n.group - 1) / n.group < 2ll * sms) n.group /= 2;
+  if (n.group < 1) n.group = 1;
+  n.div_token = make_udiv(static_cast<unsigned int>(n.per_token));
+  n.div_up = make_udiv(static_cast<unsigned int>(n.UP));
+  n.div_N = make_udiv(static_cast<unsigned int>(p.N));
+  n.div_half = make_udiv(static_cast<unsigned int>(p.rd > 0 ? p.rd / 2 : 1));
+  const long long blocks = (p.tokens + n.group - 1) / n.group;
+  const long long grid = static_cast<long long>(sms) * 8;
+  void (*k)(const RotateParams, const RotatePlan) =
+      e4 ? (vec ? rotate_kernel<T, true, true> : rotate_kernel<T, true, false>)
+         : (vec ? rotate_kernel<T, false, true> : rotate_kernel<T, false, false>);
+  return counted(launch_k(SV_PDL >= 2, k, dim3(static_cast<unsigned int>(blocks < grid ? blocks : grid)),
+                          dim3(kRotThreads), 0, st, p, n),
+                 1);
 }
 
 cudaError_t launch_rotate(const RotateParams& p, int dtype, int cache_dtype, bool vec, int sms,
@@ -301,12 +416,13 @@ cudaError_t launch_rotate(const RotateParams& p, int dtype, int cache_dtype, boo
 //
 // A block takes 16 packed rows: one lane a row finds its sequence (the last b
 // with offsets[b] <= r) and its page, then all threads convert (row, k or v,
-// head) runs of 8 elements.
+// head) runs of 8 elements, four of a thread's runs in flight at once.
 
 constexpr int kReadRows = 16;
 
 template <typename C, typename O, bool VEC>
-__global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadParams p) {
+__global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ CacheReadParams p, UDiv div_row,
+                                                         UDiv div_kv, UDiv div_head) {
   dep_enter();
   __shared__ long long src[kReadRows];   // element offset of the token, -1: zeros, -2: no row
   __shared__ long long ssrc[kReadRows];  // scale offset of head 0
@@ -334,40 +450,68 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadParams p
   }
   __syncthreads();
   constexpr bool kCodes = sizeof(C) == 1;
-  const int runs = (p.c.dim + 7) / 8;
-  const int per_row = 2 * p.c.heads * runs;
-  for (int i = threadIdx.x; i < kReadRows * per_row; i += 256) {
-    const int row = i / per_row;
-    int x = i - row * per_row;
-    const int kv = x / (p.c.heads * runs);
-    x -= kv * p.c.heads * runs;
-    const int h = x / runs, e = (x - h * runs) * 8;
-    const long long at = src[row];
-    if (at == -2) continue;
-    float f[8] = {};
-    const int n = min(8, p.c.dim - e);
-    if (at >= 0) {
-      const C* c = static_cast<const C*>(kv ? p.c.v : p.c.k) + at + h * p.c.head_stride + e;
+  constexpr int kAhead = 4;
+  const int runs = static_cast<int>(div_head.d), per_kv = static_cast<int>(div_kv.d), per_row = static_cast<int>(div_row.d);
+  const int all = kReadRows * per_row;
+  for (int i0 = threadIdx.x; i0 < all; i0 += 256 * kAhead) {
+    alignas(16) C c[kAhead][8];
+    float scale[kAhead];
+#pragma unroll
+    for (int z = 0; z < kAhead; ++z) {
+      const int i = i0 + z * 256;
+      if (i >= all) continue;
+      const int row = quotient(i, div_row), x = i - row * per_row;
+      const int kv = quotient(x, div_kv), y = x - kv * per_kv;
+      const int h = quotient(y, div_head), e = (y - h * runs) * 8;
+      const long long at = src[row];
+      if (at < 0) continue;
+      const C* from = static_cast<const C*>(kv ? p.c.v : p.c.k) + at + h * p.c.head_stride + e;
       if (VEC) {
-        load8(c, f);
+        constexpr int kBytes = 8 * sizeof(C);
+        if (kBytes == 8) {
+          *reinterpret_cast<uint2*>(c[z]) = *reinterpret_cast<const uint2*>(from);
+        } else {
+#pragma unroll
+          for (int w = 0; w < kBytes / 16; ++w) reinterpret_cast<uint4*>(c[z])[w] = reinterpret_cast<const uint4*>(from)[w];
+        }
       } else {
 #pragma unroll
         for (int m = 0; m < 8; ++m)
-          if (m < n) f[m] = elem_f32(c[m]);
+          if (e + m < p.c.dim) c[z][m] = from[m];
       }
-      if (kCodes) {
-        const float s = __ldg((kv ? p.c.vs : p.c.ks) + ssrc[row] + static_cast<long long>(h) * p.c.page_size);
-#pragma unroll
-        for (int m = 0; m < 8; ++m) f[m] *= s;
-      }
+      if (kCodes) scale[z] = __ldg((kv ? p.c.vs : p.c.ks) + ssrc[row] + static_cast<long long>(h) * p.c.page_size);
     }
-    O* o = static_cast<O*>(kv ? p.v_out : p.k_out) + ((r0 + row) * p.c.heads + h) * p.c.dim + e;
-    if (VEC) {
-      store8(o, f);
-    } else {
 #pragma unroll
-      for (int m = 0; m < 8; ++m)
-        if (m < n) o[m] = from_f32<O>(f[m]);
+    for (int z = 0; z < kAhead; ++z) {
+      const int i = i0 + z * 256;
+      if (i >= all) continue;
+      const int row = quotient(i, div_row), x = i - row * per_row;
+      const int kv = quotient(x, div_kv), y = x - kv * per_kv;
+      const int h = quotient(y, div_head), e = (y - h * runs) * 8;
+      const long long at = src[row];
+      if (at == -2) continue;
+      float f[8] = {};
+      if (at >= 0) {
+        if (VEC) {
+          load8(c[z], f);
+        } else {
+#pragma unroll
+          for (int m = 0; m < 8; ++m)
+            if (e + m < p.c.dim) f[m] = elem_f32(c[z][m]);
+        }
+        if (kCodes) {
+#pragma unroll
+          for (int m = 0; m < 8; ++m) f[m] *= scale[z];
+        }
+      }
+      O* o = static_cast<O*>(kv ? p.v_out : p.k_out) + ((r0 + row) * p.c.heads + h) * p.c.dim + e;
+      if (VEC) {
+        store8(o, f);
+      } else {
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+          if (e + m < p.c.dim) o[m] = from_f32<O>(f[m]);
+      }
     }
   }
 }
@@ -375,14 +519,17 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadParams p
 template <typename C>
 static cudaError_t launch_read_c(const CacheReadParams& p, int out_dtype, bool vec, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned int>((p.total + kReadRows - 1) / kReadRows));
-  void (*k)(const CacheReadParams);
+  void (*k)(const CacheReadParams, UDiv, UDiv, UDiv);
   if (out_dtype == 0)
     k = vec ? cache_read_kernel<C, float, true> : cache_read_kernel<C, float, false>;
   else if (out_dtype == 1)
     k = vec ? cache_read_kernel<C, __nv_bfloat16, true> : cache_read_kernel<C, __nv_bfloat16, false>;
   else
     k = vec ? cache_read_kernel<C, __half, true> : cache_read_kernel<C, __half, false>;
-  return counted(launch_k(SV_PDL >= 2, k, grid, dim3(256), 0, st, p), 1);
+  const unsigned int runs = static_cast<unsigned int>((p.c.dim + 7) / 8), heads = static_cast<unsigned int>(p.c.heads);
+  return counted(launch_k(SV_PDL >= 2, k, grid, dim3(256), 0, st, p, make_udiv(2 * heads * runs), make_udiv(heads * runs),
+                          make_udiv(runs)),
+                 1);
 }
 
 cudaError_t launch_cache_read(const CacheReadParams& p, int cache_dtype, int out_dtype, bool vec,

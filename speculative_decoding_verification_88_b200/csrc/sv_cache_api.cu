@@ -155,6 +155,7 @@ extern "C" int spec_verify_cache_write(const sv_kv_cache* cache, const int32_t* 
   if (B == 0 || N == 0) return SV_OK;
   if (const int e = check_cache(cache, page_table, table_stride, max_pages, B, true)) return e;
   if (cache->dtype != dtype && cache->dtype != SV_E4M3) return SV_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * N > 0x7fffffffll) return SV_ERR_INVALID_ARG;
   if (!cache_len || !k || !v || !k->data || !v->data || !strides_ok(k) || !strides_ok(v)) return SV_ERR_INVALID_ARG;
   if (q && (!rope || !q->data || !q_out || !strides_ok(q) || Hq < 1 || Hq > 1024)) return SV_ERR_INVALID_ARG;
   const int D = cache->head_dim;
