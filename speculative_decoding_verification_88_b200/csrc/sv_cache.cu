@@ -27,28 +27,40 @@ namespace sv {
 constexpr int kRotThreads = 256;
 
 struct Unit {
-  int a, b;  // first elements of the two runs of 8 (pairs: first and second members)
-  int na, nb;
-  bool pair, inter;
+  int a, b;    // first elements of the two runs of 8
+  int na, nb;  // elements of each (runs of a vectorised unit are whole)
+  bool pair;   // rotary pairs
+  bool weave;  // pairs are neighbours: each run holds four (VEC), or the unit's run of 16 eight
 };
-// `turn`: the row has a rotary part.
+// `turn`: the row has a rotary part.  Vectorised units take their second run
+// half a part further on, so that neighbouring lanes read neighbouring runs.
+template <bool VEC>
 __device__ __forceinline__ Unit unit_at(int u, bool turn, int rd, int D, bool inter) {
   Unit x;
   const int np = turn ? (rd / 2 + 7) / 8 : 0;
   x.pair = u < np;
-  x.inter = inter;
-  if (x.pair) {
-    const int n = min(8, rd / 2 - 8 * u);
-    x.na = x.nb = n;
-    x.a = inter ? 16 * u : 8 * u;
-    x.b = inter ? x.a + 1 : rd / 2 + 8 * u;
+  x.weave = x.pair && inter;
+  if (x.pair && (VEC || !inter)) {
+    x.na = x.nb = min(8, rd / 2 - 8 * u);
+    x.a = 8 * u;
+    x.b = rd / 2 + 8 * u;
+  } else if (x.pair) {
+    x.na = x.nb = min(8, rd / 2 - 8 * u);
+    x.a = 16 * u;
+    x.b = x.a + 1;
   } else {
-    x.a = (turn ? rd : 0) + 16 * (u - np);
-    x.b = x.a + 8;
-    x.na = max(0, min(8, D - x.a));
-    x.nb = max(0, min(8, D - x.b));
+    const int base = turn ? rd : 0, v = u - np;
+    x.a = base + (VEC ? 8 : 16) * v;
+    x.b = VEC ? base + (D - base) / 2 + 8 * v : x.a + 8;
+    x.na = max(0, min(8, (VEC ? base + (D - base) / 2 : D) - x.a));
+    x.nb = VEC ? x.na : max(0, min(8, D - x.b));
   }
   return x;
+}
+// Angle of pair z of a unit (its lane among the row's units, rotary_dim).
+template <bool VEC>
+__device__ __forceinline__ int angle_of(int z, int lane, int rd, bool weave) {
+  return VEC && weave ? (z < 4 ? 0 : rd / 4 - 4) + 4 * lane + z : 8 * lane + z;
 }
 
 // A unit's elements as they are in memory.
@@ -62,14 +74,13 @@ __device__ __forceinline__ void load_raw(const T* row, const Unit& u, Raw<T>& r)
   if (VEC) {
     if (u.na == 0) return;
     constexpr int kWords = sizeof(T) * 8 / 16;
-    const int second = u.pair && u.inter ? u.a + 8 : u.b;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       reinterpret_cast<uint4*>(r.a)[i] = reinterpret_cast<const uint4*>(row + u.a)[i];
-      reinterpret_cast<uint4*>(r.b)[i] = reinterpret_cast<const uint4*>(row + second)[i];
+      reinterpret_cast<uint4*>(r.b)[i] = reinterpret_cast<const uint4*>(row + u.b)[i];
     }
   } else {
-    const int step = u.pair && u.inter ? 2 : 1;
+    const int step = u.weave ? 2 : 1;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (i < u.na) r.a[i] = row[u.a + i * step];
@@ -81,40 +92,39 @@ __device__ __forceinline__ void load_raw(const T* row, const Unit& u, Raw<T>& r)
 template <typename T, bool VEC>
 __device__ __forceinline__ void unpack_raw(const Raw<T>& r, const Unit& u, float (&f)[8], float (&g)[8]) {
   float x[8], y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = elem_f32(r.a[i]), y[i] = elem_f32(r.b[i]);
-  if (VEC && u.pair && u.inter) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[i] = x[2 * i], g[i] = x[2 * i + 1];
-      f[4 + i] = y[2 * i], g[4 + i] = y[2 * i + 1];
-    }
+  if (VEC) {
+    load8(r.a, x);
+    load8(r.b, y);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = VEC || i < u.na ? x[i] : 0.0f, g[i] = VEC || i < u.nb ? y[i] : 0.0f;
+    for (int i = 0; i < 8; ++i) x[i] = i < u.na ? elem_f32(r.a[i]) : 0.0f, y[i] = i < u.nb ? elem_f32(r.b[i]) : 0.0f;
+  }
+  const bool weave = VEC && u.weave;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = weave ? x[2 * i] : x[i];
+    g[i] = weave ? x[2 * i + 1] : y[i];
+    f[4 + i] = weave ? y[2 * i] : x[4 + i];
+    g[4 + i] = weave ? y[2 * i + 1] : y[4 + i];
   }
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_unit(T* row, const Unit& u, const float (&f)[8],
-                                           const float (&g)[8]) {
+__device__ __forceinline__ void store_unit(T* row, const Unit& u, const float (&f)[8], const float (&g)[8]) {
   if (VEC) {
     if (u.na == 0) return;
-    if (u.pair && u.inter) {
-      float x[8], y[8];
+    float x[8], y[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = f[i], x[2 * i + 1] = g[i];
-        y[2 * i] = f[4 + i], y[2 * i + 1] = g[4 + i];
-      }
-      store8(row + u.a, x);
-      store8(row + u.a + 8, y);
-    } else {
-      store8(row + u.a, f);
-      store8(row + u.b, g);
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = u.weave ? f[i] : f[2 * i];
+      x[2 * i + 1] = u.weave ? g[i] : f[2 * i + 1];
+      y[2 * i] = u.weave ? f[4 + i] : g[2 * i];
+      y[2 * i + 1] = u.weave ? g[4 + i] : g[2 * i + 1];
     }
+    store8(row + u.a, x);
+    store8(row + u.b, y);
   } else {
-    const int step = u.pair && u.inter ? 2 : 1;
+    const int step = u.weave ? 2 : 1;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (i < u.na) row[u.a + i * step] = from_f32<T>(f[i]);
@@ -125,46 +135,44 @@ __device__ __forceinline__ void store_unit(T* row, const Unit& u, const float (&
 
 // f, g: codes of the first and second members.
 template <bool VEC>
-__device__ __forceinline__ void store_codes(uint8_t* row, const Unit& u, const uint8_t (&f)[8], const uint8_t (&g)[8]) {
-  uint8_t lo[8], hi[8];
-  const bool weave = u.pair && u.inter;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lo[2 * i] = weave ? f[i] : f[2 * i];
-    lo[2 * i + 1] = weave ? g[i] : f[2 * i + 1];
-    hi[2 * i] = weave ? f[4 + i] : g[2 * i];
-    hi[2 * i + 1] = weave ? g[4 + i] : g[2 * i + 1];
-  }
-  const int second = weave ? u.a + 8 : u.b;
+__device__ __forceinline__ void store_codes(uint8_t* row, const Unit& u, const uint32_t (&f)[8], const uint32_t (&g)[8]) {
   if (VEC) {
     if (u.na == 0) return;
-    uint32_t w[4];
+    uint32_t w[4];  // x: runs a, y: run b
+    const auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+      return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+    };
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      w[i] = lo[4 * i] | lo[4 * i + 1] << 8 | lo[4 * i + 2] << 16 | static_cast<uint32_t>(lo[4 * i + 3]) << 24;
-      w[2 + i] = hi[4 * i] | hi[4 * i + 1] << 8 | hi[4 * i + 2] << 16 | static_cast<uint32_t>(hi[4 * i + 3]) << 24;
+      w[i] = u.weave ? four(f[2 * i], g[2 * i], f[2 * i + 1], g[2 * i + 1])
+                     : four(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+      w[2 + i] = u.weave ? four(f[4 + 2 * i], g[4 + 2 * i], f[5 + 2 * i], g[5 + 2 * i])
+                         : four(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
     }
     *reinterpret_cast<uint2*>(row + u.a) = make_uint2(w[0], w[1]);
-    *reinterpret_cast<uint2*>(row + second) = make_uint2(w[2], w[3]);
+    *reinterpret_cast<uint2*>(row + u.b) = make_uint2(w[2], w[3]);
   } else {
-    // counts in elements of each run of 8 neighbours
-    const int n0 = weave ? min(8, 2 * u.na) : u.na;
-    const int n1 = weave ? max(0, 2 * u.na - 8) : u.nb;
+    const int step = u.weave ? 2 : 1;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (i < n0) row[u.a + i] = lo[i];
-      if (i < n1) row[second + i] = hi[i];
+      if (i < u.na) row[u.a + i * step] = static_cast<uint8_t>(f[i]);
+      if (i < u.nb) row[u.b + i * step] = static_cast<uint8_t>(g[i]);
     }
   }
 }
 
-// An element of a row bound for 8 bits, exactly: x c - y s with 64-bit (c, s).
-__device__ __noinline__ double exact_elem(float x, float y, double c, double s) {
-  return fma(static_cast<double>(x), c, -(static_cast<double>(y) * s));
+__device__ __forceinline__ float code_value(uint32_t code) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3)));
 }
-__device__ __noinline__ uint8_t exact_code(double x, float scale) {
-  const double s = scale;
-  return static_cast<uint8_t>(e4m3_pair(quotient_odd(x, s, 1.0 / s), 0.0f));
+// The code of x c - y s (64-bit c, s) over `scale`, given the two neighbouring
+// codes it lies between: on which side of their midpoint m it is, is the sign
+// of one fused multiply-add (x c - y s) - m scale; the midpoint itself goes to
+// the even code.
+__device__ __noinline__ uint32_t nearer_code(uint32_t lo, uint32_t hi, float x, float y, double c, double s, float scale) {
+  const double m = 0.5 * (static_cast<double>(code_value(lo)) + code_value(hi));
+  const double v = fma(static_cast<double>(x), c, -(static_cast<double>(y) * s));
+  const double d = fma(-m, static_cast<double>(scale), v);
+  return d > 0.0 ? hi : d < 0.0 ? lo : (hi & 1u ? lo : hi);
 }
 
 struct RotatePlan {
@@ -182,7 +190,7 @@ constexpr int kRotAngles = 1024; // most (cos, sin) pairs of a group
 
 // E4: the pool holds codes and scales.
 template <typename T, bool E4, bool VEC>
-__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_constant__ RotateParams p,
+__global__ void __launch_bounds__(kRotThreads, E4 || !VEC ? 2 : 4) rotate_kernel(const __grid_constant__ RotateParams p,
                                                              const __grid_constant__ RotatePlan n) {
   dep_enter();
   constexpr int kUnits = sizeof(T) == 4 ? 2 : 4;  // units a thread has in flight
@@ -211,7 +219,7 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_consta
         const int b = quotient(t, n.div_N), j = t - b * p.N;
         const int kind = r < p.Hq ? 0 : r < p.Hq + p.c.heads ? 1 : 2;
         const int h = kind == 0 ? r : kind == 1 ? r - p.Hq : r - p.Hq - p.c.heads;
-        const Unit u = unit_at(lane, turn && kind < 2, p.rd, p.D, p.interleaved != 0);
+        const Unit u = unit_at<VEC>(lane, turn && kind < 2, p.rd, p.D, p.interleaved != 0);
         const RowsView& src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
         load_raw<T, VEC>(static_cast<const T*>(src.p) + b * src.sb + j * src.sn + h * src.sh, u, raw[i]);
       }
@@ -283,8 +291,8 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_consta
         const long long at = k < group ? dst[k] : -2;
         const bool live = k < group && (kind == 0 ? at != -2 : at >= 0);
         const bool turned = turn && kind < 2;
-        const Unit u = unit_at(lane, turned, p.rd, p.D, p.interleaved != 0);
-        const int first = k * half_rd + 8 * lane;  // this unit's angles
+        const Unit u = unit_at<VEC>(lane, turned, p.rd, p.D, p.interleaved != 0);
+        const auto angle = [&](int z) { return k * half_rd + angle_of<VEC>(z, lane, p.rd, u.weave); };
         float f[8] = {}, g[8] = {};
         if (live && u.na > 0) unpack_raw<T, VEC>(raw[i], u, f, g);
         const bool pair = u.pair && turned;
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_consta
 #pragma unroll
             for (int z = 0; z < 8; ++z) {
               if (VEC || z < u.na) {
-                const float2 w = cs[first + z];
+                const float2 w = cs[angle(z)];
                 const float x = f[z], y = g[z];
                 f[z] = fmaf(x, w.x, -y * w.y);
                 g[z] = fmaf(y, w.x, x * w.y);
@@ -314,49 +322,59 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_consta
 #pragma unroll
           for (int z = 0; z < 8; ++z) {
             x[z] = f[z], y[z] = g[z], e[z] = 0.0f;
-            odd |= !isfinite(f[z]) || !isfinite(g[z]);
+            odd |= !(fabsf(f[z]) < INFINITY) | !(fabsf(g[z]) < INFINITY);
             if (pair && (VEC || z < u.na)) {
-              const float2 w = cs[first + z];
+              const float2 w = cs[angle(z)];
               x[z] = fmaf(f[z], w.x, -g[z] * w.y);
               y[z] = fmaf(g[z], w.x, f[z] * w.y);
               e[z] = (fabsf(f[z]) + fabsf(g[z])) * (fabsf(p.magnitude) * 0x1p-20f);
             }
-            top = fmaxf(top, fmaxf(fabsf(x[z]), fabsf(y[z])));
+            top = fmax3(top, fabsf(x[z]), fabsf(y[z]));
             slack = fmaxf(slack, e[z]);
           }
-          if (kind == 0) top = 0.0f, slack = 0.0f, odd = false;
           for (int o = n.UP >> 1; o > 0; o >>= 1) {
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             slack = fmaxf(slack, __shfl_xor_sync(0xffffffffu, slack, o));
             odd |= __shfl_xor_sync(0xffffffffu, static_cast<int>(odd), o) != 0;
           }
-          double most = 0.0;
-          const float near = top - 2.0f * slack;
+          float scale;
+          if (__any_sync(0xffffffffu, turned && kind == 1)) {
+            double most = top;
+            if (turned) {
+              most = 0.0;
+              const float near = top - 2.0f * slack;
 #pragma unroll
-          for (int z = 0; z < 8; ++z) {
-            const double2 w = pair && (VEC || z < u.na) ? csd[E4 ? first + z : 0] : make_double2(1.0, 0.0);
-            if (fabsf(x[z]) >= near) most = fmax(most, fabs(exact_elem(f[z], g[z], w.x, w.y)));
-            if (fabsf(y[z]) >= near) most = fmax(most, fabs(exact_elem(g[z], f[z], w.x, -w.y)));
+              for (int z = 0; z < 8; ++z) {
+                if (fabsf(x[z]) >= near || fabsf(y[z]) >= near) {
+                  const double2 w = pair && (VEC || z < u.na) ? csd[E4 ? angle(z) : 0] : make_double2(1.0, 0.0);
+                  const double a = f[z], d = g[z];
+                  most = fmax(most, fmax(fabs(fma(a, w.x, -(d * w.y))), fabs(fma(d, w.x, a * w.y))));
+                }
+              }
+            }
+            for (int o = n.UP >> 1; o > 0; o >>= 1) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, o));
+            scale = static_cast<float>(most / 448.0);
+          } else {
+            scale = __fdiv_rn(top, 448.0f);
           }
-          for (int o = n.UP >> 1; o > 0; o >>= 1) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, o));
+          if (odd || !(scale < INFINITY)) scale = __int_as_float(0x7fc00000);
           if (live && kind != 0) {
-            float scale = static_cast<float>(most / 448.0);
-            if (odd || !isfinite(scale)) scale = __int_as_float(0x7fc00000);
-            // tiny scales have no 32-bit reciprocal: all such codes are exact ones
-            const bool fine = scale > 0x1p-100f;
-            const float inv = fine ? 1.0f / scale : 0.0f;
-            uint8_t cx[8], cy[8];
+            // (tiny scales have no 32-bit reciprocal; they are multiplied up with the row)
+            const float up = scale < 0x1p-100f ? 0x1p80f : 1.0f;
+            const float inv = scale > 0.0f ? 1.0f / (scale * up) : 0.0f;
+            uint32_t cx[8], cy[8];
 #pragma unroll
             for (int z = 0; z < 8; ++z) {
-              const float qx = x[z] * inv, qy = y[z] * inv;
-              const float dx = fmaf(fabsf(qx), 0x1p-21f, e[z] * inv), dy = fmaf(fabsf(qy), 0x1p-21f, e[z] * inv);
+              const float qx = x[z] * up * inv, qy = y[z] * up * inv;
+              const float ez = e[z] * up * inv;
+              const float dx = fmaf(fabsf(qx), 0x1p-21f, ez), dy = fmaf(fabsf(qy), 0x1p-21f, ez);
               const uint32_t wx = e4m3_pair(qx - dx, qx + dx), wy = e4m3_pair(qy - dy, qy + dy);
-              cx[z] = static_cast<uint8_t>(wx), cy[z] = static_cast<uint8_t>(wy);
-              const bool sure_x = fine && (wx & 0xffu) == (wx >> 8), sure_y = fine && (wy & 0xffu) == (wy >> 8);
-              if (!(sure_x && sure_y)) {
-                const double2 w = pair && (VEC || z < u.na) ? csd[E4 ? first + z : 0] : make_double2(1.0, 0.0);
-                if (!sure_x) cx[z] = scale == 0.0f ? 0 : exact_code(exact_elem(f[z], g[z], w.x, w.y), scale);
-                if (!sure_y) cy[z] = scale == 0.0f ? 0 : exact_code(exact_elem(g[z], f[z], w.x, -w.y), scale);
+              cx[z] = wx & 0xffu, cy[z] = wy & 0xffu;
+              const bool both = cx[z] == wx >> 8 && cy[z] == wy >> 8;
+              if (!both) {
+                const double2 w = pair && (VEC || z < u.na) ? csd[E4 ? angle(z) : 0] : make_double2(1.0, 0.0);
+                if (cx[z] != wx >> 8) cx[z] = nearer_code(cx[z], wx >> 8, f[z], g[z], w.x, w.y, scale);
+                if (cy[z] != wy >> 8) cy[z] = nearer_code(cy[z], wy >> 8, g[z], f[z], w.x, -w.y, scale);
               }
             }
             store_codes<VEC>(static_cast<uint8_t*>(kind == 1 ? p.c.k : p.c.v) + at + h * p.c.head_stride, u, cx, cy);
@@ -394,7 +412,7 @@ static cudaError_t launch_rotate_t(const RotateParams& p, bool e4, bool vec, int
   n.div_N = make_udiv(static_cast<unsigned int>(p.N));
   n.div_half = make_udiv(static_cast<unsigned int>(p.rd > 0 ? p.rd / 2 : 1));
   const long long blocks = (p.tokens + n.group - 1) / n.group;
-  const long long grid = static_cast<long long>(sms) * 8;
+  const long long grid = static_cast<long long>(sms) * (e4 || !vec ? 2 : 4);  // the blocks that fit at once
   void (*k)(const RotateParams, const RotatePlan) =
       e4 ? (vec ? rotate_kernel<T, true, true> : rotate_kernel<T, true, false>)
          : (vec ? rotate_kernel<T, false, true> : rotate_kernel<T, false, false>);

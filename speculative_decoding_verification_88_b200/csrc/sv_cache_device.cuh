@@ -119,18 +119,7 @@ __device__ __forceinline__ void store8(__half* p, const float (&f)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// x / s rounded to the nearest e4m3 value as if in exact arithmetic: the
-// quotient in 64 bits (with inv = 1/s rounded; the remainder step makes it
-// the correctly rounded one, so exact ties stay ties: Markstein, "Computation
-// of elementary functions on the IBM RISC System/6000 processor", 1990), then
-// to 32 bits rounding to odd, which the final rounding to 4 significant bits
-// cannot tell from the exact value (Boldo and Melquiond, 2008).
-__device__ __forceinline__ float quotient_odd(double x, double s, double inv) {
-  const double q0 = x * inv;
-  const double q = fma(fma(-q0, s, x), inv, q0);
-  const float f = __double2float_rz(q);
-  return static_cast<double>(f) == q ? f : __uint_as_float(__float_as_uint(f) | 1u);
-}
+// Two e4m3 codes, rounded to nearest, ties to even, saturating.
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
