@@ -2,6 +2,8 @@
 // 8 bits with one scale a row), its read-back and the move of accepted rows.
 // All four move data once and are bound by memory, or, for a few tokens, by
 // one launch's latency.
+#include <type_traits>
+
 #include "sv_cache_device.cuh"
 
 namespace sv {
@@ -175,249 +177,351 @@ __device__ __noinline__ uint32_t nearer_code(uint32_t lo, uint32_t hi, float x, 
   return d > 0.0 ? hi : d < 0.0 ? lo : (hi & 1u ? lo : hi);
 }
 
+// The same where the element is held exactly (not turned), in 32 bits; both
+// codes as a pair.  (Products of normal size only: the sum must not underflow.)
+__device__ __forceinline__ uint32_t nearer_code(uint32_t pair, float x, float scale) {
+  const uint32_t lo = pair & 0xffu, hi = pair >> 8 & 0xffu;
+  const float d = fmaf(-0.5f * (code_value(lo) + code_value(hi)), scale, x);
+  return d > 0.0f ? hi : d < 0.0f ? lo : (hi & 1u ? lo : hi);
+}
+
 struct RotatePlan {
   int UP;         // lanes of a row (8-bit pools: a power of two, for the row's reduction)
-  int group;      // tokens a block takes at a time
-  int per_token;  // units of a token: rows * UP
-  UDiv div_token, div_up, div_N, div_half;  // / per_token, / UP, / N, / (rd / 2)
+  int units;      // of them in use
+  int rows;       // rows a block takes at a time
+  int passes;     // until a token's rows are done
+  int group;      // tokens whose angles a block prepares together
+  UDiv div_N, div_half;  // / N, / (rd / 2)
 };
 __device__ __forceinline__ int quotient(int n, const UDiv& d) {
   return d.m == 0u ? n : static_cast<int>(__umulhi(static_cast<unsigned int>(n), d.m) >> d.shift);
 }
 
-constexpr int kRotGroup = 16;    // most tokens a block takes at a time
-constexpr int kRotAngles = 1024; // most (cos, sin) pairs of a group
+constexpr int kRotGroup = 4;      // most tokens of a group
+constexpr int kRotAngles = 1024;  // their (cos, sin) pairs: rotary_dim <= 512
 
-// E4: the pool holds codes and scales.
-template <typename T, bool E4, bool VEC>
-__global__ void __launch_bounds__(kRotThreads, E4 || !VEC ? 2 : 4) rotate_kernel(const __grid_constant__ RotateParams p,
-                                                             const __grid_constant__ RotatePlan n) {
+// Places (dst: element offset, -1: none, -2: padding; sdst: the scales') and
+// (cos, sin) of a group of tokens.
+template <bool E4>
+__device__ __forceinline__ void prepare_tokens(const RotateParams& p, const RotatePlan& n, long long t0, int group, float2* cs,
+                                               double2* csd, long long* dst, long long* sdst, long long* pos) {
+  const int tid = threadIdx.x, half_rd = p.rd / 2;
+  __syncthreads();  // the last group's are done with
+  if (tid < group) {
+    const int t = static_cast<int>(t0) + tid;
+    const int b = quotient(t, n.div_N), j = t - b * p.N;
+    long long at = -1, sat = 0, where = 0;
+    if (p.count && j >= __ldg(p.count + b)) {
+      at = -2;
+    } else if (p.positions) {
+      where = __ldg(p.positions + t);
+    } else {
+      int depth = j;
+      if (p.parent) {
+        const int* par = p.parent + static_cast<long long>(b) * p.N;
+        depth = 0;
+        for (int x = j; x > 0; ++depth) {  // parents decrease, so this ends
+          const int up = __ldg(par + x);
+          if (up < 0 || up >= x) {
+            raise_flag(p.ctrl, kFlagInvalidTree);
+            break;
+          }
+          x = up;
+        }
+      }
+      const long long len = max(0, __ldg(p.cache_len + b));
+      where = len + depth;
+      int page, place;
+      if (p.write && find_place(p.c, b, len + j, page, place, p.ctrl)) {
+        at = page * p.c.page_stride + place * p.c.token_stride;
+        sat = static_cast<long long>(page) * p.c.heads * p.c.page_size + place;
+      }
+    }
+    dst[tid] = at;
+    sdst[tid] = sat;
+    pos[tid] = where;
+  }
+  __syncthreads();
+  if (!p.inv_freq) return;
+  for (int i = tid; i < group * half_rd; i += blockDim.x) {
+    const int k = quotient(i, n.div_half), f = i - k * half_rd;
+    const double turns = static_cast<double>(pos[k]) * __ldg(p.inv_freq + f) * 0.15915494309189533577;
+    const double half = 2.0 * (turns - rint(turns));
+    float s, c;
+    sincospif(static_cast<float>(half), &s, &c);
+    s = p.inverse ? -s : s;
+    cs[i] = make_float2(c * p.magnitude, s * p.magnitude);
+    if (E4) {
+      double sd, cd;
+      sincospi(half, &sd, &cd);
+      csd[i] = make_double2(cd * p.magnitude, sd * p.magnitude);
+    }
+  }
+  __syncthreads();
+}
+
+// The (cos, sin) of a unit's eight pairs: two runs of four.
+template <bool VEC>
+__device__ __forceinline__ void load_angles(const float2* run0, const float2* run1, int n, float2 (&w)[8]) {
+  if (VEC) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 x = reinterpret_cast<const float4*>(run0)[i], y = reinterpret_cast<const float4*>(run1)[i];
+      w[2 * i] = make_float2(x.x, x.y), w[2 * i + 1] = make_float2(x.z, x.w);
+      w[4 + 2 * i] = make_float2(y.x, y.y), w[5 + 2 * i] = make_float2(y.z, y.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) w[i] = i < 4 ? run0[i] : run1[i - 4];
+  }
+}
+
+// Turns a unit in 32 bits.
+template <bool VEC>
+__device__ __forceinline__ void turn_unit(const Unit& u, const float2 (&w)[8], float (&f)[8], float (&g)[8]) {
+#pragma unroll
+  for (int z = 0; z < 8; ++z) {
+    if (VEC || z < u.na) {
+      const float x = f[z], y = g[z];
+      f[z] = fmaf(x, w[z].x, -y * w[z].y);
+      g[z] = fmaf(y, w[z].x, x * w[z].y);
+    }
+  }
+}
+
+// A unit of a row bound for 8 bits: codes, and the scale from the row's first
+// lane.  All lanes of the row take part (live: whether this one stores).
+// f, g: the elements as read; pair: they are to be turned.
+template <bool VEC>
+__device__ __forceinline__ void code_unit(const Unit& u, int UP, bool first_lane, bool live, bool pair, bool turned_row,
+                                          float magnitude, const float2 (&w)[8], const double2* cd0, const double2* cd1,
+                                          uint8_t* out, float* scale_out, const float (&f)[8], const float (&g)[8]) {
+  // e: a bound of the 32-bit error of both members of a pair (angle and
+  // functions, two products, a sum: under 8 roundings of each term).
+  float x[8], y[8], e[8];
+  float top = 0.0f, slack = 0.0f;
+  bool odd = false;  // an infinity or a NaN
+#pragma unroll
+  for (int z = 0; z < 8; ++z) {
+    x[z] = f[z], y[z] = g[z], e[z] = 0.0f;
+    odd |= !(fabsf(f[z]) + fabsf(g[z]) < INFINITY);
+  }
+  if (pair) {
+    turn_unit<VEC>(u, w, x, y);
+#pragma unroll
+    for (int z = 0; z < 8; ++z) {
+      if (VEC || z < u.na) e[z] = (fabsf(f[z]) + fabsf(g[z])) * (fabsf(magnitude) * 0x1p-20f);
+    }
+  }
+#pragma unroll
+  for (int z = 0; z < 8; ++z) {
+    top = fmax3(top, fabsf(x[z]), fabsf(y[z]));
+    slack = fmaxf(slack, e[z]);
+  }
+  // (the sum above may overflow where neither element is odd)
+  if (odd) {
+    odd = false;
+#pragma unroll
+    for (int z = 0; z < 8; ++z) odd |= !(fabsf(f[z]) < INFINITY) | !(fabsf(g[z]) < INFINITY);
+  }
+  for (int o = UP >> 1; o > 0; o >>= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    odd |= __shfl_xor_sync(0xffffffffu, static_cast<int>(odd), o) != 0;
+  }
+  const auto exact = [&](int z) {
+    return pair && (VEC || z < u.na) ? (z < 4 ? cd0[z] : cd1[z - 4]) : make_double2(1.0, 0.0);
+  };
+  float scale;
+  if (__any_sync(0xffffffffu, turned_row)) {
+    for (int o = UP >> 1; o > 0; o >>= 1) slack = fmaxf(slack, __shfl_xor_sync(0xffffffffu, slack, o));
+    double most = 0.0;
+    const float near = top - 2.0f * slack;
+#pragma unroll
+    for (int z = 0; z < 8; ++z) {
+      if (fabsf(x[z]) >= near || fabsf(y[z]) >= near) {
+        const double2 d = exact(z);
+        const double a = f[z], b = g[z];
+        most = fmax(most, fmax(fabs(fma(a, d.x, -(b * d.y))), fabs(fma(b, d.x, a * d.y))));
+      }
+    }
+    for (int o = UP >> 1; o > 0; o >>= 1) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, o));
+    scale = static_cast<float>(most / 448.0);
+  } else {
+    scale = __fdiv_rn(top, 448.0f);
+  }
+  if (odd || !(scale < INFINITY)) scale = __int_as_float(0x7fc00000);
+  if (!live) return;
+  float inv = scale > 0.0f ? 1.0f / scale : 0.0f;
+  if (scale < 0x1p-100f && scale > 0.0f) {  // the reciprocal may be out of range
+    inv = 1.0f / (scale * 0x1p80f);
+#pragma unroll
+    for (int z = 0; z < 8; ++z) x[z] *= 0x1p80f, y[z] *= 0x1p80f, e[z] *= 0x1p80f;
+  }
+  uint32_t cx[8], cy[8];
+#pragma unroll
+  for (int z = 0; z < 8; ++z) {
+    const float qx = x[z] * inv, qy = y[z] * inv, ez = e[z] * inv;
+    const float dx = fmaf(fabsf(qx), 0x1p-21f, ez), dy = fmaf(fabsf(qy), 0x1p-21f, ez);
+    cx[z] = e4m3_pair(qx - dx, qx + dx);
+    cy[z] = e4m3_pair(qy - dy, qy + dy);
+    if (((cx[z] ^ cx[z] >> 8) | (cy[z] ^ cy[z] >> 8)) & 0xffu) {
+      if (pair || scale < 0x1p-60f) {
+        const double2 d = exact(z);
+        if ((cx[z] ^ cx[z] >> 8) & 0xffu) cx[z] = nearer_code(cx[z] & 0xffu, cx[z] >> 8, f[z], g[z], d.x, d.y, scale);
+        if ((cy[z] ^ cy[z] >> 8) & 0xffu) cy[z] = nearer_code(cy[z] & 0xffu, cy[z] >> 8, g[z], f[z], d.x, -d.y, scale);
+      } else {
+        cx[z] = nearer_code(cx[z], f[z], scale);
+        cy[z] = nearer_code(cy[z], g[z], scale);
+      }
+    }
+  }
+  store_codes<VEC>(out, u, cx, cy);
+  if (first_lane) *scale_out = scale;
+}
+
+// A thread keeps its lane of the row and goes through rows (passes) and
+// tokens; four rows' loads are in flight before the first is turned.
+// WRITE: k and v rows as well, into the pool; E4: in 8 bits.
+template <typename T, bool WRITE, bool E4, bool VEC, bool INTER>
+__global__ void __launch_bounds__(kRotThreads, E4 || !VEC ? 2 : 4)
+    rotate_kernel(const __grid_constant__ RotateParams p, const __grid_constant__ RotatePlan n) {
   dep_enter();
-  constexpr int kUnits = sizeof(T) == 4 ? 2 : 4;  // units a thread has in flight
-  __shared__ float2 cs[kRotAngles];
-  __shared__ double2 csd[E4 ? kRotAngles : 1];
-  __shared__ long long dst[kRotGroup];  // element offset of the token's place; -1: none, -2: padding
-  __shared__ long long sdst[kRotGroup]; // its scales
-  __shared__ int depth_of[kRotGroup];
+  constexpr int kAhead = sizeof(T) == 4 || !VEC ? 2 : 4;
+  __shared__ __align__(16) float2 cs[kRotAngles];
+  __shared__ __align__(16) double2 csd[E4 ? kRotAngles : 1];
+  __shared__ long long dst[kRotGroup], sdst[kRotGroup], pos[kRotGroup];
   const int tid = threadIdx.x;
   const bool turn = p.inv_freq != nullptr;
   const int half_rd = p.rd / 2;
-  const int units = n.group * n.per_token;
+  const int slot = tid / n.UP, lane = tid - slot * n.UP;
+  const Unit turned = unit_at<VEC>(lane, turn, p.rd, p.D, INTER), plain = unit_at<VEC>(lane, false, 0, p.D, false);
+  const int a0 = angle_of<VEC>(0, lane, p.rd, turned.weave), a1 = angle_of<VEC>(4, lane, p.rd, turned.weave);
+  const int rows = p.Hq + (WRITE ? 2 * p.c.heads : 0);
   for (long long t0 = static_cast<long long>(blockIdx.x) * n.group; t0 < p.tokens;
        t0 += static_cast<long long>(gridDim.x) * n.group) {
     const int group = static_cast<int>(min(static_cast<long long>(n.group), p.tokens - t0));
-    for (int base = 0; base < units; base += kRotThreads * kUnits) {
-      Raw<T> raw[kUnits];
-      // ---- loads
+    prepare_tokens<E4>(p, n, t0, group, cs, csd, dst, sdst, pos);
+    int k = 0, pass = 0;  // next row to load, and its token's places in q, k and v
+    int b = quotient(static_cast<int>(t0), n.div_N), j = static_cast<int>(t0) - b * p.N;
+    const T *q_at = nullptr, *k_at = nullptr, *v_at = nullptr;
+    const int all = group * n.passes;
+#pragma unroll 1
+    for (int it = 0; it < all; it += kAhead) {
+      Raw<T> raw[kAhead];
+      int ks[kAhead], rs[kAhead];
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int id = base + tid + kRotThreads * i;
-        const int k = quotient(id, n.div_token), rem = id - k * n.per_token;
-        const int r = quotient(rem, n.div_up), lane = rem - r * n.UP;
-        if (k >= group) continue;
-        const int t = static_cast<int>(t0) + k;
-        const int b = quotient(t, n.div_N), j = t - b * p.N;
-        const int kind = r < p.Hq ? 0 : r < p.Hq + p.c.heads ? 1 : 2;
-        const int h = kind == 0 ? r : kind == 1 ? r - p.Hq : r - p.Hq - p.c.heads;
-        const Unit u = unit_at<VEC>(lane, turn && kind < 2, p.rd, p.D, p.interleaved != 0);
-        const RowsView& src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-        load_raw<T, VEC>(static_cast<const T*>(src.p) + b * src.sb + j * src.sn + h * src.sh, u, raw[i]);
-      }
-      // ---- places and angles
-      if (base == 0) {
-        if (tid < group) {
-          const int t = static_cast<int>(t0) + tid;
-          const int b = quotient(t, n.div_N), j = t - b * p.N;
-          long long at = -1, sat = 0;
-          int depth = j;
-          if (p.count && j >= __ldg(p.count + b)) {
-            at = -2;
-          } else if (!p.positions) {
-            if (p.parent) {
-              const int* par = p.parent + static_cast<long long>(b) * p.N;
-              depth = 0;
-              for (int x = j; x > 0; ++depth) {  // parents decrease, so this ends
-                const int up = __ldg(par + x);
-                if (up < 0 || up >= x) {
-                  raise_flag(p.ctrl, kFlagInvalidTree);
-                  break;
-                }
-                x = up;
-              }
-            }
-            int page, place;
-            if (p.write && find_place(p.c, b, max(0, __ldg(p.cache_len + b)) + static_cast<long long>(j), page, place,
-                                      p.ctrl)) {
-              at = page * p.c.page_stride + place * p.c.token_stride;
-              sat = static_cast<long long>(page) * p.c.heads * p.c.page_size + place;
-            }
+      for (int z = 0; z < kAhead; ++z) {
+        if (pass == 0 && it + z < all) {
+          q_at = static_cast<const T*>(p.q.p) + b * p.q.sb + j * p.q.sn;
+          if (WRITE) {
+            k_at = static_cast<const T*>(p.k.p) + b * p.k.sb + j * p.k.sn;
+            v_at = static_cast<const T*>(p.v.p) + b * p.v.sb + j * p.v.sn;
           }
-          dst[tid] = at;
-          sdst[tid] = sat;
-          depth_of[tid] = depth;
         }
-        __syncthreads();
-        if (turn) {
-          for (int i = tid; i < group * half_rd; i += kRotThreads) {
-            const int k = quotient(i, n.div_half), f = i - k * half_rd;
-            const int t = static_cast<int>(t0) + k;
-            const long long pos = p.positions ? __ldg(p.positions + t)
-                                              : max(0, __ldg(p.cache_len + quotient(t, n.div_N))) +
-                                                    static_cast<long long>(depth_of[k]);
-            const double turns = static_cast<double>(pos) * __ldg(p.inv_freq + f) * 0.15915494309189533577;
-            const double half = 2.0 * (turns - rint(turns));
-            float s, c;
-            sincospif(static_cast<float>(half), &s, &c);
-            s = p.inverse ? -s : s;
-            cs[i] = make_float2(c * p.magnitude, s * p.magnitude);
+        const int r = pass * n.rows + slot;
+        const bool in = it + z < all && slot < n.rows && r < rows;
+        ks[z] = k;
+        rs[z] = in ? r : -1;
+        if (in) {
+          if (!WRITE || r < p.Hq)
+            load_raw<T, VEC>(q_at + r * p.q.sh, turned, raw[z]);
+          else if (r < p.Hq + p.c.heads)
+            load_raw<T, VEC>(k_at + (r - p.Hq) * p.k.sh, turned, raw[z]);
+          else
+            load_raw<T, VEC>(v_at + (r - p.Hq - p.c.heads) * p.v.sh, plain, raw[z]);
+        }
+        if (++pass == n.passes) {
+          pass = 0;
+          ++k;
+          if (++j == p.N) {
+            j = 0;
+            ++b;
+          }
+        }
+      }
+#pragma unroll
+      for (int z = 0; z < kAhead; ++z) {
+        if (it + z >= all) continue;
+        const int r = rs[z];
+        const long long at = dst[ks[z]];
+        const int base = ks[z] * half_rd;
+        float f[8], g[8];
+        float2 w[8];
+        if (!WRITE || r < p.Hq) {
+          if (r >= 0 && at != -2 && turned.na > 0) {
+            unpack_raw<T, VEC>(raw[z], turned, f, g);
+            if (turned.pair) {
+              load_angles<VEC>(cs + base + a0, cs + base + a1, turned.na, w);
+              turn_unit<VEC>(turned, w, f, g);
+            }
+            store_unit<T, VEC>(static_cast<T*>(p.q_out) + (t0 + ks[z]) * p.qo_st + r * p.qo_sh, turned, f, g);
+          }
+        }
+        if (WRITE) {
+          const bool mine = r >= p.Hq, key = mine && r < p.Hq + p.c.heads;
+          const int h = r - p.Hq - (key ? 0 : p.c.heads);
+          const Unit& u = key ? turned : plain;
+          const bool live = mine && at >= 0;
+          const bool pair = key && turned.pair;
+          if (E4 ? __any_sync(0xffffffffu, live) : live && u.na > 0) {
             if (E4) {
-              double sd, cd;
-              sincospi(half, &sd, &cd);
-              csd[i] = make_double2(cd * p.magnitude, sd * p.magnitude);
-            }
-          }
-          __syncthreads();
-        }
-      }
-      // ---- turn and store
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int id = base + tid + kRotThreads * i;
-        if (!E4 && id >= units) continue;
-        const int k = quotient(id, n.div_token), rem = id - k * n.per_token;
-        const int r = quotient(rem, n.div_up), lane = rem - r * n.UP;
-        const int kind = r < p.Hq ? 0 : r < p.Hq + p.c.heads ? 1 : 2;
-        const int h = kind == 0 ? r : kind == 1 ? r - p.Hq : r - p.Hq - p.c.heads;
-        const long long at = k < group ? dst[k] : -2;
-        const bool live = k < group && (kind == 0 ? at != -2 : at >= 0);
-        const bool turned = turn && kind < 2;
-        const Unit u = unit_at<VEC>(lane, turned, p.rd, p.D, p.interleaved != 0);
-        const auto angle = [&](int z) { return k * half_rd + angle_of<VEC>(z, lane, p.rd, u.weave); };
-        float f[8] = {}, g[8] = {};
-        if (live && u.na > 0) unpack_raw<T, VEC>(raw[i], u, f, g);
-        const bool pair = u.pair && turned;
-        if ((!E4 || kind == 0) && live) {
-          if (pair) {
-#pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              if (VEC || z < u.na) {
-                const float2 w = cs[angle(z)];
-                const float x = f[z], y = g[z];
-                f[z] = fmaf(x, w.x, -y * w.y);
-                g[z] = fmaf(y, w.x, x * w.y);
-              }
+              for (int i = 0; i < 8; ++i) f[i] = g[i] = 0.0f;
             }
-          }
-          T* out = kind == 0 ? static_cast<T*>(p.q_out) + (t0 + k) * p.qo_st + h * p.qo_sh
-                             : static_cast<T*>(kind == 1 ? p.c.k : p.c.v) + at + h * p.c.head_stride;
-          store_unit<T, VEC>(out, u, f, g);
-        }
-        if (E4 && __any_sync(0xffffffffu, live && kind != 0)) {
-          // Every lane takes part in the row's reductions.  e: a bound of the
-          // 32-bit error of both members of a pair (angle and functions, two
-          // products, a sum: under 8 roundings of each term).
-          float x[8], y[8], e[8];
-          float top = 0.0f, slack = 0.0f;
-          bool odd = false;  // an infinity or a NaN
-#pragma unroll
-          for (int z = 0; z < 8; ++z) {
-            x[z] = f[z], y[z] = g[z], e[z] = 0.0f;
-            odd |= !(fabsf(f[z]) < INFINITY) | !(fabsf(g[z]) < INFINITY);
-            if (pair && (VEC || z < u.na)) {
-              const float2 w = cs[angle(z)];
-              x[z] = fmaf(f[z], w.x, -g[z] * w.y);
-              y[z] = fmaf(g[z], w.x, f[z] * w.y);
-              e[z] = (fabsf(f[z]) + fabsf(g[z])) * (fabsf(p.magnitude) * 0x1p-20f);
+            if (live && u.na > 0) unpack_raw<T, VEC>(raw[z], u, f, g);
+            if (pair) load_angles<VEC>(cs + base + a0, cs + base + a1, u.na, w);
+            if (E4) {
+              code_unit<VEC>(u, n.UP, lane == 0, live, pair, key && turn, p.magnitude, w, csd + (E4 ? base + a0 : 0),
+                             csd + (E4 ? base + a1 : 0),
+                             static_cast<uint8_t*>(key ? p.c.k : p.c.v) + at + h * p.c.head_stride,
+                             (key ? p.c.ks : p.c.vs) + sdst[ks[z]] + static_cast<long long>(h) * p.c.page_size, f, g);
+            } else {
+              if (pair) turn_unit<VEC>(u, w, f, g);
+              store_unit<T, VEC>(static_cast<T*>(key ? p.c.k : p.c.v) + at + h * p.c.head_stride, u, f, g);
             }
-            top = fmax3(top, fabsf(x[z]), fabsf(y[z]));
-            slack = fmaxf(slack, e[z]);
-          }
-          for (int o = n.UP >> 1; o > 0; o >>= 1) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            slack = fmaxf(slack, __shfl_xor_sync(0xffffffffu, slack, o));
-            odd |= __shfl_xor_sync(0xffffffffu, static_cast<int>(odd), o) != 0;
-          }
-          float scale;
-          if (__any_sync(0xffffffffu, turned && kind == 1)) {
-            double most = top;
-            if (turned) {
-              most = 0.0;
-              const float near = top - 2.0f * slack;
-#pragma unroll
-              for (int z = 0; z < 8; ++z) {
-                if (fabsf(x[z]) >= near || fabsf(y[z]) >= near) {
-                  const double2 w = pair && (VEC || z < u.na) ? csd[E4 ? angle(z) : 0] : make_double2(1.0, 0.0);
-                  const double a = f[z], d = g[z];
-                  most = fmax(most, fmax(fabs(fma(a, w.x, -(d * w.y))), fabs(fma(d, w.x, a * w.y))));
-                }
-              }
-            }
-            for (int o = n.UP >> 1; o > 0; o >>= 1) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, o));
-            scale = static_cast<float>(most / 448.0);
-          } else {
-            scale = __fdiv_rn(top, 448.0f);
-          }
-          if (odd || !(scale < INFINITY)) scale = __int_as_float(0x7fc00000);
-          if (live && kind != 0) {
-            // (tiny scales have no 32-bit reciprocal; they are multiplied up with the row)
-            const float up = scale < 0x1p-100f ? 0x1p80f : 1.0f;
-            const float inv = scale > 0.0f ? 1.0f / (scale * up) : 0.0f;
-            uint32_t cx[8], cy[8];
-#pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              const float qx = x[z] * up * inv, qy = y[z] * up * inv;
-              const float ez = e[z] * up * inv;
-              const float dx = fmaf(fabsf(qx), 0x1p-21f, ez), dy = fmaf(fabsf(qy), 0x1p-21f, ez);
-              const uint32_t wx = e4m3_pair(qx - dx, qx + dx), wy = e4m3_pair(qy - dy, qy + dy);
-              cx[z] = wx & 0xffu, cy[z] = wy & 0xffu;
-              const bool both = cx[z] == wx >> 8 && cy[z] == wy >> 8;
-              if (!both) {
-                const double2 w = pair && (VEC || z < u.na) ? csd[E4 ? angle(z) : 0] : make_double2(1.0, 0.0);
-                if (cx[z] != wx >> 8) cx[z] = nearer_code(cx[z], wx >> 8, f[z], g[z], w.x, w.y, scale);
-                if (cy[z] != wy >> 8) cy[z] = nearer_code(cy[z], wy >> 8, g[z], f[z], w.x, -w.y, scale);
-              }
-            }
-            store_codes<VEC>(static_cast<uint8_t*>(kind == 1 ? p.c.k : p.c.v) + at + h * p.c.head_stride, u, cx, cy);
-            if (lane == 0)
-              (kind == 1 ? p.c.ks : p.c.vs)[sdst[k] + static_cast<long long>(h) * p.c.page_size] = scale;
           }
         }
       }
     }
-    __syncthreads();  // the angles and places may be overwritten now
   }
 }
 
 template <typename T>
 static cudaError_t launch_rotate_t(const RotateParams& p, bool e4, bool vec, int sms, cudaStream_t st) {
-  const int np = p.inv_freq ? (p.rd / 2 + 7) / 8 + (p.D - p.rd + 15) / 16 : 0;
-  int units = p.write || !p.inv_freq ? (p.D + 15) / 16 : 0;
-  if (np > units) units = np;
   RotatePlan n{};
-  n.UP = units;
+  const int np = p.inv_freq ? (p.rd / 2 + 7) / 8 + (p.D - p.rd + 15) / 16 : 0;
+  n.units = p.write || !p.inv_freq ? (p.D + 15) / 16 : 0;
+  if (np > n.units) n.units = np;
+  n.UP = n.units;
   if (e4)
-    for (n.UP = 1; n.UP < units;) n.UP <<= 1;
+    for (n.UP = 1; n.UP < n.units;) n.UP <<= 1;
+  // As few passes as the block's size allows, with as few idle threads.
   const int rows = p.Hq + (p.write ? 2 * p.c.heads : 0);
-  n.per_token = rows * n.UP;
-  // Tokens together until every thread has its units (more would only delay
-  // the first stores), unless that leaves SMs without a block.
-  const int most = kRotThreads * (sizeof(T) == 4 ? 2 : 4);
-  n.group = most / n.per_token;
+  n.passes = (rows * n.UP + kRotThreads - 1) / kRotThreads;
+  if (n.passes * (kRotThreads / n.UP) < rows) ++n.passes;
+  n.rows = (rows + n.passes - 1) / n.passes;
+  const int threads = (n.rows * n.UP + 31) / 32 * 32;
+  // blocks that fit at once (64 registers a thread, 128 for the larger forms)
+  const long long fit = static_cast<long long>(sms) * ((e4 || !vec ? 512 : 1024) / threads);
+  n.group = kRotGroup;
   if (p.rd > 0 && n.group > kRotAngles / (p.rd / 2)) n.group = kRotAngles / (p.rd / 2);
-  if (n.group > kRotGroup) n.group = kRotGroup;
-  while (n.group > 1 && (p.tokens + n.group - 1) / n.group < 2ll * sms) n.group /= 2;
-  if (n.group < 1) n.group = 1;
-  n.div_token = make_udiv(static_cast<unsigned int>(n.per_token));
-  n.div_up = make_udiv(static_cast<unsigned int>(n.UP));
+  while (n.group > 1 && p.tokens / n.group < 4 * fit) n.group /= 2;
   n.div_N = make_udiv(static_cast<unsigned int>(p.N));
   n.div_half = make_udiv(static_cast<unsigned int>(p.rd > 0 ? p.rd / 2 : 1));
   const long long blocks = (p.tokens + n.group - 1) / n.group;
-  const long long grid = static_cast<long long>(sms) * (e4 || !vec ? 2 : 4);  // the blocks that fit at once
+  const auto pick = [&](auto write, auto coded, auto wide) {
+    constexpr bool W = decltype(write)::value, E = decltype(coded)::value, V = decltype(wide)::value;
+    return p.interleaved ? rotate_kernel<T, W, E, V, true> : rotate_kernel<T, W, E, V, false>;
+  };
+  const std::true_type yes{};
+  const std::false_type no{};
   void (*k)(const RotateParams, const RotatePlan) =
-      e4 ? (vec ? rotate_kernel<T, true, true> : rotate_kernel<T, true, false>)
-         : (vec ? rotate_kernel<T, false, true> : rotate_kernel<T, false, false>);
-  return counted(launch_k(SV_PDL >= 2, k, dim3(static_cast<unsigned int>(blocks < grid ? blocks : grid)),
-                          dim3(kRotThreads), 0, st, p, n),
+      !p.write ? (vec ? pick(no, no, yes) : pick(no, no, no))
+      : e4     ? (vec ? pick(yes, yes, yes) : pick(yes, yes, no))
+               : (vec ? pick(yes, no, yes) : pick(yes, no, no));
+  return counted(launch_k(SV_PDL >= 2, k, dim3(static_cast<unsigned int>(blocks < fit ? blocks : fit)),
+                          dim3(threads), 0, st, p, n),
                  1);
 }
 
