@@ -135,34 +135,6 @@ __device__ __forceinline__ void store_unit(T* row, const Unit& u, const float (&
   }
 }
 
-// f, g: codes of the first and second members.
-template <bool VEC>
-__device__ __forceinline__ void store_codes(uint8_t* row, const Unit& u, const uint32_t (&f)[8], const uint32_t (&g)[8]) {
-  if (VEC) {
-    if (u.na == 0) return;
-    uint32_t w[4];  // x: runs a, y: run b
-    const auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-      return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
-    };
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      w[i] = u.weave ? four(f[2 * i], g[2 * i], f[2 * i + 1], g[2 * i + 1])
-                     : four(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-      w[2 + i] = u.weave ? four(f[4 + 2 * i], g[4 + 2 * i], f[5 + 2 * i], g[5 + 2 * i])
-                         : four(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
-    }
-    *reinterpret_cast<uint2*>(row + u.a) = make_uint2(w[0], w[1]);
-    *reinterpret_cast<uint2*>(row + u.b) = make_uint2(w[2], w[3]);
-  } else {
-    const int step = u.weave ? 2 : 1;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i < u.na) row[u.a + i * step] = static_cast<uint8_t>(f[i]);
-      if (i < u.nb) row[u.b + i * step] = static_cast<uint8_t>(g[i]);
-    }
-  }
-}
-
 __device__ __forceinline__ float code_value(uint32_t code) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3)));
 }
@@ -177,12 +149,19 @@ __device__ __noinline__ uint32_t nearer_code(uint32_t lo, uint32_t hi, float x, 
   return d > 0.0 ? hi : d < 0.0 ? lo : (hi & 1u ? lo : hi);
 }
 
-// The same where the element is held exactly (not turned), in 32 bits; both
-// codes as a pair.  (Products of normal size only: the sum must not underflow.)
-__device__ __forceinline__ uint32_t nearer_code(uint32_t pair, float x, float scale) {
-  const uint32_t lo = pair & 0xffu, hi = pair >> 8 & 0xffu;
-  const float d = fmaf(-0.5f * (code_value(lo) + code_value(hi)), scale, x);
-  return d > 0.0f ? hi : d < 0.0f ? lo : (hi & 1u ? lo : hi);
+// x / s for an element that is held exactly, rounded to odd: the last bit says
+// whether anything was cut off, so that rounding it again, to 4 significant
+// bits, gives what rounding the exact quotient gives (Boldo and Melquiond,
+// "Emulation of FMA and correctly rounded sums: proved algorithms using
+// rounding to odd", 2008).  The remainder of a quotient that is right to a
+// unit in the last place is exact in one fused multiply-add.
+__device__ __forceinline__ float quotient_odd(float x, float s, float inv) {
+  const float q0 = x * inv;
+  const float q = fmaf(fmaf(-q0, s, x), inv, q0);
+  const float r = fmaf(-q, s, x);
+  const uint32_t bits = __float_as_uint(q);
+  const uint32_t cut = (__float_as_uint(r) ^ bits) & 0x80000000u ? bits - 1u : bits;  // towards zero
+  return r == 0.0f ? q : __uint_as_float(cut | 1u);
 }
 
 struct RotatePlan {
@@ -290,48 +269,66 @@ __device__ __forceinline__ void turn_unit(const Unit& u, const float2 (&w)[8], f
   }
 }
 
+// Members of pair z of a unit (or elements z of its two runs), z a constant.
+template <typename T, bool VEC>
+__device__ __forceinline__ void member(const Raw<T>& r, const Unit& u, bool weave, int z, float& f, float& g) {
+  if (VEC && weave) {
+    f = elem_f32(z < 4 ? r.a[2 * z] : r.b[2 * z - 8]);
+    g = elem_f32(z < 4 ? r.a[2 * z + 1] : r.b[2 * z - 7]);
+  } else {
+    f = VEC || z < u.na ? elem_f32(r.a[z]) : 0.0f;
+    g = VEC || z < u.nb ? elem_f32(r.b[z]) : 0.0f;
+  }
+}
+
 // A unit of a row bound for 8 bits: codes, and the scale from the row's first
-// lane.  All lanes of the row take part (live: whether this one stores).
-// f, g: the elements as read; pair: they are to be turned.
-template <bool VEC>
-__device__ __forceinline__ void code_unit(const Unit& u, int UP, bool first_lane, bool live, bool pair, bool turned_row,
-                                          float magnitude, const float2 (&w)[8], const double2* cd0, const double2* cd1,
-                                          uint8_t* out, float* scale_out, const float (&f)[8], const float (&g)[8]) {
+// lane.  All lanes of the row take part (live: whether this one stores; the
+// others' elements are zeros).  Elements are unpacked and turned twice, for
+// the maximum and for the codes, rather than held.
+template <typename T, bool VEC, bool INTER>
+__device__ __forceinline__ void code_unit(const Raw<T>& raw, const Unit& u, int UP, bool first_lane, bool live, bool pair,
+                                          bool turned_row, float magnitude, const float2* w0, const float2* w1,
+                                          const double2* cd0, const double2* cd1, uint8_t* out, float* scale_out) {
+  const bool weave = INTER && u.weave;
   // e: a bound of the 32-bit error of both members of a pair (angle and
   // functions, two products, a sum: under 8 roundings of each term).
-  float x[8], y[8], e[8];
+  const float grain = pair ? fabsf(magnitude) * 0x1p-20f : 0.0f;
+  const auto at = [&](int z, float& f, float& g, float& x, float& y) {
+    f = g = 0.0f;
+    if (live) member<T, VEC>(raw, u, weave, z, f, g);
+    x = f, y = g;
+    if (pair && (VEC || z < u.na)) {
+      const float2 w = z < 4 ? w0[z] : w1[z - 4];
+      x = fmaf(f, w.x, -g * w.y);
+      y = fmaf(g, w.x, f * w.y);
+    }
+  };
+  const auto exact = [&](int z) {
+    return pair && (VEC || z < u.na) ? (z < 4 ? cd0[z] : cd1[z - 4]) : make_double2(1.0, 0.0);
+  };
   float top = 0.0f, slack = 0.0f;
   bool odd = false;  // an infinity or a NaN
 #pragma unroll
   for (int z = 0; z < 8; ++z) {
-    x[z] = f[z], y[z] = g[z], e[z] = 0.0f;
-    odd |= !(fabsf(f[z]) + fabsf(g[z]) < INFINITY);
+    float f, g, x, y;
+    at(z, f, g, x, y);
+    odd |= !(fabsf(f) < INFINITY) | !(fabsf(g) < INFINITY);
+    top = fmax3(top, fabsf(x), fabsf(y));
+    slack = fmaxf(slack, fabsf(f) + fabsf(g));
   }
-  if (pair) {
-    turn_unit<VEC>(u, w, x, y);
-#pragma unroll
-    for (int z = 0; z < 8; ++z) {
-      if (VEC || z < u.na) e[z] = (fabsf(f[z]) + fabsf(g[z])) * (fabsf(magnitude) * 0x1p-20f);
-    }
-  }
-#pragma unroll
-  for (int z = 0; z < 8; ++z) {
-    top = fmax3(top, fabsf(x[z]), fabsf(y[z]));
-    slack = fmaxf(slack, e[z]);
-  }
-  // (the sum above may overflow where neither element is odd)
-  if (odd) {
+  slack *= grain;
+  for (int o = UP >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  odd = __any_sync(0xffffffffu, odd);
+  if (odd) {  // some row of the warp: which one
     odd = false;
 #pragma unroll
-    for (int z = 0; z < 8; ++z) odd |= !(fabsf(f[z]) < INFINITY) | !(fabsf(g[z]) < INFINITY);
+    for (int z = 0; z < 8; ++z) {
+      float f, g, x, y;
+      at(z, f, g, x, y);
+      odd |= !(fabsf(f) < INFINITY) | !(fabsf(g) < INFINITY);
+    }
+    for (int o = UP >> 1; o > 0; o >>= 1) odd |= __shfl_xor_sync(0xffffffffu, static_cast<int>(odd), o) != 0;
   }
-  for (int o = UP >> 1; o > 0; o >>= 1) {
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    odd |= __shfl_xor_sync(0xffffffffu, static_cast<int>(odd), o) != 0;
-  }
-  const auto exact = [&](int z) {
-    return pair && (VEC || z < u.na) ? (z < 4 ? cd0[z] : cd1[z - 4]) : make_double2(1.0, 0.0);
-  };
   float scale;
   if (__any_sync(0xffffffffu, turned_row)) {
     for (int o = UP >> 1; o > 0; o >>= 1) slack = fmaxf(slack, __shfl_xor_sync(0xffffffffu, slack, o));
@@ -339,9 +336,11 @@ __device__ __forceinline__ void code_unit(const Unit& u, int UP, bool first_lane
     const float near = top - 2.0f * slack;
 #pragma unroll
     for (int z = 0; z < 8; ++z) {
-      if (fabsf(x[z]) >= near || fabsf(y[z]) >= near) {
+      float f, g, x, y;
+      at(z, f, g, x, y);
+      if (fmaxf(fabsf(x), fabsf(y)) >= near) {
         const double2 d = exact(z);
-        const double a = f[z], b = g[z];
+        const double a = f, b = g;
         most = fmax(most, fmax(fabs(fma(a, d.x, -(b * d.y))), fabs(fma(b, d.x, a * d.y))));
       }
     }
@@ -352,31 +351,46 @@ __device__ __forceinline__ void code_unit(const Unit& u, int UP, bool first_lane
   }
   if (odd || !(scale < INFINITY)) scale = __int_as_float(0x7fc00000);
   if (!live) return;
-  float inv = scale > 0.0f ? 1.0f / scale : 0.0f;
-  if (scale < 0x1p-100f && scale > 0.0f) {  // the reciprocal may be out of range
-    inv = 1.0f / (scale * 0x1p80f);
-#pragma unroll
-    for (int z = 0; z < 8; ++z) x[z] *= 0x1p80f, y[z] *= 0x1p80f, e[z] *= 0x1p80f;
-  }
-  uint32_t cx[8], cy[8];
+  // Small rows are multiplied up (by a power of two): neither the reciprocal
+  // nor a remainder may leave the normal range.
+  const float up = scale < 0x1p-60f ? 0x1p80f : 1.0f;
+  const float s = scale * up, inv = scale > 0.0f ? 1.0f / s : 0.0f;
+  uint32_t wa[2] = {0u, 0u}, wb[2] = {0u, 0u};
 #pragma unroll
   for (int z = 0; z < 8; ++z) {
-    const float qx = x[z] * inv, qy = y[z] * inv, ez = e[z] * inv;
-    const float dx = fmaf(fabsf(qx), 0x1p-21f, ez), dy = fmaf(fabsf(qy), 0x1p-21f, ez);
-    cx[z] = e4m3_pair(qx - dx, qx + dx);
-    cy[z] = e4m3_pair(qy - dy, qy + dy);
-    if (((cx[z] ^ cx[z] >> 8) | (cy[z] ^ cy[z] >> 8)) & 0xffu) {
-      if (pair || scale < 0x1p-60f) {
+    float f, g, x, y;
+    at(z, f, g, x, y);
+    uint32_t cx, cy;
+    if (turned_row) {
+      const float qx = x * up * inv, qy = y * up * inv, e = (fabsf(f) + fabsf(g)) * grain * up * inv;
+      const float dx = fmaf(fabsf(qx), 0x1p-21f, e), dy = fmaf(fabsf(qy), 0x1p-21f, e);
+      cx = e4m3_pair(qx - dx, qx + dx);
+      cy = e4m3_pair(qy - dy, qy + dy);
+      if (((cx ^ cx >> 8) | (cy ^ cy >> 8)) & 0xffu) {
         const double2 d = exact(z);
-        if ((cx[z] ^ cx[z] >> 8) & 0xffu) cx[z] = nearer_code(cx[z] & 0xffu, cx[z] >> 8, f[z], g[z], d.x, d.y, scale);
-        if ((cy[z] ^ cy[z] >> 8) & 0xffu) cy[z] = nearer_code(cy[z] & 0xffu, cy[z] >> 8, g[z], f[z], d.x, -d.y, scale);
-      } else {
-        cx[z] = nearer_code(cx[z], f[z], scale);
-        cy[z] = nearer_code(cy[z], g[z], scale);
+        if ((cx ^ cx >> 8) & 0xffu) cx = nearer_code(cx & 0xffu, cx >> 8 & 0xffu, f, g, d.x, d.y, scale);
+        if ((cy ^ cy >> 8) & 0xffu) cy = nearer_code(cy & 0xffu, cy >> 8 & 0xffu, g, f, d.x, -d.y, scale);
       }
+      cx &= 0xffu, cy &= 0xffu;
+    } else {
+      const uint32_t two = e4m3_pair(quotient_odd(x * up, s, inv), quotient_odd(y * up, s, inv));
+      cx = two & 0xffu, cy = two >> 8;
+    }
+    if (!VEC) {
+      const int step = u.weave ? 2 : 1;
+      if (z < u.na) out[u.a + z * step] = static_cast<uint8_t>(cx);
+      if (z < u.nb) out[u.b + z * step] = static_cast<uint8_t>(cy);
+    } else if (weave) {
+      (z < 4 ? wa : wb)[(z & 3) >> 1] |= (cx | cy << 8) << (z & 1 ? 16 : 0);
+    } else {
+      wa[z >> 2] |= cx << 8 * (z & 3);
+      wb[z >> 2] |= cy << 8 * (z & 3);
     }
   }
-  store_codes<VEC>(out, u, cx, cy);
+  if (VEC && u.na > 0) {
+    *reinterpret_cast<uint2*>(out + u.a) = make_uint2(wa[0], wa[1]);
+    *reinterpret_cast<uint2*>(out + u.b) = make_uint2(wb[0], wb[1]);
+  }
   if (first_lane) *scale_out = scale;
 }
 
@@ -384,10 +398,10 @@ __device__ __forceinline__ void code_unit(const Unit& u, int UP, bool first_lane
 // tokens; four rows' loads are in flight before the first is turned.
 // WRITE: k and v rows as well, into the pool; E4: in 8 bits.
 template <typename T, bool WRITE, bool E4, bool VEC, bool INTER>
-__global__ void __launch_bounds__(kRotThreads, E4 || !VEC ? 2 : 4)
+__global__ void __launch_bounds__(kRotThreads, E4 ? 3 : VEC ? 4 : 2)
     rotate_kernel(const __grid_constant__ RotateParams p, const __grid_constant__ RotatePlan n) {
   dep_enter();
-  constexpr int kAhead = sizeof(T) == 4 || !VEC ? 2 : 4;
+  constexpr int kAhead = sizeof(T) == 4 || !VEC || E4 ? 2 : 4;
   __shared__ __align__(16) float2 cs[kRotAngles];
   __shared__ __align__(16) double2 csd[E4 ? kRotAngles : 1];
   __shared__ long long dst[kRotGroup], sdst[kRotGroup], pos[kRotGroup];
@@ -464,22 +478,19 @@ __global__ void __launch_bounds__(kRotThreads, E4 || !VEC ? 2 : 4)
           const Unit& u = key ? turned : plain;
           const bool live = mine && at >= 0;
           const bool pair = key && turned.pair;
-          if (E4 ? __any_sync(0xffffffffu, live) : live && u.na > 0) {
-            if (E4) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) f[i] = g[i] = 0.0f;
+          if (E4) {
+            if (__any_sync(0xffffffffu, live))
+              code_unit<T, VEC, INTER>(raw[z], u, n.UP, lane == 0, live && u.na > 0, pair, key && turn, p.magnitude,
+                                       cs + base + a0, cs + base + a1, csd + (E4 ? base + a0 : 0), csd + (E4 ? base + a1 : 0),
+                                       static_cast<uint8_t*>(key ? p.c.k : p.c.v) + at + h * p.c.head_stride,
+                                       (key ? p.c.ks : p.c.vs) + sdst[ks[z]] + static_cast<long long>(h) * p.c.page_size);
+          } else if (live && u.na > 0) {
+            unpack_raw<T, VEC>(raw[z], u, f, g);
+            if (pair) {
+              load_angles<VEC>(cs + base + a0, cs + base + a1, u.na, w);
+              turn_unit<VEC>(u, w, f, g);
             }
-            if (live && u.na > 0) unpack_raw<T, VEC>(raw[z], u, f, g);
-            if (pair) load_angles<VEC>(cs + base + a0, cs + base + a1, u.na, w);
-            if (E4) {
-              code_unit<VEC>(u, n.UP, lane == 0, live, pair, key && turn, p.magnitude, w, csd + (E4 ? base + a0 : 0),
-                             csd + (E4 ? base + a1 : 0),
-                             static_cast<uint8_t*>(key ? p.c.k : p.c.v) + at + h * p.c.head_stride,
-                             (key ? p.c.ks : p.c.vs) + sdst[ks[z]] + static_cast<long long>(h) * p.c.page_size, f, g);
-            } else {
-              if (pair) turn_unit<VEC>(u, w, f, g);
-              store_unit<T, VEC>(static_cast<T*>(key ? p.c.k : p.c.v) + at + h * p.c.head_stride, u, f, g);
-            }
+            store_unit<T, VEC>(static_cast<T*>(key ? p.c.k : p.c.v) + at + h * p.c.head_stride, u, f, g);
           }
         }
       }
@@ -502,8 +513,8 @@ static cudaError_t launch_rotate_t(const RotateParams& p, bool e4, bool vec, int
   if (n.passes * (kRotThreads / n.UP) < rows) ++n.passes;
   n.rows = (rows + n.passes - 1) / n.passes;
   const int threads = (n.rows * n.UP + 31) / 32 * 32;
-  // blocks that fit at once (64 registers a thread, 128 for the larger forms)
-  const long long fit = static_cast<long long>(sms) * ((e4 || !vec ? 512 : 1024) / threads);
+  // blocks that fit at once (64 registers a thread, 80 or 128 in the larger forms)
+  const long long fit = static_cast<long long>(sms) * ((e4 ? 768 : vec ? 1024 : 512) / threads);
   n.group = kRotGroup;
   if (p.rd > 0 && n.group > kRotAngles / (p.rd / 2)) n.group = kRotAngles / (p.rd / 2);
   while (n.group > 1 && p.tokens / n.group < 4 * fit) n.group /= 2;
