@@ -547,20 +547,21 @@ cudaError_t launch_rotate(const RotateParams& p, int dtype, int cache_dtype, boo
 
 // ------------------------------------------------------------ read-back
 //
-// A block takes 16 packed rows: one lane a row finds its sequence (the last b
+// A block takes up to 32 packed rows (fewer where there are few): one lane a row finds its sequence (the last b
 // with offsets[b] <= r) and its page, then all threads convert (row, k or v,
-// head) runs of 8 elements, four of a thread's runs in flight at once.
+// head) runs of 16 elements (8 where a head has no whole number of them), four of a
+// thread's runs in flight at once.
 
-constexpr int kReadRows = 16;
+constexpr int kReadRows = 32;
 
-template <typename C, typename O, bool VEC>
-__global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ CacheReadParams p, UDiv div_row,
+template <typename C, typename O, bool VEC, int RUN>
+__global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ CacheReadParams p, int rows, UDiv div_row,
                                                          UDiv div_kv, UDiv div_head) {
   dep_enter();
   __shared__ long long src[kReadRows];   // element offset of the token, -1: zeros, -2: no row
   __shared__ long long ssrc[kReadRows];  // scale offset of head 0
-  const long long r0 = static_cast<long long>(blockIdx.x) * kReadRows;
-  if (threadIdx.x < kReadRows) {
+  const long long r0 = static_cast<long long>(blockIdx.x) * rows;
+  if (threadIdx.x < rows) {
     const long long r = r0 + threadIdx.x;
     long long at = -2, sat = 0;
     if (r < p.total && r >= __ldg(p.offsets) && r < __ldg(p.offsets + p.B)) {
@@ -585,9 +586,9 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__
   constexpr bool kCodes = sizeof(C) == 1;
   constexpr int kAhead = 4;
   const int runs = static_cast<int>(div_head.d), per_kv = static_cast<int>(div_kv.d), per_row = static_cast<int>(div_row.d);
-  const int all = kReadRows * per_row;
+  const int all = rows * per_row;
   for (int i0 = threadIdx.x; i0 < all; i0 += 256 * kAhead) {
-    alignas(16) C c[kAhead][8];
+    alignas(16) C c[kAhead][RUN];
     float scale[kAhead];
 #pragma unroll
     for (int z = 0; z < kAhead; ++z) {
@@ -595,12 +596,12 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__
       if (i >= all) continue;
       const int row = quotient(i, div_row), x = i - row * per_row;
       const int kv = quotient(x, div_kv), y = x - kv * per_kv;
-      const int h = quotient(y, div_head), e = (y - h * runs) * 8;
+      const int h = quotient(y, div_head), e = (y - h * runs) * RUN;
       const long long at = src[row];
       if (at < 0) continue;
       const C* from = static_cast<const C*>(kv ? p.c.v : p.c.k) + at + h * p.c.head_stride + e;
       if (VEC) {
-        constexpr int kBytes = 8 * sizeof(C);
+        constexpr int kBytes = RUN * sizeof(C);
         if (kBytes == 8) {
           *reinterpret_cast<uint2*>(c[z]) = *reinterpret_cast<const uint2*>(from);
         } else {
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__
         }
       } else {
 #pragma unroll
-        for (int m = 0; m < 8; ++m)
+        for (int m = 0; m < RUN; ++m)
           if (e + m < p.c.dim) c[z][m] = from[m];
       }
       if (kCodes) scale[z] = __ldg((kv ? p.c.vs : p.c.ks) + ssrc[row] + static_cast<long long>(h) * p.c.page_size);
@@ -620,66 +621,72 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__
       if (i >= all) continue;
       const int row = quotient(i, div_row), x = i - row * per_row;
       const int kv = quotient(x, div_kv), y = x - kv * per_kv;
-      const int h = quotient(y, div_head), e = (y - h * runs) * 8;
+      const int h = quotient(y, div_head), e = (y - h * runs) * RUN;
       const long long at = src[row];
       if (at == -2) continue;
-      float f[8] = {};
-      if (at >= 0) {
+      O* o = static_cast<O*>(kv ? p.v_out : p.k_out) + ((r0 + row) * p.c.heads + h) * p.c.dim + e;
+#pragma unroll
+      for (int half = 0; half < RUN; half += 8) {
+        float f[8] = {};
+        if (at >= 0) {
+          if (VEC) {
+            load8(c[z] + half, f);
+          } else {
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+              if (e + m < p.c.dim) f[m] = elem_f32(c[z][m]);
+          }
+          if (kCodes) {
+#pragma unroll
+            for (int m = 0; m < 8; ++m) f[m] *= scale[z];
+          }
+        }
         if (VEC) {
-          load8(c[z], f);
+          store8(o + half, f);
         } else {
 #pragma unroll
           for (int m = 0; m < 8; ++m)
-            if (e + m < p.c.dim) f[m] = elem_f32(c[z][m]);
+            if (e + m < p.c.dim) o[m] = from_f32<O>(f[m]);
         }
-        if (kCodes) {
-#pragma unroll
-          for (int m = 0; m < 8; ++m) f[m] *= scale[z];
-        }
-      }
-      O* o = static_cast<O*>(kv ? p.v_out : p.k_out) + ((r0 + row) * p.c.heads + h) * p.c.dim + e;
-      if (VEC) {
-        store8(o, f);
-      } else {
-#pragma unroll
-        for (int m = 0; m < 8; ++m)
-          if (e + m < p.c.dim) o[m] = from_f32<O>(f[m]);
       }
     }
   }
 }
 
 template <typename C>
-static cudaError_t launch_read_c(const CacheReadParams& p, int out_dtype, bool vec, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned int>((p.total + kReadRows - 1) / kReadRows));
-  void (*k)(const CacheReadParams, UDiv, UDiv, UDiv);
-  if (out_dtype == 0)
-    k = vec ? cache_read_kernel<C, float, true> : cache_read_kernel<C, float, false>;
-  else if (out_dtype == 1)
-    k = vec ? cache_read_kernel<C, __nv_bfloat16, true> : cache_read_kernel<C, __nv_bfloat16, false>;
-  else
-    k = vec ? cache_read_kernel<C, __half, true> : cache_read_kernel<C, __half, false>;
-  const unsigned int runs = static_cast<unsigned int>((p.c.dim + 7) / 8), heads = static_cast<unsigned int>(p.c.heads);
-  return counted(launch_k(SV_PDL >= 2, k, grid, dim3(256), 0, st, p, make_udiv(2 * heads * runs), make_udiv(heads * runs),
+static cudaError_t launch_read_c(const CacheReadParams& p, int out_dtype, bool vec, int sms, cudaStream_t st) {
+  int rows = kReadRows;  // a block's: as many as leave two blocks for each SM
+  while (rows > 1 && p.total < 2ll * sms * rows) rows /= 2;
+  const dim3 grid(static_cast<unsigned int>((p.total + rows - 1) / rows));
+  void (*k)(const CacheReadParams, int, UDiv, UDiv, UDiv);
+  const bool wide = vec && p.c.dim % 16 == 0;
+  const auto pick = [&](auto out) {
+    using O = decltype(out);
+    return wide ? cache_read_kernel<C, O, true, 16> : vec ? cache_read_kernel<C, O, true, 8> : cache_read_kernel<C, O, false, 8>;
+  };
+  k = out_dtype == 0 ? pick(float{}) : out_dtype == 1 ? pick(__nv_bfloat16{}) : pick(__half{});
+  const unsigned int runs = static_cast<unsigned int>(wide ? p.c.dim / 16 : (p.c.dim + 7) / 8), heads = static_cast<unsigned int>(p.c.heads);
+  return counted(launch_k(SV_PDL >= 2, k, grid, dim3(256), 0, st, p, rows, make_udiv(2 * heads * runs), make_udiv(heads * runs),
                           make_udiv(runs)),
                  1);
 }
 
-cudaError_t launch_cache_read(const CacheReadParams& p, int cache_dtype, int out_dtype, bool vec,
+cudaError_t launch_cache_read(const CacheReadParams& p, int cache_dtype, int out_dtype, bool vec, int sms,
                               cudaStream_t st) {
   if (p.total <= 0 || p.B <= 0) return cudaSuccess;
-  if (cache_dtype == 0) return launch_read_c<float>(p, out_dtype, vec, st);
-  if (cache_dtype == 1) return launch_read_c<__nv_bfloat16>(p, out_dtype, vec, st);
-  if (cache_dtype == 2) return launch_read_c<__half>(p, out_dtype, vec, st);
-  return launch_read_c<__nv_fp8_e4m3>(p, out_dtype, vec, st);
+  if (cache_dtype == 0) return launch_read_c<float>(p, out_dtype, vec, sms, st);
+  if (cache_dtype == 1) return launch_read_c<__nv_bfloat16>(p, out_dtype, vec, sms, st);
+  if (cache_dtype == 2) return launch_read_c<__half>(p, out_dtype, vec, sms, st);
+  return launch_read_c<__nv_fp8_e4m3>(p, out_dtype, vec, sms, st);
 }
 
 // ---------------------------------------------------------------- commit
 //
 // A thread owns one column (16 bytes, or one element) of one (layer, k or v,
-// head) and moves it through the sequence's accepted nodes in order.  Row j
-// only receives from rows at or after j, so a row is always read before it is
-// overwritten, and no two threads touch the same bytes.
+// head) and moves it through the sequence's accepted nodes in order, four at a
+// time.  Row j only receives from rows after j, so a row is always read before
+// it is overwritten (those of one four are read before any of them is
+// written), and no two threads touch the same bytes.
 
 __device__ __forceinline__ void write_len(const CacheCommitParams& p, int b, int n, long long len) {
   const long long end = len + n + 1;
@@ -695,7 +702,8 @@ __global__ void __launch_bounds__(256) cache_commit_kernel(const CacheCommitPara
   const int b = blockIdx.y;
   const int n = min(max(__ldg(p.accepted + b), 0), p.N - 1);
   const long long len = max(0, __ldg(p.cache_len + b));
-  __shared__ long long off[64], soff[64], dst[64], sdst[64];  // element and scale offsets, -1: no move
+  __shared__ long long off[64], soff[64], dst[64], sdst[64];  // element and scale offsets of the moves
+  __shared__ int moves;
   if (threadIdx.x < 64) {
     const int j = threadIdx.x;
     long long a = -1, as = -1, d = -1, ds = -1;
@@ -714,7 +722,16 @@ __global__ void __launch_bounds__(256) cache_commit_kernel(const CacheCommitPara
         }
       }
     }
-    off[j] = a, soff[j] = as, dst[j] = d, sdst[j] = ds;
+    // the moves in order, without gaps
+    __shared__ unsigned int in[2];
+    const unsigned int word = __ballot_sync(0xffffffffu, a >= 0);
+    if ((j & 31) == 0) in[j >> 5] = word;
+    asm volatile("bar.sync 1, 64;" ::: "memory");
+    if (a >= 0) {
+      const int at = __popc(word & ((1u << (j & 31)) - 1u)) + (j >= 32 ? __popc(in[0]) : 0);
+      off[at] = a, soff[at] = as, dst[at] = d, sdst[at] = ds;
+    }
+    if (j == 0) moves = __popc(in[0]) + __popc(in[1]);
   }
   __syncthreads();
   // When new_len is cache_len, which other blocks may still have to read, the
@@ -732,16 +749,19 @@ __global__ void __launch_bounds__(256) cache_commit_kernel(const CacheCommitPara
     if (w < words) {
       unsigned char* base = static_cast<unsigned char*>(kv ? p.c.v : p.c.k);
       const long long col = layer * p.c.layer_stride + h * p.c.head_stride;
-      for (int j = 1; j <= n; ++j) {
-        if (off[j] < 0) continue;
-        const W v = reinterpret_cast<const W*>(base + (col + off[j]) * es)[w];
-        reinterpret_cast<W*>(base + (col + dst[j]) * es)[w] = v;
+      for (int j = 0; j < moves; j += 4) {
+        W v[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          if (j + z < moves) v[z] = reinterpret_cast<const W*>(base + (col + off[j + z]) * es)[w];
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          if (j + z < moves) reinterpret_cast<W*>(base + (col + dst[j + z]) * es)[w] = v[z];
       }
     } else {
       float* base = (kv ? p.c.vs : p.c.ks) + layer * p.c.scale_layer_stride +
                     static_cast<long long>(h) * p.c.page_size;
-      for (int j = 1; j <= n; ++j)
-        if (off[j] >= 0) base[sdst[j]] = base[soff[j]];
+      for (int j = 0; j < moves; ++j) base[sdst[j]] = base[soff[j]];
     }
   }
 }
@@ -753,15 +773,16 @@ __global__ void cache_len_kernel(const CacheCommitParams p) {
   write_len(p, b, min(max(__ldg(p.accepted + b), 0), p.N - 1), max(0, p.cache_len[b]));
 }
 
-cudaError_t launch_cache_commit(const CacheCommitParams& p, int es, bool vec, cudaStream_t st) {
+cudaError_t launch_cache_commit(const CacheCommitParams& p, int es, bool vec, int sms, cudaStream_t st) {
   if (p.B <= 0) return cudaSuccess;
   const bool moves = p.path && p.N > 1;
   if (moves) {
     const int wb = vec ? 16 : es;
     const int words = p.c.dim * es / wb;
     const long long items = static_cast<long long>(p.c.layers) * 2 * p.c.heads * (words + (p.c.ks ? 1 : 0));
-    const long long blocks = (items + 255) / 256;
-    const dim3 grid(static_cast<unsigned int>(blocks < 4096 ? blocks : 4096), static_cast<unsigned int>(p.B));
+    // one wave of blocks: each looks up its sequence's places once
+    const long long blocks = (items + 255) / 256, most = 8ll * sms / p.B + 1;
+    const dim3 grid(static_cast<unsigned int>(blocks < most ? blocks : most), static_cast<unsigned int>(p.B));
     void (*k)(const CacheCommitParams, int, int) = wb == 16  ? cache_commit_kernel<uint4>
                                                    : wb == 4 ? cache_commit_kernel<uint32_t>
                                                    : wb == 2 ? cache_commit_kernel<uint16_t>

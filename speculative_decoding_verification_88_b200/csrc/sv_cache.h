@@ -93,8 +93,8 @@ struct AttnParams {
 cudaError_t launch_rotate(const RotateParams& p, int dtype, int cache_dtype, bool vec, int sms,
                           cudaStream_t st);
 cudaError_t launch_cache_read(const CacheReadParams& p, int cache_dtype, int out_dtype, bool vec,
-                              cudaStream_t st);
-cudaError_t launch_cache_commit(const CacheCommitParams& p, int elem_bytes, bool vec,
+                              int sms, cudaStream_t st);
+cudaError_t launch_cache_commit(const CacheCommitParams& p, int elem_bytes, bool vec, int sms,
                                 cudaStream_t st);
 cudaError_t launch_attention_plain(const AttnParams& p, int q_dtype, int cache_dtype,
                                    cudaStream_t st);

@@ -205,7 +205,9 @@ extern "C" int spec_verify_cache_read(const sv_kv_cache* cache, const int32_t* p
   p.k_out = k_out, p.v_out = v_out, p.ctrl = ctrl_of(workspace);
   const bool vec = cache->head_dim % 8 == 0 && aligned(k_out, 16) && aligned(v_out, 16) &&
                    pool_on(cache, ces, ces == 1 ? 8 : 16);
-  return launch_cache_read(p, cache->dtype, out_dtype, vec, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  const int n = sms();
+  if (n <= 0) return SV_ERR_CUDA;
+  return launch_cache_read(p, cache->dtype, out_dtype, vec, n, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? SV_OK
              : SV_ERR_CUDA;
 }
@@ -227,7 +229,9 @@ extern "C" int spec_verify_cache_commit(const sv_kv_cache* cache, const int32_t*
   p.B = B, p.N = N, p.new_len = new_len, p.ctrl = ctrl_of(workspace);
   const int es = bytes_of(cache->dtype);
   const bool vec = cache->head_dim * es % 16 == 0 && pool_on(cache, es, 16);
-  return launch_cache_commit(p, es, vec, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  const int n = sms();
+  if (n <= 0) return SV_ERR_CUDA;
+  return launch_cache_commit(p, es, vec, n, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 extern "C" size_t spec_verify_tree_attention_scratch_size(int B, int N, int Hq, int num_heads, int head_dim) {
