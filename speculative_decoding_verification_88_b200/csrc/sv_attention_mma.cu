@@ -53,6 +53,8 @@ struct Split {
   __device__ __forceinline__ long long start(int c) const { return each * c + min(c, more); }
 };
 
+// Scratch: what each block found, for the joining grid, then the partial results.
+constexpr size_t kPlanBytes = 16384;
 __host__ __device__ inline size_t slot_floats(int DP) { return static_cast<size_t>(kTile) * (DP + 2); }
 
 }  // namespace
@@ -74,6 +76,7 @@ struct MmaParams {
   int qbox;     // nodes of a query box (the tensor map's); 0: plain loads
   int split;    // copies of the rows in the 128 lanes, each with a share of a tile's columns
   UDiv div_G;   // / a.G
+  UDiv div_one, div_two;  // / rows of the only row tile, / 256 (the joining grid)
 };
 
 namespace {
@@ -97,6 +100,7 @@ __device__ __forceinline__ int tiles_of(const AttnParams& a, int b) {
 struct Found {
   Split split;
   int b, h, pr, t0;  // sequence, cache head, pair of row tiles, tile
+  int tiles;         // of an item of that sequence
 };
 __device__ __forceinline__ void find_share(const AttnParams& a, int pairs, int blocks, int c, long long* sums, Found* f) {
   const int tid = threadIdx.x;
@@ -144,6 +148,7 @@ __device__ __forceinline__ void find_share(const AttnParams& a, int pairs, int b
     f->t0 = static_cast<int>(rem - static_cast<long long>(item) * t);
     f->h = item / pairs;
     f->pr = item - f->h * pairs;
+    f->tiles = t;
     f->b = b;
   }
   __syncthreads();
@@ -675,7 +680,6 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
   constexpr uint32_t kShapeS = mma_shape(kBf16, kTile, false);
   constexpr uint32_t kShapeO = mma_shape(kBf16, DP, true);
 
-  dep_enter();
   const uint32_t entry = kData + (E4 ? 2 * p.scale_bytes : 0);
   const uint32_t qbytes = static_cast<uint32_t>(p.qtiles) * p.qrows * DP * 2;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -727,8 +731,13 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
   __syncthreads();
   tmem_fence_after();
   const int cta = blockIdx.x;
+  // Launched as a programmatic dependent: all of the above may overlap the
+  // kernel before this one, whose end is waited for here.
+  dep_enter();
   find_share(a, p.pairs, gridDim.x, cta, s->sums, &s->found);
   const uint32_t tmem = s->tmem;
+  static_assert(kMaxCtas * sizeof(Found) <= kPlanBytes, "every block's plan fits");
+  if (tid == 0) static_cast<Found*>(a.scratch)[cta] = s->found;
 
   if (s->found.b >= 0) {
     Walk w;
@@ -1256,13 +1265,14 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
         const int col0 = two ? 0 : g * (DP / 2), ncol = two ? DP : DP / 2;
         const int D = a.c.dim, head = h * a.G + (row0 + row - node * a.G);
         const int slot = 2 * cta + (w.first ? 0 : 1);
-        float* part = static_cast<float*>(a.scratch) + (static_cast<size_t>(slot) * p.qtiles + (row >> 7)) * slot_floats(DP);
+        float* part = static_cast<float*>(a.scratch) + kPlanBytes / 4 +
+                      (static_cast<size_t>(slot) * p.qtiles + (row >> 7)) * slot_floats(DP);
         // The queries are done with: their buffer takes the result's rows, one
         // after the other, and behind them what the copies hand over.
         unsigned char* const staged = qs + buf * qbytes;
         float4* const handed =
             reinterpret_cast<float4*>(staged + lanes * DP * 2) + g * (SPLIT - 1) * 4 * lanes;
-#pragma unroll 1
+#pragma unroll 2
         for (int c = 0; c < ncol; c += 16) {
           float o[16];
           if (warp_live) {
@@ -1349,23 +1359,20 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
 
 // ----------------------------------------------------------------- joining
 //
-// Block j looks at the boundary between shares j and j + 1.  The blocks whose
-// boundaries cut one item share its rows' columns (runs of 8), so that each
-// reads about as much as one share wrote.
+// Block j looks at the boundary between shares j and j + 1, which the first
+// grid's block j + 1 left in its plan.  The blocks whose boundaries cut one
+// item share its rows' columns (runs of 8), so that each reads about as much
+// as one share wrote.
 template <typename QT, int DP>
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __grid_constant__ MmaParams p, int grid) {
-  __shared__ long long sums[256];
-  __shared__ Found found;
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __grid_constant__ MmaParams p) {
+  dep_enter();
   const AttnParams& a = p.a;
   const int j = blockIdx.x + 1;
-  find_share(a, p.pairs, grid, j, sums, &found);
+  const Found found = static_cast<const Found*>(a.scratch)[j];
   const Split split = found.split;
   const int b = found.b, h = found.h;
-  // The split depends on nothing that the first grid writes: only here is its
-  // end waited for (which all blocks do, so that a later grid may rely on it).
-  griddep_wait();
   if (b < 0 || found.t0 == 0) return;  // no such share, or one that starts with an item
-  const long long lo = split.start(j) - found.t0, hi = lo + tiles_of(a, b);
+  const long long lo = split.start(j) - found.t0, hi = lo + found.tiles;
   int first = j, last = j;  // boundaries inside the item
   while (first > 1 && split.start(first - 1) > lo) --first;
   while (last + 1 < split.n && split.start(last + 1) < hi) ++last;
@@ -1375,80 +1382,62 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
   const int rows = min(two ? 2 * kTile : kTile, p.R - row0);
   const int D = a.c.dim;
   const int units = rows * (D / 8), blocks = last - first + 1, me = j - first;
-  const size_t tile = slot_floats(DP);
-  const float* scratch = static_cast<const float*>(a.scratch);
-  const int slot0 = 2 * (first - 1) + (split.start(first - 1) < lo ? 1 : 0);
-  const auto part = [&](int i, int row) {
-    const int slot = i == 0 ? slot0 : 2 * (first - 1 + i);
-    return scratch + (static_cast<size_t>(slot) * p.qtiles + (row >> 7)) * tile;
-  };
-  // A row's factors, for the rows this block has columns of: 2^(m - M) / l of
-  // each part; a block whose boundaries cut one item has at most kMaxCtas
-  // parts, of which kParts are kept here at a time.
-  constexpr int kParts = 8;
-  __shared__ float factor[kParts][2 * kTile];
-  __shared__ float top[2 * kTile], inv[2 * kTile];
-  for (int row = threadIdx.x; row < rows; row += kJoinThreads) {
-    float M = -INFINITY, L = 0.0f;
-#pragma unroll 4
-    for (int x = 0; x < parts; ++x)
-      M = fmaxf(M, reinterpret_cast<const float2*>(part(x, row) + static_cast<size_t>(kTile) * DP)[row & 127].x);
-#pragma unroll 4
-    for (int x = 0; x < parts; ++x) {
-      const float2 ml = reinterpret_cast<const float2*>(part(x, row) + static_cast<size_t>(kTile) * DP)[row & 127];
-      const float f = ml.x == M ? 1.0f : ex2f(ml.x - M);
-      if (ml.y != 0.0f) L = fmaf(ml.y, f, L);
-    }
-    top[row] = M;
-    inv[row] = L == 0.0f ? 0.0f : 1.0f / L;
-    if (a.lse && me == 0) {
-      const int node = div_rows(row0 + row, p.div_G), head = h * a.G + (row0 + row - node * a.G);
-      a.lse[(static_cast<long long>(b) * a.N + node) * a.Hq + head] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
-    }
-  }
   const int u0 = static_cast<int>(static_cast<long long>(units) * me / blocks);
   const int u1 = static_cast<int>(static_cast<long long>(units) * (me + 1) / blocks);
-  for (int i0 = u0; i0 < u1; i0 += kJoinThreads) {
-    const int i = i0 + threadIdx.x;
-    const bool in = i < u1;
-    const int row = in ? i % rows : 0, c = in ? i / rows : 0;
-    float o[8] = {};
-    for (int x0 = 0; x0 < parts; x0 += kParts) {
-      const int n = min(kParts, parts - x0);
-      float4 y[2][4];
-      __syncthreads();  // top and inv are there; the last factors have been used
-      if (i0 == u0 || parts > kParts)
-        for (int z = threadIdx.x; z < n * rows; z += kJoinThreads) {
-          const int x = z / rows, r = z % rows;
-          const float2 ml = reinterpret_cast<const float2*>(part(x0 + x, r) + static_cast<size_t>(kTile) * DP)[r & 127];
-          const float f = ml.x == top[r] ? 1.0f : ex2f(ml.x - top[r]);
-          factor[x][r] = ml.y == 0.0f ? 0.0f : f * inv[r];
+  const float* scratch = static_cast<const float*>(a.scratch) + kPlanBytes / 4;
+  const int slot0 = 2 * (first - 1) + (split.start(first - 1) < lo ? 1 : 0);
+  const UDiv& by_rows = two && rows == 2 * kTile ? p.div_two : p.div_one;
+  const auto part = [&](int i, int row) {
+    const int slot = i == 0 ? slot0 : 2 * (first - 1 + i);
+    return scratch + (static_cast<size_t>(slot) * p.qtiles + (row >> 7)) * slot_floats(DP);
+  };
+  const auto stats = [&](int i, int row) {
+    return reinterpret_cast<const float2*>(part(i, row) + static_cast<size_t>(kTile) * DP)[row & 127];
+  };
+  constexpr int kAhead = 4;  // parts whose loads are in flight together
+  for (int i = u0 + static_cast<int>(threadIdx.x); i < u1; i += kJoinThreads) {
+    int c = div_rows(i, by_rows), row = i - c * static_cast<int>(by_rows.d);
+    if (static_cast<int>(by_rows.d) != rows) c = i / rows, row = i - c * rows;
+    float M = -INFINITY, L = 0.0f, o[8] = {};
+    for (int x0 = 0; x0 < parts; x0 += kAhead) {
+      float2 ml[kAhead];
+      float4 y0[kAhead], y1[kAhead];
+#pragma unroll
+      for (int z = 0; z < kAhead; ++z) {
+        ml[z] = make_float2(-INFINITY, 0.0f);
+        if (x0 + z < parts) {
+          const float4* q = reinterpret_cast<const float4*>(part(x0 + z, row));
+          ml[z] = stats(x0 + z, row);
+          y0[z] = q[static_cast<size_t>(2 * c) * kTile + (row & 127)];
+          y1[z] = q[static_cast<size_t>(2 * c + 1) * kTile + (row & 127)];
         }
-      __syncthreads();
-      for (int x = 0; x < n; x += 4) {
+      }
+      float top = M;
 #pragma unroll
-        for (int z = 0; z < 4; ++z)
-          if (x + z < n) {
-            const float4* q = reinterpret_cast<const float4*>(part(x0 + x + z, row));
-            y[0][z] = q[static_cast<size_t>(2 * c) * kTile + (row & 127)];
-            y[1][z] = q[static_cast<size_t>(2 * c + 1) * kTile + (row & 127)];
-          }
+      for (int z = 0; z < kAhead; ++z) top = fmaxf(top, ml[z].x);
+      const float keep = M == top ? 1.0f : ex2f(M - top);
+      L *= keep;
 #pragma unroll
-        for (int z = 0; z < 4; ++z)
-          if (x + z < n) {
-            const float f = factor[x + z][row];
-            if (f == 0.0f) continue;
-            o[0] = fmaf(y[0][z].x, f, o[0]), o[1] = fmaf(y[0][z].y, f, o[1]), o[2] = fmaf(y[0][z].z, f, o[2]);
-            o[3] = fmaf(y[0][z].w, f, o[3]), o[4] = fmaf(y[1][z].x, f, o[4]), o[5] = fmaf(y[1][z].y, f, o[5]);
-            o[6] = fmaf(y[1][z].z, f, o[6]), o[7] = fmaf(y[1][z].w, f, o[7]);
-          }
+      for (int x = 0; x < 8; ++x) o[x] = keep == 0.0f ? 0.0f : o[x] * keep;
+      M = top;
+#pragma unroll
+      for (int z = 0; z < kAhead; ++z) {
+        if (ml[z].y == 0.0f) continue;
+        const float f = ml[z].x == M ? 1.0f : ex2f(ml[z].x - M);
+        L = fmaf(ml[z].y, f, L);
+        if (f == 0.0f) continue;
+        o[0] = fmaf(y0[z].x, f, o[0]), o[1] = fmaf(y0[z].y, f, o[1]), o[2] = fmaf(y0[z].z, f, o[2]);
+        o[3] = fmaf(y0[z].w, f, o[3]), o[4] = fmaf(y1[z].x, f, o[4]), o[5] = fmaf(y1[z].y, f, o[5]);
+        o[6] = fmaf(y1[z].z, f, o[6]), o[7] = fmaf(y1[z].w, f, o[7]);
       }
     }
-    if (in) {
-      const int node = div_rows(row0 + row, p.div_G), head = h * a.G + (row0 + row - node * a.G);
-      const long long out_row = (static_cast<long long>(b) * a.N + node) * a.Hq + head;
-      store8(static_cast<QT*>(a.out) + out_row * D + c * 8, o);
-    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) o[x] *= inv;
+    const int node = div_rows(row0 + row, p.div_G), head = h * a.G + (row0 + row - node * a.G);
+    const long long out_row = (static_cast<long long>(b) * a.N + node) * a.Hq + head;
+    store8(static_cast<QT*>(a.out) + out_row * D + c * 8, o);
+    if (a.lse && c == 0) a.lse[out_row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
   }
 }
 
@@ -1551,11 +1540,11 @@ cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[5], int grid, cud
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev] = true;
   }
-  e = counted(launch_k(SV_PDL >= 2, kernel, dim3(grid), dim3(E4 ? 512 : 384), smem, st, p, maps[0], maps[1], maps[2],
+  e = counted(launch_k(SV_PDL >= 1, kernel, dim3(grid), dim3(E4 ? 512 : 384), smem, st, p, maps[0], maps[1], maps[2],
                        maps[3], maps[4]),
               1);
   if (e != cudaSuccess || grid < 2) return e;
-  return counted(launch_k(SV_PDL >= 1, attention_join_kernel<QT, DP>, dim3(grid - 1), dim3(kJoinThreads), 0, st, p, grid), 1);
+  return counted(launch_k(SV_PDL >= 1, attention_join_kernel<QT, DP>, dim3(grid - 1), dim3(kJoinThreads), 0, st, p), 1);
 }
 
 template <typename QT, bool E4>
@@ -1570,7 +1559,7 @@ cudaError_t launch_split(MmaParams& p, const CUtensorMap (&maps)[5], int grid, c
 
 size_t attention_scratch_bytes(int N, int G, int dim) {
   const int halves = (N * G + kTile - 1) / kTile;
-  return static_cast<size_t>(2 * kMaxCtas) * (halves > 1 ? 2 : 1) * slot_floats(dim <= 64 ? 64 : 128) * 4;
+  return kPlanBytes + static_cast<size_t>(2 * kMaxCtas) * (halves > 1 ? 2 : 1) * slot_floats(dim <= 64 ? 64 : 128) * 4;
 }
 
 bool attention_mma_takes(const AttnParams& a, int cache_dtype) {
@@ -1588,6 +1577,8 @@ cudaError_t launch_attention_mma(const AttnParams& a, int q_dtype, int cache_dty
   p.a = a;
   p.R = a.N * a.G;
   p.div_G = make_udiv(static_cast<unsigned int>(a.G));
+  p.div_one = make_udiv(static_cast<unsigned int>(p.R < kTile ? p.R : kTile));
+  p.div_two = make_udiv(2 * kTile);
   p.halves = (p.R + kTile - 1) / kTile;
   p.pairs = (p.halves + 1) / 2;
   p.qtiles = p.halves > 1 ? 2 : 1;
