@@ -23,10 +23,16 @@
 // in 16 bits, and the division by the sum at the end makes up for it.
 //
 // Weights enter the second product in the values' 16-bit type.  8-bit pools
-// are widened to 16-bit floats in shared memory (exact) by four converter
-// warps, K's scales multiply S and V's scales the weights; queries are scaled
-// by a power of two a row so that they fit 16-bit floats exactly, and the
-// weights by a power of two that follows the largest scale of V.
+// go into the products as they are, by the 8-bit instructions: queries are
+// scaled by a power of two a row and written as a sum of two (bfloat16) or
+// three (16-bit floats) 8-bit terms of 4 significant bits each, which is
+// exact down to 2^-18 of the row's largest element; the weights are a sum of
+// three.  An 8-bit product of n terms costs n/2 of a 16-bit one, and K and V
+// cross shared memory once, without a widened copy (widening them to 16 bits
+// first, by four warps, bound the kernel by shared memory: 2450 cycles a tile
+// of 128 tokens instead of the 1425 that its 32 KB take from memory).  K's
+// scales multiply S; V's multiply the weights, which a power of two that
+// follows the largest of them keeps in the 8-bit range.
 #include <cuda.h>
 
 #include <initializer_list>
@@ -39,11 +45,12 @@ namespace {
 
 constexpr int kTile = 128;        // tokens a tile, rows a half item
 constexpr int kMaxCtas = 148;     // scratch is sized for this many blocks
-constexpr int kScaleRing = 4;     // tiles whose scales are held
 constexpr int kMaxStages = 8;
-constexpr int kConvStages = 3;    // widened tiles (8-bit pools)
+constexpr int kScaleRing = kMaxStages;  // most tiles whose scales are held (8-bit pools)
 constexpr int kJoinThreads = 512;
 constexpr float kLazy = 8.0f;     // log2 of what a weight may exceed 1 by
+// 8-bit weights: the largest is near 2^6, and at most 2^8.5 < 448.
+constexpr float kBase8 = 6.0f, kLazy8 = 8.5f;
 
 // Work split shared by the two grids: of T tiles block c of n takes
 // [start(c), start(c + 1)), the first T % n blocks one more than the others.
@@ -70,7 +77,10 @@ struct MmaParams {
   int qtiles;   // row tiles of an item: 1 or 2
   int qrows;    // rows a Q tile has room for (a multiple of 8; the product reads 128, the rest is never used)
   int qbufs;    // Q buffers: 2, or 1 where two row tiles leave no room
-  int scale_bytes;  // one scale array of a ring entry (8-bit pools)
+  int scale_bytes;  // one scale array of a tile (8-bit pools)
+  int scale_log;    // log2 of the tiles whose scales are held: 3, or 2 with up to 4 ring entries.  The ring
+                    // may be `stages` entries ahead, and a tile's scales are needed until the
+                    // product of the queries with the keys two tiles on: 2^scale_log >= stages / 2 + 2
   int negate;   // the scale is negative: Q is negated instead
   int zero;     // the scale is zero: Q is zero and the scale 1
   int qbox;     // nodes of a query box (the tensor map's); 0: plain loads
@@ -221,26 +231,33 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_
   return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | static_cast<uint64_t>(lbo >> 4) << 16 |
          static_cast<uint64_t>(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
-// f32 accumulator, 16-bit operands (bf16 or f16), M = 128; V is read
+// f32 accumulator, 16-bit operands (bf16 or f16) or e4m3, M = 128; V is read
 // transposed (its columns are the fast axis).
 __host__ __device__ constexpr uint32_t mma_shape(bool bf16, int n, bool b_transposed) {
-  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_transposed ? 1u << 16 : 0u) |
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) /* f16 and e4m3: 0 */ | (b_transposed ? 1u << 16 : 0u) |
          static_cast<uint32_t>(n / 8) << 17 | 8u << 24;
 }
+#define SV_MMA(KIND, A, CONSTRAINT)                                                                      \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                           \
+               "tcgen05.mma.cta_group::1.kind::" KIND " [%0], " A ", %2, %3, p;\n\t}" ::"r"(d),            \
+               CONSTRAINT(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))                           \
+               : "memory")
+// D (+)= A B: A from shared (ss) or tensor memory (ts).
+template <bool E4>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
-      : "memory");
+  if (E4)
+    SV_MMA("f8f6f4", "%1", "l");
+  else
+    SV_MMA("f16", "%1", "l");
 }
+template <bool E4>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
-      : "memory");
+  if (E4)
+    SV_MMA("f8f6f4", "[%1]", "r");
+  else
+    SV_MMA("f16", "[%1]", "r");
 }
+#undef SV_MMA
 __device__ __forceinline__ bool elect_one() {
   uint32_t is;
   asm volatile(
@@ -270,6 +287,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                : "memory");
 }
+__device__ __forceinline__ void tmem_st4(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -292,28 +314,20 @@ __device__ __forceinline__ uint32_t pack_weights<__half>(float lo, float hi) {
   return d;
 }
 
-// Two codes as 16-bit floats (exact).
-__device__ __forceinline__ uint32_t half_pair(uint16_t codes) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(codes));
-  return d;
-}
+// A value's leading 4 significant bits (towards zero): an e4m3 value, where
+// its exponent allows.
+__device__ __forceinline__ float leading4(float x) { return __uint_as_float(__float_as_uint(x) & 0xfff00000u); }
 
-// Whether any 16-bit element of a word is an infinity or a NaN.
-template <typename M>
-__device__ __forceinline__ bool odd_word(uint32_t w);
-template <>
-__device__ __forceinline__ bool odd_word<__nv_bfloat16>(uint32_t w) {
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-template <>
-__device__ __forceinline__ bool odd_word<__half>(uint32_t w) {
-  return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+// Whether any element of a word is an infinity or a NaN.
+template <typename T, bool E4>
+__device__ __forceinline__ bool odd_word(uint32_t w) {
+  if (E4) return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u;
+  constexpr uint32_t e = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+  return (w & e) == e || (w >> 16 & e) == e;
 }
 
 struct Control {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t cfull[kConvStages], cempty[kConvStages];
   uint64_t scale_full[kScaleRing];
   uint64_t s_full[2], p_ready[2][2], o_done, q_full[2], q_empty[2], q_tma, drained;
   uint32_t tmem;
@@ -325,10 +339,7 @@ struct Control {
   int parent[2][64];
   float qscale[2][2 * kTile];
   float2 ml[2][kTile];
-  alignas(16) float ones[kTile];
-  alignas(16) float kscale[kScaleRing][kTile];
-  alignas(16) float vscale[kScaleRing][kTile];
-  float vmax[kScaleRing][2];
+  alignas(16) float ones[4 * kTile];  // (as scales are laid out, in boxes of 8 to 128 tokens)
   long long sums[256];
   Found found;
 };
@@ -360,128 +371,77 @@ __device__ __forceinline__ bool gave_up(const Control* s) { return *reinterpret_
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// Largest score of a row's tile (times K's scales).  Both passes over a tile
-// read 16 columns ahead of the arithmetic.
-// NC: chunks of 16 columns.
-template <bool E4, int NC>
-__device__ __forceinline__ float tile_max(uint32_t s_addr, const float* ks) {
+// Largest score of a row's tile, NC chunks of 16 columns.  Both passes over a
+// tile read a chunk ahead of the arithmetic.
+template <int NC>
+__device__ __forceinline__ float tile_max(uint32_t s_addr) {
   float top[2] = {-INFINITY, -INFINITY};
   uint32_t v[2][16];
   tmem_ld16(s_addr, v[0]);
-  float4 kn[4];
-  if (E4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) kn[i] = *reinterpret_cast<const float4*>(ks + i * 4);
-  }
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    float4 kc[4];
-    if (E4) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) kc[i] = kn[i];
-      if (c < NC - 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) kn[i] = *reinterpret_cast<const float4*>(ks + (c + 1) * 16 + i * 4);
-      }
-    }
-    tmem_wait_ld();
-    if (c < NC - 1) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      float f[4];
-#pragma unroll
-      for (int z = 0; z < 4; ++z) f[z] = __uint_as_float(v[c & 1][i + z]);
-      if (E4) f[0] *= kc[i >> 2].x, f[1] *= kc[i >> 2].y, f[2] *= kc[i >> 2].z, f[3] *= kc[i >> 2].w;
-      top[0] = fmax3(top[0], f[0], f[1]);
-      top[1] = fmax3(top[1], f[2], f[3]);
-    }
-  }
-  return fmaxf(top[0], top[1]);
-}
-
-// Weights 2^(s c2 - shift) of a row's tile into tensor memory over the
-// scores (times V's scales); returns their sum (without the scales).
-// `half` (nullable) is told when the first half of the columns is there.
-template <typename M, bool E4, int NC>
-__device__ __forceinline__ float tile_weights(uint32_t s_addr, uint32_t p_addr, const float* ks, const float* vs, float c2,
-                                              float shift, uint64_t* half) {
-  const unsigned long long c22 = splat2(c2), sh2 = splat2(-shift);
-  unsigned long long sum[2] = {0ull, 0ull};
-  uint32_t v[2][16];
-  tmem_ld16(s_addr, v[0]);
-  ulonglong2 kn[4], vn[4];
-  if (E4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      kn[i] = *reinterpret_cast<const ulonglong2*>(ks + i * 4);
-      vn[i] = *reinterpret_cast<const ulonglong2*>(vs + i * 4);
-    }
-  }
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    uint32_t out[8];
-    ulonglong2 kc[4], vc[4];
-    if (E4) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        kc[i] = kn[i];
-        vc[i] = vn[i];
-      }
-      if (c < NC - 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          kn[i] = *reinterpret_cast<const ulonglong2*>(ks + (c + 1) * 16 + i * 4);
-          vn[i] = *reinterpret_cast<const ulonglong2*>(vs + (c + 1) * 16 + i * 4);
-        }
-      }
-    }
     tmem_wait_ld();
     if (c < NC - 1) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       const uint32_t* w = &v[c & 1][i];
-      unsigned long long x = pack2(__uint_as_float(w[0]), __uint_as_float(w[1]));
-      unsigned long long y = pack2(__uint_as_float(w[2]), __uint_as_float(w[3]));
-      if (E4) {
-        x = mul2(x, kc[i >> 2].x);
-        y = mul2(y, kc[i >> 2].y);
-      }
-      x = fma2(x, c22, sh2);
-      y = fma2(y, c22, sh2);
+      top[0] = fmax3(top[0], __uint_as_float(w[0]), __uint_as_float(w[1]));
+      top[1] = fmax3(top[1], __uint_as_float(w[2]), __uint_as_float(w[3]));
+    }
+  }
+  return fmaxf(top[0], top[1]);
+}
+
+// Tells `bar` that this warp's part of a hand-over is in tensor memory.
+__device__ __forceinline__ void hand_over(uint64_t* bar) {
+  tmem_wait_st();
+  tmem_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// Weights 2^(s c2 - shift) of a row's tile into tensor memory over the scores;
+// returns their sum.  `half` is told when the first half of 128 columns is there.
+template <typename M, int NC>
+__device__ __forceinline__ float tile_weights(uint32_t s_addr, uint32_t p_addr, float c2, float shift, uint64_t* half) {
+  const unsigned long long c22 = splat2(c2), sh2 = splat2(-shift);
+  unsigned long long sum[2] = {0ull, 0ull};
+  uint32_t v[2][16];
+  tmem_ld16(s_addr, v[0]);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    uint32_t out[8];
+    tmem_wait_ld();
+    if (c < NC - 1) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const uint32_t* w = &v[c & 1][i];
+      unsigned long long x = fma2(pack2(__uint_as_float(w[0]), __uint_as_float(w[1])), c22, sh2);
+      unsigned long long y = fma2(pack2(__uint_as_float(w[2]), __uint_as_float(w[3])), c22, sh2);
       float f[4];
       unpack2(x, f[0], f[1]);
       unpack2(y, f[2], f[3]);
       f[0] = ex2f(f[0]);
       f[1] = ex2f(f[1]);
       x = pack2(f[0], f[1]);
-      if (!E4 && (i & 4)) {
+      if (i & 4) {
         // a quarter of them on the FMA pipe, whose polynomial knows no NaN
         float p2, p3;
         unpack2(ex2_poly_x2(f[2], f[3]), p2, p3);
         f[2] = f[2] == f[2] ? p2 : f[2];
         f[3] = f[3] == f[3] ? p3 : f[3];
-        y = pack2(f[2], f[3]);
       } else {
         f[2] = ex2f(f[2]);
         f[3] = ex2f(f[3]);
-        y = pack2(f[2], f[3]);
       }
+      y = pack2(f[2], f[3]);
       sum[0] = add2(sum[0], x);
       sum[1] = add2(sum[1], y);
-      if (E4) {
-        unpack2(mul2(x, vc[i >> 2].x), f[0], f[1]);
-        unpack2(mul2(y, vc[i >> 2].y), f[2], f[3]);
-      }
       out[i >> 1] = pack_weights<M>(f[0], f[1]);
       out[(i >> 1) + 1] = pack_weights<M>(f[2], f[3]);
     }
     tmem_st8(p_addr + c * 8, out);
-    if (NC == 8 && c == 3) {
-      tmem_wait_st();
-      tmem_fence_before();
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(half);
-    }
+    if (NC == 8 && c == 3) hand_over(half);
   }
   float a, b, d, e;
   unpack2(sum[0], a, b);
@@ -489,11 +449,65 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, uint32_t p_addr, 
   return (a + b) + (d + e);
 }
 
+// ---- the same for 8-bit pools.  A tile's scales lie in boxes of u = 8, 16 or
+// 32 tokens, 32 floats apart.
+struct Scales {
+  const float *k, *v;
+  int low, mul;  // u - 1, 32 / u
+  __device__ __forceinline__ int at(int col) const { return (col & ~low) * mul + (col & low); }
+};
+// v *= K's scales of 16 columns from `col`.
+__device__ __forceinline__ void scale_chunk(uint32_t (&v)[16], const Scales& sc, int col) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 8) {
+    const float4 a = *reinterpret_cast<const float4*>(sc.k + sc.at(col + i));
+    const float4 b = *reinterpret_cast<const float4*>(sc.k + sc.at(col + i) + 4);
+    const float k[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int z = 0; z < 8; ++z) v[i + z] = __float_as_uint(__uint_as_float(v[i + z]) * k[z]);
+  }
+}
+__device__ __forceinline__ void max_chunk(const uint32_t (&v)[16], float (&top)[2]) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    top[0] = fmax3(top[0], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+    top[1] = fmax3(top[1], __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+  }
+}
+// 16 columns' weights, times V's scales, as three 8-bit terms: columns [4 c,
+// 4 c + 4) of three blocks of 32 over the scores, at 0, 64 and 96.
+__device__ __forceinline__ void weigh_chunk(const uint32_t (&v)[16], const Scales& sc, int col, uint32_t s_addr, float c2,
+                                            float shift, float (&sum)[2]) {
+  uint32_t o1[4], o2[4], o3[4];
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const float4 w = *reinterpret_cast<const float4*>(sc.v + sc.at(col + (i & 8)) + (i & 4));
+    const float vs[4] = {w.x, w.y, w.z, w.w};
+    float a[4], b[4], c[4];
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      const float f = ex2f(fmaf(__uint_as_float(v[i + z]), c2, -shift));
+      sum[z & 1] += f;
+      const float x = f * vs[z];
+      a[z] = leading4(x);
+      const float r = x - a[z];
+      b[z] = leading4(r);
+      c[z] = r - b[z];
+    }
+    o1[i >> 2] = e4m3_pair(a[0], a[1]) | e4m3_pair(a[2], a[3]) << 16;
+    o2[i >> 2] = e4m3_pair(b[0], b[1]) | e4m3_pair(b[2], b[3]) << 16;
+    o3[i >> 2] = e4m3_pair(c[0], c[1]) | e4m3_pair(c[2], c[3]) << 16;
+  }
+  tmem_st4(s_addr + col / 4, o1);
+  tmem_st4(s_addr + 64 + col / 4, o2);
+  tmem_st4(s_addr + 96 + col / 4, o3);
+}
+
 // Puts -inf where a column is masked (bit i of word c allows column 32 c + i),
 // before the two passes.  8-bit pools: K's scales enter here, so that a scale
 // of a masked column does not matter, and the passes take ones.
 template <bool E4>
-__device__ __forceinline__ void mask_tile(uint32_t s_addr, const float* ks, const uint32_t (&words)[4], int lo, int hi) {
+__device__ __forceinline__ void mask_tile(uint32_t s_addr, const Scales& sc, const uint32_t (&words)[4], int lo, int hi) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const uint32_t word = words[c];
@@ -504,11 +518,9 @@ __device__ __forceinline__ void mask_tile(uint32_t s_addr, const float* ks, cons
       uint32_t v[16];
       tmem_ld16(s_addr + c * 32 + z * 16, v);
       tmem_wait_ld();
+      if (E4) scale_chunk(v, sc, c * 32 + z * 16);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (E4) v[i] = __float_as_uint(__uint_as_float(v[i]) * ks[c * 32 + z * 16 + i]);
-        v[i] = word >> (z * 16 + i) & 1u ? v[i] : 0xff800000u;
-      }
+      for (int i = 0; i < 16; ++i) v[i] = word >> (z * 16 + i) & 1u ? v[i] : 0xff800000u;
       tmem_st16(s_addr + c * 32 + z * 16, v);
     }
   }
@@ -525,7 +537,9 @@ __device__ __forceinline__ int div_rows(int n, const UDiv& d) {
 // one TMA box for 64 columns where rows of whole nodes fill a row tile.
 template <typename QT, int DP, bool E4, int SPLIT>
 __device__ __forceinline__ void load_segment(const MmaParams& p, const CUtensorMap* qmap, const Walk& w, Control* s,
-                                             unsigned char* q_tiles, int buf, uint32_t phase, int tid) {
+                                             unsigned char* q_tiles, unsigned char* q_terms, int buf, uint32_t phase,
+                                             int tid) {
+  constexpr int kTerms = std::is_same<QT, __nv_bfloat16>::value ? 2 : 3;
   const AttnParams& a = p.a;
   const int row0 = w.row0();
   const int rows = min(2 * w.pr + 1 < p.halves ? 2 * kTile : kTile, p.R - row0);
@@ -588,31 +602,58 @@ __device__ __forceinline__ void load_segment(const MmaParams& p, const CUtensorM
       if (in) v = *place(r0);
       if (p.zero) v = make_uint4(0u, 0u, 0u, 0u);
       if (p.negate) v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
-      if (E4) {
-        // a power of two brings the row's largest element to 2^14..2^15
-        float f[8];
-        load8(reinterpret_cast<const QT*>(&v), f);
-        float top = 0.0f;
+      if (!E4) {
+        if (in) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
-#pragma unroll
-        for (int o = 1; o < kUnits; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int ex = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
-        const bool plain = top == 0.0f || !(top < INFINITY);
-        const float up = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(14 - ex + 127) << 23);
-        if (in && j == 0)
-          s->qscale[buf][r0] = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(ex - 14 + 127) << 23);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= up;
-        store8(reinterpret_cast<__half*>(&v), f);
+          for (int i = 0; i < SPLIT; ++i) *place(r0 + i * (kTile / SPLIT)) = v;
+        }
+        continue;
       }
-      if (in) {
+      // a power of two brings the row's largest element to 2^7..2^8
+      float f[8];
+      load8(reinterpret_cast<const QT*>(&v), f);
+      float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < SPLIT; ++i) *place(r0 + i * (kTile / SPLIT)) = v;
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+#pragma unroll
+      for (int o = 1; o < kUnits; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int ex = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+      const bool plain = top == 0.0f || !(top < INFINITY);
+      const float up = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(7 - ex + 127) << 23);
+      if (in && j == 0)
+        s->qscale[buf][r0] = plain ? 1.0f : __uint_as_float(static_cast<unsigned int>(ex - 7 + 127) << 23);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f[i] *= up;
+        if (!(fabsf(f[i]) < INFINITY)) f[i] = __int_as_float(0x7fc00000);  // the 8-bit type has no infinity
+      }
+#pragma unroll
+      for (int n = 0; n < kTerms; ++n) {
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          float t[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            t[z] = n == kTerms - 1 ? f[i + z] : leading4(f[i + z]);
+            f[i + z] -= t[z];
+          }
+          w[i >> 2] = e4m3_pair(t[0], t[1]) | e4m3_pair(t[2], t[3]) << 16;
+        }
+        if (in) {
+#pragma unroll
+          for (int i = 0; i < SPLIT; ++i) {
+            const int r = (r0 & 127) + i * (kTile / SPLIT);
+            *reinterpret_cast<uint2*>(q_terms + ((r0 >> 7) * kTerms + n) * p.qrows * 128 + r * 128 +
+                                      (((j >> 1) ^ (r & 7)) * 16) + (j & 1) * 8) = make_uint2(w[0], w[1]);
+          }
+        }
       }
     }
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  // (the next queries arrive in the same place)
+  if (E4) asm volatile("bar.sync 2, 64;" ::: "memory");
 }
 
 // What the infinities and NaN of the drafted tokens in `seen` add to one
@@ -666,27 +707,29 @@ __device__ __forceinline__ int v_entry(bool two, int t, int T) { return two ? 2 
 // takes a share of a tile's columns, as a sequence of its own that is joined
 // at the segment's end.
 template <typename QT, int DP, bool E4, int SPLIT>
-__global__ void __launch_bounds__(E4 ? 512 : 384, 1)
+__global__ void __launch_bounds__(384, 1)
     attention_mma_kernel(const __grid_constant__ MmaParams p, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ksmap,
                          const __grid_constant__ CUtensorMap vsmap, const __grid_constant__ CUtensorMap qmap) {
-  using MT = typename std::conditional<E4, __half, QT>::type;  // operands of the products
-  constexpr int kRow = E4 ? DP : DP * 2;             // bytes of a token's row in a TMA tile
-  constexpr int kData = kTile * kRow;
-  constexpr int kLoader = E4 ? 14 : 10;              // first of the two warps that load queries ahead
-  constexpr int kConv = kTile * DP * 2;
+  constexpr int kRow = E4 ? 128 : DP * 2;            // bytes of a token's row in a tile
+  constexpr uint32_t entry = kTile * kRow;
+  constexpr int kLoader = 10;                        // first of the two warps that load queries ahead
   constexpr int kChunks = DP / 64;
-  constexpr bool kBf16 = std::is_same<MT, __nv_bfloat16>::value;
+  constexpr bool kBf16 = !E4 && std::is_same<QT, __nv_bfloat16>::value;
+  constexpr int kTerms = std::is_same<QT, __nv_bfloat16>::value ? 2 : 3;  // 8-bit terms of a query
   constexpr uint32_t kShapeS = mma_shape(kBf16, kTile, false);
   constexpr uint32_t kShapeO = mma_shape(kBf16, DP, true);
 
-  const uint32_t entry = kData + (E4 ? 2 * p.scale_bytes : 0);
-  const uint32_t qbytes = static_cast<uint32_t>(p.qtiles) * p.qrows * DP * 2;
+  // A row tile of queries, and a buffer of an item's (16 bits, or the terms);
+  // 8-bit pools: where the queries arrive in 16 bits, and the ring of scales.
+  const uint32_t qtile = static_cast<uint32_t>(p.qrows) * (E4 ? kTerms * 128 : DP * 2);
+  const uint32_t qbytes = p.qtiles * qtile;
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* qs = smem;
-  unsigned char* conv = qs + p.qbufs * qbytes;                            // E4 only
-  unsigned char* ring = conv + (E4 ? kConvStages * kConv : 0);
-  Control* s = reinterpret_cast<Control*>(ring + p.stages * entry);
+  unsigned char* qraw = qs + p.qbufs * qbytes;
+  unsigned char* ring = qraw + (E4 ? p.qtiles * p.qrows * DP * 2 : 0);
+  unsigned char* scale_ring = ring + p.stages * entry;
+  Control* s = reinterpret_cast<Control*>(scale_ring + (E4 ? 2 * p.scale_bytes << p.scale_log : 0));
   const AttnParams& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -697,13 +740,9 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&s->full[i], 1);
-      mbar_init(&s->empty[i], E4 ? 2 : 1);
+      mbar_init(&s->empty[i], 1);
     }
-    for (int i = 0; i < kConvStages; ++i) {
-      mbar_init(&s->cfull[i], 2);
-      mbar_init(&s->cempty[i], 1);
-    }
-    for (int i = 0; i < kScaleRing; ++i) mbar_init(&s->scale_full[i], 2);
+    for (int i = 0; i < kScaleRing; ++i) mbar_init(&s->scale_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s->s_full[i], 1);
       for (int z = 0; z < 2; ++z) mbar_init(&s->p_ready[i][z], 4);
@@ -718,7 +757,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
     s->abort = 0;
     s->stop = 0;
   }
-  if (tid < kTile) s->ones[tid] = 1.0f;
+  for (int i = tid; i < 4 * kTile; i += 384) s->ones[i] = 1.0f;
   if (tid == 0) {
     mbar_fence_init();
   }
@@ -745,7 +784,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
     if (warp == 8) {
       // ------------------------------------------------ producer: TMA loads
       const int nbox = kTile / p.box;
-      uint32_t e = 0, slot = 0, phase = 0;  // ring entries filled, the next one's place
+      uint32_t e = 0, slot = 0, phase = 0, tile = 0;  // ring entries filled, the next one's place; tiles of keys
       bool stop = false;  // the same in all lanes
       do {
         const bool two = 2 * w.pr + 1 < p.halves;
@@ -770,8 +809,11 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
           if (__any_sync(0xffffffffu, gave_up(s))) stop = true;
           if (stop) return;
           const uint32_t dst = smem_addr(ring + slot * entry);
-          if (lane == 0)
-            mbar_arrive_expect_tx(&s->full[slot], kData + (E4 && !values ? 2 * kTile * 4 : 0));
+          const uint32_t ti = tile & ((1u << p.scale_log) - 1u);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&s->full[slot], entry);
+            if (E4 && !values) mbar_arrive_expect_tx(&s->scale_full[ti], 2 * kTile * 4);
+          }
           __syncwarp();
           if (lane < nbox) {
             const CUtensorMap* map = values ? &vmap : &kmap;
@@ -779,9 +821,9 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
             if (E4) {
               tma_4d(dst + lane * p.box * kRow, map, 0, y, z, page, &s->full[slot]);
               if (!values) {
-                const uint32_t sd = dst + kData + lane * max(p.box * 4, 128);
-                tma_3d(sd, &ksmap, place, h, page, &s->full[slot]);
-                tma_3d(sd + p.scale_bytes, &vsmap, place, h, page, &s->full[slot]);
+                const uint32_t sd = smem_addr(scale_ring) + ti * 2 * p.scale_bytes + lane * max(p.box * 4, 128);
+                tma_3d(sd, &ksmap, place, h, page, &s->scale_full[ti]);
+                tma_3d(sd + p.scale_bytes, &vsmap, place, h, page, &s->scale_full[ti]);
               }
             } else {
 #pragma unroll
@@ -789,6 +831,7 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
                 tma_4d(dst + c * kTile * 128 + lane * p.box * 128, map, c * 64, y, z, page, &s->full[slot]);
             }
           }
+          if (!values) ++tile;
           ++e;
           if (++slot == static_cast<uint32_t>(p.stages)) slot = 0, phase ^= 1u;
         };
@@ -813,27 +856,28 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
         const uint32_t n = min(e, static_cast<uint32_t>(p.stages));
         for (uint32_t i = e - n; i < e; ++i)
           while (!mbar_try_wait(&s->full[i % p.stages], (i / p.stages) & 1u) && global_ns() - t0 < kWaitLimitNs) {}
+        if (E4)
+          for (uint32_t i = tile - min(tile, 1u << p.scale_log); i < tile; ++i)
+            while (!mbar_try_wait(&s->scale_full[i & ((1u << p.scale_log) - 1u)], (i >> p.scale_log) & 1u) &&
+                   global_ns() - t0 < kWaitLimitNs) {}
       }
     } else if (warp == 9) {
       // ------------------------------------------------ MMA issue
       // The whole warp walks the loop, so that addresses and descriptors stay
       // in uniform registers; one elected thread issues.
-      const uint32_t stages = E4 ? kConvStages : p.stages;
-      const uint32_t step_bytes = E4 ? kConv : entry;
-      const uint32_t chunk = p.qrows * 128 >> 4;  // Q's next 64 columns
-      uint64_t* const fullb = E4 ? s->cfull : s->full;
-      uint64_t* const emptyb = E4 ? s->cempty : s->empty;
+      const uint32_t stages = p.stages;
+      const uint32_t chunk = p.qrows * 128 >> 4;  // Q's next 64 columns, or its next term
       // The ring is read in its own order; a tile stays until its last product.
       uint32_t next = 0, next_phase = 0, kslot = 0, vslot = 0;
       const auto take = [&](uint32_t& slot) {
         slot = next;
-        wait(s, &fullb[slot], next_phase, a.ctrl);
+        wait(s, &s->full[slot], next_phase, a.ctrl);
         if (++next == stages) next = 0, next_phase ^= 1u;
       };
       const uint32_t acc = __shfl_sync(0xffffffffu, tmem, 0);
       const uint64_t q0 = operand(smem_addr(qs), 16, 1024);
-      const uint64_t k0 = operand(smem_addr(E4 ? conv : ring), 16, 1024);
-      const uint64_t v0 = operand(smem_addr(E4 ? conv : ring), kTile * 128, 1024);
+      const uint64_t k0 = operand(smem_addr(ring), 16, 1024);
+      const uint64_t v0 = operand(smem_addr(ring), kTile * 128, 1024);
       uint32_t seg = 0, np = 0;  // np: phases of p_ready, one bit a warpgroup
       bool stop = false;
       do {
@@ -849,42 +893,57 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
           if (x < U) {
             if (!shared) take(kslot);
             tmem_fence_after();
-            const uint64_t qd = q1 + (shared ? kTile * DP * 2 >> 4 : 0);
-            const uint64_t kd = k0 + kslot * (step_bytes >> 4);
+            const uint64_t qd = q1 + (shared ? qtile >> 4 : 0);
+            const uint64_t kd = k0 + kslot * (entry >> 4);
             if (elect_one()) {
+              // 32 bytes of a 128-byte row a step: 16 elements (64 are the next
+              // block of rows), or 32 of 8 bits (then the next term)
 #pragma unroll
-              for (int k = 0; k < DP / 16; ++k) {
-                // 16 elements are 32 bytes of a 128-byte row; 64 are the next block of rows
-                mma_ss(acc + g * kTile, qd + (k / 4) * chunk + (k % 4) * 2,
-                       kd + (k / 4) * (kTile * 128 >> 4) + (k % 4) * 2, kShapeS, k > 0);
+              for (int k = 0; k < (E4 ? kTerms * DP / 32 : DP / 16); ++k) {
+                constexpr int kSteps = E4 ? DP / 32 : 4;
+                mma_ss<E4>(acc + g * kTile, qd + (k / kSteps) * chunk + (k % kSteps) * 2,
+                           kd + (E4 ? 0 : (k / 4) * (kTile * 128 >> 4)) + (k % kSteps) * 2, kShapeS, k > 0);
               }
               mma_commit(&s->s_full[g]);
-              if (!two || g == 1) mma_commit(&emptyb[kslot]);
+              if (!two || g == 1) mma_commit(&s->empty[kslot]);
             }
             __syncwarp();
           }
           if (x > 0) {
             const uint32_t f = g ^ 1u;  // unit x - 1
             if (!two || f == 0) take(vslot);
-            const uint64_t vd = v0 + vslot * (step_bytes >> 4);
+            const uint64_t vd = v0 + vslot * (entry >> 4);
             const uint32_t o = acc + 2 * kTile + f * DP, pw = acc + f * kTile;
             const bool add = x > 2;
+            const auto accumulate = [&](int half) {
+              if (E4) {
+                // 32 tokens a step, three terms of the weights in blocks of 32 columns
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                  for (int n = 0; n < 3; ++n)
+                    mma_ts<E4>(o, pw + (n > 0 ? 32 + 32 * n : 0) + (2 * half + k) * 8,
+                               vd + static_cast<uint64_t>(2 * half + k) * (32 * 128 >> 4), kShapeO,
+                               add || half > 0 || k > 0 || n > 0);
+              } else {
+#pragma unroll
+                for (int k = 0; k < kTile / 32; ++k)
+                  mma_ts<E4>(o, pw + (half * 4 + k) * 8, vd + static_cast<uint64_t>(half * 4 + k) * (16 * 128 >> 4), kShapeO,
+                             add || half > 0 || k > 0);
+              }
+            };
             wait(s, &s->p_ready[f][0], np >> f & 1u, a.ctrl);
             tmem_fence_after();
             if (elect_one()) {
-#pragma unroll
-              for (int k = 0; k < kTile / 32; ++k)
-                mma_ts(o, pw + k * 8, vd + k * (16 * 128 >> 4), kShapeO, add || k > 0);
+              accumulate(0);
             }
             __syncwarp();
             wait(s, &s->p_ready[f][1], np >> f & 1u, a.ctrl);
             np ^= 1u << f;
             tmem_fence_after();
             if (elect_one()) {
-#pragma unroll
-              for (int k = kTile / 32; k < kTile / 16; ++k)
-                mma_ts(o, pw + k * 8, vd + k * (16 * 128 >> 4), kShapeO, true);
-              if (!two || f == 1) mma_commit(&emptyb[vslot]);
+              accumulate(1);
+              if (!two || f == 1) mma_commit(&s->empty[vslot]);
               if (x == U) mma_commit(&s->o_done);
             }
             __syncwarp();
@@ -930,130 +989,13 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
         if (seg >= static_cast<uint32_t>(p.qbufs)) empty();
         if (stop) break;
         const uint32_t buf = buffer(seg);
-        load_segment<QT, DP, E4, SPLIT>(p, &qmap, w, s, qs + buf * qbytes, buf, seg & 1u, lt);
+        load_segment<QT, DP, E4, SPLIT>(p, &qmap, w, s, E4 ? qraw : qs + buf * qbytes, qs + buf * qbytes, buf, seg & 1u, lt);
         __syncwarp();
         if (lane == 0) mbar_arrive(&s->q_full[buf]);
         ++seg;
         more = w.next(a, p.pairs);
       }
       while (!stop && oldest < seg) empty();
-    } else if (warp >= 10) {
-      // ------------------------------------------------ 8-bit to 16-bit tiles
-      if (E4) {
-        // Two teams of two warps take alternate ring entries, so that one's
-        // waits and latencies overlap the other's conversions.
-        const int team = (warp - 10) >> 1, cw = (warp - 10) & 1;
-        uint32_t slot = 0, phase = 0, cslot = 0, cphase = 0, tile = 0, seg = 0, e = 0;
-        bool stop = false;  // the same in all lanes
-        constexpr int kLanes = DP / 8;        // lanes a row, 8 codes each
-        constexpr int kRows = 32 / kLanes;    // rows a step
-        constexpr int kSteps = 64 / kRows;    // steps of this warp's 64 rows
-        constexpr int kPeriod = 8 / kRows;    // steps after which the swizzle (row & 7) repeats
-        constexpr int kBatch = 16;            // steps whose codes are held at once
-        const int row0 = cw * 64 + lane / kLanes;
-        uint32_t line[kPeriod];               // where this lane's 16 bytes of a row go
-#pragma unroll
-        for (int k = 0; k < kPeriod; ++k) {
-          const int row = row0 + k * kRows, unit = lane % kLanes;
-          line[k] = (unit >> 3) * kTile * 128 + row * 128 + (((unit & 7) ^ (row & 7)) * 16);
-        }
-        const int box_bytes = max(p.box * 4, 128);
-        do {
-          const bool two = 2 * w.pr + 1 < p.halves;
-          const int T = w.t1 - w.t0;
-#pragma unroll 1
-          for (int i = 0; i < 2 * T; ++i, ++e) {
-            if ((e & 1u) == static_cast<uint32_t>(team)) {
-              const bool values = two ? i & 1 : i == 2 * T - 1 || (i > 0 && (i & 1) == 0);
-              const int t = two ? i >> 1 : !values ? (i + 1) >> 1 : i == 2 * T - 1 ? T - 1 : (i >> 1) - 1;
-              const unsigned char* src = ring + slot * entry;
-              const long long tok0 = static_cast<long long>(w.t0 + t) * kTile;
-              const uint32_t ti = (tile + t) % kScaleRing;
-              unsigned char* const dst = conv + cslot * kConv;
-              const auto widen = [&](const uint2& c, int it) {
-                *reinterpret_cast<uint4*>(dst + line[it % kPeriod] + it / kPeriod * 1024) =
-                    make_uint4(half_pair(static_cast<uint16_t>(c.x)), half_pair(static_cast<uint16_t>(c.x >> 16)),
-                               half_pair(static_cast<uint16_t>(c.y)), half_pair(static_cast<uint16_t>(c.y >> 16)));
-              };
-              const uint2* codes = reinterpret_cast<const uint2*>(src + row0 * DP + lane % kLanes * 8);
-              wait(s, &s->full[slot], phase, a.ctrl);
-              if (!values) {
-                // scales of this warp's 64 tokens; places past the end count as 0
-                float top = 0.0f;
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  const int x = cw * 64 + z * 32 + lane;
-                  const unsigned char* at = src + kData + x / p.box * box_bytes + x % p.box * 4;
-                  const bool in = tok0 + x < w.total;
-                  const float ks = in ? *reinterpret_cast<const float*>(at) : 0.0f;
-                  float vs = in ? *reinterpret_cast<const float*>(at + p.scale_bytes) : 0.0f;
-                  if (in && tok0 + x >= w.len && !(fabsf(vs) < INFINITY)) {
-                    atomicOr(&s->odd[seg & 3][(tok0 + x - w.len) >> 5], 1u << ((tok0 + x - w.len) & 31));
-                    vs = 0.0f;
-                  }
-                  s->kscale[ti][x] = ks;
-                  s->vscale[ti][x] = vs;
-                  top = fmaxf(top, fabsf(vs) < INFINITY ? fabsf(vs) : 0.0f);
-                }
-                top = warp_max(top);
-                if (lane == 0) s->vmax[ti][cw] = top;
-              }
-              if (tok0 + kTile <= w.len) {
-#pragma unroll
-                for (int h = 0; h < kSteps; h += kBatch) {
-                  uint2 c[kBatch];
-#pragma unroll
-                  for (int it = 0; it < kBatch; ++it) c[it] = codes[(h + it) * kRows * DP / 8];
-                  if (h == 0) wait(s, &s->cempty[cslot], cphase ^ 1u, a.ctrl);
-                  if (h + kBatch >= kSteps) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s->empty[slot]);  // the rest of the tile is in registers
-                  }
-#pragma unroll
-                  for (int it = 0; it < kBatch; ++it) widen(c[it], h + it);
-                }
-              } else {
-                wait(s, &s->cempty[cslot], cphase ^ 1u, a.ctrl);
-#pragma unroll 1
-                for (int i1 = 0; i1 < kSteps; i1 += kPeriod)
-#pragma unroll
-                  for (int k = 0; k < kPeriod; ++k) {
-                    const int it = i1 + k;
-                    uint2 c = codes[it * kRows * DP / 8];
-                    const long long tok = tok0 + row0 + it * kRows;
-                    if (tok >= w.total) c = make_uint2(0u, 0u);
-                    if (values && tok >= w.len && tok < w.total) {
-                      // a drafted token's NaN must reach its own descendants only:
-                      // it counts as zero here, and its row is listed
-                      const uint32_t any = (((c.x & 0x7f7f7f7fu) + 0x01010101u) | ((c.y & 0x7f7f7f7fu) + 0x01010101u)) &
-                                           0x80808080u;
-                      if (any) {
-                        c = make_uint2(0u, 0u);
-                        atomicOr(&s->odd[seg & 3][(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
-                      }
-                    }
-                    *reinterpret_cast<uint4*>(dst + line[k] + i1 / kPeriod * 1024) =
-                        make_uint4(half_pair(static_cast<uint16_t>(c.x)), half_pair(static_cast<uint16_t>(c.x >> 16)),
-                                   half_pair(static_cast<uint16_t>(c.y)), half_pair(static_cast<uint16_t>(c.y >> 16)));
-                  }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s->empty[slot]);
-              }
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              __syncwarp();
-              if (lane == 0) {
-                mbar_arrive(&s->cfull[cslot]);
-                if (!values) mbar_arrive(&s->scale_full[ti]);
-              }
-            }
-            if (++slot == static_cast<uint32_t>(p.stages)) slot = 0, phase ^= 1u;
-            if (++cslot == kConvStages) cslot = 0, cphase ^= 1u;
-          }
-          tile += T;
-          ++seg;
-          stop = __any_sync(0xffffffffu, gave_up(s));
-        } while (!stop && w.next(a, p.pairs));
-      }
     } else {
       // ------------------------------------------------ softmax warpgroups
       const int g = warp >> 2, r = tid & 127;
@@ -1104,25 +1046,30 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
           const long long tok0 = static_cast<long long>(w.t0 + t) * kTile;
           const bool tail = tok0 + kTile > w.len;           // drafted tokens or the end
           const bool masked = tail || tok0 + kTile > w.total || missing;
-          const uint32_t ti = (tile_base + t) % kScaleRing;
+          const uint32_t ti = (tile_base + t) & ((1u << p.scale_log) - 1u);
           wait(s, &s->s_full[g], ns & 1u, a.ctrl);
           ++ns;
+          Scales sc{};
           if (E4) {
-            wait(s, &s->scale_full[ti], ((tile_base + t) / kScaleRing) & 1u, a.ctrl);
+            wait(s, &s->scale_full[ti], ((tile_base + t) >> p.scale_log) & 1u, a.ctrl);
+            sc.k = reinterpret_cast<const float*>(scale_ring + ti * 2 * p.scale_bytes);
+            sc.v = sc.k + p.scale_bytes / 4;
+            sc.low = min(p.box, 32) - 1;
+            sc.mul = 32 / min(p.box, 32);
           }
           __syncwarp();
           tmem_fence_after();
-          if (!E4 && tail && (!two || g == 0)) {
+          if (tail) {
             // Values of places past the end may be anything: zeros, so that a
             // zero weight stays zero.  A drafted token's infinities and NaN
             // are taken out as well and added by hand to the rows that see it.
-            const uint32_t e = base + v_entry(two, t, T), slot = e % p.stages;
-            wait(s, &s->full[slot], (e / p.stages) & 1u, a.ctrl);
             const long long tok = tok0 + r;
-            if (tok >= w.len) {
+            if ((!two || g == 0) && tok >= w.len) {
+              const uint32_t e = base + v_entry(two, t, T), slot = e % p.stages;
+              wait(s, &s->full[slot], (e / p.stages) & 1u, a.ctrl);
               uint4* line = reinterpret_cast<uint4*>(ring + slot * entry + r * 128);
 #pragma unroll 1
-              for (int c = 0; c < kChunks; ++c, line += kTile * 8) {
+              for (int c = 0; c < (E4 ? 1 : kChunks); ++c, line += kTile * 8) {
                 if (tok >= w.total) {
 #pragma unroll
                   for (int q = 0; q < 8; ++q) line[q ^ (r & 7)] = make_uint4(0u, 0u, 0u, 0u);
@@ -1131,14 +1078,18 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
 #pragma unroll
                   for (int q = 0; q < 8; ++q) {
                     const uint4 v = line[q ^ (r & 7)];
-                    odd |= odd_word<MT>(v.x) | odd_word<MT>(v.y) | odd_word<MT>(v.z) | odd_word<MT>(v.w);
+                    odd |= odd_word<QT, E4>(v.x) | odd_word<QT, E4>(v.y) | odd_word<QT, E4>(v.z) | odd_word<QT, E4>(v.w);
                   }
                   if (odd) {
                     uint32_t* y = reinterpret_cast<uint32_t*>(line);
 #pragma unroll 1
                     for (int q = 0; q < 32; ++q) {
-                      if (odd_word<MT>(y[q] & 0xffffu)) y[q] &= 0xffff0000u;
-                      if (odd_word<MT>(y[q] & 0xffff0000u)) y[q] &= 0xffffu;
+                      if (E4) {
+                        if (odd_word<QT, E4>(y[q])) y[q] = 0u;
+                      } else {
+                        if (odd_word<QT, E4>(y[q] & 0xffffu)) y[q] &= 0xffff0000u;
+                        if (odd_word<QT, E4>(y[q] & 0xffff0000u)) y[q] &= 0xffffu;
+                      }
                     }
                     atomicOr(&s->odd[seg & 3][(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
                   }
@@ -1146,10 +1097,24 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
               }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (E4) {
+              // The same for V's scales, by each warpgroup for itself (what two
+              // write is the same).
+              float* vs = const_cast<float*>(sc.v) + sc.at(r & ~7) + (r & 7);
+              if (tok >= w.total) {
+                *vs = 0.0f;
+              } else if (tok >= w.len && !(fabsf(*vs) < INFINITY)) {
+                *vs = 0.0f;
+                atomicOr(&s->odd[seg & 3][(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
+              }
+              if (g == 0)
+                asm volatile("bar.sync 3, 128;" ::: "memory");
+              else
+                asm volatile("bar.sync 4, 128;" ::: "memory");
+            }
           }
           __syncwarp();
           if (warp_live) {
-            const float* ks = s->kscale[ti];
             if (masked) {
               uint32_t words[4];
 #pragma unroll
@@ -1172,19 +1137,53 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
                 }
                 words[c] = y;
               }
-              mask_tile<E4>(s_addr, ks, words, copy * 4 / SPLIT, (copy * 4 + 4) / SPLIT);
-              ks = s->ones;
+              mask_tile<E4>(s_addr, sc, words, copy * 4 / SPLIT, (copy * 4 + 4) / SPLIT);
+              sc.k = s->ones;
             }
             const int c0 = copy * (8 / SPLIT);
-            float top = tile_max<E4, 8 / SPLIT>(s_addr + c0 * 16, ks + c0 * 16);
+            // 8-bit pools: the terms of the weights lie over the upper half of
+            // the scores, which is read first and held (a split row's share is
+            // held whole)
+            constexpr int kHeld = E4 ? (SPLIT > 1 ? 8 / SPLIT : 4) : 1;
+            uint32_t held[kHeld][16];
+            float top;
+            if (E4) {
+              float t2[2] = {-INFINITY, -INFINITY};
+              const int h0 = SPLIT > 1 ? c0 : 4;
+#pragma unroll
+              for (int c = 0; c < kHeld; ++c) tmem_ld16(s_addr + (h0 + c) * 16, held[c]);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < kHeld; ++c) {
+                scale_chunk(held[c], sc, (h0 + c) * 16);
+                max_chunk(held[c], t2);
+              }
+              if (SPLIT == 1) {
+#pragma unroll 2
+                for (int c = 0; c < 4; ++c) {
+                  uint32_t v[16];
+                  tmem_ld16(s_addr + c * 16, v);
+                  tmem_wait_ld();
+                  scale_chunk(v, sc, c * 16);
+                  max_chunk(v, t2);
+                }
+              }
+              top = fmaxf(t2[0], t2[1]);
+            } else {
+              top = tile_max<8 / SPLIT>(s_addr + c0 * 16);
+            }
             top = top == -INFINITY ? -INFINITY : top * c2;
             bool raise;
             float Mn = M;
             if (E4) {
-              const float vm = fmaxf(s->vmax[ti][0], s->vmax[ti][1]);
+              // the tile's largest finite scale of V, four tokens a lane
+              const float4 x = *reinterpret_cast<const float4*>(sc.v + sc.at(lane * 4 & ~7) + (lane * 4 & 4));
+              const float y0 = fabsf(x.x) < INFINITY ? fabsf(x.x) : 0.0f, y1 = fabsf(x.y) < INFINITY ? fabsf(x.y) : 0.0f;
+              const float y2 = fabsf(x.z) < INFINITY ? fabsf(x.z) : 0.0f, y3 = fabsf(x.w) < INFINITY ? fabsf(x.w) : 0.0f;
+              const float vm = warp_max(fmaxf(fmaxf(y0, y1), fmaxf(y2, y3)));
               const int ve = max(vexp, min(max(static_cast<int>(__float_as_uint(vm) >> 23) - 126, -60), 100));  // vm <= 2^ve
-              raise = top > M - vexp + kLazy || ve > vexp;
-              if (__any_sync(0xffffffffu, raise)) Mn = fmaxf(M - vexp, top) + ve;
+              raise = top > M - vexp + kLazy8 || ve > vexp;
+              if (__any_sync(0xffffffffu, raise)) Mn = fmaxf(M - vexp + kBase8, top) - kBase8 + ve;
               vexp = ve;
             } else {
               raise = top > M + kLazy;
@@ -1209,16 +1208,42 @@ __global__ void __launch_bounds__(E4 ? 512 : 384, 1)
             }
             M = Mn;
             const float shift = M == -INFINITY ? 0.0f : M;
-            const float* vs = s->vscale[ti];
-            l += tile_weights<MT, E4, 8 / SPLIT>(s_addr + c0 * 16, s_addr + c0 * 8, ks + c0 * 16, vs + c0 * 16, c2, shift,
-                                                    &s->p_ready[g][0]);
+            if (E4) {
+              float sum[2] = {0.0f, 0.0f};
+              if (SPLIT == 1) {
+#pragma unroll 2
+                for (int c = 0; c < 4; ++c) {
+                  uint32_t v[16];
+                  tmem_ld16(s_addr + c * 16, v);
+                  tmem_wait_ld();
+                  scale_chunk(v, sc, c * 16);
+                  weigh_chunk(v, sc, c * 16, s_addr, c2, shift, sum);
+                }
+                hand_over(&s->p_ready[g][0]);
+              }
+              const int h0 = SPLIT > 1 ? c0 : 4;
+#pragma unroll
+              for (int c = 0; c < kHeld; ++c) weigh_chunk(held[c], sc, (h0 + c) * 16, s_addr, c2, shift, sum);
+              l += sum[0] + sum[1];
+            } else {
+              l += tile_weights<QT, 8 / SPLIT>(s_addr + c0 * 16, s_addr + c0 * 8, c2, shift, &s->p_ready[g][0]);
+            }
             if (SPLIT > 1) {
               // the other copies' columns count as zero here
-              const uint32_t none[16] = {};
-              const int mine = copy * (4 / SPLIT) ;
+              const uint32_t none[E4 ? 8 : 16] = {};
+              if constexpr (E4) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                if (c < mine || c >= mine + 4 / SPLIT) tmem_st16(s_addr + c * 16, none);
+                for (int c = 0; c < 4; ++c)
+                  if (c < copy * (4 / SPLIT) || c >= (copy + 1) * (4 / SPLIT)) {
+                    tmem_st8(s_addr + c * 8, none);
+                    tmem_st8(s_addr + 64 + c * 8, none);
+                    tmem_st8(s_addr + 96 + c * 8, none);
+                  }
+              } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  if (c < copy * (4 / SPLIT) || c >= (copy + 1) * (4 / SPLIT)) tmem_st16(s_addr + c * 16, none);
+              }
             }
             tmem_wait_st();
           }
@@ -1475,7 +1500,7 @@ bool pool_map(CUtensorMap* m, const CacheView& c, void* base, int dtype, int box
   // an axis of one entry may have any stride: give it a valid one
   for (int i = 0; i < 3; ++i)
     if (dim[i + 1] == 1) st[i] = (i == 0 ? static_cast<cuuint64_t>(dp) * es : st[i - 1]);
-  cuuint32_t bx[4] = {static_cast<cuuint32_t>(dtype == 3 ? dp : 64), static_cast<cuuint32_t>(box), 1, 1};
+  cuuint32_t bx[4] = {static_cast<cuuint32_t>(dtype == 3 ? 128 : 64), static_cast<cuuint32_t>(box), 1, 1};
   if (head_first) {
     const cuuint64_t d = dim[1];
     dim[1] = dim[2], dim[2] = d;
@@ -1485,7 +1510,7 @@ bool pool_map(CUtensorMap* m, const CacheView& c, void* base, int dtype, int box
   }
   const cuuint32_t one[4] = {1, 1, 1, 1};
   return encoder()(m, type, 4, base, dim, st, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   dtype == 3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 bool scale_map(CUtensorMap* m, const CacheView& c, void* base, int box) {
@@ -1522,13 +1547,21 @@ cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[5], int grid, cud
   constexpr int kLimit = 227 * 1024;
   const int boxes = kTile / p.box;
   p.scale_bytes = E4 ? boxes * (p.box * 4 > 128 ? p.box * 4 : 128) : 0;
-  const int entry = kTile * DP * (E4 ? 1 : 2) + 2 * p.scale_bytes;
+  const int entry = kTile * (E4 ? 128 : DP * 2);
+  constexpr int kTerms = std::is_same<QT, __nv_bfloat16>::value ? 2 : 3;
   p.qrows = p.qtiles == 2 || p.split > 1 ? kTile : (p.R + 7) / 8 * 8;
   p.qbufs = p.qtiles == 2 ? 1 : 2;
-  const int fixed = p.qbufs * p.qtiles * p.qrows * DP * 2 + (E4 ? kConvStages * kTile * DP * 2 : 0) +
-                    static_cast<int>(sizeof(Control));
-  p.stages = (kLimit - fixed) / entry;
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  const int qrow = E4 ? kTerms * 128 : DP * 2;
+  int fixed = 0;
+  for (p.scale_log = 3; p.scale_log >= 2; --p.scale_log) {
+    fixed = p.qtiles * p.qrows * (p.qbufs * qrow + (E4 ? DP * 2 : 0)) + (E4 ? 2 * p.scale_bytes << p.scale_log : 0) +
+            static_cast<int>(sizeof(Control));
+    p.stages = (kLimit - fixed) / entry;
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    if (p.stages > 4 || p.scale_log == 2) break;
+  }
+  // Keys of the next tile have to fit beside the values of this one.
+  if (p.stages < 2) return cudaErrorInvalidValue;
   const size_t smem = fixed + static_cast<size_t>(p.stages) * entry;
   const auto kernel = attention_mma_kernel<QT, DP, E4, SPLIT>;
   static bool done[64] = {};
@@ -1540,7 +1573,7 @@ cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[5], int grid, cud
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev] = true;
   }
-  e = counted(launch_k(SV_PDL >= 1, kernel, dim3(grid), dim3(E4 ? 512 : 384), smem, st, p, maps[0], maps[1], maps[2],
+  e = counted(launch_k(SV_PDL >= 1, kernel, dim3(grid), dim3(384), smem, st, p, maps[0], maps[1], maps[2],
                        maps[3], maps[4]),
               1);
   if (e != cudaSuccess || grid < 2) return e;
