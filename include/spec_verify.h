@@ -553,8 +553,10 @@ int spec_verify_cache_read(const sv_kv_cache *cache, const int32_t *page_table,
  * infinities and NaN included.
  * 1 <= N <= 64, Hq a multiple of num_heads, Hq <= 1024, head_dim <= 256,
  * scale finite.  Scores, softmax statistics and sums are held in 32 bits;
- * the weights enter the second product rounded to the type of the values
- * (to 16-bit floats for an SV_E4M3 pool).
+ * the weights enter the second product rounded to q's type, or, for an
+ * SV_E4M3 pool, as a sum of 8-bit terms that rounds no more coarsely.  For
+ * such a pool q is a sum of 8-bit terms as well, within 2^-18 of each row's
+ * largest element.
  * scratch: device memory of spec_verify_tree_attention_scratch_size bytes,
  * 16-byte aligned, never read before it is written: no initialisation, but
  * not shared by two calls that may run at the same time.

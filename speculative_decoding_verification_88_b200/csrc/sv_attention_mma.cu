@@ -26,8 +26,9 @@
 // go into the products as they are, by the 8-bit instructions: queries are
 // scaled by a power of two a row and written as a sum of two (bfloat16) or
 // three (16-bit floats) 8-bit terms of 4 significant bits each, which is
-// exact down to 2^-18 of the row's largest element; the weights are a sum of
-// three.  An 8-bit product of n terms costs n/2 of a 16-bit one, and K and V
+// exact down to 2^-18 of the row's largest element; the weights likewise, so
+// that they keep 8 or 12 significant bits, no fewer than the output's type.
+// An 8-bit product of n terms costs n/2 of a 16-bit one, and K and V
 // cross shared memory once, without a widened copy (widening them to 16 bits
 // first, by four warps, bound the kernel by shared memory: 2450 cycles a tile
 // of 128 tokens instead of the 1425 that its 32 KB take from memory).  K's
@@ -459,12 +460,13 @@ struct Scales {
 // v *= K's scales of 16 columns from `col`.
 __device__ __forceinline__ void scale_chunk(uint32_t (&v)[16], const Scales& sc, int col) {
 #pragma unroll
-  for (int i = 0; i < 16; i += 8) {
-    const float4 a = *reinterpret_cast<const float4*>(sc.k + sc.at(col + i));
-    const float4 b = *reinterpret_cast<const float4*>(sc.k + sc.at(col + i) + 4);
-    const float k[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  for (int i = 0; i < 16; i += 4) {
+    const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(sc.k + sc.at(col + (i & 8)) + (i & 4));
+    float f[4];
+    unpack2(mul2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), k.x), f[0], f[1]);
+    unpack2(mul2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), k.y), f[2], f[3]);
 #pragma unroll
-    for (int z = 0; z < 8; ++z) v[i + z] = __float_as_uint(__uint_as_float(v[i + z]) * k[z]);
+    for (int z = 0; z < 4; ++z) v[i + z] = __float_as_uint(f[z]);
   }
 }
 __device__ __forceinline__ void max_chunk(const uint32_t (&v)[16], float (&top)[2]) {
@@ -474,33 +476,42 @@ __device__ __forceinline__ void max_chunk(const uint32_t (&v)[16], float (&top)[
     top[1] = fmax3(top[1], __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
   }
 }
-// 16 columns' weights, times V's scales, as three 8-bit terms: columns [4 c,
-// 4 c + 4) of three blocks of 32 over the scores, at 0, 64 and 96.
-__device__ __forceinline__ void weigh_chunk(const uint32_t (&v)[16], const Scales& sc, int col, uint32_t s_addr, float c2,
-                                            float shift, float (&sum)[2]) {
-  uint32_t o1[4], o2[4], o3[4];
+// Columns of the weights' terms over the scores: blocks of 32 at 0, 64 and 96.
+__host__ __device__ constexpr uint32_t term_column(int n) { return n > 0 ? 32 + 32 * n : 0; }
+// 16 columns' weights, times V's scales, as TERMS 8-bit terms: columns [col / 4,
+// col / 4 + 4) of each block.
+template <int TERMS>
+__device__ __forceinline__ void weigh_chunk(const uint32_t (&v)[16], const Scales& sc, int col, uint32_t s_addr,
+                                            unsigned long long c22, unsigned long long sh2, unsigned long long (&sum)[2]) {
+  uint32_t out[TERMS][4];
 #pragma unroll
   for (int i = 0; i < 16; i += 4) {
-    const float4 w = *reinterpret_cast<const float4*>(sc.v + sc.at(col + (i & 8)) + (i & 4));
-    const float vs[4] = {w.x, w.y, w.z, w.w};
-    float a[4], b[4], c[4];
+    const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(sc.v + sc.at(col + (i & 8)) + (i & 4));
+    uint32_t codes[TERMS][2];
 #pragma unroll
-    for (int z = 0; z < 4; ++z) {
-      const float f = ex2f(fmaf(__uint_as_float(v[i + z]), c2, -shift));
-      sum[z & 1] += f;
-      const float x = f * vs[z];
-      a[z] = leading4(x);
-      const float r = x - a[z];
-      b[z] = leading4(r);
-      c[z] = r - b[z];
+    for (int z = 0; z < 2; ++z) {
+      const unsigned long long e =
+          fma2(pack2(__uint_as_float(v[i + 2 * z]), __uint_as_float(v[i + 2 * z + 1])), c22, sh2);
+      float a, b;
+      unpack2(e, a, b);
+      unsigned long long x = pack2(ex2f(a), ex2f(b));
+      sum[z] = add2(sum[z], x);
+      x = mul2(x, z ? w.y : w.x);
+#pragma unroll
+      for (int n = 0; n < TERMS; ++n) {
+        unpack2(x, a, b);
+        if (n < TERMS - 1) {
+          a = leading4(a), b = leading4(b);
+          x = sub2(x, pack2(a, b));
+        }
+        codes[n][z] = e4m3_pair(a, b);
+      }
     }
-    o1[i >> 2] = e4m3_pair(a[0], a[1]) | e4m3_pair(a[2], a[3]) << 16;
-    o2[i >> 2] = e4m3_pair(b[0], b[1]) | e4m3_pair(b[2], b[3]) << 16;
-    o3[i >> 2] = e4m3_pair(c[0], c[1]) | e4m3_pair(c[2], c[3]) << 16;
+#pragma unroll
+    for (int n = 0; n < TERMS; ++n) out[n][i >> 2] = codes[n][0] | codes[n][1] << 16;
   }
-  tmem_st4(s_addr + col / 4, o1);
-  tmem_st4(s_addr + 64 + col / 4, o2);
-  tmem_st4(s_addr + 96 + col / 4, o3);
+#pragma unroll
+  for (int n = 0; n < TERMS; ++n) tmem_st4(s_addr + term_column(n) + col / 4, out[n]);
 }
 
 // Puts -inf where a column is masked (bit i of word c allows column 32 c + i),
@@ -716,7 +727,7 @@ __global__ void __launch_bounds__(384, 1)
   constexpr int kLoader = 10;                        // first of the two warps that load queries ahead
   constexpr int kChunks = DP / 64;
   constexpr bool kBf16 = !E4 && std::is_same<QT, __nv_bfloat16>::value;
-  constexpr int kTerms = std::is_same<QT, __nv_bfloat16>::value ? 2 : 3;  // 8-bit terms of a query
+  constexpr int kTerms = std::is_same<QT, __nv_bfloat16>::value ? 2 : 3;  // 8-bit terms of queries and weights
   constexpr uint32_t kShapeS = mma_shape(kBf16, kTile, false);
   constexpr uint32_t kShapeO = mma_shape(kBf16, DP, true);
 
@@ -917,12 +928,12 @@ __global__ void __launch_bounds__(384, 1)
             const bool add = x > 2;
             const auto accumulate = [&](int half) {
               if (E4) {
-                // 32 tokens a step, three terms of the weights in blocks of 32 columns
+                // 32 tokens a step, each with the terms of the weights
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                  for (int n = 0; n < 3; ++n)
-                    mma_ts<E4>(o, pw + (n > 0 ? 32 + 32 * n : 0) + (2 * half + k) * 8,
+                  for (int n = 0; n < kTerms; ++n)
+                    mma_ts<E4>(o, pw + term_column(n) + (2 * half + k) * 8,
                                vd + static_cast<uint64_t>(2 * half + k) * (32 * 128 >> 4), kShapeO,
                                add || half > 0 || k > 0 || n > 0);
               } else {
@@ -1047,8 +1058,6 @@ __global__ void __launch_bounds__(384, 1)
           const bool tail = tok0 + kTile > w.len;           // drafted tokens or the end
           const bool masked = tail || tok0 + kTile > w.total || missing;
           const uint32_t ti = (tile_base + t) & ((1u << p.scale_log) - 1u);
-          wait(s, &s->s_full[g], ns & 1u, a.ctrl);
-          ++ns;
           Scales sc{};
           if (E4) {
             wait(s, &s->scale_full[ti], ((tile_base + t) >> p.scale_log) & 1u, a.ctrl);
@@ -1056,9 +1065,8 @@ __global__ void __launch_bounds__(384, 1)
             sc.v = sc.k + p.scale_bytes / 4;
             sc.low = min(p.box, 32) - 1;
             sc.mul = 32 / min(p.box, 32);
+            __syncwarp();
           }
-          __syncwarp();
-          tmem_fence_after();
           if (tail) {
             // Values of places past the end may be anything: zeros, so that a
             // zero weight stays zero.  A drafted token's infinities and NaN
@@ -1113,7 +1121,20 @@ __global__ void __launch_bounds__(384, 1)
                 asm volatile("bar.sync 4, 128;" ::: "memory");
             }
           }
+          int ve = vexp;
+          if (E4 && warp_live) {
+            // the tile's largest finite scale of V, four tokens a lane
+            __syncwarp();
+            const float4 x = *reinterpret_cast<const float4*>(sc.v + sc.at(lane * 4 & ~7) + (lane * 4 & 4));
+            const float y0 = fabsf(x.x) < INFINITY ? fabsf(x.x) : 0.0f, y1 = fabsf(x.y) < INFINITY ? fabsf(x.y) : 0.0f;
+            const float y2 = fabsf(x.z) < INFINITY ? fabsf(x.z) : 0.0f, y3 = fabsf(x.w) < INFINITY ? fabsf(x.w) : 0.0f;
+            const float vm = warp_max(fmaxf(fmaxf(y0, y1), fmaxf(y2, y3)));
+            ve = max(vexp, min(max(static_cast<int>(__float_as_uint(vm) >> 23) - 126, -60), 100));  // vm <= 2^ve
+          }
+          wait(s, &s->s_full[g], ns & 1u, a.ctrl);
+          ++ns;
           __syncwarp();
+          tmem_fence_after();
           if (warp_live) {
             if (masked) {
               uint32_t words[4];
@@ -1150,11 +1171,11 @@ __global__ void __launch_bounds__(384, 1)
             if (E4) {
               float t2[2] = {-INFINITY, -INFINITY};
               const int h0 = SPLIT > 1 ? c0 : 4;
-#pragma unroll
-              for (int c = 0; c < kHeld; ++c) tmem_ld16(s_addr + (h0 + c) * 16, held[c]);
-              tmem_wait_ld();
+              tmem_ld16(s_addr + h0 * 16, held[0]);
 #pragma unroll
               for (int c = 0; c < kHeld; ++c) {
+                tmem_wait_ld();
+                if (c < kHeld - 1) tmem_ld16(s_addr + (h0 + c + 1) * 16, held[c + 1]);
                 scale_chunk(held[c], sc, (h0 + c) * 16);
                 max_chunk(held[c], t2);
               }
@@ -1176,12 +1197,6 @@ __global__ void __launch_bounds__(384, 1)
             bool raise;
             float Mn = M;
             if (E4) {
-              // the tile's largest finite scale of V, four tokens a lane
-              const float4 x = *reinterpret_cast<const float4*>(sc.v + sc.at(lane * 4 & ~7) + (lane * 4 & 4));
-              const float y0 = fabsf(x.x) < INFINITY ? fabsf(x.x) : 0.0f, y1 = fabsf(x.y) < INFINITY ? fabsf(x.y) : 0.0f;
-              const float y2 = fabsf(x.z) < INFINITY ? fabsf(x.z) : 0.0f, y3 = fabsf(x.w) < INFINITY ? fabsf(x.w) : 0.0f;
-              const float vm = warp_max(fmaxf(fmaxf(y0, y1), fmaxf(y2, y3)));
-              const int ve = max(vexp, min(max(static_cast<int>(__float_as_uint(vm) >> 23) - 126, -60), 100));  // vm <= 2^ve
               raise = top > M - vexp + kLazy8 || ve > vexp;
               if (__any_sync(0xffffffffu, raise)) Mn = fmaxf(M - vexp + kBase8, top) - kBase8 + ve;
               vexp = ve;
@@ -1209,7 +1224,8 @@ __global__ void __launch_bounds__(384, 1)
             M = Mn;
             const float shift = M == -INFINITY ? 0.0f : M;
             if (E4) {
-              float sum[2] = {0.0f, 0.0f};
+              const unsigned long long c22 = splat2(c2), sh2 = splat2(-shift);
+              unsigned long long sum[2] = {0ull, 0ull};
               if (SPLIT == 1) {
 #pragma unroll 2
                 for (int c = 0; c < 4; ++c) {
@@ -1217,14 +1233,17 @@ __global__ void __launch_bounds__(384, 1)
                   tmem_ld16(s_addr + c * 16, v);
                   tmem_wait_ld();
                   scale_chunk(v, sc, c * 16);
-                  weigh_chunk(v, sc, c * 16, s_addr, c2, shift, sum);
+                  weigh_chunk<kTerms>(v, sc, c * 16, s_addr, c22, sh2, sum);
                 }
                 hand_over(&s->p_ready[g][0]);
               }
               const int h0 = SPLIT > 1 ? c0 : 4;
 #pragma unroll
-              for (int c = 0; c < kHeld; ++c) weigh_chunk(held[c], sc, (h0 + c) * 16, s_addr, c2, shift, sum);
-              l += sum[0] + sum[1];
+              for (int c = 0; c < kHeld; ++c) weigh_chunk<kTerms>(held[c], sc, (h0 + c) * 16, s_addr, c22, sh2, sum);
+              float y0, y1, y2, y3;
+              unpack2(sum[0], y0, y1);
+              unpack2(sum[1], y2, y3);
+              l += (y0 + y1) + (y2 + y3);
             } else {
               l += tile_weights<QT, 8 / SPLIT>(s_addr + c0 * 16, s_addr + c0 * 8, c2, shift, &s->p_ready[g][0]);
             }
@@ -1235,9 +1254,8 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                   if (c < copy * (4 / SPLIT) || c >= (copy + 1) * (4 / SPLIT)) {
-                    tmem_st8(s_addr + c * 8, none);
-                    tmem_st8(s_addr + 64 + c * 8, none);
-                    tmem_st8(s_addr + 96 + c * 8, none);
+#pragma unroll
+                    for (int n = 0; n < kTerms; ++n) tmem_st8(s_addr + term_column(n) + c * 8, none);
                   }
               } else {
 #pragma unroll

@@ -473,8 +473,8 @@ def test_cache_commit_in_place_lengths_and_bad_entries(dev):
 
 def check_attention(q, cache, table, clen, parent=None, count=None, scale=None, workspace=None):
     """The bound, term by term: the output's own rounding; the weights' rounding
-    (u of their type, 16-bit floats for 8-bit pools, plus 2^-25 of the largest
-    weight where such a float is subnormal); twice the scores' error in the
+    (u of the queries' type, plus 2^-25 of the largest weight where a 16-bit
+    float is subnormal); twice the scores' error in the
     exponent (head_dim + 16 roundings of 32 bits with truncating adds, and the
     exponential's 2^-21); 32-bit sums over the tokens."""
     got = sv.tree_attention(q, cache, table, clen, parent, count=count, scale=scale, lse=True, workspace=workspace)
@@ -484,7 +484,12 @@ def check_attention(q, cache, table, clen, parent=None, count=None, scale=None, 
                                           None if count is None else count.tolist(), scale)
     D, n = q.shape[-1], max(1, int(clen.max())) + q.shape[1]
     coded = cache.k.dtype == torch.float8_e4m3fn
-    uw = u(torch.float16 if coded else q.dtype)
+    # 8-bit pools: a weight in [2^e, 2^(e+1)) enters as terms of 4 significant
+    # bits.  The first leaves a remainder below 2^(e-3), which the second rounds
+    # with a step of at most 2^(e-7): half of that is 2^-8 of the weight, u of
+    # bfloat16.  Of the second's remainder, below 2^(e-7), a third (for 16-bit
+    # floats) leaves half a step of 2^(e-11): 2^-12, under u of float16.
+    uw = u(q.dtype)
     score = smax * (D + 16) * 2.0 ** -23
     tiny = 0.0
     if coded or q.dtype == torch.float16:
