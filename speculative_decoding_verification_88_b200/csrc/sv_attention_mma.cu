@@ -48,16 +48,22 @@ constexpr int kTile = 128;        // tokens a tile, rows a half item
 constexpr int kMaxCtas = 148;     // scratch is sized for this many blocks
 constexpr int kMaxStages = 8;
 constexpr int kScaleRing = kMaxStages;  // most tiles whose scales are held (8-bit pools)
+// A segment's queries, last tile and result cost about as much as three tiles
+// (64 trees of 26 nodes: the blocks' ends lay between 103 and 133 us without
+// them in the split); they count where a block has several tiles.
+constexpr int kExtra = 3;
 constexpr int kJoinThreads = 512;
 constexpr float kLazy = 8.0f;     // log2 of what a weight may exceed 1 by
 // 8-bit weights: the largest is near 2^6, and at most 2^8.5 < 448.
 constexpr float kBase8 = 6.0f, kLazy8 = 8.5f;
 
-// Work split shared by the two grids: of T tiles block c of n takes
-// [start(c), start(c + 1)), the first T % n blocks one more than the others.
+// Work split shared by the two grids.  An item counts as its tiles and `extra`
+// more at its front, for what a segment costs besides its tiles; of all these
+// units block c of n takes [start(c), start(c + 1)), the first blocks one more
+// than the others.  A boundary among an item's extra units is one before it.
 struct Split {
   long long each;
-  int n, more;
+  int n, more, extra;
   __device__ __forceinline__ long long start(int c) const { return each * c + min(c, more); }
 };
 
@@ -110,7 +116,7 @@ __device__ __forceinline__ int tiles_of(const AttnParams& a, int b) {
 // block; all of them take part in the barriers.  b < 0: block c has none.
 struct Found {
   Split split;
-  int b, h, pr, t0;  // sequence, cache head, pair of row tiles, tile
+  int b, h, pr, into;  // sequence, cache head, pair of row tiles, units of that item before the share
   int tiles;         // of an item of that sequence
 };
 __device__ __forceinline__ void find_share(const AttnParams& a, int pairs, int blocks, int c, long long* sums, Found* f) {
@@ -140,23 +146,28 @@ __device__ __forceinline__ void find_share(const AttnParams& a, int pairs, int b
     for (int i = 0; i < 8; ++i) sums[tid * 8 + i] = incl - run + s[i];
     if (tid == 31) {
       f->split.n = static_cast<int>(min(static_cast<long long>(blocks), incl));
-      f->split.each = incl / f->split.n;
-      f->split.more = static_cast<int>(incl - f->split.each * f->split.n);
+      f->split.extra = incl >= 4ll * f->split.n ? kExtra : 0;
+      const long long units = incl + static_cast<long long>(f->split.extra) * a.B * per_b;
+      f->split.each = units / f->split.n;
+      f->split.more = static_cast<int>(units - f->split.each * f->split.n);
       f->b = -1;
     }
   }
   __syncthreads();
+  const int extra = f->split.extra;
   const long long x = c < f->split.n ? f->split.start(c) : -1;
-  if (tid < 256 && mine > 0 && x >= sums[tid] && x < sums[tid] + mine) {
-    long long rem = x - sums[tid];
+  const int seqs = min(a.B - tid * per, per);  // this thread's sequences
+  const long long first = sums[tid & 255] + static_cast<long long>(extra) * per_b * tid * per;
+  if (tid < 256 && seqs > 0 && x >= first && x < first + mine + static_cast<long long>(extra) * per_b * seqs) {
+    long long rem = x - first;
     int b = tid * per, t = tiles_of(a, b);
 #pragma unroll 1
-    while (rem >= static_cast<long long>(t) * per_b) {
-      rem -= static_cast<long long>(t) * per_b;
+    while (rem >= static_cast<long long>(t + extra) * per_b) {
+      rem -= static_cast<long long>(t + extra) * per_b;
       t = tiles_of(a, ++b);
     }
-    const int item = static_cast<int>(rem / t);
-    f->t0 = static_cast<int>(rem - static_cast<long long>(item) * t);
+    const int item = static_cast<int>(rem / (t + extra));
+    f->into = static_cast<int>(rem - static_cast<long long>(item) * (t + extra));
     f->h = item / pairs;
     f->pr = item - f->h * pairs;
     f->tiles = t;
@@ -167,7 +178,8 @@ __device__ __forceinline__ void find_share(const AttnParams& a, int pairs, int b
 
 // A block's segments in order, as every role walks them.
 struct Walk {
-  long long left;  // tiles of the share not yet walked
+  long long left;  // units of the share not yet walked, from this segment's item on
+  int extra;
   int b, h, pr;    // sequence, cache head, pair of row tiles
   int tiles;       // of an item of b
   int t0, t1;      // this segment's tiles
@@ -179,16 +191,20 @@ struct Walk {
     const long long t = (total + kTile - 1) / kTile;
     tiles = t < 1 ? 1 : static_cast<int>(t);
   }
-  __device__ __forceinline__ void begin(const AttnParams& a, const Found& f, long long share) {
-    left = share;
-    b = f.b, h = f.h, pr = f.pr, t0 = f.t0;
+  // False: the share has no tile.
+  __device__ __forceinline__ bool begin(const AttnParams& a, const Found& f, long long share) {
+    extra = f.split.extra;
+    b = f.b, h = f.h, pr = f.pr;
     first = true;
     load(a);
-    t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + left));
+    left = share + f.into;
+    t0 = max(0, f.into - extra);
+    t1 = static_cast<int>(min(static_cast<long long>(tiles), left - extra));
+    return t1 > t0;
   }
   __device__ __forceinline__ bool next(const AttnParams& a, int pairs) {
-    left -= t1 - t0;
-    if (left <= 0) return false;
+    left -= tiles + extra;
+    if (left <= extra) return false;
     first = false;
     t0 = 0;
     if (++pr == pairs) {
@@ -199,7 +215,7 @@ struct Walk {
         load(a);
       }
     }
-    t1 = static_cast<int>(min(static_cast<long long>(tiles), left));
+    t1 = static_cast<int>(min(static_cast<long long>(tiles), left - extra));
     return true;
   }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
@@ -789,9 +805,8 @@ __global__ void __launch_bounds__(384, 1)
   static_assert(kMaxCtas * sizeof(Found) <= kPlanBytes, "every block's plan fits");
   if (tid == 0) static_cast<Found*>(a.scratch)[cta] = s->found;
 
-  if (s->found.b >= 0) {
-    Walk w;
-    w.begin(a, s->found, s->found.split.start(cta + 1) - s->found.split.start(cta));
+  Walk w;
+  if (s->found.b >= 0 && w.begin(a, s->found, s->found.split.start(cta + 1) - s->found.split.start(cta))) {
     if (warp == 8) {
       // ------------------------------------------------ producer: TMA loads
       const int nbox = kTile / p.box;
@@ -1414,10 +1429,10 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
   const Found found = static_cast<const Found*>(a.scratch)[j];
   const Split split = found.split;
   const int b = found.b, h = found.h;
-  if (b < 0 || found.t0 == 0) return;  // no such share, or one that starts with an item
-  const long long lo = split.start(j) - found.t0, hi = lo + found.tiles;
+  if (b < 0 || found.into <= split.extra) return;  // no such share, or one that starts with an item
+  const long long lo = split.start(j) - found.into, hi = lo + split.extra + found.tiles;
   int first = j, last = j;  // boundaries inside the item
-  while (first > 1 && split.start(first - 1) > lo) --first;
+  while (first > 1 && split.start(first - 1) > lo + split.extra) --first;
   while (last + 1 < split.n && split.start(last + 1) < hi) ++last;
   const int parts = last - first + 2;
   const bool two = 2 * found.pr + 1 < p.halves;
