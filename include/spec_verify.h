@@ -89,7 +89,10 @@ const char *spec_verify_status_string(int status);
  * at each replay.  Calls launch: stochastic 1; greedy, multi-candidate and
  * multi-candidate rows 1 or 2 (calls of up to 512 MB of target logits stream
  * the rows in one grid and finalize in a second); threshold and tree greedy
- * 1; tree stochastic 3; commit 1; Philox 1.  Thread-safe; never fails.
+ * 1; tree stochastic 3; commit 1; Philox 1; rotary, cache write and cache
+ * read 1; tree attention 2, or 1 (a batch that fits one block, and layouts
+ * that the tensor cores' form does not take); cache commit 1 or 2.
+ * Thread-safe; never fails.
  */
 unsigned long long spec_verify_kernel_launches(void);
 
@@ -415,9 +418,10 @@ int spec_verify_greedy_noalloc_read_device_status(uint32_t *flags_host, int clea
  * is L + its depth in the tree, which is its cache position once
  * spec_verify_cache_commit has moved the accepted path.
  *
- * Shared conventions: `workspace` is nullable and only receives the SV_FLAG_*
- * bits (as in spec_verify_commit: its first 256 bytes, any other verify
- * workspace will do).  A page table entry outside [0, num_pages) is never
+ * Shared conventions: `workspace` only receives the SV_FLAG_* bits (as in
+ * spec_verify_commit: its first 256 bytes, any other verify workspace will
+ * do); NULL: they go to a status word that the library holds on each device,
+ * which spec_verify_cache_read_device_status reads.  A page table entry outside [0, num_pages) is never
  * followed (SV_FLAG_INVALID_PAGE); a token at or past max_pages * page_size
  * has no place (SV_FLAG_CAPACITY).  What then happens to it is said at each
  * call.  Entries that hold no token are not looked at.
@@ -537,6 +541,12 @@ int spec_verify_cache_read(const sv_kv_cache *cache, const int32_t *page_table,
                            int out_dtype, void *workspace, void *stream);
 
 /*
+ * Copy the current device's status word of the calls made without a workspace
+ * to *flags_host, synchronising the stream; clear it if `clear`.
+ */
+int spec_verify_cache_read_device_status(uint32_t *flags_host, int clear, void *stream);
+
+/*
  * Attention of N drafted tokens of each sequence over the cache, in which
  * their own keys and values have been written (spec_verify_cache_write):
  *   out[b, i, h] = sum_t w_t v_t,  w = softmax_t(scale q[b, i, h] . k_t)
@@ -556,7 +566,7 @@ int spec_verify_cache_read(const sv_kv_cache *cache, const int32_t *page_table,
  * the weights enter the second product rounded to q's type, or, for an
  * SV_E4M3 pool, as a sum of 8-bit terms that rounds no more coarsely.  For
  * such a pool q is a sum of 8-bit terms as well, within 2^-18 of each row's
- * largest element.
+ * largest element, and an infinity in a row of q makes the row NaN.
  * scratch: device memory of spec_verify_tree_attention_scratch_size bytes,
  * 16-byte aligned, never read before it is written: no initialisation, but
  * not shared by two calls that may run at the same time.

@@ -41,6 +41,7 @@ EXPORTS = (
     "spec_verify_rotary_frequencies", "spec_verify_rotary", "spec_verify_cache_write",
     "spec_verify_cache_read", "spec_verify_tree_attention_scratch_size",
     "spec_verify_tree_attention", "spec_verify_cache_commit",
+    "spec_verify_cache_read_device_status",
 )
 
 _lib = None
@@ -150,6 +151,8 @@ def load_library(path: str | None = None):
         lib.spec_verify_tree_attention.restype = I
         lib.spec_verify_cache_commit.argtypes = [C, P, I64, I, P, P, P, I, I, P, P, P]
         lib.spec_verify_cache_commit.restype = I
+        lib.spec_verify_cache_read_device_status.argtypes = [ctypes.POINTER(U32), I, P]
+        lib.spec_verify_cache_read_device_status.restype = I
         lib.spec_verify_kernel_launches.argtypes = []
         lib.spec_verify_kernel_launches.restype = U64
         if path is None:
@@ -760,14 +763,26 @@ def _table(page_table, B, device):
     return t.data_ptr(), t.stride(0), t.shape[1]
 
 
-def _status(workspace, device, stream):
-    """Where a call reports its flags: the workspace's status word."""
-    ws = workspace
-    if ws is None:
-        ws = _default_ws.get((device, _raw_stream(device.index))) or default_workspace(device)
-    if ws.buf is None:
-        ws.ensure(256, stream)
-    return ws.buf.data_ptr()
+def _status(workspace, stream):
+    """Where a call reports its flags: the workspace, or the device's own word (None)."""
+    if workspace is None:
+        return None
+    if workspace.buf is None:
+        workspace.ensure(256, stream)
+    return workspace.buf.data_ptr()
+
+
+def cache_device_status(clear: bool = True, device=None, stream=None) -> int:
+    """Sticky SV_FLAG_* bits raised on `device` by the cache-side calls that were
+    given no workspace (synchronises the stream)."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else \
+        torch.device(device)
+    v = ctypes.c_uint32(0)
+    with torch.cuda.device(dev):
+        _check(load_library().spec_verify_cache_read_device_status(
+            ctypes.byref(v), int(clear), _stream_ptr(stream, dev)),
+            "spec_verify_cache_read_device_status")
+    return int(v.value)
 
 
 def cache_write(cache: KVCache, page_table: torch.Tensor, cache_len: torch.Tensor,
@@ -810,7 +825,7 @@ def cache_write(cache: KVCache, page_table: torch.Tensor, cache_len: torch.Tenso
         qo = q_out.data_ptr()
     _launch(lib.spec_verify_cache_write, "spec_verify_cache_write", dev, stream,
             (cache._c, table, tstride, pages, lens, par, cnt, kr, vr, code_t, B, N,
-             None if rope is None else rope._c, qr, Hq, qo, _status(workspace, dev, stream)))
+             None if rope is None else rope._c, qr, Hq, qo, _status(workspace, stream)))
     return q_out
 
 
@@ -835,7 +850,7 @@ def cache_read(cache: KVCache, page_table: torch.Tensor, offsets: torch.Tensor, 
         return res
     _launch(lib.spec_verify_cache_read, "spec_verify_cache_read", dev, stream,
             (cache._c, table, tstride, pages, offs, st0, B, int(total), res["k"].data_ptr(),
-             res["v"].data_ptr(), _TYPES[dtype], _status(workspace, dev, stream)))
+             res["v"].data_ptr(), _TYPES[dtype], _status(workspace, stream)))
     return res
 
 
@@ -877,7 +892,7 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     _launch(lib.spec_verify_tree_attention, "spec_verify_tree_attention", dev, stream,
             (qr, code_t, cache._c, table, tstride, pages, lens, par, cnt, B, N, Hq, float(scale),
              res["out"].data_ptr(), res["lse"].data_ptr() if lse else None,
-             _status(workspace, dev, stream), scratch.data_ptr(), scratch.shape[0]))
+             _status(workspace, stream), scratch.data_ptr(), scratch.shape[0]))
     return res
 
 
@@ -905,5 +920,5 @@ def cache_commit(cache: KVCache, page_table: torch.Tensor, cache_len: torch.Tens
         new_len = _keep(torch.empty(B, dtype=torch.int32, device=dev), stream)
     _launch(lib.spec_verify_cache_commit, "spec_verify_cache_commit", dev, stream,
             (cache._c, table, tstride, pages, lens, accepted, path, B, N,
-             _ints(new_len, (B,), dev, "new_len"), _status(workspace, dev, stream)))
+             _ints(new_len, (B,), dev, "new_len"), _status(workspace, stream)))
     return new_len

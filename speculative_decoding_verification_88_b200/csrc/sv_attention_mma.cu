@@ -1594,7 +1594,7 @@ cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[5], int grid, cud
     if (p.stages > 4 || p.scale_log == 2) break;
   }
   // Keys of the next tile have to fit beside the values of this one.
-  if (p.stages < 2) return cudaErrorInvalidValue;
+  if (p.stages < 2) return cudaErrorNotSupported;
   const size_t smem = fixed + static_cast<size_t>(p.stages) * entry;
   const auto kernel = attention_mma_kernel<QT, DP, E4, SPLIT>;
   static bool done[64] = {};
@@ -1659,7 +1659,7 @@ cudaError_t launch_attention_mma(const AttnParams& a, int q_dtype, int cache_dty
   bool ok = pool_map(&maps[0], a.c, a.c.k, cache_dtype, p.box, p.head_first) &&
             pool_map(&maps[1], a.c, a.c.v, cache_dtype, p.box, p.head_first);
   if (cache_dtype == 3) ok = ok && scale_map(&maps[2], a.c, a.c.ks, p.box) && scale_map(&maps[3], a.c, a.c.vs, p.box);
-  if (!ok) return cudaErrorInvalidValue;
+  if (!ok) return cudaErrorNotSupported;  // nothing launched: the plain form takes the call
   // rows of whole nodes that fill a row tile, or all rows at once
   const int box = p.R <= kTile ? a.N : kTile % a.G == 0 ? kTile / a.G : 0;
   p.qbox = box > 0 && query_map(&maps[4], a, q_dtype, box) ? box : 0;

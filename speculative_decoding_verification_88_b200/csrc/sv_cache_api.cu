@@ -1,5 +1,6 @@
 // sv_cache_api.cu -- C ABI of the cache-side calls (include/spec_verify.h):
-// argument validation, frequencies and dispatch.  Host code only.
+// argument validation, frequencies, dispatch and the status word.
+#include <atomic>
 #include <cmath>
 
 #include "spec_verify.h"
@@ -73,7 +74,25 @@ int sms() {
   return n;
 }
 
-Ctrl* ctrl_of(void* workspace) { return static_cast<Ctrl*>(workspace); }
+// Where calls without a workspace report their flags: held by the library, so
+// that a captured graph may be replayed at any time.
+__device__ Ctrl g_status;
+
+// The control block of a call: the workspace's, or the current device's own.
+int ctrl_of(void* workspace, Ctrl** ctrl) {
+  *ctrl = static_cast<Ctrl*>(workspace);
+  if (workspace) return SV_OK;
+  static std::atomic<void*> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SV_ERR_CUDA;
+  void* at = dev < 64 ? known[dev].load(std::memory_order_relaxed) : nullptr;
+  if (!at) {
+    if (cudaGetSymbolAddress(&at, g_status) != cudaSuccess || !at) return SV_ERR_CUDA;
+    if (dev < 64) known[dev].store(at, std::memory_order_relaxed);
+  }
+  *ctrl = static_cast<Ctrl*>(at);
+  return SV_OK;
+}
 
 }  // namespace
 }  // namespace sv
@@ -177,7 +196,7 @@ extern "C" int spec_verify_cache_write(const sv_kv_cache* cache, const int32_t* 
     p.magnitude = rope->magnitude;
   }
   p.c = view(cache, page_table, table_stride, max_pages);
-  p.ctrl = ctrl_of(workspace);
+  if (const int e = ctrl_of(workspace, &p.ctrl)) return e;
   const bool vec = D % 16 == 0 && p.rd % 16 == 0 && rows_on(k, es, 16) && rows_on(v, es, 16) &&
                    (!q || (rows_on(q, es, 16) && aligned(q_out, 16))) && pool_on(cache, ces, ces == 1 ? 8 : 16);
   const int n = sms();
@@ -202,7 +221,8 @@ extern "C" int spec_verify_cache_read(const sv_kv_cache* cache, const int32_t* p
   CacheReadParams p{};
   p.c = view(cache, page_table, table_stride, max_pages);
   p.offsets = offsets, p.start = start, p.B = B, p.total = total;
-  p.k_out = k_out, p.v_out = v_out, p.ctrl = ctrl_of(workspace);
+  p.k_out = k_out, p.v_out = v_out;
+  if (const int e = ctrl_of(workspace, &p.ctrl)) return e;
   const bool vec = cache->head_dim % 8 == 0 && aligned(k_out, 16) && aligned(v_out, 16) &&
                    pool_on(cache, ces, ces == 1 ? 8 : 16);
   const int n = sms();
@@ -210,6 +230,13 @@ extern "C" int spec_verify_cache_read(const sv_kv_cache* cache, const int32_t* p
   return launch_cache_read(p, cache->dtype, out_dtype, vec, n, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? SV_OK
              : SV_ERR_CUDA;
+}
+
+extern "C" int spec_verify_cache_read_device_status(uint32_t* flags_host, int clear, void* stream) {
+  if (!flags_host) return SV_ERR_INVALID_ARG;
+  Ctrl* ctrl = nullptr;
+  if (const int e = ctrl_of(nullptr, &ctrl)) return e;
+  return spec_verify_read_device_status(ctrl, flags_host, clear, stream);
 }
 
 extern "C" int spec_verify_cache_commit(const sv_kv_cache* cache, const int32_t* page_table,
@@ -226,7 +253,8 @@ extern "C" int spec_verify_cache_commit(const sv_kv_cache* cache, const int32_t*
   CacheCommitParams p{};
   p.c = view(cache, page_table, table_stride, max_pages);
   p.cache_len = cache_len, p.accepted = accepted_len, p.path = path;
-  p.B = B, p.N = N, p.new_len = new_len, p.ctrl = ctrl_of(workspace);
+  p.B = B, p.N = N, p.new_len = new_len;
+  if (const int e = ctrl_of(workspace, &p.ctrl)) return e;
   const int es = bytes_of(cache->dtype);
   const bool vec = cache->head_dim * es % 16 == 0 && pool_on(cache, es, 16);
   const int n = sms();
@@ -265,15 +293,13 @@ extern "C" int spec_verify_tree_attention(const sv_rows* q, int q_dtype, const s
   p.cache_len = cache_len, p.parent = parent, p.count = count;
   p.B = B, p.N = N, p.Hq = Hq, p.G = Hq / cache->num_heads;
   p.c2 = static_cast<float>(1.4426950408889634 * scale);
-  p.out = out, p.lse = lse, p.ctrl = ctrl_of(workspace), p.scratch = scratch;
+  p.out = out, p.lse = lse, p.scratch = scratch;
+  if (const int e = ctrl_of(workspace, &p.ctrl)) return e;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (attention_mma_takes(p, cache->dtype)) {
-    const int n = sms();
-    if (n <= 0) return SV_ERR_CUDA;
-    e = launch_attention_mma(p, q_dtype, cache->dtype, n, st);
-  } else {
-    e = launch_attention_plain(p, q_dtype, cache->dtype, st);
-  }
+  const int n = sms();
+  if (n <= 0) return SV_ERR_CUDA;
+  cudaError_t e = cudaErrorNotSupported;
+  if (attention_mma_takes(p, cache->dtype)) e = launch_attention_mma(p, q_dtype, cache->dtype, n, st);
+  if (e == cudaErrorNotSupported) e = launch_attention_plain(p, q_dtype, cache->dtype, st);
   return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

@@ -1,0 +1,327 @@
+"""Cache-side calls as programs may make them: large and ragged batches, two
+calls at once, other streams, captured graphs, shared and repeated indices,
+empty batches, queries and rows that are not finite.  Results are compared
+with 64-bit forms, or bit for bit with the same call made alone.
+"""
+import math
+
+import pytest
+import torch
+
+import speculative_decoding_verification_88_b200 as sv
+from speculative_decoding_verification_88_b200 import build as svbuild
+
+from test_gpu_cache import T, bits, check_attention, empty_pool, make, trees
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    svbuild.build()
+
+
+@pytest.fixture
+def dev():
+    return torch.device("cuda:0")
+
+
+def launches(fn):
+    lib = sv.load_library()
+    n = lib.spec_verify_kernel_launches()
+    fn()
+    return lib.spec_verify_kernel_launches() - n
+
+
+def heads(B, N, H, D, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(B, N, H, D, generator=g).to(dtype).cuda()
+
+
+# --------------------------------------------------------- batches and splits
+
+@pytest.mark.parametrize("qt,kv", [("bf16", "bf16"), ("fp16", "e4m3")])
+@pytest.mark.parametrize("B,Hkv,G,N", [(300, 1, 2, 2), (297, 2, 1, 1), (520, 1, 1, 3)])
+def test_attention_of_many_short_sequences(dev, qt, kv, B, Hkv, G, N):
+    """More sequences than the split's threads, lengths 0 to 140, some all padding."""
+    lens = [(37 * b) % 141 for b in range(B)]
+    cache, table, clen = make(lens, N, 16, Hkv, 64, T[kv], seed=B)
+    count = torch.tensor([(b % 4 + 1) * N // 4 if b % 3 else N for b in range(B)], dtype=torch.int32, device=dev)
+    check_attention(heads(B, N, Hkv * G, 64, T[qt], 1), cache, table, clen, trees(B, N, 2), count)
+
+
+@pytest.mark.parametrize("qt,kv", [("bf16", "bf16"), ("bf16", "e4m3"), ("fp16", "e4m3")])
+def test_attention_of_one_long_sequence_next_to_short_ones(dev, qt, kv):
+    """One sequence over all blocks, others of one tile before and behind it."""
+    lens = [3, 60000, 0, 127]
+    cache, table, clen = make(lens, 3, 64, 1, 64, T[kv], seed=5)
+    check_attention(heads(4, 3, 3, 64, T[qt], 6), cache, table, clen)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("tiles", [147, 148, 149, 591, 592, 593])
+def test_attention_where_the_split_changes(dev, kv, tiles):
+    """Tiles (128 tokens each) around one and four for each of 148 blocks."""
+    cache, table, clen = make([tiles * 128 - 1], 1, 128, 1, 16, T[kv], seed=tiles)
+    check_attention(heads(1, 1, 2, 16, T["bf16"], tiles), cache, table, clen)
+
+
+@pytest.mark.parametrize("qt,kv", [("fp16", "e4m3"), ("bf16", "e4m3"), ("fp16", "fp16")])
+@pytest.mark.parametrize("page", [8, 24])
+def test_attention_with_the_least_shared_memory(dev, qt, kv, page):
+    """Two row tiles and the smallest boxes: the fewest ring entries."""
+    cache, table, clen = make([700, 0, 33], 64, page, 1, 128, T[kv], seed=page)
+    check_attention(heads(3, 64, 4, 128, T[qt], 3), cache, table, clen, trees(3, 64, 4))
+
+
+# ------------------------------------------------------------ views and values
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_attention_of_broadcast_and_transposed_queries_and_tables(dev, kv):
+    cache, table, clen = make([200], 5, 16, 2, 64, T[kv])
+    clen = clen.repeat(3)
+    one = heads(1, 5, 4, 64, T["bf16"], 1)
+    want = sv.tree_attention(one.repeat(3, 1, 1, 1), cache, table.repeat(3, 1), clen)["out"]
+    assert torch.equal(want, sv.tree_attention(one.expand(3, 5, 4, 64), cache, table.expand(3, -1), clen)["out"])
+    turned = one.repeat(3, 1, 1, 1).transpose(1, 2).contiguous().transpose(1, 2)
+    assert torch.equal(want, sv.tree_attention(turned, cache, table.repeat(3, 1), clen)["out"])
+    same = heads(1, 1, 1, 64, T["bf16"], 2)
+    want = sv.tree_attention(same.repeat(3, 5, 4, 1), cache, table.repeat(3, 1), clen)["out"]
+    assert torch.equal(want, sv.tree_attention(same.expand(3, 5, 4, 64), cache, table.repeat(3, 1), clen)["out"])
+
+
+@pytest.mark.parametrize("qt,kv", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3"), ("fp16", "e4m3")])
+@pytest.mark.parametrize("page,D,layout,L", [(16, 64, "hnd", 300), (16, 128, "nhd", 40), (12, 66, "padded", 50)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_attention_of_queries_that_are_not_finite(dev, qt, kv, page, D, layout, L, bad):
+    """Their own rows are NaN (the keys have both signs), all others as without them."""
+    cache, table, clen = make([L], 4, page, 2, D, T[kv], layout)
+    q = heads(1, 4, 6, D, T[qt], 1)
+    clean = sv.tree_attention(q, cache, table, clen, lse=True)
+    q[0, 1, 2, 7] = bad
+    q[0, 3, 5] = bad
+    got = sv.tree_attention(q, cache, table, clen, lse=True)
+    odd = torch.zeros(1, 4, 6, dtype=torch.bool, device=dev)
+    odd[0, 1, 2] = odd[0, 3, 5] = True
+    assert torch.isnan(got["out"][odd]).all()
+    assert torch.equal(got["out"][~odd], clean["out"][~odd]) and torch.equal(got["lse"][~odd], clean["lse"][~odd])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page,D,layout", [(16, 64, "hnd"), (12, 66, "padded")])
+def test_attention_to_nothing_but_bad_pages(dev, kv, page, D, layout):
+    """Zeros and -inf, not NaN, where no page of a row is valid."""
+    cache, table, clen = make([200, 100], 3, page, 1, D, T[kv], layout)
+    q = heads(2, 3, 2, D, T["bf16"], 1)
+    want = sv.tree_attention(q, cache, table, clen, lse=True)
+    table[0] = -1
+    got = sv.tree_attention(q, cache, table, clen, lse=True)
+    assert (got["out"][0] == 0).all() and (got["lse"][0] == -math.inf).all()
+    assert torch.equal(got["out"][1], want["out"][1]) and torch.equal(got["lse"][1], want["lse"][1])
+
+
+def test_two_sequences_that_share_their_context(dev):
+    """The same pages in two rows of the table, as shared prefixes have them."""
+    cache, table, clen = make([128, 128], 4, 16, 2, 64, T["bf16"])
+    alone = table.clone()
+    table[1, :8] = table[0, :8]
+    q = heads(1, 4, 4, 64, T["bf16"], 1).repeat(2, 1, 1, 1)
+    got = sv.tree_attention(q, cache, table, clen)["out"]
+    assert torch.equal(got[0], sv.tree_attention(q, cache, alone, clen)["out"][0])
+    offs = torch.tensor([0, 128, 256], dtype=torch.int32, device=dev)
+    rows = sv.cache_read(cache, table, offs, 256)
+    assert torch.equal(rows["k"][:128], rows["k"][128:])
+
+
+def test_commit_of_a_path_that_names_one_node_twice(dev):
+    """Each row receives what the named row held before the call."""
+    cache, table, clen = make([20], 8, 16, 2, 64, T["bf16"])
+    offs = torch.tensor([0, 28], dtype=torch.int32, device=dev)
+    was = sv.cache_read(cache, table, offs, 28)
+    path = torch.tensor([[0, 5, 5, 3, 7, 7, 7, 7]], dtype=torch.int32, device=dev)
+    acc = torch.tensor([7], dtype=torch.int32, device=dev)
+    new = sv.cache_commit(cache, table, clen, {"accepted_len": acc, "path": path})
+    now = sv.cache_read(cache, table, offs, 28)
+    assert new.tolist() == [28]
+    at = list(range(20)) + [20 + j for j in (0, 5, 5, 3, 7, 7, 7, 7)]
+    assert torch.equal(now["k"], was["k"][at]) and torch.equal(now["v"], was["v"][at])
+
+
+# ------------------------------------------------------ empty and tiny batches
+
+def test_empty_batches_do_nothing(dev):
+    cache, table, clen = make([5], 2, 16, 2, 64, T["bf16"])
+    before = bits(cache.k), bits(cache.v)
+    none_t, none_l = table[:0], clen[:0]
+
+    def calls():
+        for B, N in ((0, 3), (1, 0)):
+            t, ln = (none_t, none_l) if B == 0 else (table, clen)
+            k = torch.zeros(B, N, 2, 64, dtype=torch.bfloat16, device=dev)
+            sv.cache_write(cache, t, ln, k, k)
+        q = torch.zeros(0, 3, 4, 64, dtype=torch.bfloat16, device=dev)
+        assert sv.tree_attention(q, cache, none_t, none_l)["out"].shape == q.shape
+        offs = torch.zeros(2, dtype=torch.int32, device=dev)
+        assert sv.cache_read(cache, table, offs, 0)["k"].shape == (0, 2, 64)
+        assert sv.cache_commit(cache, none_t, none_l, {"accepted_len": none_l}).shape == (0,)
+        x = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device=dev)
+        pos = torch.zeros(0, dtype=torch.int32, device=dev)
+        assert sv.rotary(x, pos, sv.rotary_frequencies(64, device=dev)).shape == x.shape
+
+    assert launches(calls) == 0
+    assert torch.equal(bits(cache.k), before[0]) and torch.equal(bits(cache.v), before[1])
+
+
+def test_launch_counts(dev):
+    """As documented, for both forms of attention and of the commit."""
+    rope = sv.rotary_frequencies(64, device=dev)
+    for page, layout, L, grids in ((16, "hnd", 900, 2), (128, "hnd", 20, 1), (12, "padded", 900, 1)):
+        cache, table, clen = make([L], 3, page, 1, 64, T["bf16"], layout)
+        if page == 128:
+            table = table[:, :1].contiguous()
+        q = heads(1, 3, 2, 64, T["bf16"], 1)
+        assert launches(lambda: sv.tree_attention(q, cache, table, clen)) == grids
+        k = heads(1, 3, 1, 64, T["bf16"], 2)
+        assert launches(lambda: sv.cache_write(cache, table, clen, k, k, rope=rope, q=q)) == 1
+        pos = torch.zeros(1, 3, dtype=torch.int32, device=dev)
+        assert launches(lambda: sv.rotary(q, pos, rope)) == 1
+        res = {"accepted_len": torch.ones_like(clen), "path": torch.tensor([[0, 2, -1]], dtype=torch.int32, device=dev)}
+        assert launches(lambda: sv.cache_commit(cache, table, clen, res)) == 1
+        assert launches(lambda: sv.cache_commit(cache, table, clen, res, new_len=clen)) == 2
+        offs = torch.tensor([0, 10], dtype=torch.int32, device=dev)
+        assert launches(lambda: sv.cache_read(cache, table, offs, 10)) == 1
+
+
+# ------------------------------------------------------------ at the same time
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_calls_at_once_on_two_streams_of_one_cache(dev, kv):
+    """Readers of one pool on two streams, and a writer of other pages of it."""
+    cache, table, clen = make([900, 2000, 40], 8, 16, 2, 128, T[kv])
+    qs = [heads(3, 8, 8, 128, T["bf16"], s) for s in (1, 2)]
+    parents = [trees(3, 8, s) for s in (3, 4)]
+    want = [sv.tree_attention(q, cache, table, clen, p)["out"] for q, p in zip(qs, parents)]
+    offs = torch.tensor([0, 900, 2900, 2940], dtype=torch.int32, device=dev)
+    rows = sv.cache_read(cache, table, offs, 2940)
+    spare = empty_pool(8, 16, 2, 128, T[kv])
+    own = torch.arange(8, dtype=torch.int32, device=dev)[None].contiguous()
+    k = heads(1, 100, 2, 128, T["bf16"], 9)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(sv.tree_attention(qs[i], cache, table, clen, parents[i])["out"])
+        with torch.cuda.stream(streams[2]):
+            sv.cache_write(spare, own, torch.zeros_like(clen[:1]), k, k)
+            back = sv.cache_read(cache, table, offs, 2940)
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+    assert torch.equal(back["k"], rows["k"]) and torch.equal(back["v"], rows["v"])
+
+
+def test_flags_of_calls_without_a_workspace(dev):
+    """They reach the device's own word, from eager calls on any stream and from
+    a graph replayed after workspaces have come, grown and gone."""
+    cache, table, clen = make([40, 40], 2, 16, 2, 64, T["bf16"])
+    table[1, 0] = 10 ** 6
+    q = heads(2, 2, 4, 64, T["bf16"], 1)
+    sv.cache_device_status()
+    want = sv.tree_attention(q, cache, table, clen)["out"]
+    assert sv.cache_device_status(clear=False) == sv.SV_FLAG_INVALID_PAGE
+    assert sv.cache_device_status() == sv.SV_FLAG_INVALID_PAGE and sv.cache_device_status() == 0
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    sv.tree_attention(q, cache, table, clen, stream=other)
+    assert sv.cache_device_status(stream=other) == sv.SV_FLAG_INVALID_PAGE
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = sv.tree_attention(q, cache, table, clen)["out"]
+    assert sv.cache_device_status() == 0
+    for n in (1 << 10, 1 << 20, 1 << 24):
+        sv.default_workspace(dev).ensure(n)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and sv.cache_device_status() == sv.SV_FLAG_INVALID_PAGE
+
+
+def test_captured_step_replayed_on_new_contents(dev):
+    """One captured step, replayed while lengths, tables and trees change in
+    place, gives what eager calls give on the same contents."""
+    B, N = 3, 6
+    cache, table, clen = make([30, 0, 200], 64, 16, 2, 64, T["e4m3"])
+    rope = sv.rotary_frequencies(64, device=dev)
+    parent = trees(B, N, 1)
+    q, k, v = (heads(B, N, h, 64, T["bf16"], h) for h in (4, 2, 2))
+    path = torch.zeros(B, N, dtype=torch.int32, device=dev)
+    acc = torch.zeros(B, dtype=torch.int32, device=dev)
+
+    def step(c, lens):
+        turned = sv.cache_write(c, table, lens, k, v, parent=parent, rope=rope, q=q)
+        out = sv.tree_attention(turned, c, table, lens, parent)["out"]
+        return out, sv.cache_commit(c, table, lens, {"accepted_len": acc, "path": path}, new_len=lens)
+
+    twin = sv.KVCache(*(x.clone() for x in (cache.k, cache.v, cache.k_scale, cache.v_scale)))
+    lens = clen.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, _ = step(cache, clen)
+    for s in range(5):
+        parent.copy_(trees(B, N, 10 + s))
+        path.copy_(torch.tensor([[0, 1, 3, -1, -1, -1], [0, 2, 4, 5, -1, -1], [0, -1, -1, -1, -1, -1]], dtype=torch.int32))
+        acc.copy_(torch.tensor([2, 3, 0], dtype=torch.int32))
+        q.add_(0.25)
+        graph.replay()
+        want, _ = step(twin, lens)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(clen, lens)
+        assert torch.equal(bits(cache.k_scale), bits(twin.k_scale))
+        assert torch.equal(bits(cache.k.view(torch.uint8)), bits(twin.k.view(torch.uint8)))
+
+
+def test_results_in_the_callers_tensors(dev):
+    """Preallocated results are used and are all that is written."""
+    cache, table, clen = make([100, 7], 3, 16, 2, 64, T["bf16"])
+    q = heads(2, 3, 4, 64, T["bf16"], 1)
+    want = sv.tree_attention(q, cache, table, clen, lse=True)
+    room = torch.full((4, 3, 4, 64), 7.0, dtype=torch.bfloat16, device=dev)
+    res = sv.tree_attention(q, cache, table, clen, lse=True, out={"out": room[1:3], "lse": torch.empty(2, 3, 4, device=dev)})
+    assert res["out"].data_ptr() == room[1].data_ptr()
+    assert torch.equal(room[1:3], want["out"]) and torch.equal(res["lse"], want["lse"])
+    assert (room[0] == 7).all() and (room[3] == 7).all()
+    odd = torch.full((2 * 3 * 4 * 64 + 9,), 7.0, dtype=torch.bfloat16, device=dev)
+    sv.tree_attention(q, cache, table, clen, out={"out": odd[1:-8].view(2, 3, 4, 64)})  # on 2-byte boundaries only
+    # another kernel: both round the result (2^-8 of it each) and one its weights
+    # (2^-8 of the sum of w |v|); neither exceeds the largest |v|
+    top = torch.nan_to_num(cache.v.float(), 0.0).abs().max().item()
+    assert (odd[1:-8].view(2, 3, 4, 64).float() - want["out"].float()).abs().max() <= 3 * 2.0 ** -8 * top + 2.0 ** -12
+    assert odd[0] == 7 and (odd[-8:] == 7).all()
+
+
+def test_layers_of_one_pool(dev):
+    """Each layer's calls work on that layer alone; a commit moves all."""
+    layers, N = 3, 4
+    cache = empty_pool(6, 16, 2, 64, T["e4m3"], layers=layers)
+    table = torch.tensor([[4, 0, 3]], dtype=torch.int32, device=dev)
+    clen = torch.tensor([30], dtype=torch.int32, device=dev)
+    zero = torch.zeros_like(clen)
+    rows = [heads(1, 34, 2, 64, T["bf16"], s) for s in range(layers)]
+    for i, x in enumerate(rows):
+        sv.cache_write(cache.layer(i), table, zero, x, x * 2)
+    offs = torch.tensor([0, 34], dtype=torch.int32, device=dev)
+    was = [sv.cache_read(cache.layer(i), table, offs, 34) for i in range(layers)]
+    q = heads(1, N, 4, 64, T["bf16"], 9)
+    for i in range(layers):
+        alone = empty_pool(6, 16, 2, 64, T["e4m3"])
+        sv.cache_write(alone, table, zero, rows[i], rows[i] * 2)
+        assert torch.equal(sv.tree_attention(q, cache.layer(i), table, clen)["out"],
+                           sv.tree_attention(q, alone, table, clen)["out"])
+    path = torch.tensor([[0, 2, 3, -1]], dtype=torch.int32, device=dev)
+    sv.cache_commit(cache, table, clen, {"accepted_len": zero + 2, "path": path})
+    at = list(range(31)) + [32, 33, 33]
+    for i in range(layers):
+        now = sv.cache_read(cache.layer(i), table, offs, 34)
+        assert torch.equal(now["k"], was[i]["k"][at]) and torch.equal(now["v"], was[i]["v"][at])
