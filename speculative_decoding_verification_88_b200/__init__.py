@@ -569,7 +569,7 @@ _ROPE = {"none": 0, "linear": 1, "bands": 2, "yarn": 3}
 # looked up without making objects.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = torch.cuda.current_device
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch(fn, what, device, stream, args):
@@ -589,6 +589,21 @@ def _keep(t, stream):
     if stream is not None:
         t.record_stream(stream)
     return t
+
+
+def _result(out, key, shape, dtype, device, stream):
+    """_out, refusing a caller's tensor on another device."""
+    made = _out(out, key, shape, dtype, device)
+    if made.device != device:
+        raise ValueError(f"out[{key!r}] must be on {device}")
+    return made if stream is None else _keep(made, stream)
+
+
+def _like(t, stream):
+    """A new contiguous tensor of t's shape and type."""
+    made = torch.empty_like(t) if t.is_contiguous() else \
+        torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return made if stream is None else _keep(made, stream)
 
 
 def _ints(t, shape, device, name):
@@ -734,8 +749,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, rope: Rotary, *, inverse: b
     if rope.inv_freq.device != dev:
         raise ValueError("the rotary frequencies must be on x's device")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        _keep(out, stream)
+        out = _like(x, stream)
     elif out.dtype != x.dtype or out.device != dev or out.shape != x.shape:
         raise ValueError("out must have x's type, device and shape")
     if x.numel() == 0:
@@ -757,10 +771,11 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, rope: Rotary, *, inverse: b
 
 def _table(page_table, B, device):
     t = page_table
-    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 2 or
-            t.shape[0] != B or t.device != device or (t.shape[1] > 1 and t.stride(1) != 1)):
+    shape, stride = (t.shape, t.stride()) if isinstance(t, torch.Tensor) else ((), ())
+    if (len(shape) != 2 or t.dtype is not torch.int32 or shape[0] != B or t.device != device or
+            (stride[1] != 1 and shape[1] > 1)):
         raise TypeError(f"page_table must be int32 [{B}, max_pages] on {device}, rows contiguous")
-    return t.data_ptr(), t.stride(0), t.shape[1]
+    return t.data_ptr(), stride[0], shape[1]
 
 
 def _status(workspace, stream):
@@ -815,10 +830,9 @@ def cache_write(cache: KVCache, page_table: torch.Tensor, cache_len: torch.Tenso
         _, qr = _rows(q, None, cache.head_dim, "q", k)
         Hq = q.shape[2]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = _like(q, stream)
             if cnt is not None:
                 q_out.zero_()  # padding rows are left as they were
-            _keep(q_out, stream)
         elif (q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.device != dev or
               not q_out.is_contiguous()):
             raise ValueError("q_out must be a contiguous tensor like q")
@@ -845,7 +859,7 @@ def cache_read(cache: KVCache, page_table: torch.Tensor, offsets: torch.Tensor, 
     st0 = _optional_ints(start, (B,), dev, "start")
     table, tstride, pages = _table(page_table, B, dev)
     shape = (int(total), cache.num_heads, cache.head_dim)
-    res = {x: _keep(_out(out, x, shape, dtype, dev), stream) for x in ("k", "v")}
+    res = {x: _result(out, x, shape, dtype, dev, stream) for x in ("k", "v")}
     if total == 0:
         return res
     _launch(lib.spec_verify_cache_read, "spec_verify_cache_read", dev, stream,
@@ -880,11 +894,11 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     cnt = _optional_ints(count, (B,), dev, "count")
     table, tstride, pages = _table(page_table, B, dev)
     if out is None:
-        res = {"out": _keep(torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev), stream)}
+        res = {"out": _like(q, stream)}
     else:
-        res = {"out": _out(out, "out", (B, N, Hq, D), q.dtype, dev)}
+        res = {"out": _result(out, "out", (B, N, Hq, D), q.dtype, dev, stream)}
     if lse:
-        res["lse"] = _keep(_out(out, "lse", (B, N, Hq), torch.float32, dev), stream)
+        res["lse"] = _result(out, "lse", (B, N, Hq), torch.float32, dev, stream)
     if scale is None:
         scale = D ** -0.5
     need = _scratch_bytes(B, N, Hq, cache.num_heads, D)

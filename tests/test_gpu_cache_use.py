@@ -325,3 +325,71 @@ def test_layers_of_one_pool(dev):
     for i in range(layers):
         now = sv.cache_read(cache.layer(i), table, offs, 34)
         assert torch.equal(now["k"], was[i]["k"][at]) and torch.equal(now["v"], was[i]["v"][at])
+
+
+def test_refusals_of_the_python_calls(dev):
+    """Tensors of another type, shape, device or layout are refused before any launch."""
+    cache, table, clen = make([40], 3, 16, 2, 64, T["bf16"])
+    q, k = heads(1, 3, 4, 64, T["bf16"], 1), heads(1, 3, 2, 64, T["bf16"], 2)
+    rope = sv.rotary_frequencies(64, device=dev)
+    offs = torch.tensor([0, 10], dtype=torch.int32, device=dev)
+    acc = torch.zeros_like(clen)
+    pos = torch.zeros(1, 3, dtype=torch.int32, device=dev)
+    wide = torch.zeros(1, 3, 4, 128, dtype=torch.bfloat16, device=dev)[..., ::2]
+    coded = empty_pool(4, 16, 2, 64, T["e4m3"])
+    bad = [
+        lambda: sv.tree_attention(q.cpu(), cache, table, clen),
+        lambda: sv.tree_attention(q.float(), cache, table, clen),
+        lambda: sv.tree_attention(q.half(), cache, table, clen),
+        lambda: sv.tree_attention(q[..., :32].contiguous(), cache, table, clen),
+        lambda: sv.tree_attention(q[:, :, :3].contiguous(), cache, table, clen),
+        lambda: sv.tree_attention(wide, cache, table, clen),
+        lambda: sv.tree_attention(q, cache, table.long(), clen),
+        lambda: sv.tree_attention(q, cache, table.cpu(), clen),
+        lambda: sv.tree_attention(q, cache, table[0], clen),
+        lambda: sv.tree_attention(q, cache, table.repeat(2, 1), clen),
+        lambda: sv.tree_attention(q, cache, table, clen.long()),
+        lambda: sv.tree_attention(q, cache, table, clen, pos[:, :2]),
+        lambda: sv.tree_attention(q, cache, table, clen, scale=math.inf),
+        lambda: sv.tree_attention(q, cache, table, clen, out={"out": torch.empty(1, 3, 4, 64, dtype=torch.bfloat16)}),
+        lambda: sv.tree_attention(q, cache, table, clen, out={"out": torch.empty_like(q).float()}),
+        lambda: sv.tree_attention(heads(1, 65, 4, 64, T["bf16"], 1), cache, table, clen),
+        lambda: sv.tree_attention(q[:, :0], cache, table, clen),
+        lambda: sv.cache_write(cache, table, clen, k, k.half()),
+        lambda: sv.cache_write(cache, table, clen, k.half(), k.half()),
+        lambda: sv.cache_write(cache, table, clen, k, k[:, :2]),
+        lambda: sv.cache_write(cache, table, clen, q, q),
+        lambda: sv.cache_write(cache, table, clen, k, k, q=q),
+        lambda: sv.cache_write(cache, table, clen, k, k, q=q.half(), rope=rope),
+        lambda: sv.cache_write(cache, table, clen, k, k, rope=sv.rotary_frequencies(128, device=dev)),
+        lambda: sv.cache_write(cache, table, clen, k, k, count=clen[0]),
+        lambda: sv.cache_read(cache, table, offs, 10, torch.float8_e4m3fn),
+        lambda: sv.cache_read(cache, table, offs.long(), 10),
+        lambda: sv.cache_read(cache, table, offs, 10, start=offs),
+        lambda: sv.cache_read(cache, table, offs, 10, out={"k": torch.empty(10, 2, 64, dtype=torch.bfloat16)}),
+        lambda: sv.cache_commit(cache, table, clen, {"accepted_len": acc.long()}),
+        lambda: sv.cache_commit(cache, table, clen, {"accepted_len": acc, "path": pos[0]}),
+        lambda: sv.cache_commit(cache, table, clen, {"accepted_len": acc, "path": pos}, new_len=clen.long()),
+        lambda: sv.rotary(q, pos.long(), rope),
+        lambda: sv.rotary(q, pos[0], rope),
+        lambda: sv.rotary(coded.k[:1, :3], pos[:, :2], rope),
+        lambda: sv.rotary(q, pos, sv.rotary_frequencies(128, device=dev)),
+        lambda: sv.rotary(q, pos, rope, out=q.float()),
+        lambda: sv.rotary(wide, pos, rope),
+        lambda: sv.Rotary(rope.inv_freq.float()),
+        lambda: sv.Rotary(rope.inv_freq.cpu()),
+        lambda: sv.rotary_frequencies(63, device=dev),
+        lambda: sv.KVCache(coded.k, coded.v),
+        lambda: sv.KVCache(cache.k, cache.v, coded.k_scale, coded.v_scale),
+        lambda: sv.KVCache(cache.k, cache.v.contiguous()[:1]),
+        lambda: sv.KVCache(cache.k.cpu(), cache.v.cpu()),
+        lambda: cache.layer(0),
+    ]
+
+    def all_of_them():
+        for i, call in enumerate(bad):
+            with pytest.raises((TypeError, ValueError, RuntimeError)):
+                call()
+                pytest.fail(f"call {i} was not refused")
+
+    assert launches(all_of_them) == 0
