@@ -412,9 +412,10 @@ __global__ void __launch_bounds__(kRotThreads, E4 ? 3 : VEC ? 4 : 2)
   const Unit turned = unit_at<VEC>(lane, turn, p.rd, p.D, INTER), plain = unit_at<VEC>(lane, false, 0, p.D, false);
   const int a0 = angle_of<VEC>(0, lane, p.rd, turned.weave), a1 = angle_of<VEC>(4, lane, p.rd, turned.weave);
   const int rows = p.Hq + (WRITE ? 2 * p.c.heads : 0);
-  for (long long t0 = static_cast<long long>(blockIdx.x) * n.group; t0 < p.tokens;
-       t0 += static_cast<long long>(gridDim.x) * n.group) {
-    const int group = static_cast<int>(min(static_cast<long long>(n.group), p.tokens - t0));
+  // an even share of the tokens, a group at a time
+  const long long t1 = p.tokens * (blockIdx.x + 1ll) / gridDim.x;
+  for (long long t0 = p.tokens * blockIdx.x / gridDim.x; t0 < t1; t0 += n.group) {
+    const int group = static_cast<int>(min(static_cast<long long>(n.group), t1 - t0));
     prepare_tokens<E4>(p, n, t0, group, cs, csd, dst, sdst, pos);
     int k = 0, pass = 0;  // next row to load, and its token's places in q, k and v
     int b = quotient(static_cast<int>(t0), n.div_N), j = static_cast<int>(t0) - b * p.N;
@@ -515,12 +516,14 @@ static cudaError_t launch_rotate_t(const RotateParams& p, bool e4, bool vec, int
   const int threads = (n.rows * n.UP + 31) / 32 * 32;
   // blocks that fit at once (64 registers a thread, 80 or 128 in the larger forms)
   const long long fit = static_cast<long long>(sms) * ((e4 ? 768 : vec ? 1024 : 512) / threads);
+  const int blocks = static_cast<int>(p.tokens < fit ? p.tokens : fit);
   n.group = kRotGroup;
   if (p.rd > 0 && n.group > kRotAngles / (p.rd / 2)) n.group = kRotAngles / (p.rd / 2);
-  while (n.group > 1 && p.tokens / n.group < 4 * fit) n.group /= 2;
+  // groups of one size in a block's share
+  const long long share = (p.tokens + blocks - 1) / blocks, rounds = (share + n.group - 1) / n.group;
+  n.group = static_cast<int>((share + rounds - 1) / rounds);
   n.div_N = make_udiv(static_cast<unsigned int>(p.N));
   n.div_half = make_udiv(static_cast<unsigned int>(p.rd > 0 ? p.rd / 2 : 1));
-  const long long blocks = (p.tokens + n.group - 1) / n.group;
   const auto pick = [&](auto write, auto coded, auto wide) {
     constexpr bool W = decltype(write)::value, E = decltype(coded)::value, V = decltype(wide)::value;
     return p.interleaved ? rotate_kernel<T, W, E, V, true> : rotate_kernel<T, W, E, V, false>;
@@ -531,9 +534,7 @@ static cudaError_t launch_rotate_t(const RotateParams& p, bool e4, bool vec, int
       !p.write ? (vec ? pick(no, no, yes) : pick(no, no, no))
       : e4     ? (vec ? pick(yes, yes, yes) : pick(yes, yes, no))
                : (vec ? pick(yes, no, yes) : pick(yes, no, no));
-  return counted(launch_k(SV_PDL >= 2, k, dim3(static_cast<unsigned int>(blocks < fit ? blocks : fit)),
-                          dim3(threads), 0, st, p, n),
-                 1);
+  return counted(launch_k(SV_PDL >= 2, k, dim3(blocks), dim3(threads), 0, st, p, n), 1);
 }
 
 cudaError_t launch_rotate(const RotateParams& p, int dtype, int cache_dtype, bool vec, int sms,
