@@ -395,13 +395,14 @@ __device__ __forceinline__ void code_unit(const Raw<T>& raw, const Unit& u, int 
 }
 
 // A thread keeps its lane of the row and goes through rows (passes) and
-// tokens; four rows' loads are in flight before the first is turned.
+// tokens; the next rows' loads are in flight while it turns and codes one or
+// two, the first ones' while the block prepares the angles.
 // WRITE: k and v rows as well, into the pool; E4: in 8 bits.
 template <typename T, bool WRITE, bool E4, bool VEC, bool INTER>
 __global__ void __launch_bounds__(kRotThreads, E4 ? 3 : VEC ? 4 : 2)
     rotate_kernel(const __grid_constant__ RotateParams p, const __grid_constant__ RotatePlan n) {
   dep_enter();
-  constexpr int kAhead = sizeof(T) == 4 || !VEC || E4 ? 2 : 4;
+  constexpr int kRun = sizeof(T) == 4 || !VEC || E4 ? 1 : 2;
   __shared__ __align__(16) float2 cs[kRotAngles];
   __shared__ __align__(16) double2 csd[E4 ? kRotAngles : 1];
   __shared__ long long dst[kRotGroup], sdst[kRotGroup], pos[kRotGroup];
@@ -416,17 +417,17 @@ __global__ void __launch_bounds__(kRotThreads, E4 ? 3 : VEC ? 4 : 2)
   const long long t1 = p.tokens * (blockIdx.x + 1ll) / gridDim.x;
   for (long long t0 = p.tokens * blockIdx.x / gridDim.x; t0 < t1; t0 += n.group) {
     const int group = static_cast<int>(min(static_cast<long long>(n.group), t1 - t0));
-    prepare_tokens<E4>(p, n, t0, group, cs, csd, dst, sdst, pos);
     int k = 0, pass = 0;  // next row to load, and its token's places in q, k and v
     int b = quotient(static_cast<int>(t0), n.div_N), j = static_cast<int>(t0) - b * p.N;
     const T *q_at = nullptr, *k_at = nullptr, *v_at = nullptr;
     const int all = group * n.passes;
-#pragma unroll 1
-    for (int it = 0; it < all; it += kAhead) {
-      Raw<T> raw[kAhead];
-      int ks[kAhead], rs[kAhead];
+    struct Rows {
+      Raw<T> raw[kRun];
+      int k[kRun], r[kRun];
+    };
+    const auto fetch = [&](Rows& x, int it) {
 #pragma unroll
-      for (int z = 0; z < kAhead; ++z) {
+      for (int z = 0; z < kRun; ++z) {
         if (pass == 0 && it + z < all) {
           q_at = static_cast<const T*>(p.q.p) + b * p.q.sb + j * p.q.sn;
           if (WRITE) {
@@ -436,15 +437,15 @@ __global__ void __launch_bounds__(kRotThreads, E4 ? 3 : VEC ? 4 : 2)
         }
         const int r = pass * n.rows + slot;
         const bool in = it + z < all && slot < n.rows && r < rows;
-        ks[z] = k;
-        rs[z] = in ? r : -1;
+        x.k[z] = k;
+        x.r[z] = in ? r : -1;
         if (in) {
           if (!WRITE || r < p.Hq)
-            load_raw<T, VEC>(q_at + r * p.q.sh, turned, raw[z]);
+            load_raw<T, VEC>(q_at + r * p.q.sh, turned, x.raw[z]);
           else if (r < p.Hq + p.c.heads)
-            load_raw<T, VEC>(k_at + (r - p.Hq) * p.k.sh, turned, raw[z]);
+            load_raw<T, VEC>(k_at + (r - p.Hq) * p.k.sh, turned, x.raw[z]);
           else
-            load_raw<T, VEC>(v_at + (r - p.Hq - p.c.heads) * p.v.sh, plain, raw[z]);
+            load_raw<T, VEC>(v_at + (r - p.Hq - p.c.heads) * p.v.sh, plain, x.raw[z]);
         }
         if (++pass == n.passes) {
           pass = 0;
@@ -455,22 +456,24 @@ __global__ void __launch_bounds__(kRotThreads, E4 ? 3 : VEC ? 4 : 2)
           }
         }
       }
+    };
+    const auto finish = [&](const Rows& x, int it) {
 #pragma unroll
-      for (int z = 0; z < kAhead; ++z) {
+      for (int z = 0; z < kRun; ++z) {
         if (it + z >= all) continue;
-        const int r = rs[z];
-        const long long at = dst[ks[z]];
-        const int base = ks[z] * half_rd;
+        const int r = x.r[z];
+        const long long at = dst[x.k[z]];
+        const int base = x.k[z] * half_rd;
         float f[8], g[8];
         float2 w[8];
         if (!WRITE || r < p.Hq) {
           if (r >= 0 && at != -2 && turned.na > 0) {
-            unpack_raw<T, VEC>(raw[z], turned, f, g);
+            unpack_raw<T, VEC>(x.raw[z], turned, f, g);
             if (turned.pair) {
               load_angles<VEC>(cs + base + a0, cs + base + a1, turned.na, w);
               turn_unit<VEC>(turned, w, f, g);
             }
-            store_unit<T, VEC>(static_cast<T*>(p.q_out) + (t0 + ks[z]) * p.qo_st + r * p.qo_sh, turned, f, g);
+            store_unit<T, VEC>(static_cast<T*>(p.q_out) + (t0 + x.k[z]) * p.qo_st + r * p.qo_sh, turned, f, g);
           }
         }
         if (WRITE) {
@@ -481,12 +484,12 @@ __global__ void __launch_bounds__(kRotThreads, E4 ? 3 : VEC ? 4 : 2)
           const bool pair = key && turned.pair;
           if (E4) {
             if (__any_sync(0xffffffffu, live))
-              code_unit<T, VEC, INTER>(raw[z], u, n.UP, lane == 0, live && u.na > 0, pair, key && turn, p.magnitude,
+              code_unit<T, VEC, INTER>(x.raw[z], u, n.UP, lane == 0, live && u.na > 0, pair, key && turn, p.magnitude,
                                        cs + base + a0, cs + base + a1, csd + (E4 ? base + a0 : 0), csd + (E4 ? base + a1 : 0),
                                        static_cast<uint8_t*>(key ? p.c.k : p.c.v) + at + h * p.c.head_stride,
-                                       (key ? p.c.ks : p.c.vs) + sdst[ks[z]] + static_cast<long long>(h) * p.c.page_size);
+                                       (key ? p.c.ks : p.c.vs) + sdst[x.k[z]] + static_cast<long long>(h) * p.c.page_size);
           } else if (live && u.na > 0) {
-            unpack_raw<T, VEC>(raw[z], u, f, g);
+            unpack_raw<T, VEC>(x.raw[z], u, f, g);
             if (pair) {
               load_angles<VEC>(cs + base + a0, cs + base + a1, u.na, w);
               turn_unit<VEC>(u, w, f, g);
@@ -494,6 +497,21 @@ __global__ void __launch_bounds__(kRotThreads, E4 ? 3 : VEC ? 4 : 2)
             store_unit<T, VEC>(static_cast<T*>(key ? p.c.k : p.c.v) + at + h * p.c.head_stride, u, f, g);
           }
         }
+      }
+    };
+    Rows x, y;
+    fetch(x, 0);
+    prepare_tokens<E4>(p, n, t0, group, cs, csd, dst, sdst, pos);
+#pragma unroll 1
+    for (int it = 0; it < all; it += kRun) {
+      fetch(y, it + kRun);
+      finish(x, it);
+      if (WRITE) {  // (long code: not twice)
+        x = y;
+      } else {
+        it += kRun;
+        fetch(x, it + kRun);
+        finish(y, it);
       }
     }
   }
