@@ -168,6 +168,7 @@ struct RotatePlan {
   int UP;         // lanes of a row (8-bit pools: a power of two, for the row's reduction)
   int units;      // of them in use
   int rows;       // rows a block takes at a time
+  int turn;       // rows of a warp
   int passes;     // until a token's rows are done
   int group;      // tokens whose angles a block prepares together
   UDiv div_N, div_half;  // / N, / (rd / 2)
@@ -176,7 +177,7 @@ __device__ __forceinline__ int quotient(int n, const UDiv& d) {
   return d.m == 0u ? n : static_cast<int>(__umulhi(static_cast<unsigned int>(n), d.m) >> d.shift);
 }
 
-constexpr int kRotGroup = 4;      // most tokens of a group
+constexpr int kRotGroup = 16;     // most tokens of a group
 constexpr int kRotAngles = 1024;  // their (cos, sin) pairs: rotary_dim <= 512
 
 // Places (dst: element offset, -1: none, -2: padding; sdst: the scales') and
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kRotThreads, E4 ? 3 : VEC ? 4 : 2)
   const long long t1 = p.tokens * (blockIdx.x + 1ll) / gridDim.x;
   for (long long t0 = p.tokens * blockIdx.x / gridDim.x; t0 < t1; t0 += n.group) {
     const int group = static_cast<int>(min(static_cast<long long>(n.group), t1 - t0));
-    int k = 0, pass = 0;  // next row to load, and its token's places in q, k and v
+    int k = 0, pass = 0, place = slot;  // next row to load, and its token's places in q, k and v
     int b = quotient(static_cast<int>(t0), n.div_N), j = static_cast<int>(t0) - b * p.N;
     const T *q_at = nullptr, *k_at = nullptr, *v_at = nullptr;
     const int all = group * n.passes;
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kRotThreads, E4 ? 3 : VEC ? 4 : 2)
             v_at = static_cast<const T*>(p.v.p) + b * p.v.sb + j * p.v.sn;
           }
         }
-        const int r = pass * n.rows + slot;
+        const int r = pass * n.rows + place;
         const bool in = it + z < all && slot < n.rows && r < rows;
         x.k[z] = k;
         x.r[z] = in ? r : -1;
@@ -450,6 +451,8 @@ __global__ void __launch_bounds__(kRotThreads, E4 ? 3 : VEC ? 4 : 2)
         if (++pass == n.passes) {
           pass = 0;
           ++k;
+          // a warp's rows move on with the tokens: some are more work
+          if (E4 && (place += n.turn) >= n.rows) place -= n.rows;
           if (++j == p.N) {
             j = 0;
             ++b;
@@ -531,6 +534,7 @@ static cudaError_t launch_rotate_t(const RotateParams& p, bool e4, bool vec, int
   n.passes = (rows * n.UP + kRotThreads - 1) / kRotThreads;
   if (n.passes * (kRotThreads / n.UP) < rows) ++n.passes;
   n.rows = (rows + n.passes - 1) / n.passes;
+  n.turn = n.rows > 32 / n.UP ? 32 / n.UP : 0;
   const int threads = (n.rows * n.UP + 31) / 32 * 32;
   // blocks that fit at once (64 registers a thread, 80 or 128 in the larger forms)
   const long long fit = static_cast<long long>(sms) * ((e4 ? 768 : vec ? 1024 : 512) / threads);
