@@ -679,8 +679,9 @@ __device__ __forceinline__ void load_segment(const MmaParams& p, const CUtensorM
     }
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  // (the next queries arrive in the same place)
-  if (E4) asm volatile("bar.sync 2, 64;" ::: "memory");
+  // Both warps have seen these queries arrive before the next ones are asked
+  // for (on the same barrier, and for 8-bit pools in the same place).
+  asm volatile("bar.sync 2, 64;" ::: "memory");
 }
 
 // What the infinities and NaN of the drafted tokens in `seen` add to one
@@ -1082,7 +1083,15 @@ __global__ void __launch_bounds__(384, 1)
             sc.mul = 32 / min(p.box, 32);
             __syncwarp();
           }
+          const auto scores = [&] {
+            wait(s, &s->s_full[g], ns & 1u, a.ctrl);
+            ++ns;
+          };
           if (tail) {
+            // The scores first: with them every ring entry up to this tile's keys
+            // has been filled, so the slot of its values has at most one phase to
+            // go, which is what a wait on a phase's parity can tell.
+            scores();
             // Values of places past the end may be anything: zeros, so that a
             // zero weight stays zero.  A drafted token's infinities and NaN
             // are taken out as well and added by hand to the rows that see it.
@@ -1146,8 +1155,7 @@ __global__ void __launch_bounds__(384, 1)
             const float vm = warp_max(fmaxf(fmaxf(y0, y1), fmaxf(y2, y3)));
             ve = max(vexp, min(max(static_cast<int>(__float_as_uint(vm) >> 23) - 126, -60), 100));  // vm <= 2^ve
           }
-          wait(s, &s->s_full[g], ns & 1u, a.ctrl);
-          ++ns;
+          if (!tail) scores();
           __syncwarp();
           tmem_fence_after();
           if (warp_live) {
@@ -1208,7 +1216,9 @@ __global__ void __launch_bounds__(384, 1)
             } else {
               top = tile_max<8 / SPLIT>(s_addr + c0 * 16);
             }
-            top = top == -INFINITY ? -INFINITY : top * c2;
+            // (lanes without a row hold anything: they must not make the others
+            // raise their maximum, or the roundings differ from call to call)
+            top = !live || top == -INFINITY ? -INFINITY : top * c2;
             bool raise;
             float Mn = M;
             if (E4) {
@@ -1593,8 +1603,9 @@ cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[5], int grid, cud
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     if (p.stages > 4 || p.scale_log == 2) break;
   }
-  // Keys of the next tile have to fit beside the values of this one.
-  if (p.stages < 2) return cudaErrorNotSupported;
+  // Keys of the next tile have to fit beside the values of this one, and with
+  // one row tile the values of the last one too (the wait for a tail's values).
+  if (p.stages < (p.qtiles == 2 ? 2 : 3)) return cudaErrorNotSupported;
   const size_t smem = fixed + static_cast<size_t>(p.stages) * entry;
   const auto kernel = attention_mma_kernel<QT, DP, E4, SPLIT>;
   static bool done[64] = {};

@@ -74,6 +74,78 @@ def test_attention_with_the_least_shared_memory(dev, qt, kv, page):
     check_attention(heads(3, 64, 4, 128, T[qt], 3), cache, table, clen, trees(3, 64, 4))
 
 
+def attention64(q, cache, table, clen, parent):
+    """The formula in 64 bits on the GPU, a sequence at a time: out, and the sums of w |v|."""
+    B, N, Hq, D = q.shape
+    H, page = cache.num_heads, cache.page_size
+    out = torch.zeros(B, N, Hq, D, dtype=torch.float64, device=q.device)
+    wabs = torch.zeros_like(out)
+    k8, v8 = (x.view(torch.uint8) if cache.k_scale is not None else x for x in (cache.k, cache.v))
+    for b in range(B):
+        L = int(clen[b])
+        t = torch.arange(L + N, device=q.device)
+        pg, pl = table[b].long()[t // page], t % page
+        rows = []
+        for x, sc in ((k8, cache.k_scale), (v8, cache.v_scale)):
+            r = x[pg, pl]
+            r = r.double() if sc is None else r.view(T["e4m3"]).double() * sc.transpose(1, 2)[pg, pl].double()[..., None]
+            rows.append(r.permute(1, 0, 2))  # [H, tokens, D]
+        see = torch.zeros(N, L + N, dtype=torch.bool)
+        see[:, :L] = True
+        up = parent[b].tolist()
+        for i in range(N):
+            j = i
+            see[i, L + j] = True
+            while j > 0:
+                j = up[j]
+                see[i, L + j] = True
+        qb = q[b].double().view(N, H, Hq // H, D).permute(1, 2, 0, 3)  # [H, G, N, D]
+        s = qb @ rows[0][:, None].transpose(-1, -2) * D ** -0.5
+        w = torch.softmax(s.masked_fill(~see.to(q.device), -math.inf), -1)
+        out[b] = (w @ rows[1][:, None]).permute(2, 0, 1, 3).reshape(N, Hq, D)
+        wabs[b] = (w @ rows[1][:, None].abs()).permute(2, 0, 1, 3).reshape(N, Hq, D)
+    return out, wabs
+
+
+@pytest.mark.parametrize("qt,kv,B,N,Hkv,G,D,page", [
+    ("bf16", "bf16", 64, 26, 8, 4, 128, 64), ("fp16", "fp16", 48, 5, 8, 4, 128, 16),
+    ("bf16", "e4m3", 96, 26, 8, 4, 128, 64), ("fp16", "e4m3", 64, 9, 8, 8, 64, 32),
+    ("bf16", "bf16", 24, 40, 8, 8, 128, 64), ("bf16", "bf16", 200, 4, 8, 1, 64, 128)])
+def test_attention_of_batches_that_wait_for_memory(dev, qt, kv, B, N, Hkv, G, D, page):
+    """Every block walks several sequences, and the products wait for the tiles:
+    each tile's wait has to be for that very tile.  The bound as in
+    check_attention, with scores of at most 60 (|q k| of 128 unit elements
+    over sqrt(128), four standard deviations a factor)."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 4000, (B,), generator=g).tolist()
+    need = [-(-(n + N) // page) for n in lens]
+    order = torch.randperm(sum(need), generator=g).int()
+    table = torch.full((B, max(need)), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    cache, table = empty_pool(sum(need), page, Hkv, D, T[kv]), table.to(dev)
+    clen = torch.tensor(lens, dtype=torch.int32, device=dev)
+    gg = torch.Generator("cuda").manual_seed(B)
+    zero = torch.zeros(1, dtype=torch.int32, device=dev)
+    for b, n in enumerate(lens):
+        k, v = (torch.randn(1, n + N, Hkv, D, device=dev, generator=gg).to(T[qt]) for _ in range(2))
+        sv.cache_write(cache, table[b:b + 1], zero, k, v)
+    q = torch.randn(B, N, Hkv * G, D, device=dev, generator=gg).to(T[qt])
+    parent = trees(B, N, B)
+    runs = [sv.tree_attention(q, cache, table, clen, parent)["out"] for _ in range(12)]
+    want, wabs = attention64(q, cache, table, clen, parent)
+    u = torch.finfo(T[qt]).eps / 2
+    score = 60 * (D + 16) * 2.0 ** -23
+    tiny = 4100 * 2.0 ** -25 * 16  # weights below the 16-bit float's or the last term's range, |v| < 8
+    tol = u * want.abs() + (u + 2 * (score + 2.0 ** -21) + 4100 * 2.0 ** -23) * (1 + 2 * u) * wabs + tiny * (qt == "fp16" or kv == "e4m3")
+    over = ((runs[0].double() - want).abs() - tol).amax(dim=(1, 3)).flatten()
+    assert not (over > 0).any() and not torch.isnan(runs[0]).any(), f"{int((over > 0).sum())} of {over.numel()} (sequence, head)s off"
+    for r in runs[1:]:
+        assert torch.equal(r, runs[0])
+
+
 # ------------------------------------------------------------ views and values
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
