@@ -242,37 +242,39 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
 }
 
 // Shared-memory operand with 128-byte swizzle: rows of 128 bytes, groups of 8
-// rows `sbo` bytes apart; for an operand whose rows run along K (V), `lbo` is
-// the distance to the next 64 columns.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | static_cast<uint64_t>(lbo >> 4) << 16 |
-         static_cast<uint64_t>(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// rows 1024 bytes apart; for an operand whose rows run along K (V), `lbo` is
+// the distance to the next 64 columns.  The low word of its descriptor; the
+// high word is the same for all.
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t lbo) {
+  return (addr & 0x3ffffu) >> 4 | (lbo >> 4) << 16;
 }
+constexpr uint32_t kOperandHigh = 1024u >> 4 | 1u << 14 | 2u << 29;
 // f32 accumulator, 16-bit operands (bf16 or f16) or e4m3, M = 128; V is read
 // transposed (its columns are the fast axis).
 __host__ __device__ constexpr uint32_t mma_shape(bool bf16, int n, bool b_transposed) {
   return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) /* f16 and e4m3: 0 */ | (b_transposed ? 1u << 16 : 0u) |
          static_cast<uint32_t>(n / 8) << 17 | 8u << 24;
 }
-#define SV_MMA(KIND, A, CONSTRAINT)                                                                      \
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                           \
-               "tcgen05.mma.cta_group::1.kind::" KIND " [%0], " A ", %2, %3, p;\n\t}" ::"r"(d),            \
-               CONSTRAINT(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))                           \
+#define SV_MMA(KIND, A, MOVE_A)                                                                                \
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t" MOVE_A                  \
+               "mov.b64 y, {%2, %5};\n\t"                                                                     \
+               "tcgen05.mma.cta_group::1.kind::" KIND " [%0], " A ", y, %3, p;\n\t}" ::"r"(d),                 \
+               "r"(a), "r"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "n"(kOperandHigh)                  \
                : "memory")
-// D (+)= A B: A from shared (ss) or tensor memory (ts).
+// D (+)= A B: A from shared (ss, by its low word) or tensor memory (ts).
 template <bool E4>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add) {
   if (E4)
-    SV_MMA("f8f6f4", "%1", "l");
+    SV_MMA("f8f6f4", "x", "mov.b64 x, {%1, %5};\n\t");
   else
-    SV_MMA("f16", "%1", "l");
+    SV_MMA("f16", "x", "mov.b64 x, {%1, %5};\n\t");
 }
 template <bool E4>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add) {
   if (E4)
-    SV_MMA("f8f6f4", "[%1]", "r");
+    SV_MMA("f8f6f4", "[%1]", "");
   else
-    SV_MMA("f16", "[%1]", "r");
+    SV_MMA("f16", "[%1]", "");
 }
 #undef SV_MMA
 __device__ __forceinline__ bool elect_one() {
@@ -902,9 +904,9 @@ __global__ void __launch_bounds__(384, 1)
         if (++next == stages) next = 0, next_phase ^= 1u;
       };
       const uint32_t acc = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint64_t q0 = operand(smem_addr(qs), 16, 1024);
-      const uint64_t k0 = operand(smem_addr(ring), 16, 1024);
-      const uint64_t v0 = operand(smem_addr(ring), kTile * 128, 1024);
+      const uint32_t q0 = operand(smem_addr(qs), 16);
+      const uint32_t k0 = operand(smem_addr(ring), 16);
+      const uint32_t v0 = operand(smem_addr(ring), kTile * 128);
       uint32_t seg = 0, np = 0;  // np: phases of p_ready, one bit a warpgroup
       bool stop = false;
       do {
@@ -912,7 +914,7 @@ __global__ void __launch_bounds__(384, 1)
         const int T = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0), U = two ? 2 * T : T;
         const uint32_t buf = p.qbufs == 2 ? seg & 1u : 0u;
         wait(s, &s->q_full[buf], (p.qbufs == 2 ? seg >> 1 : seg) & 1u, a.ctrl);
-        const uint64_t q1 = q0 + buf * (qbytes >> 4);
+        const uint32_t q1 = q0 + buf * (qbytes >> 4);
 #pragma unroll 1
         for (int x = 0; x <= U; ++x) {
           const uint32_t g = x & 1;
@@ -920,8 +922,8 @@ __global__ void __launch_bounds__(384, 1)
           if (x < U) {
             if (!shared) take(kslot);
             tmem_fence_after();
-            const uint64_t qd = q1 + (shared ? qtile >> 4 : 0);
-            const uint64_t kd = k0 + kslot * (entry >> 4);
+            const uint32_t qd = q1 + (shared ? qtile >> 4 : 0);
+            const uint32_t kd = k0 + kslot * (entry >> 4);
             if (elect_one()) {
               // 32 bytes of a 128-byte row a step: 16 elements (64 are the next
               // block of rows), or 32 of 8 bits (then the next term)
@@ -939,7 +941,7 @@ __global__ void __launch_bounds__(384, 1)
           if (x > 0) {
             const uint32_t f = g ^ 1u;  // unit x - 1
             if (!two || f == 0) take(vslot);
-            const uint64_t vd = v0 + vslot * (entry >> 4);
+            const uint32_t vd = v0 + vslot * (entry >> 4);
             const uint32_t o = acc + 2 * kTile + f * DP, pw = acc + f * kTile;
             const bool add = x > 2;
             const auto accumulate = [&](int half) {
@@ -950,12 +952,12 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                   for (int n = 0; n < kTerms; ++n)
                     mma_ts<E4>(o, pw + term_column(n) + (2 * half + k) * 8,
-                               vd + static_cast<uint64_t>(2 * half + k) * (32 * 128 >> 4), kShapeO,
+                               vd + (2 * half + k) * (32 * 128 >> 4), kShapeO,
                                add || half > 0 || k > 0 || n > 0);
               } else {
 #pragma unroll
                 for (int k = 0; k < kTile / 32; ++k)
-                  mma_ts<E4>(o, pw + (half * 4 + k) * 8, vd + static_cast<uint64_t>(half * 4 + k) * (16 * 128 >> 4), kShapeO,
+                  mma_ts<E4>(o, pw + (half * 4 + k) * 8, vd + (half * 4 + k) * (16 * 128 >> 4), kShapeO,
                              add || half > 0 || k > 0);
               }
             };
