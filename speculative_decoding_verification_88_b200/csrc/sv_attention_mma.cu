@@ -419,6 +419,17 @@ __device__ __forceinline__ void hand_over(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
+// 2^x of two on the FMA pipe, with the special function unit's zero for masked
+// scores and its NaN, both of which the polynomial does not know.
+__device__ __forceinline__ void fma_ex2(float& a, float& b) {
+  float p, q, za, zb;
+  unpack2(ex2_poly_x2(a, b), p, q);
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(za) : "f"(a));
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(zb) : "f"(b));
+  a = a > -126.0f ? p : za;
+  b = b > -126.0f ? q : zb;
+}
+
 // Weights 2^(s c2 - shift) of a row's tile into tensor memory over the scores;
 // returns their sum.  `half` is told when the first half of 128 columns is there.
 template <typename M, int NC>
@@ -444,11 +455,7 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, uint32_t p_addr, 
       f[1] = ex2f(f[1]);
       x = pack2(f[0], f[1]);
       if (i & 4) {
-        // a quarter of them on the FMA pipe, whose polynomial knows no NaN
-        float p2, p3;
-        unpack2(ex2_poly_x2(f[2], f[3]), p2, p3);
-        f[2] = f[2] == f[2] ? p2 : f[2];
-        f[3] = f[3] == f[3] ? p3 : f[3];
+        fma_ex2(f[2], f[3]);  // a quarter of them
       } else {
         f[2] = ex2f(f[2]);
         f[3] = ex2f(f[3]);
@@ -1629,7 +1636,8 @@ cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[5], int grid, cud
 template <typename QT, bool E4>
 cudaError_t launch_split(MmaParams& p, const CUtensorMap (&maps)[5], int grid, cudaStream_t st) {
   const bool wide = p.a.c.dim > 64;
-  if (p.split == 4) return wide ? launch_mma<QT, 128, E4, 4>(p, maps, grid, st) : launch_mma<QT, 64, E4, 4>(p, maps, grid, st);
+  if constexpr (E4)
+    if (p.split == 4) return wide ? launch_mma<QT, 128, E4, 4>(p, maps, grid, st) : launch_mma<QT, 64, E4, 4>(p, maps, grid, st);
   if (p.split == 2) return wide ? launch_mma<QT, 128, E4, 2>(p, maps, grid, st) : launch_mma<QT, 64, E4, 2>(p, maps, grid, st);
   return wide ? launch_mma<QT, 128, E4, 1>(p, maps, grid, st) : launch_mma<QT, 64, E4, 1>(p, maps, grid, st);
 }
@@ -1667,7 +1675,10 @@ cudaError_t launch_attention_mma(const AttnParams& a, int q_dtype, int cache_dty
   p.negate = a.c2 < 0.0f;
   p.zero = a.c2 == 0.0f;
   p.a.c2 = p.zero ? 1.0f : a.c2 < 0.0f ? -a.c2 : a.c2;
-  p.split = p.R <= 32 ? 4 : p.R <= 64 ? 2 : 1;
+  // Few rows: copies of them share a tile's columns.  Two 125,000-token
+  // sequences, 20 rows (us, 1 / 2 / 4 copies): 8 bits 207 / 132 / 130, 64
+  // sequences 155 / 116 / 108; 16 bits 170 / 160 / 161.
+  p.split = p.R <= 32 && cache_dtype == 3 ? 4 : p.R <= 64 ? 2 : 1;
   CUtensorMap maps[5] = {};
   bool ok = pool_map(&maps[0], a.c, a.c.k, cache_dtype, p.box, p.head_first) &&
             pool_map(&maps[1], a.c, a.c.v, cache_dtype, p.box, p.head_first);

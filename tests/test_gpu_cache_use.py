@@ -11,7 +11,7 @@ import torch
 import speculative_decoding_verification_88_b200 as sv
 from speculative_decoding_verification_88_b200 import build as svbuild
 
-from test_gpu_cache import T, bits, check_attention, empty_pool, make, trees
+from test_gpu_cache import T, bits, check_attention, empty_pool, fill, make, trees
 
 pytestmark = pytest.mark.gpu
 
@@ -177,6 +177,29 @@ def test_attention_of_queries_that_are_not_finite(dev, qt, kv, page, D, layout, 
     odd[0, 1, 2] = odd[0, 3, 5] = True
     assert torch.isnan(got["out"][odd]).all()
     assert torch.equal(got["out"][~odd], clean["out"][~odd]) and torch.equal(got["lse"][~odd], clean["lse"][~odd])
+
+
+@pytest.mark.parametrize("qt,kv", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3"), ("fp16", "e4m3")])
+@pytest.mark.parametrize("G", [1, 2, 10, 20])
+def test_attention_past_the_largest_values(dev, qt, kv, G):
+    """A masked place's weight is zero, not merely small: the largest finite
+    values behind it (an 8-bit row's scale 2^118) do not show."""
+    lens, N, D = [100, 126, 130], 6, 64
+    cache, table, clen = make(lens, N, 16, 2, D, T[kv])
+    parent = torch.tensor([[0, 0, 0, 1, 2, 2]] * 3, dtype=torch.int32, device=dev)
+    q = heads(3, N, 2 * G, D, T[qt], 1)
+    clean = sv.tree_attention(q, cache, table, clen, parent)["out"]
+    for b, n in enumerate(lens):
+        for j in (1, 4):
+            top = torch.finfo(T[qt]).max if kv != "e4m3" else 448.0 * 2.0 ** 118
+            pos = [n + j]
+            fill(cache, table, b, pos, torch.full((1, 2, D), 0.5), torch.full((1, 2, D), top))
+    got = sv.tree_attention(q, cache, table, clen, parent)["out"]
+    for j in (0, 2, 5):  # their paths do not meet nodes 1 and 4
+        if kv == "e4m3":  # (the tile's weights share a factor that follows V's scales)
+            assert torch.isfinite(got[:, j]).all()
+        else:
+            assert torch.equal(got[:, j], clean[:, j])
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
