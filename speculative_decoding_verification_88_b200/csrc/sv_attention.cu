@@ -26,8 +26,13 @@ __device__ __forceinline__ unsigned long long ancestor_bits(const int* parent, i
   return m;
 }
 
-// The plain form, for every layout: one block a row, its warps take every
-// fourth token, a lane every 32nd element of the head.
+// The plain form, for the layouts that the tensor cores' form does not take
+// (heads over 128 elements, or rows, pages or scales that a tensor map cannot
+// address): one block a row, its warps take every fourth token, a lane every
+// 32nd element of the head.  Each row reads all keys and values itself, which
+// bounds it: one user's chain of 5 over 500 tokens takes 109 us for the other
+// form's 12, 64 trees of 26 nodes 23.7 ms for 0.14.  Over ten tokens both take
+// a launch's latency (8.6 and 11 us).
 template <typename T, typename C>
 __global__ void __launch_bounds__(128) attention_plain_kernel(const AttnParams p) {
   dep_enter();

@@ -5,7 +5,8 @@
 // N G rows that read the same keys and values.  An item is (sequence, cache
 // head, up to 256 of these rows); its cached tokens are cut into tiles of
 // 128, and all tiles of all items, in order, are dealt out evenly over one
-// block per SM, so that ragged lengths balance and a single long sequence
+// block per SM (an item counts as three tiles more, about what a segment costs
+// besides its tiles), so that ragged lengths balance and a single long sequence
 // uses every SM.  A block's share is a run of segments (a range of one item's
 // tiles).  A segment that covers its item writes the result; any other leaves
 // (maximum, sum, unnormalised output) in scratch, and a second grid joins
@@ -34,6 +35,17 @@
 // of 128 tokens instead of the 1425 that its 32 KB take from memory).  K's
 // scales multiply S; V's multiply the weights, which a power of two that
 // follows the largest of them keeps in the 8-bit range.
+//
+// What it takes and what bounds it (8 cache heads of 128; calls back to back):
+//   64 trees of 26 nodes, 32 query heads, 700 to 4096 tokens, 16 bits: 143 us,
+//     4.6 TB/s of K and V: memory, and the blocks' ends (106 to 124 us) and
+//     the joining grid (7 us) behind it;
+//   2 chains of 5, 64 query heads, 125,000 tokens, 8 bits: 168 us, 3.2 TB/s:
+//     the turns of the products (1024 cycles a tile) and the softmax, 2050
+//     cycles a tile in all;
+//   8 trees of 64, 64 query heads, 3750 tokens, 16 bits: 85 us, 0.69 PFLOP/s:
+//     the same turns (twice 1024 cycles of 3800 a tile), and joining (11 us).
+// The plain form of sv_attention.cu takes 23.7, 59 and 20 ms for them.
 #include <cuda.h>
 
 #include <initializer_list>
@@ -563,10 +575,6 @@ __device__ __forceinline__ void mask_tile(uint32_t s_addr, const Scales& sc, con
   tmem_wait_st();
 }
 
-__device__ __forceinline__ int div_rows(int n, const UDiv& d) {
-  return d.m == 0u ? n : static_cast<int>(__umulhi(static_cast<unsigned int>(n), d.m) >> d.shift);
-}
-
 // What a segment needs besides its tiles, by 64 threads: the queries in the
 // products' layout, the parents, and whether a page is missing.  Plain loads
 // take microseconds each behind a full queue of tiles, so the queries come by
@@ -604,7 +612,7 @@ __device__ __forceinline__ void load_segment(const MmaParams& p, const CUtensorM
     const QT* const q = static_cast<const QT*>(a.q.p) + w.b * a.q.sb + static_cast<long long>(w.h * a.G) * a.q.sh + j * 8;
 #pragma unroll 1
     for (int rr = first; rr < rows; rr += kStride) {
-      const int nd = div_rows(row0 + rr, p.div_G);
+      const int nd = quotient(row0 + rr, p.div_G);
       const uint16_t* src = reinterpret_cast<const uint16_t*>(q + nd * a.q.sn + (row0 + rr - nd * a.G) * a.q.sh);
       uint32_t y[4] = {0u, 0u, 0u, 0u};
       if (j * 8 < D) {
@@ -720,7 +728,7 @@ __device__ __forceinline__ void store_segment(const MmaParams& p, const Walk& w,
   const AttnParams& a = p.a;
   const int row0 = w.row0();
   const int rows = min(2 * w.pr + 1 < p.halves ? 2 * kTile : kTile, p.R - row0);
-  const int n0 = div_rows(row0, p.div_G), n1 = div_rows(row0 + rows - 1, p.div_G);
+  const int n0 = quotient(row0, p.div_G), n1 = quotient(row0 + rows - 1, p.div_G);
   for (int nd = n0 + tid; nd <= n1; nd += 64) {
     const int r0 = max(nd * a.G, row0), r1 = min((nd + 1) * a.G, row0 + rows);
     QT* dst = static_cast<QT*>(a.out) +
@@ -1054,7 +1062,7 @@ __global__ void __launch_bounds__(384, 1)
         const int row = two ? g * kTile + r : r - copy * lanes;  // row within the item
         const bool live = row < rows;
         const bool warp_live = two ? g * kTile + (warp & 3) * 32 < rows : ((warp & 3) * 32) % lanes < rows;
-        const int node = live ? div_rows(row0 + row, p.div_G) : 0;
+        const int node = live ? quotient(row0 + row, p.div_G) : 0;
         // the node's ancestors and itself; nothing at or below an invalid parent
         unsigned long long mask = live && node < w.nodes ? 1ull << node : 0ull;
         if (mask && !a.parent) {
@@ -1473,7 +1481,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
   };
   constexpr int kAhead = 4;  // parts whose loads are in flight together
   for (int i = u0 + static_cast<int>(threadIdx.x); i < u1; i += kJoinThreads) {
-    int c = div_rows(i, by_rows), row = i - c * static_cast<int>(by_rows.d);
+    int c = quotient(i, by_rows), row = i - c * static_cast<int>(by_rows.d);
     if (static_cast<int>(by_rows.d) != rows) c = i / rows, row = i - c * rows;
     float M = -INFINITY, L = 0.0f, o[8] = {};
     for (int x0 = 0; x0 < parts; x0 += kAhead) {
@@ -1511,7 +1519,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
     for (int x = 0; x < 8; ++x) o[x] *= inv;
-    const int node = div_rows(row0 + row, p.div_G), head = h * a.G + (row0 + row - node * a.G);
+    const int node = quotient(row0 + row, p.div_G), head = h * a.G + (row0 + row - node * a.G);
     const long long out_row = (static_cast<long long>(b) * a.N + node) * a.Hq + head;
     store8(static_cast<QT*>(a.out) + out_row * D + c * 8, o);
     if (a.lse && c == 0) a.lse[out_row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2;
@@ -1602,7 +1610,7 @@ cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[5], int grid, cud
   const int entry = kTile * (E4 ? 128 : DP * 2);
   constexpr int kTerms = std::is_same<QT, __nv_bfloat16>::value ? 2 : 3;
   p.qrows = p.qtiles == 2 || p.split > 1 ? kTile : (p.R + 7) / 8 * 8;
-  p.qbufs = p.qtiles == 2 ? 1 : 2;
+  p.qbufs = p.qtiles == 2 ? 1 : 2;  // (the trees of 26 nodes with 1: 134 us for 122)
   const int qrow = E4 ? kTerms * 128 : DP * 2;
   int fixed = 0;
   for (p.scale_log = 3; p.scale_log >= 2; --p.scale_log) {

@@ -41,6 +41,10 @@ __device__ __forceinline__ bool find_place(const CacheView& c, int b, long long 
   return true;
 }
 
+__device__ __forceinline__ int quotient(int n, const UDiv& d) {
+  return d.m == 0u ? n : static_cast<int>(__umulhi(static_cast<unsigned int>(n), d.m) >> d.shift);
+}
+
 __device__ __forceinline__ float elem_f32(float v) { return v; }
 __device__ __forceinline__ float elem_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float elem_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
