@@ -565,7 +565,7 @@ int spec_verify_cache_read_device_status(uint32_t *flags_host, int clear, void *
  * scale finite.  Scores, softmax statistics and sums are held in 32 bits;
  * the weights enter the second product rounded to q's type, or, for an
  * SV_E4M3 pool, as a sum of 8-bit terms that rounds no more coarsely.  For
- * such a pool q is a sum of 8-bit terms as well, within 2^-18 of each row's
+ * such a pool q is a sum of 8-bit terms as well, within 2^-17 of each row's
  * largest element, and an infinity in a row of q makes the row NaN.
  * scratch: device memory of spec_verify_tree_attention_scratch_size bytes,
  * 16-byte aligned, never read before it is written: no initialisation, but

@@ -593,9 +593,12 @@ def _keep(t, stream):
 
 def _result(out, key, shape, dtype, device, stream):
     """_out, refusing a caller's tensor on another device."""
-    made = _out(out, key, shape, dtype, device)
-    if made.device != device:
-        raise ValueError(f"out[{key!r}] must be on {device}")
+    if out is None:
+        made = torch.empty(shape, dtype=dtype, device=device)
+    else:
+        made = _out(out, key, shape, dtype, device)
+        if made.device != device:
+            raise ValueError(f"out[{key!r}] must be on {device}")
     return made if stream is None else _keep(made, stream)
 
 
@@ -611,10 +614,6 @@ def _ints(t, shape, device, name):
             t.device != device or not t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on {device}")
     return t.data_ptr()
-
-
-def _optional_ints(t, shape, device, name):
-    return None if t is None else _ints(t, shape, device, name)
 
 
 def _rows(t, heads, dim, name, like=None):
@@ -739,34 +738,47 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, rope: Rotary, *, inverse: b
     float16; last axis contiguous), positions [T] or [B, N] int32.  `inverse`
     turns back (the transposed map, hence the gradient).  `out` may be x."""
     lib = load_library()
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype not in _TYPES or \
-            x.dtype == torch.float8_e4m3fn:
+    code = _TYPES.get(x.dtype) if isinstance(x, torch.Tensor) else None
+    if code is None or code == SV_E4M3 or not x.is_cuda:
         raise TypeError("x must be a CUDA tensor of float32, bfloat16 or float16")
-    if x.dim() not in (3, 4):
-        raise ValueError(f"x must be [T, H, D] or [B, N, H, D], got shape {tuple(x.shape)}")
-    dev = x.device
-    pos = _ints(positions, x.shape[:-2], dev, "positions")
+    shape, dev = x.shape, x.device
+    if len(shape) == 4:
+        B, N, H, D = shape
+        lead, T = (B, N), B * N
+    elif len(shape) == 3:
+        T, H, D = shape
+        lead = (T,)
+    else:
+        raise ValueError(f"x must be [T, H, D] or [B, N, H, D], got shape {tuple(shape)}")
+    pos = _ints(positions, lead, dev, "positions")
     if rope.inv_freq.device != dev:
         raise ValueError("the rotary frequencies must be on x's device")
     if out is None:
         out = _like(x, stream)
-    elif out.dtype != x.dtype or out.device != dev or out.shape != x.shape:
+        to = (H * D, D)
+    elif out.dtype != x.dtype or out.device != dev or out.shape != shape:
         raise ValueError("out must have x's type, device and shape")
+    else:
+        to = _token_strides(out, "out")
     if x.numel() == 0:
         return out
-    H, D = x.shape[-2:]
-    strides = []
-    for t, name in ((x, "x"), (out, "out")):
-        s = t.stride()
-        if s[-1] != 1:
-            raise ValueError(f"{name}: the last axis must be contiguous")
-        if t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1 and s[0] != t.shape[1] * s[1]:
-            raise ValueError(f"{name}: tokens must be evenly spaced over B and N")
-        strides.append((s[1] if t.dim() == 4 and t.shape[1] > 1 else s[0], s[-2]))
     _launch(lib.spec_verify_rotary, "spec_verify_rotary", dev, stream,
-            (x.data_ptr(), _TYPES[x.dtype], *strides[0], pos, rope._c, int(inverse),
-             x.numel() // (H * D), H, D, out.data_ptr(), *strides[1]))
+            (x.data_ptr(), code, *_token_strides(x, "x"), pos, rope._c, int(inverse), T, H, D,
+             out.data_ptr(), *to))
     return out
+
+
+def _token_strides(t, name):
+    """Strides of tokens and heads of a [T, H, D] or [B, N, H, D] tensor."""
+    s = t.stride()
+    if s[-1] != 1 and t.numel() > 0:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    if len(s) == 3:
+        return s[0], s[1]
+    B, N = t.shape[:2]
+    if B > 1 and N > 1 and s[0] != N * s[1]:
+        raise ValueError(f"{name}: tokens must be evenly spaced over B and N")
+    return (s[1] if N > 1 else s[0]), s[2]
 
 
 def _table(page_table, B, device):
@@ -820,8 +832,8 @@ def cache_write(cache: KVCache, page_table: torch.Tensor, cache_len: torch.Tenso
     if rope is not None and rope.inv_freq.device != dev:
         raise ValueError("the rotary frequencies must be on the cache's device")
     lens = _ints(cache_len, (B,), dev, "cache_len")
-    par = _optional_ints(parent, (B, N), dev, "parent")
-    cnt = _optional_ints(count, (B,), dev, "count")
+    par = None if parent is None else _ints(parent, (B, N), dev, "parent")
+    cnt = None if count is None else _ints(count, (B,), dev, "count")
     table, tstride, pages = _table(page_table, B, dev)
     qr, Hq, qo = None, 0, None
     if q is not None:
@@ -856,7 +868,7 @@ def cache_read(cache: KVCache, page_table: torch.Tensor, offsets: torch.Tensor, 
     if B < 0 or dtype not in _TYPES or dtype == torch.float8_e4m3fn:
         raise ValueError("offsets must be [B + 1] and dtype float32, bfloat16 or float16")
     offs = _ints(offsets, (B + 1,), dev, "offsets")
-    st0 = _optional_ints(start, (B,), dev, "start")
+    st0 = None if start is None else _ints(start, (B,), dev, "start")
     table, tstride, pages = _table(page_table, B, dev)
     shape = (int(total), cache.num_heads, cache.head_dim)
     res = {x: _result(out, x, shape, dtype, dev, stream) for x in ("k", "v")}
@@ -890,8 +902,8 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     if q.device != dev:
         raise ValueError("q must be on the cache's device")
     lens = _ints(cache_len, (B,), dev, "cache_len")
-    par = _optional_ints(parent, (B, N), dev, "parent")
-    cnt = _optional_ints(count, (B,), dev, "count")
+    par = None if parent is None else _ints(parent, (B, N), dev, "parent")
+    cnt = None if count is None else _ints(count, (B,), dev, "count")
     table, tstride, pages = _table(page_table, B, dev)
     if out is None:
         res = {"out": _like(q, stream)}
@@ -902,7 +914,9 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     if scale is None:
         scale = D ** -0.5
     need = _scratch_bytes(B, N, Hq, cache.num_heads, D)
-    scratch = _keep(torch.empty(max(need, 16), dtype=torch.uint8, device=dev), stream)
+    scratch = torch.empty(need or 16, dtype=torch.uint8, device=dev)
+    if stream is not None:
+        _keep(scratch, stream)
     _launch(lib.spec_verify_tree_attention, "spec_verify_tree_attention", dev, stream,
             (qr, code_t, cache._c, table, tstride, pages, lens, par, cnt, B, N, Hq, float(scale),
              res["out"].data_ptr(), res["lse"].data_ptr() if lse else None,

@@ -26,9 +26,10 @@
 // Weights enter the second product in the values' 16-bit type.  8-bit pools
 // go into the products as they are, by the 8-bit instructions: queries are
 // scaled by a power of two a row and written as a sum of two (bfloat16) or
-// three (16-bit floats) 8-bit terms of 4 significant bits each, which is
-// exact down to 2^-18 of the row's largest element; the weights likewise, so
-// that they keep 8 or 12 significant bits, no fewer than the output's type.
+// three (16-bit floats) 8-bit terms of 4 significant bits each, exact but for
+// elements so small that the step of the smallest codes, 2^-9, counts: half of
+// it, with the largest element at 2^7 or more, is 2^-17 of that one.  The
+// weights likewise, so that they keep 8 or 12 significant bits, no fewer than the output's type.
 // An 8-bit product of n terms costs n/2 of a 16-bit one, and K and V
 // cross shared memory once, without a widened copy (widening them to 16 bits
 // first, by four warps, bound the kernel by shared memory: 2450 cycles a tile
@@ -48,6 +49,7 @@
 // The plain form of sv_attention.cu takes 23.7, 59 and 20 ms for them.
 #include <cuda.h>
 
+#include <atomic>
 #include <initializer_list>
 #include <type_traits>
 
@@ -365,8 +367,7 @@ struct Control {
   int abort;
   int stop;              // abort, as the softmax warpgroups agreed on it
   int bad[2];            // a page of the segment is missing (by Q buffer)
-  unsigned int odd[4][2];  // drafted tokens whose values hold an infinity or a NaN (by segment: the
-                           // converters may be two segments ahead)
+  unsigned int odd[2][2];  // drafted tokens whose values hold an infinity or a NaN (by segment)
   int parent[2][64];
   float qscale[2][2 * kTile];
   float2 ml[2][kTile];
@@ -792,7 +793,7 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&s->s_full[i], 1);
       for (int z = 0; z < 2; ++z) mbar_init(&s->p_ready[i][z], 4);
       s->bad[i] = 0;
-      for (int z = 0; z < 4; ++z) s->odd[z][i] = 0u;
+      for (int z = 0; z < 2; ++z) s->odd[z][i] = 0u;
       mbar_init(&s->q_full[i], 2);
       mbar_init(&s->q_empty[i], 8);
     }
@@ -1140,7 +1141,7 @@ __global__ void __launch_bounds__(384, 1)
                         if (odd_word<QT, E4>(y[q] & 0xffff0000u)) y[q] &= 0xffffu;
                       }
                     }
-                    atomicOr(&s->odd[seg & 3][(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
+                    atomicOr(&s->odd[seg & 1][(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
                   }
                 }
               }
@@ -1154,7 +1155,7 @@ __global__ void __launch_bounds__(384, 1)
                 *vs = 0.0f;
               } else if (tok >= w.len && !(fabsf(*vs) < INFINITY)) {
                 *vs = 0.0f;
-                atomicOr(&s->odd[seg & 3][(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
+                atomicOr(&s->odd[seg & 1][(tok - w.len) >> 5], 1u << ((tok - w.len) & 31));
               }
               if (g == 0)
                 asm volatile("bar.sync 3, 128;" ::: "memory");
@@ -1322,7 +1323,7 @@ __global__ void __launch_bounds__(384, 1)
         if (mask == 0ull) M = -INFINITY, l = 0.0f;
         s->ml[g][r] = make_float2(M, l);
         softmax_sync();
-        const unsigned int odd0 = s->odd[seg & 3][0], odd1 = s->odd[seg & 3][1];
+        const unsigned int odd0 = s->odd[seg & 1][0], odd1 = s->odd[seg & 1][1];
         float f0 = 1.0f, f1 = 0.0f;
         if (!two) {
           // all copies of the row in both groups; a group without a tile has
@@ -1425,7 +1426,7 @@ __global__ void __launch_bounds__(384, 1)
         tmem_fence_before();
         if (tid == 0) s->stop = gave_up(s);
         softmax_sync();  // O, ml and odd may be overwritten now
-        if (tid < 2) s->odd[seg & 3][tid] = 0u;
+        if (tid < 2) s->odd[seg & 1][tid] = 0u;
         if (tid == 2) s->bad[buf] = 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&s->q_empty[buf]);
@@ -1625,7 +1626,7 @@ cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[5], int grid, cud
   if (p.stages < (p.qtiles == 2 ? 2 : 3)) return cudaErrorNotSupported;
   const size_t smem = fixed + static_cast<size_t>(p.stages) * entry;
   const auto kernel = attention_mma_kernel<QT, DP, E4, SPLIT>;
-  static bool done[64] = {};
+  static std::atomic<bool> done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

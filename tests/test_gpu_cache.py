@@ -491,6 +491,13 @@ def check_attention(q, cache, table, clen, parent=None, count=None, scale=None, 
     # floats) leaves half a step of 2^(e-11): 2^-12, under u of float16.
     uw = u(q.dtype)
     score = smax * (D + 16) * 2.0 ** -23
+    if coded:
+        # q's terms: its row is scaled so that the largest element lies in [2^7, 2^8),
+        # and the smallest codes are 2^-9 apart, so an element is off by at most 2^-10,
+        # 2^-17 of the largest, and a score by that times the sum of |k|.
+        k = torch.nan_to_num(cache.k.float()) * torch.nan_to_num(cache.k_scale).transpose(1, 2)[..., None]
+        score = score + abs(D ** -0.5 if scale is None else scale) * 2.0 ** -17 * \
+            q.double().cpu().abs().amax(-1) * k.abs().sum(-1).max().item()
     tiny = 0.0
     if coded or q.dtype == torch.float16:
         top = 448.0 * torch.nan_to_num(cache.v_scale).max().item() * 2 if coded else \

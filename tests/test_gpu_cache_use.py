@@ -50,6 +50,17 @@ def test_attention_of_many_short_sequences(dev, qt, kv, B, Hkv, G, N):
     check_attention(heads(B, N, Hkv * G, 64, T[qt], 1), cache, table, clen, trees(B, N, 2), count)
 
 
+@pytest.mark.parametrize("qt,kv", [("bf16", "bf16"), ("fp16", "e4m3")])
+@pytest.mark.parametrize("lens,N,Hkv,G,D,page", [
+    ([130, 3], 2, 2, 2, 8, 16), ([130, 3], 2, 3, 1, 24, 8), ([70], 3, 2, 2, 120, 16), ([70], 3, 1, 2, 1, 16),
+    ([70], 3, 2, 1, 3, 5), ([20], 2, 1, 3, 255, 16), ([300], 2, 1, 512, 32, 16), ([100], 64, 1, 16, 64, 16),
+    ([40], 1, 1, 1024, 16, 32), ([700], 2, 1, 2, 64, 4096), ([5 * (b % 3) for b in range(2000)], 1, 1, 1, 16, 16)])
+def test_attention_of_unusual_sizes(dev, qt, kv, lens, N, Hkv, G, D, page):
+    """The smallest, largest and odd heads, groups, pages and batches."""
+    cache, table, clen = make(lens, N, page, Hkv, D, T[kv], seed=D)
+    check_attention(heads(len(lens), N, Hkv * G, D, T[qt], 1), cache, table, clen, trees(len(lens), N, 2))
+
+
 @pytest.mark.parametrize("qt,kv", [("bf16", "bf16"), ("bf16", "e4m3"), ("fp16", "e4m3")])
 def test_attention_of_one_long_sequence_next_to_short_ones(dev, qt, kv):
     """One sequence over all blocks, others of one tile before and behind it."""
