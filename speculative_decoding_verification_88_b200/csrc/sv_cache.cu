@@ -291,11 +291,167 @@ __device__ __forceinline__ void member(const Raw<T>& r, const Unit& u, bool weav
   }
 }
 
-// A unit of a row bound for 8 bits: codes, and the scale from the row's first
-// lane.  All lanes of the row take part (live: whether this one stores; the
+// A unit of a row that is not turned: 16 exact elements in two runs of 8.  A
+// code is taken when x / scale from below and from above, 2^-21 of it apart
+// from the product with the rounded reciprocal (off by 2^-22 at most), give the
+// same one; others (16-bit elements are often 448ths of one another, and then
+// close to the middle of two codes), and rows whose scale is tiny, zero or NaN,
+// are divided with rounding to odd.
+template <typename T>
+__device__ __forceinline__ void code_exact_unit(const Raw<T>& raw, const Unit& u, int UP, bool first_lane, bool live,
+                                                uint8_t* out, float* scale_out) {
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+  if (live) {
+    float f[8], g[8];
+    load8(raw.a, f);
+    load8(raw.b, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = f[i], x[8 + i] = g[i];
+  }
+  float top = 0.0f;
+  unsigned long long zero = 0ull;  // stays so unless an element is an infinity or a NaN
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    top = fmax3(top, fabsf(x[i]), fabsf(x[i + 1]));
+    zero = fma2(pack2(x[i], x[i + 1]), 0ull, zero);
+  }
+  float z0, z1;
+  unpack2(zero, z0, z1);
+  const uint32_t odd = __ballot_sync(0xffffffffu, !(z0 + z1 == 0.0f));
+  for (int o = UP >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float scale = __fdiv_rn(top, 448.0f);
+  const int lane = threadIdx.x & 31;
+  const uint32_t row = (UP == 32 ? 0xffffffffu : (1u << UP) - 1u) << (lane & ~(UP - 1));
+  if (odd & row) scale = __int_as_float(0x7fc00000);
+  if (!live) return;
+  const float inv = 1.0f / scale;
+  const unsigned long long lo = splat2(inv * (1.0f - 0x1p-21f)), hi = splat2(inv * (1.0f + 0x1p-21f));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  if (scale >= 0x1p-60f) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      float a, b, c, d;
+      unpack2(mul2(pack2(x[i], x[i + 1]), lo), a, b);
+      unpack2(mul2(pack2(x[i], x[i + 1]), hi), c, d);
+      uint32_t two = e4m3_pair(a, b);
+      if (two != e4m3_pair(c, d)) two = e4m3_pair(quotient_odd(x[i], scale, inv), quotient_odd(x[i + 1], scale, inv));
+      w[i >> 2] |= two << (i & 2 ? 16 : 0);
+    }
+  } else {
+    const float up = 0x1p80f, s = scale * up, is = scale > 0.0f ? 1.0f / s : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2)
+      w[i >> 2] |= e4m3_pair(quotient_odd(x[i] * up, s, is), quotient_odd(x[i + 1] * up, s, is)) << (i & 2 ? 16 : 0);
+  }
+  *reinterpret_cast<uint2*>(out + u.a) = make_uint2(w[0], w[1]);
+  *reinterpret_cast<uint2*>(out + u.b) = make_uint2(w[2], w[3]);
+  if (first_lane) *scale_out = scale;
+}
+
+// A unit of a turned row, 8 pairs of which `pair` says whether they are turned.
+// |f| + |g| of a pair is at most 2 / magnitude of the row's largest result, so
+// that bounds every element's 32-bit error.
+template <typename T, bool INTER>
+__device__ __forceinline__ void code_turned_unit(const Raw<T>& raw, const Unit& u, int UP, bool first_lane, bool live, bool pair,
+                                                 float magnitude, const float2* w0, const float2* w1, const double2* cd0,
+                                                 const double2* cd1, uint8_t* out, float* scale_out) {
+  const bool weave = INTER && u.weave;
+  const auto exact = [&](int z) { return pair ? (z < 4 ? cd0[z] : cd1[z - 4]) : make_double2(1.0, 0.0); };
+  float x[8], y[8], top = 0.0f;
+  unsigned long long zero = 0ull;  // stays so unless an element is an infinity or a NaN
+#pragma unroll
+  for (int z = 0; z < 8; ++z) {
+    float f = 0.0f, g = 0.0f;
+    if (live) member<T, true>(raw, u, weave, z, f, g);
+    zero = fma2(pack2(f, g), 0ull, zero);
+    x[z] = f, y[z] = g;
+    if (pair) {
+      const float2 w = z < 4 ? w0[z] : w1[z - 4];
+      x[z] = fmaf(f, w.x, -g * w.y);
+      y[z] = fmaf(g, w.x, f * w.y);
+    }
+    top = fmax3(top, fabsf(x[z]), fabsf(y[z]));
+  }
+  float z0, z1;
+  unpack2(zero, z0, z1);
+  const uint32_t odd = __ballot_sync(0xffffffffu, !(z0 + z1 == 0.0f));
+  for (int o = UP >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  double most = 0.0;
+  // Twice the error bound, 2^-20 of at most 2 top.  In rows near the type's end,
+  // where sums may overflow, every element is computed in 64 bits.
+  const bool huge = !(top < 0x1p120f);
+  const float near = huge ? 0.0f : top - top * 0x1.1p-18f;
+#pragma unroll
+  for (int z = 0; z < 8; ++z) {
+    if (fmaxf(fabsf(x[z]), fabsf(y[z])) >= near) {
+      float f = 0.0f, g = 0.0f;
+      if (live) member<T, true>(raw, u, weave, z, f, g);
+      const double2 d = exact(z);
+      const double a = f, b = g;
+      most = fmax(most, fmax(fabs(fma(a, d.x, -(b * d.y))), fabs(fma(b, d.x, a * d.y))));
+    }
+  }
+  for (int o = UP >> 1; o > 0; o >>= 1) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, o));
+  float scale = static_cast<float>(most / 448.0);
+  const int lane = threadIdx.x & 31;
+  const uint32_t row = (UP == 32 ? 0xffffffffu : (1u << UP) - 1u) << (lane & ~(UP - 1));
+  if ((odd & row) || !(scale < INFINITY)) scale = __int_as_float(0x7fc00000);
+  if (!live) return;
+  // Small rows are multiplied up, huge ones down (by a power of two): neither
+  // the reciprocal nor a sum may leave the normal range.
+  const float up = huge ? 0x1p-8f : scale < 0x1p-60f ? 0x1p80f : 1.0f;
+  if (up != 1.0f) {
+#pragma unroll
+    for (int z = 0; z < 8; ++z) {
+      float f, g;
+      member<T, true>(raw, u, weave, z, f, g);
+      f *= up, g *= up;
+      const float2 w = pair ? (z < 4 ? w0[z] : w1[z - 4]) : make_float2(1.0f, 0.0f);
+      x[z] = fmaf(f, w.x, -g * w.y);
+      y[z] = fmaf(g, w.x, f * w.y);
+    }
+  }
+  const float s = scale * up, inv = scale > 0.0f ? 1.0f / s : 0.0f;
+  // per |f| + |g|: 2^-20 for the turn, 2^-21 for the quotient
+  const float grain = pair ? fabsf(magnitude) * 0x1.8p-20f * inv : 0x1p-21f * inv;
+  uint32_t wa[2] = {0u, 0u}, wb[2] = {0u, 0u};
+#pragma unroll
+  for (int z = 0; z < 8; ++z) {
+    float f, g;
+    member<T, true>(raw, u, weave, z, f, g);
+    const float d = fmaf(fabsf(g), up, fabsf(f) * up) * grain;
+    const unsigned long long q = mul2(pack2(x[z], y[z]), splat2(inv));
+    float a, b, c, e;
+    unpack2(sub2(q, splat2(d)), a, b);
+    unpack2(add2(q, splat2(d)), c, e);
+    uint32_t two = e4m3_pair(a, b);
+    const uint32_t over = e4m3_pair(c, e);
+    if (two != over) {
+      const double2 t = exact(z);
+      uint32_t cx = two & 0xffu, cy = two >> 8;
+      if (cx != (over & 0xffu)) cx = nearer_code(cx, over & 0xffu, f, g, t.x, t.y, scale);
+      if (cy != over >> 8) cy = nearer_code(cy, over >> 8, g, f, t.x, -t.y, scale);
+      two = cx | cy << 8;
+    }
+    if (weave) {
+      (z < 4 ? wa : wb)[(z & 3) >> 1] |= two << (z & 1 ? 16 : 0);
+    } else {
+      wa[z >> 2] |= (two & 0xffu) << 8 * (z & 3);
+      wb[z >> 2] |= (two >> 8) << 8 * (z & 3);
+    }
+  }
+  *reinterpret_cast<uint2*>(out + u.a) = make_uint2(wa[0], wa[1]);
+  *reinterpret_cast<uint2*>(out + u.b) = make_uint2(wb[0], wb[1]);
+  if (first_lane) *scale_out = scale;
+}
+
+// The same for a unit of any layout, turned or not: codes, and the scale from
+// the row's first lane.  All lanes of the row take part (live: whether this one stores; the
 // others' elements are zeros).  Elements are unpacked and turned twice, for
 // the maximum and for the codes, rather than held.
-template <typename T, bool VEC, bool INTER>
+template <typename T, bool INTER>
 __device__ __forceinline__ void code_unit(const Raw<T>& raw, const Unit& u, int UP, bool first_lane, bool live, bool pair,
                                           bool turned_row, float magnitude, const float2* w0, const float2* w1,
                                           const double2* cd0, const double2* cd1, uint8_t* out, float* scale_out) {
@@ -303,18 +459,19 @@ __device__ __forceinline__ void code_unit(const Raw<T>& raw, const Unit& u, int 
   // e: a bound of the 32-bit error of both members of a pair (angle and
   // functions, two products, a sum: under 8 roundings of each term).
   const float grain = pair ? fabsf(magnitude) * 0x1p-20f : 0.0f;
-  const auto at = [&](int z, float& f, float& g, float& x, float& y) {
+  const auto at = [&](int z, float& f, float& g, float& x, float& y, float up = 1.0f) {
     f = g = 0.0f;
-    if (live) member<T, VEC>(raw, u, weave, z, f, g);
+    if (live) member<T, false>(raw, u, weave, z, f, g);
+    f *= up, g *= up;
     x = f, y = g;
-    if (pair && (VEC || z < u.na)) {
+    if (pair && z < u.na) {
       const float2 w = z < 4 ? w0[z] : w1[z - 4];
       x = fmaf(f, w.x, -g * w.y);
       y = fmaf(g, w.x, f * w.y);
     }
   };
   const auto exact = [&](int z) {
-    return pair && (VEC || z < u.na) ? (z < 4 ? cd0[z] : cd1[z - 4]) : make_double2(1.0, 0.0);
+    return pair && z < u.na ? (z < 4 ? cd0[z] : cd1[z - 4]) : make_double2(1.0, 0.0);
   };
   float top = 0.0f, slack = 0.0f;
   bool odd = false;  // an infinity or a NaN
@@ -343,7 +500,7 @@ __device__ __forceinline__ void code_unit(const Raw<T>& raw, const Unit& u, int 
   if (__any_sync(0xffffffffu, turned_row)) {
     for (int o = UP >> 1; o > 0; o >>= 1) slack = fmaxf(slack, __shfl_xor_sync(0xffffffffu, slack, o));
     double most = 0.0;
-    const float near = top - 2.0f * slack;
+    const float near = top < 0x1p120f ? top - 2.0f * slack : 0.0f;  // (sums may overflow)
 #pragma unroll
     for (int z = 0; z < 8; ++z) {
       float f, g, x, y;
@@ -361,45 +518,33 @@ __device__ __forceinline__ void code_unit(const Raw<T>& raw, const Unit& u, int 
   }
   if (odd || !(scale < INFINITY)) scale = __int_as_float(0x7fc00000);
   if (!live) return;
-  // Small rows are multiplied up (by a power of two): neither the reciprocal
-  // nor a remainder may leave the normal range.
-  const float up = scale < 0x1p-60f ? 0x1p80f : 1.0f;
+  // Small rows are multiplied up, huge ones down (by a power of two): neither
+  // the reciprocal nor a remainder or a sum may leave the normal range.
+  const float up = !(top < 0x1p120f) ? 0x1p-8f : scale < 0x1p-60f ? 0x1p80f : 1.0f;
   const float s = scale * up, inv = scale > 0.0f ? 1.0f / s : 0.0f;
-  uint32_t wa[2] = {0u, 0u}, wb[2] = {0u, 0u};
 #pragma unroll
   for (int z = 0; z < 8; ++z) {
     float f, g, x, y;
-    at(z, f, g, x, y);
+    at(z, f, g, x, y, up);
     uint32_t cx, cy;
     if (turned_row) {
-      const float qx = x * up * inv, qy = y * up * inv, e = (fabsf(f) + fabsf(g)) * grain * up * inv;
+      const float qx = x * inv, qy = y * inv, e = (fabsf(f) + fabsf(g)) * grain * inv;
       const float dx = fmaf(fabsf(qx), 0x1p-21f, e), dy = fmaf(fabsf(qy), 0x1p-21f, e);
       cx = e4m3_pair(qx - dx, qx + dx);
       cy = e4m3_pair(qy - dy, qy + dy);
       if (((cx ^ cx >> 8) | (cy ^ cy >> 8)) & 0xffu) {
         const double2 d = exact(z);
-        if ((cx ^ cx >> 8) & 0xffu) cx = nearer_code(cx & 0xffu, cx >> 8 & 0xffu, f, g, d.x, d.y, scale);
-        if ((cy ^ cy >> 8) & 0xffu) cy = nearer_code(cy & 0xffu, cy >> 8 & 0xffu, g, f, d.x, -d.y, scale);
+        if ((cx ^ cx >> 8) & 0xffu) cx = nearer_code(cx & 0xffu, cx >> 8 & 0xffu, f, g, d.x, d.y, s);
+        if ((cy ^ cy >> 8) & 0xffu) cy = nearer_code(cy & 0xffu, cy >> 8 & 0xffu, g, f, d.x, -d.y, s);
       }
       cx &= 0xffu, cy &= 0xffu;
     } else {
-      const uint32_t two = e4m3_pair(quotient_odd(x * up, s, inv), quotient_odd(y * up, s, inv));
+      const uint32_t two = e4m3_pair(quotient_odd(x, s, inv), quotient_odd(y, s, inv));
       cx = two & 0xffu, cy = two >> 8;
     }
-    if (!VEC) {
-      const int step = u.weave ? 2 : 1;
-      if (z < u.na) out[u.a + z * step] = static_cast<uint8_t>(cx);
-      if (z < u.nb) out[u.b + z * step] = static_cast<uint8_t>(cy);
-    } else if (weave) {
-      (z < 4 ? wa : wb)[(z & 3) >> 1] |= (cx | cy << 8) << (z & 1 ? 16 : 0);
-    } else {
-      wa[z >> 2] |= cx << 8 * (z & 3);
-      wb[z >> 2] |= cy << 8 * (z & 3);
-    }
-  }
-  if (VEC && u.na > 0) {
-    *reinterpret_cast<uint2*>(out + u.a) = make_uint2(wa[0], wa[1]);
-    *reinterpret_cast<uint2*>(out + u.b) = make_uint2(wb[0], wb[1]);
+    const int step = u.weave ? 2 : 1;
+    if (z < u.na) out[u.a + z * step] = static_cast<uint8_t>(cx);
+    if (z < u.nb) out[u.b + z * step] = static_cast<uint8_t>(cy);
   }
   if (first_lane) *scale_out = scale;
 }
@@ -495,11 +640,19 @@ __global__ void __launch_bounds__(kRotThreads, E4 ? 3 : VEC ? 4 : 2)
           const bool live = mine && at >= 0;
           const bool pair = key && turned.pair;
           if (E4) {
-            if (__any_sync(0xffffffffu, live))
-              code_unit<T, VEC, INTER>(x.raw[z], u, n.UP, lane == 0, live && u.na > 0, pair, key && turn, p.magnitude,
-                                       cs + base + a0, cs + base + a1, csd + (E4 ? base + a0 : 0), csd + (E4 ? base + a1 : 0),
-                                       static_cast<uint8_t*>(key ? p.c.k : p.c.v) + at + h * p.c.head_stride,
-                                       (key ? p.c.ks : p.c.vs) + sdst[x.k[z]] + static_cast<long long>(h) * p.c.page_size);
+            if (__any_sync(0xffffffffu, live)) {
+              uint8_t* const to = static_cast<uint8_t*>(key ? p.c.k : p.c.v) + at + h * p.c.head_stride;
+              float* const scale = (key ? p.c.ks : p.c.vs) + sdst[x.k[z]] + static_cast<long long>(h) * p.c.page_size;
+              const float2 *w0 = cs + base + a0, *w1 = cs + base + a1;
+              const double2 *cd0 = csd + (E4 ? base + a0 : 0), *cd1 = csd + (E4 ? base + a1 : 0);
+              const bool mine_live = live && u.na > 0;
+              if constexpr (!VEC)
+                code_unit<T, INTER>(x.raw[z], u, n.UP, lane == 0, mine_live, pair, key && turn, p.magnitude, w0, w1, cd0, cd1, to, scale);
+              else if (__any_sync(0xffffffffu, live && key && turn))
+                code_turned_unit<T, INTER>(x.raw[z], u, n.UP, lane == 0, mine_live, pair, p.magnitude, w0, w1, cd0, cd1, to, scale);
+              else
+                code_exact_unit<T>(x.raw[z], u, n.UP, lane == 0, mine_live, to, scale);
+            }
           } else if (live && u.na > 0) {
             unpack_raw<T, VEC>(x.raw[z], u, f, g);
             if (pair) {

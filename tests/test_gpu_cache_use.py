@@ -11,7 +11,7 @@ import torch
 import speculative_decoding_verification_88_b200 as sv
 from speculative_decoding_verification_88_b200 import build as svbuild
 
-from test_gpu_cache import T, bits, check_attention, empty_pool, fill, make, trees
+from test_gpu_cache import T, bits, check_attention, check_write, empty_pool, expect_write, fill, make, snapshot, trees
 
 pytestmark = pytest.mark.gpu
 
@@ -251,6 +251,40 @@ def test_commit_of_a_path_that_names_one_node_twice(dev):
     assert new.tolist() == [28]
     at = list(range(20)) + [20 + j for j in (0, 5, 5, 3, 7, 7, 7, 7)]
     assert torch.equal(now["k"], was["k"][at]) and torch.equal(now["v"], was["v"][at])
+
+
+@pytest.mark.parametrize("src", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rd,layout", [(128, 128, "hnd"), (96, 32, "nhd"), (66, 22, "padded")])
+def test_turned_rows_at_the_ends_of_their_type(dev, src, interleaved, D, rd, layout):
+    """Codes and scales of turned 8-bit rows are those of exact arithmetic: rows
+    up to the type's largest value (whose sums pass it), tiny and zero ones, one
+    element alone, values that are 448ths of one another, both zeros; a row with
+    an infinity or a NaN has a NaN scale and leaves its neighbours alone."""
+    H, N = 2, 12
+    cache, table, clen = make([9], N, 16, H, D, T["e4m3"], layout)
+    top = torch.finfo(T[src]).max
+    g = torch.Generator().manual_seed(D)
+    k = torch.randn(1, N, H, D, generator=g).double()
+    k[0, 0] *= top / k[0, 0].abs().amax()
+    k[0, 1] = top * torch.randn(H, D, generator=g).sign()
+    k[0, 2] = top / 3
+    k[0, 3] *= torch.finfo(T[src]).tiny
+    k[0, 4] = 0.0
+    k[0, 5] = -0.0
+    k[0, 6] = 0.0
+    k[0, 6, 0, D // 2 - 1], k[0, 6, 1, 0] = 3.0, -5.0
+    k[0, 7, 0, 3], k[0, 7, 1, D - 1] = math.inf, math.nan
+    k[0, 8] = torch.arange(D) * 0.75 * 2.0 ** -4 + 0.75 * 17
+    k[0, 8, :, 0] = 448 * 0.75
+    k[0, 9] = (torch.arange(D) - D // 2) * 2.0 ** -9
+    k[0, 10] *= 1e-42
+    k = k.to(T[src]).to(dev)
+    rope = sv.rotary_frequencies(rd, interleaved=interleaved, device=dev)
+    for turn in (rope, None):
+        before = snapshot(cache)
+        sv.cache_write(cache, table, clen, k, k, rope=turn)
+        check_write(cache, before, expect_write(cache, table, [9], k, k, None, None, turn), k, turn)
 
 
 # ------------------------------------------------------ empty and tiny batches
