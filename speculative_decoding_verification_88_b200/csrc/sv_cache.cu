@@ -1,11 +1,11 @@
 // sv_cache.cu -- rotary positions, the paged cache's write (as it is, or in
 // 8 bits with one scale a row), its read-back and the move of accepted rows.
 // All four move data once.  Long inputs are bound by memory (16-bit rotary of
-// 16,000 tokens with 40 heads of 128: 63 us, 5.2 TB/s; read-back of 32
+// 16,000 tokens with 40 heads of 128: 60 us, 5.5 TB/s; read-back of 32
 // sequences from 8 bits: 76 us, 5.3 TB/s; 64 accepted paths in 32 layers: 18
 // us, 3.4 TB/s), but for the write into 8 bits, which is bound by the
 // instructions of exact codes (8 x 1000 tokens, 8 + 8 cache heads and 32 query
-// heads: 65 us, 2.8 TB/s; into 16 bits 55 us).  A few tokens take one launch's
+// heads: 52 us, 3.5 TB/s; into 16 bits 39 us).  A few tokens take one launch's
 // latency, 4 to 6 us on the GPU.
 #include <type_traits>
 
@@ -25,9 +25,9 @@ namespace sv {
 // then work on a half turn at most.
 //
 // Rows whose parts are multiples of 16 elements on 16-byte boundaries (8-bit
-// pools: 8) move 16 bytes a load (VEC), others one element: rotary 63 against
-// 572 us at the size above, the 8-bit write 66 against 184, the 16-bit one 55
-// against 125.
+// pools: 8) move 16 bytes a load (VEC), others one element: rotary 60 against
+// 568 us at the size above, the 8-bit write 52 against 181, the 16-bit one 39
+// against 124.
 //
 // 8-bit rows: the codes are those of exact arithmetic, rounded once.  32-bit
 // arithmetic decides nearly all of them: a code is taken when the values an
@@ -185,7 +185,7 @@ struct RotatePlan {
 };
 
 // A group's warps wait for one another twice; with up to 16 tokens (4) the
-// 8-bit write takes 66 (76) us and rotary 63 (65).
+// 8-bit write takes 52 (60) us and rotary 64 (66).
 constexpr int kRotGroup = 16;     // most tokens of a group
 constexpr int kRotAngles = 1024;  // their (cos, sin) pairs: rotary_dim <= 512
 
@@ -550,14 +550,14 @@ __device__ __forceinline__ void code_unit(const Raw<T>& raw, const Unit& u, int 
 }
 
 // A thread keeps its lane of the row and goes through rows (passes) and
-// tokens; the next rows' loads are in flight while it turns and codes one or
-// two, the first ones' while the block prepares the angles.
+// tokens; the next row's loads are in flight while it turns and codes one, the
+// first one's while the block prepares the angles (two rows at a time spill:
+// 16-bit writes 56 us for 39).
 // WRITE: k and v rows as well, into the pool; E4: in 8 bits.
 template <typename T, bool WRITE, bool E4, bool VEC, bool INTER>
 __global__ void __launch_bounds__(kRotThreads, E4 ? 3 : VEC ? 4 : 2)
     rotate_kernel(const __grid_constant__ RotateParams p, const __grid_constant__ RotatePlan n) {
   dep_enter();
-  constexpr int kRun = sizeof(T) == 4 || !VEC || E4 ? 1 : 2;
   __shared__ __align__(16) float2 cs[kRotAngles];
   __shared__ __align__(16) double2 csd[E4 ? kRotAngles : 1];
   __shared__ long long dst[kRotGroup], sdst[kRotGroup], pos[kRotGroup];
@@ -576,106 +576,100 @@ __global__ void __launch_bounds__(kRotThreads, E4 ? 3 : VEC ? 4 : 2)
     int b = quotient(static_cast<int>(t0), n.div_N), j = static_cast<int>(t0) - b * p.N;
     const T *q_at = nullptr, *k_at = nullptr, *v_at = nullptr;
     const int all = group * n.passes;
-    struct Rows {
-      Raw<T> raw[kRun];
-      int k[kRun], r[kRun];
+    struct Row {
+      Raw<T> raw;
+      int k, r;
     };
-    const auto fetch = [&](Rows& x, int it) {
-#pragma unroll
-      for (int z = 0; z < kRun; ++z) {
-        if (pass == 0 && it + z < all) {
-          q_at = static_cast<const T*>(p.q.p) + b * p.q.sb + j * p.q.sn;
-          if (WRITE) {
-            k_at = static_cast<const T*>(p.k.p) + b * p.k.sb + j * p.k.sn;
-            v_at = static_cast<const T*>(p.v.p) + b * p.v.sb + j * p.v.sn;
-          }
-        }
-        const int r = pass * n.rows + place;
-        const bool in = it + z < all && slot < n.rows && r < rows;
-        x.k[z] = k;
-        x.r[z] = in ? r : -1;
-        if (in) {
-          if (!WRITE || r < p.Hq)
-            load_raw<T, VEC>(q_at + r * p.q.sh, turned, x.raw[z]);
-          else if (r < p.Hq + p.c.heads)
-            load_raw<T, VEC>(k_at + (r - p.Hq) * p.k.sh, turned, x.raw[z]);
-          else
-            load_raw<T, VEC>(v_at + (r - p.Hq - p.c.heads) * p.v.sh, plain, x.raw[z]);
-        }
-        if (++pass == n.passes) {
-          pass = 0;
-          ++k;
-          // a warp's rows move on with the tokens: some are more work
-          if (E4 && (place += n.turn) >= n.rows) place -= n.rows;
-          if (++j == p.N) {
-            j = 0;
-            ++b;
-          }
-        }
-      }
-    };
-    const auto finish = [&](const Rows& x, int it) {
-#pragma unroll
-      for (int z = 0; z < kRun; ++z) {
-        if (it + z >= all) continue;
-        const int r = x.r[z];
-        const long long at = dst[x.k[z]];
-        const int base = x.k[z] * half_rd;
-        float f[8], g[8];
-        float2 w[8];
-        if (!WRITE || r < p.Hq) {
-          if (r >= 0 && at != -2 && turned.na > 0) {
-            unpack_raw<T, VEC>(x.raw[z], turned, f, g);
-            if (turned.pair) {
-              load_angles<VEC>(cs + base + a0, cs + base + a1, turned.na, w);
-              turn_unit<VEC>(turned, w, f, g);
-            }
-            store_unit<T, VEC>(static_cast<T*>(p.q_out) + (t0 + x.k[z]) * p.qo_st + r * p.qo_sh, turned, f, g);
-          }
-        }
+    const auto fetch = [&](Row& x, int it) {
+      if (pass == 0 && it < all) {
+        q_at = static_cast<const T*>(p.q.p) + b * p.q.sb + j * p.q.sn;
         if (WRITE) {
-          const bool mine = r >= p.Hq, key = mine && r < p.Hq + p.c.heads;
-          const int h = r - p.Hq - (key ? 0 : p.c.heads);
-          const Unit& u = key ? turned : plain;
-          const bool live = mine && at >= 0;
-          const bool pair = key && turned.pair;
-          if (E4) {
-            if (__any_sync(0xffffffffu, live)) {
-              uint8_t* const to = static_cast<uint8_t*>(key ? p.c.k : p.c.v) + at + h * p.c.head_stride;
-              float* const scale = (key ? p.c.ks : p.c.vs) + sdst[x.k[z]] + static_cast<long long>(h) * p.c.page_size;
-              const float2 *w0 = cs + base + a0, *w1 = cs + base + a1;
-              const double2 *cd0 = csd + (E4 ? base + a0 : 0), *cd1 = csd + (E4 ? base + a1 : 0);
-              const bool mine_live = live && u.na > 0;
-              if constexpr (!VEC)
-                code_unit<T, INTER>(x.raw[z], u, n.UP, lane == 0, mine_live, pair, key && turn, p.magnitude, w0, w1, cd0, cd1, to, scale);
-              else if (__any_sync(0xffffffffu, live && key && turn))
-                code_turned_unit<T, INTER>(x.raw[z], u, n.UP, lane == 0, mine_live, pair, p.magnitude, w0, w1, cd0, cd1, to, scale);
-              else
-                code_exact_unit<T>(x.raw[z], u, n.UP, lane == 0, mine_live, to, scale);
-            }
-          } else if (live && u.na > 0) {
-            unpack_raw<T, VEC>(x.raw[z], u, f, g);
-            if (pair) {
-              load_angles<VEC>(cs + base + a0, cs + base + a1, u.na, w);
-              turn_unit<VEC>(u, w, f, g);
-            }
-            store_unit<T, VEC>(static_cast<T*>(key ? p.c.k : p.c.v) + at + h * p.c.head_stride, u, f, g);
-          }
+          k_at = static_cast<const T*>(p.k.p) + b * p.k.sb + j * p.k.sn;
+          v_at = static_cast<const T*>(p.v.p) + b * p.v.sb + j * p.v.sn;
+        }
+      }
+      const int r = pass * n.rows + place;
+      const bool in = it < all && slot < n.rows && r < rows;
+      x.k = k;
+      x.r = in ? r : -1;
+      if (in) {
+        if (!WRITE || r < p.Hq)
+          load_raw<T, VEC>(q_at + r * p.q.sh, turned, x.raw);
+        else if (r < p.Hq + p.c.heads)
+          load_raw<T, VEC>(k_at + (r - p.Hq) * p.k.sh, turned, x.raw);
+        else
+          load_raw<T, VEC>(v_at + (r - p.Hq - p.c.heads) * p.v.sh, plain, x.raw);
+      }
+      if (++pass == n.passes) {
+        pass = 0;
+        ++k;
+        // a warp's rows move on with the tokens: some are more work
+        if (E4 && (place += n.turn) >= n.rows) place -= n.rows;
+        if (++j == p.N) {
+          j = 0;
+          ++b;
         }
       }
     };
-    Rows x, y;
+    const auto finish = [&](const Row& x, int it) {
+      if (it >= all) return;
+      const int r = x.r;
+      const long long at = dst[x.k];
+      const int base = x.k * half_rd;
+      float f[8], g[8];
+      float2 w[8];
+      if (!WRITE || r < p.Hq) {
+        if (r >= 0 && at != -2 && turned.na > 0) {
+          unpack_raw<T, VEC>(x.raw, turned, f, g);
+          if (turned.pair) {
+            load_angles<VEC>(cs + base + a0, cs + base + a1, turned.na, w);
+            turn_unit<VEC>(turned, w, f, g);
+          }
+          store_unit<T, VEC>(static_cast<T*>(p.q_out) + (t0 + x.k) * p.qo_st + r * p.qo_sh, turned, f, g);
+        }
+      }
+      if (WRITE) {
+        const bool mine = r >= p.Hq, key = mine && r < p.Hq + p.c.heads;
+        const int h = r - p.Hq - (key ? 0 : p.c.heads);
+        const Unit& u = key ? turned : plain;
+        const bool live = mine && at >= 0;
+        const bool pair = key && turned.pair;
+        if (E4) {
+          if (__any_sync(0xffffffffu, live)) {
+            uint8_t* const to = static_cast<uint8_t*>(key ? p.c.k : p.c.v) + at + h * p.c.head_stride;
+            float* const scale = (key ? p.c.ks : p.c.vs) + sdst[x.k] + static_cast<long long>(h) * p.c.page_size;
+            const float2 *w0 = cs + base + a0, *w1 = cs + base + a1;
+            const double2 *cd0 = csd + (E4 ? base + a0 : 0), *cd1 = csd + (E4 ? base + a1 : 0);
+            const bool mine_live = live && u.na > 0;
+            if constexpr (!VEC)
+              code_unit<T, INTER>(x.raw, u, n.UP, lane == 0, mine_live, pair, key && turn, p.magnitude, w0, w1, cd0, cd1, to, scale);
+            else if (__any_sync(0xffffffffu, live && key && turn))
+              code_turned_unit<T, INTER>(x.raw, u, n.UP, lane == 0, mine_live, pair, p.magnitude, w0, w1, cd0, cd1, to, scale);
+            else
+              code_exact_unit<T>(x.raw, u, n.UP, lane == 0, mine_live, to, scale);
+          }
+        } else if (live && u.na > 0) {
+          unpack_raw<T, VEC>(x.raw, u, f, g);
+          if (pair) {
+            load_angles<VEC>(cs + base + a0, cs + base + a1, u.na, w);
+            turn_unit<VEC>(u, w, f, g);
+          }
+          store_unit<T, VEC>(static_cast<T*>(key ? p.c.k : p.c.v) + at + h * p.c.head_stride, u, f, g);
+        }
+      }
+    };
+    Row x, y;
     fetch(x, 0);
     prepare_tokens<E4>(p, n, t0, group, cs, csd, dst, sdst, pos);
 #pragma unroll 1
-    for (int it = 0; it < all; it += kRun) {
-      fetch(y, it + kRun);
+    for (int it = 0; it < all; ++it) {
+      fetch(y, it + 1);
       finish(x, it);
       if (WRITE) {  // (long code: not twice)
         x = y;
       } else {
-        it += kRun;
-        fetch(x, it + kRun);
+        ++it;
+        fetch(x, it + 1);
         finish(y, it);
       }
     }
