@@ -141,6 +141,10 @@ def test_tree_attention_scratch_size_limits(lib):
         assert size(*bad) == 0, bad
 
 
+def test_status_refusals(lib):
+    assert lib.spec_verify_cache_read_device_status(None, 0, None) == INVALID
+
+
 def test_cache_commit_refusals(lib):
     for bad in (dict(N=0), dict(N=65), dict(lens=None), dict(acc=None), dict(new=None)):
         assert call(lib, "cache_commit", **bad) == INVALID, bad

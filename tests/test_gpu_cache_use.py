@@ -121,7 +121,10 @@ def attention64(q, cache, table, clen, parent):
 @pytest.mark.parametrize("qt,kv,B,N,Hkv,G,D,page", [
     ("bf16", "bf16", 64, 26, 8, 4, 128, 64), ("fp16", "fp16", 48, 5, 8, 4, 128, 16),
     ("bf16", "e4m3", 96, 26, 8, 4, 128, 64), ("fp16", "e4m3", 64, 9, 8, 8, 64, 32),
-    ("bf16", "bf16", 24, 40, 8, 8, 128, 64), ("bf16", "bf16", 200, 4, 8, 1, 64, 128)])
+    ("bf16", "bf16", 24, 40, 8, 8, 128, 64), ("bf16", "bf16", 200, 4, 8, 1, 64, 128),
+    ("fp16", "e4m3", 16, 40, 8, 8, 128, 16), ("bf16", "e4m3", 16, 64, 8, 4, 64, 8),
+    ("bf16", "e4m3", 40, 5, 8, 8, 128, 128), ("bf16", "e4m3", 64, 3, 8, 2, 96, 16),
+    ("fp16", "fp16", 100, 13, 4, 8, 80, 32)])
 def test_attention_of_batches_that_wait_for_memory(dev, qt, kv, B, N, Hkv, G, D, page):
     """Every block walks several sequences, and the products wait for the tiles:
     each tile's wait has to be for that very tile.  The bound as in
