@@ -15,8 +15,9 @@
 // Per tile S = Q K^T (128 rows x 128 tokens) and O += P V, both by
 // tcgen05.mma from shared memory filled by TMA (P from tensor memory, where
 // it overlies S).  Two softmax warpgroups work in turn, each with its own S
-// and O in tensor memory: with at most 128 rows they take alternate tiles
-// (merged at the segment's end), with more each takes one half of the rows.
+// and O in tensor memory: with more than 128 rows each takes one half of them,
+// else they take alternate tiles or, for 8-bit pools with more than 64 rows,
+// each half of every tile's tokens (merged at the segment's end).
 // The MMA warp issues S of one while the other computes its exponentials.
 // A thread owns one row, so a row's maximum and sum need no shuffles.  The
 // running maximum is only raised when a score exceeds it by 2^8: O is then
@@ -362,7 +363,7 @@ __device__ __forceinline__ bool odd_word(uint32_t w) {
 struct Control {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t scale_full[kScaleRing];
-  uint64_t s_full[2], p_ready[2][2], o_done, q_full[2], q_empty[2], q_tma, drained;
+  uint64_t s_full[2], p_ready[2][2], pv_done[2], o_done, q_full[2], q_empty[2], q_tma, drained;
   uint32_t tmem;
   int abort;
   int stop;              // abort, as the softmax warpgroups agreed on it
@@ -403,17 +404,16 @@ __device__ __forceinline__ bool gave_up(const Control* s) { return *reinterpret_
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// Largest score of a row's tile, NC chunks of 16 columns.  Both passes over a
-// tile read a chunk ahead of the arithmetic.
-template <int NC>
+// Largest score of a row's whole tile.  Both passes over a tile read a chunk
+// ahead of the arithmetic.
 __device__ __forceinline__ float tile_max(uint32_t s_addr) {
   float top[2] = {-INFINITY, -INFINITY};
   uint32_t v[2][16];
   tmem_ld16(s_addr, v[0]);
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
+  for (int c = 0; c < 8; ++c) {
     tmem_wait_ld();
-    if (c < NC - 1) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
+    if (c < 7) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       const uint32_t* w = &v[c & 1][i];
@@ -443,49 +443,58 @@ __device__ __forceinline__ void fma_ex2(float& a, float& b) {
   b = b > -126.0f ? q : zb;
 }
 
-// Weights 2^(s c2 - shift) of a row's tile into tensor memory over the scores;
-// returns their sum.  `half` is told when the first half of 128 columns is there.
-template <typename M, int NC>
-__device__ __forceinline__ float tile_weights(uint32_t s_addr, uint32_t p_addr, float c2, float shift, uint64_t* half) {
+// Weights 2^(s c2 - shift) of 16 columns in the values' type, and their sums.
+template <typename M>
+__device__ __forceinline__ void weigh16(const uint32_t (&v)[16], unsigned long long c22, unsigned long long sh2,
+                                        unsigned long long (&sum)[2], uint32_t (&out)[8]) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    unsigned long long x = fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), c22, sh2);
+    unsigned long long y = fma2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), c22, sh2);
+    float f[4];
+    unpack2(x, f[0], f[1]);
+    unpack2(y, f[2], f[3]);
+    f[0] = ex2f(f[0]);
+    f[1] = ex2f(f[1]);
+    x = pack2(f[0], f[1]);
+    if (i & 4) {
+      fma_ex2(f[2], f[3]);  // a quarter of them
+    } else {
+      f[2] = ex2f(f[2]);
+      f[3] = ex2f(f[3]);
+    }
+    y = pack2(f[2], f[3]);
+    sum[0] = add2(sum[0], x);
+    sum[1] = add2(sum[1], y);
+    out[i >> 1] = pack_weights<M>(f[0], f[1]);
+    out[(i >> 1) + 1] = pack_weights<M>(f[2], f[3]);
+  }
+}
+__device__ __forceinline__ float total2(const unsigned long long (&sum)[2]) {
+  float a, b, d, e;
+  unpack2(sum[0], a, b);
+  unpack2(sum[1], d, e);
+  return (a + b) + (d + e);
+}
+
+// A row's whole tile into tensor memory over the scores; returns the sum.
+// `half` is told when the first half of 128 columns is there.
+template <typename M>
+__device__ __forceinline__ float tile_weights(uint32_t s_addr, float c2, float shift, uint64_t* half) {
   const unsigned long long c22 = splat2(c2), sh2 = splat2(-shift);
   unsigned long long sum[2] = {0ull, 0ull};
   uint32_t v[2][16];
   tmem_ld16(s_addr, v[0]);
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
+  for (int c = 0; c < 8; ++c) {
     uint32_t out[8];
     tmem_wait_ld();
-    if (c < NC - 1) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const uint32_t* w = &v[c & 1][i];
-      unsigned long long x = fma2(pack2(__uint_as_float(w[0]), __uint_as_float(w[1])), c22, sh2);
-      unsigned long long y = fma2(pack2(__uint_as_float(w[2]), __uint_as_float(w[3])), c22, sh2);
-      float f[4];
-      unpack2(x, f[0], f[1]);
-      unpack2(y, f[2], f[3]);
-      f[0] = ex2f(f[0]);
-      f[1] = ex2f(f[1]);
-      x = pack2(f[0], f[1]);
-      if (i & 4) {
-        fma_ex2(f[2], f[3]);  // a quarter of them
-      } else {
-        f[2] = ex2f(f[2]);
-        f[3] = ex2f(f[3]);
-      }
-      y = pack2(f[2], f[3]);
-      sum[0] = add2(sum[0], x);
-      sum[1] = add2(sum[1], y);
-      out[i >> 1] = pack_weights<M>(f[0], f[1]);
-      out[(i >> 1) + 1] = pack_weights<M>(f[2], f[3]);
-    }
-    tmem_st8(p_addr + c * 8, out);
-    if (NC == 8 && c == 3) hand_over(half);
+    if (c < 7) tmem_ld16(s_addr + (c + 1) * 16, v[(c + 1) & 1]);
+    weigh16<M>(v[c & 1], c22, sh2, sum, out);
+    tmem_st8(s_addr + c * 8, out);
+    if (c == 3) hand_over(half);
   }
-  float a, b, d, e;
-  unpack2(sum[0], a, b);
-  unpack2(sum[1], d, e);
-  return (a + b) + (d + e);
+  return total2(sum);
 }
 
 // ---- the same for 8-bit pools.  A tile's scales lie in boxes of u = 8, 16 or
@@ -514,11 +523,15 @@ __device__ __forceinline__ void max_chunk(const uint32_t (&v)[16], float (&top)[
     top[1] = fmax3(top[1], __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
   }
 }
-// Columns of the weights' terms over the scores: blocks of 32 at 0, 64 and 96.
-__host__ __device__ constexpr uint32_t term_column(int n) { return n > 0 ? 32 + 32 * n : 0; }
-// 16 columns' weights, times V's scales, as TERMS 8-bit terms: columns [col / 4,
-// col / 4 + 4) of each block.
-template <int TERMS>
+// Columns of the weights' terms over the scores, of the first or second half of
+// the tokens.  Two row tiles (a row's thread weighs the whole tile): blocks of
+// 32 at 0, 64 and 96.  Else blocks of 16 within each half's 64.
+template <bool TWO>
+__host__ __device__ constexpr uint32_t term_column(int n, int half) {
+  return TWO ? (n > 0 ? 32 + 32 * n : 0) + 16 * half : 64 * half + 16 * n;
+}
+// 16 columns' weights, times V's scales, as TERMS 8-bit terms of 4 columns each.
+template <int TERMS, bool TWO>
 __device__ __forceinline__ void weigh_chunk(const uint32_t (&v)[16], const Scales& sc, int col, uint32_t s_addr,
                                             unsigned long long c22, unsigned long long sh2, unsigned long long (&sum)[2]) {
   uint32_t out[TERMS][4];
@@ -549,18 +562,17 @@ __device__ __forceinline__ void weigh_chunk(const uint32_t (&v)[16], const Scale
     for (int n = 0; n < TERMS; ++n) out[n][i >> 2] = codes[n][0] | codes[n][1] << 16;
   }
 #pragma unroll
-  for (int n = 0; n < TERMS; ++n) tmem_st4(s_addr + term_column(n) + col / 4, out[n]);
+  for (int n = 0; n < TERMS; ++n) tmem_st4(s_addr + term_column<TWO>(n, col / 64) + (col & 63) / 4, out[n]);
 }
 
 // Puts -inf where a column is masked (bit i of word c allows column 32 c + i),
 // before the two passes.  8-bit pools: K's scales enter here, so that a scale
 // of a masked column does not matter, and the passes take ones.
 template <bool E4>
-__device__ __forceinline__ void mask_tile(uint32_t s_addr, const Scales& sc, const uint32_t (&words)[4], int lo, int hi) {
+__device__ __forceinline__ void mask_tile(uint32_t s_addr, const Scales& sc, const uint32_t (&words)[4]) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const uint32_t word = words[c];
-    if (c < lo || c >= hi) continue;
     if (!E4 && __all_sync(0xffffffffu, word == ~0u)) continue;
 #pragma unroll 1
     for (int z = 0; z < 2; ++z) {
@@ -585,6 +597,7 @@ __device__ __forceinline__ void load_segment(const MmaParams& p, const CUtensorM
                                              unsigned char* q_tiles, unsigned char* q_terms, int buf, uint32_t phase,
                                              int tid) {
   constexpr int kTerms = std::is_same<QT, __nv_bfloat16>::value ? 2 : 3;
+  constexpr int kCopies = SPLIT > 1 ? SPLIT : 1;
   const AttnParams& a = p.a;
   const int row0 = w.row0();
   const int rows = min(2 * w.pr + 1 < p.halves ? 2 * kTile : kTile, p.R - row0);
@@ -605,7 +618,7 @@ __device__ __forceinline__ void load_segment(const MmaParams& p, const CUtensorM
         const int node = SPLIT > 1 ? 0 : (row0 + i * kTile) / a.G;
 #pragma unroll
         for (int c = 0; c < DP / 64; ++c)
-          tma_4d(smem_addr(q_tiles) + (SPLIT > 1 ? i * (kTile / SPLIT) * 128 : i * kTile * DP * 2) + c * p.qrows * 128,
+          tma_4d(smem_addr(q_tiles) + (SPLIT > 1 ? i * (kTile / kCopies) * 128 : i * kTile * DP * 2) + c * p.qrows * 128,
                  qmap, c * 64, w.h * a.G, node, w.b, &s->q_tma);
       }
     }
@@ -620,7 +633,7 @@ __device__ __forceinline__ void load_segment(const MmaParams& p, const CUtensorM
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = src[2 * i] | static_cast<uint32_t>(src[2 * i + 1]) << 16;
       }
-      for (int i = 0; i < SPLIT; ++i) *place(rr + i * (kTile / SPLIT)) = make_uint4(y[0], y[1], y[2], y[3]);
+      for (int i = 0; i < kCopies; ++i) *place(rr + i * (kTile / kCopies)) = make_uint4(y[0], y[1], y[2], y[3]);
     }
   }
   if (a.parent && tid < a.N) s->parent[buf][tid] = __ldg(a.parent + static_cast<long long>(w.b) * a.N + tid);
@@ -650,7 +663,7 @@ __device__ __forceinline__ void load_segment(const MmaParams& p, const CUtensorM
       if (!E4) {
         if (in) {
 #pragma unroll
-          for (int i = 0; i < SPLIT; ++i) *place(r0 + i * (kTile / SPLIT)) = v;
+          for (int i = 0; i < kCopies; ++i) *place(r0 + i * (kTile / kCopies)) = v;
         }
         continue;
       }
@@ -687,8 +700,8 @@ __device__ __forceinline__ void load_segment(const MmaParams& p, const CUtensorM
         }
         if (in) {
 #pragma unroll
-          for (int i = 0; i < SPLIT; ++i) {
-            const int r = (r0 & 127) + i * (kTile / SPLIT);
+          for (int i = 0; i < kCopies; ++i) {
+            const int r = (r0 & 127) + i * (kTile / kCopies);
             *reinterpret_cast<uint2*>(q_terms + ((r0 >> 7) * kTerms + n) * p.qrows * 128 + r * 128 +
                                       (((j >> 1) ^ (r & 7)) * 16) + (j & 1) * 8) = make_uint2(w[0], w[1]);
           }
@@ -749,9 +762,9 @@ __device__ __forceinline__ int v_entry(bool two, int t, int T) { return two ? 2 
 }  // namespace
 
 // DP: head_dim rounded up to 64 or 128.  QT: queries and output; E4: 8-bit
-// pool.  SPLIT: with few rows, copies of them that fill the 128 lanes; each
-// takes a share of a tile's columns, as a sequence of its own that is joined
-// at the segment's end.
+// pool.  SPLIT: 0 for items of two row tiles, else the copies of the rows that
+// fill the 128 lanes (1, or with few rows 2 or 4); each takes a share of a
+// tile's columns, as a sequence of its own that is joined at the segment's end.
 template <typename QT, int DP, bool E4, int SPLIT>
 __global__ void __launch_bounds__(384, 1)
     attention_mma_kernel(const __grid_constant__ MmaParams p, const __grid_constant__ CUtensorMap kmap,
@@ -761,6 +774,15 @@ __global__ void __launch_bounds__(384, 1)
   constexpr uint32_t entry = kTile * kRow;
   constexpr int kLoader = 10;                        // first of the two warps that load queries ahead
   constexpr int kChunks = DP / 64;
+  constexpr bool two = SPLIT == 0;
+  constexpr int kCopies = two ? 1 : SPLIT;
+  // How the softmax warpgroups share the tiles.  Two row tiles: each its rows of
+  // every tile.  8-bit pools with 65 to 128 rows: each half of every tile's
+  // tokens, with an output of its own (104 rows: 160 us for 184 with tiles by
+  // turns; 40 rows in two copies 157 for 142, 16 bits the same either way).
+  // Else tiles by turns.
+  constexpr bool kHalves = E4 && SPLIT == 1, kTurns = !two && !kHalves;
+  constexpr bool kWhole = two || (kTurns && kCopies == 1);  // a thread weighs whole tiles
   constexpr bool kBf16 = !E4 && std::is_same<QT, __nv_bfloat16>::value;
   constexpr int kTerms = std::is_same<QT, __nv_bfloat16>::value ? 2 : 3;  // 8-bit terms of queries and weights
   constexpr uint32_t kShapeS = mma_shape(kBf16, kTile, false);
@@ -791,6 +813,7 @@ __global__ void __launch_bounds__(384, 1)
     for (int i = 0; i < kScaleRing; ++i) mbar_init(&s->scale_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s->s_full[i], 1);
+      mbar_init(&s->pv_done[i], 1);
       for (int z = 0; z < 2; ++z) mbar_init(&s->p_ready[i][z], 4);
       s->bad[i] = 0;
       for (int z = 0; z < 2; ++z) s->odd[z][i] = 0u;
@@ -832,7 +855,6 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t e = 0, slot = 0, phase = 0, tile = 0;  // ring entries filled, the next one's place; tiles of keys
       bool stop = false;  // the same in all lanes
       do {
-        const bool two = 2 * w.pr + 1 < p.halves;
         const int h = w.h;
         const int T = w.t1 - w.t0;
         // page (num_pages: none, which TMA fills with zeros) and place of this
@@ -926,7 +948,6 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t seg = 0, np = 0;  // np: phases of p_ready, one bit a warpgroup
       bool stop = false;
       do {
-        const bool two = __shfl_sync(0xffffffffu, 2 * w.pr + 1 < p.halves, 0);
         const int T = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0), U = two ? 2 * T : T;
         const uint32_t buf = p.qbufs == 2 ? seg & 1u : 0u;
         wait(s, &s->q_full[buf], (p.qbufs == 2 ? seg >> 1 : seg) & 1u, a.ctrl);
@@ -958,23 +979,23 @@ __global__ void __launch_bounds__(384, 1)
             const uint32_t f = g ^ 1u;  // unit x - 1
             if (!two || f == 0) take(vslot);
             const uint32_t vd = v0 + vslot * (entry >> 4);
-            const uint32_t o = acc + 2 * kTile + f * DP, pw = acc + f * kTile;
-            const bool add = x > 2;
+            const uint32_t pw = acc + f * kTile;
             const auto accumulate = [&](int half) {
+              const uint32_t o = acc + 2 * kTile + (kHalves ? half : f) * DP;
+              const bool add = kHalves ? x > 1 : x > 2 || half > 0;
               if (E4) {
                 // 32 tokens a step, each with the terms of the weights
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                   for (int n = 0; n < kTerms; ++n)
-                    mma_ts<E4>(o, pw + term_column(n) + (2 * half + k) * 8,
-                               vd + (2 * half + k) * (32 * 128 >> 4), kShapeO,
-                               add || half > 0 || k > 0 || n > 0);
+                    mma_ts<E4>(o, pw + term_column<!kHalves>(n, half) + k * 8, vd + (2 * half + k) * (32 * 128 >> 4), kShapeO,
+                               add || k > 0 || n > 0);
               } else {
 #pragma unroll
                 for (int k = 0; k < kTile / 32; ++k)
-                  mma_ts<E4>(o, pw + (half * 4 + k) * 8, vd + (half * 4 + k) * (16 * 128 >> 4), kShapeO,
-                             add || half > 0 || k > 0);
+                  mma_ts<E4>(o, pw + half * 32 + k * 8, vd + (half * 4 + k) * (16 * 128 >> 4), kShapeO,
+                             add || k > 0);
               }
             };
             wait(s, &s->p_ready[f][0], np >> f & 1u, a.ctrl);
@@ -989,6 +1010,7 @@ __global__ void __launch_bounds__(384, 1)
             if (elect_one()) {
               accumulate(1);
               if (!two || f == 1) mma_commit(&s->empty[vslot]);
+              if (kHalves) mma_commit(&s->pv_done[f]);
               if (x == U) mma_commit(&s->o_done);
             }
             __syncwarp();
@@ -1045,11 +1067,9 @@ __global__ void __launch_bounds__(384, 1)
       // ------------------------------------------------ softmax warpgroups
       const int g = warp >> 2, r = tid & 127;
       const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 (warp % 4)
-      const uint32_t s_addr = tmem + lane_base + g * kTile;
       uint32_t base = 0, tile_base = 0, ns = 0, seg = 0;
       do {
         const int h = w.h;
-        const bool two = 2 * w.pr + 1 < p.halves;
         const int T = w.t1 - w.t0;
         const int row0 = w.row0();
         const int rows = min(two ? 2 * kTile : kTile, p.R - row0);
@@ -1058,7 +1078,7 @@ __global__ void __launch_bounds__(384, 1)
         if (tid == 0 && w.t0 == 0 && w.nodes > 0 && w.len + w.nodes > w.total) raise_flag(a.ctrl, kFlagCapacity);
         const bool missing = *reinterpret_cast<volatile int*>(&s->bad[buf]) != 0;
 
-        constexpr int lanes = kTile / SPLIT;
+        constexpr int lanes = kTile / kCopies;
         const int copy = r / lanes;
         const int row = two ? g * kTile + r : r - copy * lanes;  // row within the item
         const bool live = row < rows;
@@ -1085,9 +1105,9 @@ __global__ void __launch_bounds__(384, 1)
         float M = -INFINITY, l = 0.0f;
         int vexp = -200;  // log2 of the weights' common factor (8-bit pools)
 
-        const int U = two ? 2 * T : T;
-        for (int x = g; x < U; x += 2) {
-          const int t = two ? x >> 1 : x;
+        for (int t = kTurns ? g : 0; t < T; t += kTurns ? 2 : 1) {
+          const int sb = kHalves ? t & 1 : g;  // where the scores are
+          const uint32_t s_addr = tmem + lane_base + sb * kTile;
           const long long tok0 = static_cast<long long>(w.t0 + t) * kTile;
           const bool tail = tok0 + kTile > w.len;           // drafted tokens or the end
           const bool masked = tail || tok0 + kTile > w.total || missing;
@@ -1102,8 +1122,8 @@ __global__ void __launch_bounds__(384, 1)
             __syncwarp();
           }
           const auto scores = [&] {
-            wait(s, &s->s_full[g], ns & 1u, a.ctrl);
-            ++ns;
+            wait(s, &s->s_full[sb], ns >> sb & 1u, a.ctrl);
+            ns ^= 1u << sb;
           };
           if (tail) {
             // The scores first: with them every ring entry up to this tile's keys
@@ -1114,7 +1134,7 @@ __global__ void __launch_bounds__(384, 1)
             // zero weight stays zero.  A drafted token's infinities and NaN
             // are taken out as well and added by hand to the rows that see it.
             const long long tok = tok0 + r;
-            if ((!two || g == 0) && tok >= w.len) {
+            if ((kTurns || g == 0) && tok >= w.len) {
               const uint32_t e = base + v_entry(two, t, T), slot = e % p.stages;
               wait(s, &s->full[slot], (e / p.stages) & 1u, a.ctrl);
               uint4* line = reinterpret_cast<uint4*>(ring + slot * entry + r * 128);
@@ -1177,11 +1197,15 @@ __global__ void __launch_bounds__(384, 1)
           __syncwarp();
           tmem_fence_after();
           if (warp_live) {
+            // the columns this thread weighs
+            constexpr int kNC = kHalves ? 4 : 8 / kCopies;
+            const int col0 = kHalves ? 64 * g : copy * (kTile / kCopies);
+            constexpr int kWords = kNC / 2;
+            uint32_t words[kWords];
             if (masked) {
-              uint32_t words[4];
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const long long off = tok0 + 32 * c - w.len, lim = w.total - (tok0 + 32 * c);
+              for (int c = 0; c < kWords; ++c) {
+                const long long from = tok0 + col0 + 32 * c, off = from - w.len, lim = w.total - from;
                 uint32_t y = ~0u;
                 if (off >= 64) y = 0u;
                 else if (off >= 0) y = static_cast<uint32_t>(mask >> off);
@@ -1191,7 +1215,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (missing) {
                   bool in = false;
                   if (lane < lim) {
-                    const int pi = page_of(a.c, static_cast<int>(tok0 + 32 * c + lane));
+                    const int pi = page_of(a.c, static_cast<int>(from + lane));
                     in = static_cast<unsigned int>(__ldg(a.c.table + static_cast<long long>(w.b) * a.c.table_stride + pi)) <
                          static_cast<unsigned int>(a.c.num_pages);
                   }
@@ -1199,40 +1223,68 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 words[c] = y;
               }
-              mask_tile<E4>(s_addr, sc, words, copy * 4 / SPLIT, (copy * 4 + 4) / SPLIT);
-              sc.k = s->ones;
+              if constexpr (kWhole) {
+                mask_tile<E4>(s_addr, sc, words);
+                sc.k = s->ones;
+              }
             }
-            const int c0 = copy * (8 / SPLIT);
-            // 8-bit pools: the terms of the weights lie over the upper half of
-            // the scores, which is read first and held (a split row's share is
-            // held whole)
-            constexpr int kHeld = E4 ? (SPLIT > 1 ? 8 / SPLIT : 4) : 1;
+            // Scores that are read once and held: a share of a tile, or with two
+            // row tiles and an 8-bit pool the second half, over which terms of
+            // the weights lie.
+            constexpr int kHeld = kWhole ? (E4 ? 4 : 1) : kNC;
             uint32_t held[kHeld][16];
             float top;
-            if (E4) {
+            if constexpr (!kWhole) {
+#pragma unroll
+              for (int c = 0; c < kNC; ++c) tmem_ld16(s_addr + col0 + c * 16, held[c]);
+              tmem_wait_ld();
+              if (kCopies > 1) {
+                // the other copies' weights count as zero here
+                const uint32_t none[E4 ? 8 : 16] = {};
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  if (c < copy * (4 / kCopies) || c >= (copy + 1) * (4 / kCopies)) {
+                    if constexpr (E4) {
+#pragma unroll
+                      for (int n = 0; n < kTerms; ++n) tmem_st8(s_addr + term_column<true>(n, c >> 1) + (c & 1) * 8, none);
+                    } else {
+                      tmem_st16(s_addr + c * 16, none);
+                    }
+                  }
+              }
               float t2[2] = {-INFINITY, -INFINITY};
-              const int h0 = SPLIT > 1 ? c0 : 4;
-              tmem_ld16(s_addr + h0 * 16, held[0]);
+#pragma unroll
+              for (int c = 0; c < kNC; ++c) {
+                if (E4) scale_chunk(held[c], sc, col0 + c * 16);
+                if (masked) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i)
+                    held[c][i] = words[c / 2] >> ((c & 1) * 16 + i) & 1u ? held[c][i] : 0xff800000u;
+                }
+                max_chunk(held[c], t2);
+              }
+              top = fmaxf(t2[0], t2[1]);
+            } else if constexpr (E4) {
+              float t2[2] = {-INFINITY, -INFINITY};
+              tmem_ld16(s_addr + 64, held[0]);
 #pragma unroll
               for (int c = 0; c < kHeld; ++c) {
                 tmem_wait_ld();
-                if (c < kHeld - 1) tmem_ld16(s_addr + (h0 + c + 1) * 16, held[c + 1]);
-                scale_chunk(held[c], sc, (h0 + c) * 16);
+                if (c < kHeld - 1) tmem_ld16(s_addr + (4 + c + 1) * 16, held[c + 1]);
+                scale_chunk(held[c], sc, (4 + c) * 16);
                 max_chunk(held[c], t2);
               }
-              if (SPLIT == 1) {
 #pragma unroll 2
-                for (int c = 0; c < 4; ++c) {
-                  uint32_t v[16];
-                  tmem_ld16(s_addr + c * 16, v);
-                  tmem_wait_ld();
-                  scale_chunk(v, sc, c * 16);
-                  max_chunk(v, t2);
-                }
+              for (int c = 0; c < 4; ++c) {
+                uint32_t v[16];
+                tmem_ld16(s_addr + c * 16, v);
+                tmem_wait_ld();
+                scale_chunk(v, sc, c * 16);
+                max_chunk(v, t2);
               }
               top = fmaxf(t2[0], t2[1]);
             } else {
-              top = tile_max<8 / SPLIT>(s_addr + c0 * 16);
+              top = tile_max(s_addr);
             }
             // (lanes without a row hold anything: they must not make the others
             // raise their maximum, or the roundings differ from call to call)
@@ -1252,7 +1304,14 @@ __global__ void __launch_bounds__(384, 1)
               l *= f;
             }
             // the first tile's product overwrites O
-            if (x > 1 && __any_sync(0xffffffffu, Mn != M)) {
+            if (t > (kTurns ? 1 : 0) && __any_sync(0xffffffffu, Mn != M)) {
+              if (kHalves) {
+                // (elsewhere these scores came after that product)
+                const int last = sb ^ 1;
+                wait(s, &s->pv_done[last], (ns >> last & 1u) ^ 1u, a.ctrl);
+                __syncwarp();
+                tmem_fence_after();
+              }
               const float f = M == -INFINITY ? 0.0f : Mn == M ? 1.0f : ex2f(M - Mn);
 #pragma unroll 1
               for (int c = 0; c < DP / 16; ++c) {
@@ -1266,53 +1325,42 @@ __global__ void __launch_bounds__(384, 1)
             }
             M = Mn;
             const float shift = M == -INFINITY ? 0.0f : M;
-            if (E4) {
-              const unsigned long long c22 = splat2(c2), sh2 = splat2(-shift);
-              unsigned long long sum[2] = {0ull, 0ull};
-              if (SPLIT == 1) {
+            const unsigned long long c22 = splat2(c2), sh2 = splat2(-shift);
+            unsigned long long sum[2] = {0ull, 0ull};
+            if constexpr (E4) {
+              if constexpr (kWhole) {
 #pragma unroll 2
                 for (int c = 0; c < 4; ++c) {
                   uint32_t v[16];
                   tmem_ld16(s_addr + c * 16, v);
                   tmem_wait_ld();
                   scale_chunk(v, sc, c * 16);
-                  weigh_chunk<kTerms>(v, sc, c * 16, s_addr, c22, sh2, sum);
+                  weigh_chunk<kTerms, !kHalves>(v, sc, c * 16, s_addr, c22, sh2, sum);
                 }
                 hand_over(&s->p_ready[g][0]);
               }
-              const int h0 = SPLIT > 1 ? c0 : 4;
+              const int from = kWhole ? 64 : col0;
 #pragma unroll
-              for (int c = 0; c < kHeld; ++c) weigh_chunk<kTerms>(held[c], sc, (h0 + c) * 16, s_addr, c22, sh2, sum);
-              float y0, y1, y2, y3;
-              unpack2(sum[0], y0, y1);
-              unpack2(sum[1], y2, y3);
-              l += (y0 + y1) + (y2 + y3);
-            } else {
-              l += tile_weights<QT, 8 / SPLIT>(s_addr + c0 * 16, s_addr + c0 * 8, c2, shift, &s->p_ready[g][0]);
-            }
-            if (SPLIT > 1) {
-              // the other copies' columns count as zero here
-              const uint32_t none[E4 ? 8 : 16] = {};
-              if constexpr (E4) {
+              for (int c = 0; c < kHeld; ++c) weigh_chunk<kTerms, !kHalves>(held[c], sc, from + c * 16, s_addr, c22, sh2, sum);
+              l += total2(sum);
+            } else if constexpr (!kWhole) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                  if (c < copy * (4 / SPLIT) || c >= (copy + 1) * (4 / SPLIT)) {
-#pragma unroll
-                    for (int n = 0; n < kTerms; ++n) tmem_st8(s_addr + term_column(n) + c * 8, none);
-                  }
-              } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                  if (c < copy * (4 / SPLIT) || c >= (copy + 1) * (4 / SPLIT)) tmem_st16(s_addr + c * 16, none);
+              for (int c = 0; c < kNC; ++c) {
+                uint32_t out[8];
+                weigh16<QT>(held[c], c22, sh2, sum, out);
+                tmem_st8(s_addr + (copy * kNC + c) * 8, out);
               }
+              l += total2(sum);
+            } else {
+              l += tile_weights<QT>(s_addr, c2, shift, &s->p_ready[g][0]);
             }
             tmem_wait_st();
           }
           tmem_fence_before();
           __syncwarp();
           if (lane == 0) {
-            if (SPLIT > 1 || !warp_live) mbar_arrive(&s->p_ready[g][0]);
-            mbar_arrive(&s->p_ready[g][1]);
+            if (!kHalves && (!kWhole || !warp_live)) mbar_arrive(&s->p_ready[g][0]);
+            mbar_arrive(kHalves ? &s->p_ready[sb][g] : &s->p_ready[g][1]);
           }
         }
 
@@ -1329,14 +1377,14 @@ __global__ void __launch_bounds__(384, 1)
           // all copies of the row in both groups; a group without a tile has
           // sum 0, and a NaN sum comes with a maximum of -inf
           float top = -INFINITY, sum = 0.0f;
-          float2 x[2 * SPLIT];
+          float2 x[2 * kCopies];
 #pragma unroll
-          for (int z = 0; z < 2 * SPLIT; ++z) {
+          for (int z = 0; z < 2 * kCopies; ++z) {
             x[z] = s->ml[z & 1][row + (z >> 1) * lanes];
             top = fmaxf(top, x[z].x);
           }
 #pragma unroll
-          for (int z = 0; z < 2 * SPLIT; ++z)
+          for (int z = 0; z < 2 * kCopies; ++z)
             if (x[z].y != 0.0f) sum += x[z].y * (x[z].x == top ? 1.0f : ex2f(x[z].x - top));
           const float2 x0 = s->ml[0][r], x1 = s->ml[1][r];
           f0 = x0.y == 0.0f ? 0.0f : x0.x == top ? 1.0f : ex2f(x0.x - top);
@@ -1357,7 +1405,7 @@ __global__ void __launch_bounds__(384, 1)
         // after the other, and behind them what the copies hand over.
         unsigned char* const staged = qs + buf * qbytes;
         float4* const handed =
-            reinterpret_cast<float4*>(staged + lanes * DP * 2) + g * (SPLIT - 1) * 4 * lanes;
+            reinterpret_cast<float4*>(staged + lanes * DP * 2) + g * (kCopies - 1) * 4 * lanes;
 #pragma unroll 2
         for (int c = 0; c < ncol; c += 16) {
           float o[16];
@@ -1648,7 +1696,8 @@ cudaError_t launch_split(MmaParams& p, const CUtensorMap (&maps)[5], int grid, c
   if constexpr (E4)
     if (p.split == 4) return wide ? launch_mma<QT, 128, E4, 4>(p, maps, grid, st) : launch_mma<QT, 64, E4, 4>(p, maps, grid, st);
   if (p.split == 2) return wide ? launch_mma<QT, 128, E4, 2>(p, maps, grid, st) : launch_mma<QT, 64, E4, 2>(p, maps, grid, st);
-  return wide ? launch_mma<QT, 128, E4, 1>(p, maps, grid, st) : launch_mma<QT, 64, E4, 1>(p, maps, grid, st);
+  if (p.split == 1) return wide ? launch_mma<QT, 128, E4, 1>(p, maps, grid, st) : launch_mma<QT, 64, E4, 1>(p, maps, grid, st);
+  return wide ? launch_mma<QT, 128, E4, 0>(p, maps, grid, st) : launch_mma<QT, 64, E4, 0>(p, maps, grid, st);
 }
 
 }  // namespace
@@ -1687,7 +1736,7 @@ cudaError_t launch_attention_mma(const AttnParams& a, int q_dtype, int cache_dty
   // Few rows: copies of them share a tile's columns.  Two 125,000-token
   // sequences, 20 rows (us, 1 / 2 / 4 copies): 8 bits 207 / 132 / 130, 64
   // sequences 155 / 116 / 108; 16 bits 170 / 160 / 161.
-  p.split = p.R <= 32 && cache_dtype == 3 ? 4 : p.R <= 64 ? 2 : 1;
+  p.split = p.R <= 32 && cache_dtype == 3 ? 4 : p.R <= 64 ? 2 : p.R <= kTile ? 1 : 0;
   CUtensorMap maps[5] = {};
   bool ok = pool_map(&maps[0], a.c, a.c.k, cache_dtype, p.box, p.head_first) &&
             pool_map(&maps[1], a.c, a.c.v, cache_dtype, p.box, p.head_first);

@@ -216,6 +216,25 @@ def test_attention_past_the_largest_values(dev, qt, kv, G):
             assert torch.equal(got[:, j], clean[:, j])
 
 
+@pytest.mark.parametrize("qt,kv", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3"), ("fp16", "e4m3")])
+@pytest.mark.parametrize("G", [2, 10, 26, 75])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_whose_maximum_grows(dev, qt, kv, G, D):
+    """Every tile raises some rows' maximum, with few rows and many: what has
+    been summed is scaled down each time, and not while it is being added to."""
+    n, N = 1500, 4
+    cache, table, clen = make([n], N, 16, 1, D, T[kv], seed=G)
+    g = torch.Generator().manual_seed(G)
+    sign = torch.randn(1, 1, D, generator=g).sign()
+    ramp = torch.linspace(0.1, 30, n + N)[:, None, None] * sign
+    fill(cache, table, 0, range(n + N), ramp * torch.ones(n + N, 1, D), torch.randn(n + N, 1, D, generator=g) * 3)
+    size = torch.rand(1, N, G, 1, generator=g) * 1.5
+    q = (sign[None] * size + 0.01 * torch.randn(1, N, G, D, generator=g)).to(T[qt]).to(dev)
+    got = check_attention(q, cache, table, clen)
+    for _ in range(10):
+        assert torch.equal(got["out"], sv.tree_attention(q, cache, table, clen)["out"])
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("page,D,layout", [(16, 64, "hnd"), (12, 66, "padded")])
 def test_attention_to_nothing_but_bad_pages(dev, kv, page, D, layout):
