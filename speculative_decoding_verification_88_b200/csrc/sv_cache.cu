@@ -729,9 +729,9 @@ cudaError_t launch_rotate(const RotateParams& p, int dtype, int cache_dtype, boo
 // A block takes up to 32 packed rows (fewer where there are few): one lane a
 // row finds its sequence (the last b with offsets[b] <= r) and its page, then
 // all threads convert (row, k or v, head) runs of 16 elements (8 where a head
-// has no whole number of them, or single ones where rows are unaligned: 74, 92
-// and 233 us for 32 sequences of 500 to 4096 tokens), four of a thread's runs
-// in flight at once.
+// has no whole number of them or 8-bit rows lie on 8-byte boundaries only, or
+// single ones where rows are unaligned: 74, 92 and 233 us for 32 sequences of
+// 500 to 4096 tokens), four of a thread's runs in flight at once.
 
 constexpr int kReadRows = 32;
 
@@ -835,12 +835,12 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__
 }
 
 template <typename C>
-static cudaError_t launch_read_c(const CacheReadParams& p, int out_dtype, bool vec, int sms, cudaStream_t st) {
+static cudaError_t launch_read_c(const CacheReadParams& p, int out_dtype, bool vec, bool on16, int sms, cudaStream_t st) {
   int rows = kReadRows;  // a block's: as many as leave two blocks for each SM
   while (rows > 1 && p.total < 2ll * sms * rows) rows /= 2;
   const dim3 grid(static_cast<unsigned int>((p.total + rows - 1) / rows));
   void (*k)(const CacheReadParams, int, UDiv, UDiv, UDiv);
-  const bool wide = vec && p.c.dim % 16 == 0;
+  const bool wide = vec && on16 && p.c.dim % 16 == 0;  // 16 codes are one 16-byte load
   const auto pick = [&](auto out) {
     using O = decltype(out);
     return wide ? cache_read_kernel<C, O, true, 16> : vec ? cache_read_kernel<C, O, true, 8> : cache_read_kernel<C, O, false, 8>;
@@ -852,13 +852,13 @@ static cudaError_t launch_read_c(const CacheReadParams& p, int out_dtype, bool v
                  1);
 }
 
-cudaError_t launch_cache_read(const CacheReadParams& p, int cache_dtype, int out_dtype, bool vec, int sms,
+cudaError_t launch_cache_read(const CacheReadParams& p, int cache_dtype, int out_dtype, bool vec, bool on16, int sms,
                               cudaStream_t st) {
   if (p.total <= 0 || p.B <= 0) return cudaSuccess;
-  if (cache_dtype == 0) return launch_read_c<float>(p, out_dtype, vec, sms, st);
-  if (cache_dtype == 1) return launch_read_c<__nv_bfloat16>(p, out_dtype, vec, sms, st);
-  if (cache_dtype == 2) return launch_read_c<__half>(p, out_dtype, vec, sms, st);
-  return launch_read_c<__nv_fp8_e4m3>(p, out_dtype, vec, sms, st);
+  if (cache_dtype == 0) return launch_read_c<float>(p, out_dtype, vec, on16, sms, st);
+  if (cache_dtype == 1) return launch_read_c<__nv_bfloat16>(p, out_dtype, vec, on16, sms, st);
+  if (cache_dtype == 2) return launch_read_c<__half>(p, out_dtype, vec, on16, sms, st);
+  return launch_read_c<__nv_fp8_e4m3>(p, out_dtype, vec, on16, sms, st);
 }
 
 // ---------------------------------------------------------------- commit

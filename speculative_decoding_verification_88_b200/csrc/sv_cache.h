@@ -89,11 +89,13 @@ struct AttnParams {
   void* scratch;
 };
 
-// es / cache codes follow sv_dtype.  `vec`: 16-byte vectors may be used.
+// es / cache codes follow sv_dtype.  `vec`: vectors may be used: of 16 bytes,
+// or of 8 codes of an 8-bit pool, whose rows need only lie on 8-byte boundaries
+// (`on16`: they lie on 16-byte ones).
 cudaError_t launch_rotate(const RotateParams& p, int dtype, int cache_dtype, bool vec, int sms,
                           cudaStream_t st);
 cudaError_t launch_cache_read(const CacheReadParams& p, int cache_dtype, int out_dtype, bool vec,
-                              int sms, cudaStream_t st);
+                              bool on16, int sms, cudaStream_t st);
 cudaError_t launch_cache_commit(const CacheCommitParams& p, int elem_bytes, bool vec, int sms,
                                 cudaStream_t st);
 cudaError_t launch_attention_plain(const AttnParams& p, int q_dtype, int cache_dtype,

@@ -227,7 +227,7 @@ extern "C" int spec_verify_cache_read(const sv_kv_cache* cache, const int32_t* p
                    pool_on(cache, ces, ces == 1 ? 8 : 16);
   const int n = sms();
   if (n <= 0) return SV_ERR_CUDA;
-  return launch_cache_read(p, cache->dtype, out_dtype, vec, n, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_cache_read(p, cache->dtype, out_dtype, vec, pool_on(cache, ces, 16), n, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? SV_OK
              : SV_ERR_CUDA;
 }
