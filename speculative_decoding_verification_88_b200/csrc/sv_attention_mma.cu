@@ -29,14 +29,21 @@
 // scaled by a power of two a row and written as a sum of two (bfloat16) or
 // three (16-bit floats) 8-bit terms of 4 significant bits each, exact but for
 // elements so small that the step of the smallest codes, 2^-9, counts: half of
-// it, with the largest element at 2^7 or more, is 2^-17 of that one.  The
-// weights likewise, so that they keep 8 or 12 significant bits, no fewer than the output's type.
+// it, with the largest element at 2^7 or more, is 2^-17 of that one.
+// Weights need range as well as bits: behind a token that takes most of the
+// weight, a long context's many small ones make up the rest of the sum.  They
+// are sums of three (bfloat16) or four e5m2 terms of 3 significant bits each,
+// the last one rounded, which is 2^-9 or 2^-12 of a weight at most; the largest
+// is near 2^13 and the smallest step 2^-16, so that the absolute error stays
+// below 2^-28 of the largest weight and scale.  (Two or three e4m3 terms, whose
+// smallest step is 2^-9 under 2^6, took 143 us instead of 166 for the long
+// chains below and lost such contexts: a tenth of the result at 4000 tokens.)
 // An 8-bit product of n terms costs n/2 of a 16-bit one, and K and V
 // cross shared memory once, without a widened copy (widening them to 16 bits
 // first, by four warps, bound the kernel by shared memory: 2450 cycles a tile
 // of 128 tokens instead of the 1425 that its 32 KB take from memory).  K's
-// scales multiply S; V's multiply the weights, which a power of two that
-// follows the largest of them keeps in the 8-bit range.
+// scales multiply S; V's multiply the weights, which a power of two a row that
+// follows the largest scale the row sees keeps in the 8-bit range.
 //
 // What it takes and what bounds it (8 cache heads of 128; calls back to back):
 //   64 trees of 26 nodes, 32 query heads, 700 to 4096 tokens, 16 bits: 143 us,
@@ -69,8 +76,13 @@ constexpr int kScaleRing = kMaxStages;  // most tiles whose scales are held (8-b
 constexpr int kExtra = 3;
 constexpr int kJoinThreads = 512;
 constexpr float kLazy = 8.0f;     // log2 of what a weight may exceed 1 by
-// 8-bit weights: the largest is near 2^6, and at most 2^8.5 < 448.
-constexpr float kBase8 = 6.0f, kLazy8 = 8.5f;
+// 8-bit weights: the largest is near 2^13, and at most 2^15.5 < 57344.
+constexpr float kBase8 = 13.0f, kLazy8 = 15.5f;
+// log2 of the common factor that V's scales put on them.  Beyond these the
+// weights without it (which are summed in 32 bits) would leave that type's
+// range: scales above 2^109 cost the smallest weights, 2^-30 of the largest
+// and more as the scales grow, and scales below 2^-94 the low bits.
+constexpr int kLeastScale = -94, kMostScale = 121;
 
 // Work split shared by the two grids.  An item counts as its tiles and `extra`
 // more at its front, for what a segment costs besides its tiles; of all these
@@ -264,11 +276,12 @@ __device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t lbo) {
   return (addr & 0x3ffffu) >> 4 | (lbo >> 4) << 16;
 }
 constexpr uint32_t kOperandHigh = 1024u >> 4 | 1u << 14 | 2u << 29;
-// f32 accumulator, 16-bit operands (bf16 or f16) or e4m3, M = 128; V is read
-// transposed (its columns are the fast axis).
-__host__ __device__ constexpr uint32_t mma_shape(bool bf16, int n, bool b_transposed) {
-  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) /* f16 and e4m3: 0 */ | (b_transposed ? 1u << 16 : 0u) |
-         static_cast<uint32_t>(n / 8) << 17 | 8u << 24;
+// f32 accumulator, M = 128; V is read transposed (its columns are the fast
+// axis).  Types of A and B: 16 bits f16 0, bf16 1 (both the same); 8 bits
+// e4m3 0, e5m2 1.
+__host__ __device__ constexpr uint32_t mma_shape(uint32_t a_type, uint32_t b_type, int n, bool b_transposed) {
+  return 1u << 4 | a_type << 7 | b_type << 10 | (b_transposed ? 1u << 16 : 0u) | static_cast<uint32_t>(n / 8) << 17 |
+         8u << 24;
 }
 #define SV_MMA(KIND, A, MOVE_A)                                                                                \
   asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t" MOVE_A                  \
@@ -348,9 +361,14 @@ __device__ __forceinline__ uint32_t pack_weights<__half>(float lo, float hi) {
   return d;
 }
 
-// A value's leading 4 significant bits (towards zero): an e4m3 value, where
-// its exponent allows.
+// A value's leading 4 or 3 significant bits (towards zero): an e4m3 or e5m2
+// value, where its exponent allows.
 __device__ __forceinline__ float leading4(float x) { return __uint_as_float(__float_as_uint(x) & 0xfff00000u); }
+__device__ __forceinline__ float leading3(float x) { return __uint_as_float(__float_as_uint(x) & 0xffe00000u); }
+// Two e5m2 codes, rounded to nearest, ties to even, saturating.
+__device__ __forceinline__ uint32_t e5m2_pair(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
+}
 
 // Whether any element of a word is an infinity or a NaN.
 template <typename T, bool E4>
@@ -523,17 +541,12 @@ __device__ __forceinline__ void max_chunk(const uint32_t (&v)[16], float (&top)[
     top[1] = fmax3(top[1], __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
   }
 }
-// Columns of the weights' terms over the scores, of the first or second half of
-// the tokens.  Two row tiles (a row's thread weighs the whole tile): blocks of
-// 32 at 0, 64 and 96.  Else blocks of 16 within each half's 64.
-template <bool TWO>
-__host__ __device__ constexpr uint32_t term_column(int n, int half) {
-  return TWO ? (n > 0 ? 32 + 32 * n : 0) + 16 * half : 64 * half + 16 * n;
-}
-// 16 columns' weights, times V's scales, as TERMS 8-bit terms of 4 columns each.
-template <int TERMS, bool TWO>
+// Weights take the place of their scores: the columns of 32 tokens hold the
+// terms of these one after the other, 8 columns each.
+template <int TERMS>
 __device__ __forceinline__ void weigh_chunk(const uint32_t (&v)[16], const Scales& sc, int col, uint32_t s_addr,
                                             unsigned long long c22, unsigned long long sh2, unsigned long long (&sum)[2]) {
+  // 16 columns' weights, times V's scales, as TERMS 8-bit terms of 4 columns each
   uint32_t out[TERMS][4];
 #pragma unroll
   for (int i = 0; i < 16; i += 4) {
@@ -552,17 +565,17 @@ __device__ __forceinline__ void weigh_chunk(const uint32_t (&v)[16], const Scale
       for (int n = 0; n < TERMS; ++n) {
         unpack2(x, a, b);
         if (n < TERMS - 1) {
-          a = leading4(a), b = leading4(b);
+          a = leading3(a), b = leading3(b);
           x = sub2(x, pack2(a, b));
         }
-        codes[n][z] = e4m3_pair(a, b);
+        codes[n][z] = e5m2_pair(a, b);
       }
     }
 #pragma unroll
     for (int n = 0; n < TERMS; ++n) out[n][i >> 2] = codes[n][0] | codes[n][1] << 16;
   }
 #pragma unroll
-  for (int n = 0; n < TERMS; ++n) tmem_st4(s_addr + term_column<TWO>(n, col / 64) + (col & 63) / 4, out[n]);
+  for (int n = 0; n < TERMS; ++n) tmem_st4(s_addr + (col & ~31) + 8 * n + (col & 16) / 4, out[n]);
 }
 
 // Puts -inf where a column is masked (bit i of word c allows column 32 c + i),
@@ -784,9 +797,10 @@ __global__ void __launch_bounds__(384, 1)
   constexpr bool kHalves = E4 && SPLIT == 1, kTurns = !two && !kHalves;
   constexpr bool kWhole = two || (kTurns && kCopies == 1);  // a thread weighs whole tiles
   constexpr bool kBf16 = !E4 && std::is_same<QT, __nv_bfloat16>::value;
-  constexpr int kTerms = std::is_same<QT, __nv_bfloat16>::value ? 2 : 3;  // 8-bit terms of queries and weights
-  constexpr uint32_t kShapeS = mma_shape(kBf16, kTile, false);
-  constexpr uint32_t kShapeO = mma_shape(kBf16, DP, true);
+  constexpr int kTerms = std::is_same<QT, __nv_bfloat16>::value ? 2 : 3;  // 8-bit terms of queries (e4m3),
+  constexpr int kParts = kTerms + 1;                                      // and of weights (e5m2)
+  constexpr uint32_t kShapeS = mma_shape(kBf16, kBf16, kTile, false);
+  constexpr uint32_t kShapeO = mma_shape(kBf16 || E4, kBf16, DP, true);
 
   // A row tile of queries, and a buffer of an item's (16 bits, or the terms);
   // 8-bit pools: where the queries arrive in 16 bits, and the ring of scales.
@@ -988,8 +1002,8 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                  for (int n = 0; n < kTerms; ++n)
-                    mma_ts<E4>(o, pw + term_column<!kHalves>(n, half) + k * 8, vd + (2 * half + k) * (32 * 128 >> 4), kShapeO,
+                  for (int n = 0; n < kParts; ++n)
+                    mma_ts<E4>(o, pw + 64 * half + 32 * k + 8 * n, vd + (2 * half + k) * (32 * 128 >> 4), kShapeO,
                                add || k > 0 || n > 0);
               } else {
 #pragma unroll
@@ -1185,13 +1199,29 @@ __global__ void __launch_bounds__(384, 1)
           }
           int ve = vexp;
           if (E4 && warp_live) {
-            // the tile's largest finite scale of V, four tokens a lane
+            // The largest finite scale of V among the tokens that this row sees:
+            // of the context four tokens a lane, of the drafted ones its own.
             __syncwarp();
+            const auto finite = [](float y) { return fabsf(y) < INFINITY ? fabsf(y) : 0.0f; };
+            const auto exponent = [](float y) {  // y <= 2^exponent
+              return min(max(static_cast<int>(__float_as_uint(y) >> 23) - 126, kLeastScale), kMostScale);
+            };
             const float4 x = *reinterpret_cast<const float4*>(sc.v + sc.at(lane * 4 & ~7) + (lane * 4 & 4));
-            const float y0 = fabsf(x.x) < INFINITY ? fabsf(x.x) : 0.0f, y1 = fabsf(x.y) < INFINITY ? fabsf(x.y) : 0.0f;
-            const float y2 = fabsf(x.z) < INFINITY ? fabsf(x.z) : 0.0f, y3 = fabsf(x.w) < INFINITY ? fabsf(x.w) : 0.0f;
-            const float vm = warp_max(fmaxf(fmaxf(y0, y1), fmaxf(y2, y3)));
-            ve = max(vexp, min(max(static_cast<int>(__float_as_uint(vm) >> 23) - 126, -60), 100));  // vm <= 2^ve
+            const float y[4] = {finite(x.x), finite(x.y), finite(x.z), finite(x.w)};
+            const int drafted = tail ? static_cast<int>(w.len - tok0) : kTile;  // first column of the tree
+            float old = 0.0f, young = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) (lane * 4 + i < drafted ? old : young) = fmaxf(lane * 4 + i < drafted ? old : young, y[i]);
+            ve = max(vexp, exponent(warp_max(old)));
+            if (tail && exponent(warp_max(young)) > ve) {
+              young = 0.0f;
+#pragma unroll 1
+              for (unsigned long long m = mask; m; m &= m - 1) {
+                const int col = drafted + __ffsll(static_cast<long long>(m)) - 1;
+                if (static_cast<unsigned int>(col) < static_cast<unsigned int>(kTile)) young = fmaxf(young, finite(sc.v[sc.at(col)]));
+              }
+              ve = max(ve, exponent(young));
+            }
           }
           if (!tail) scores();
           __syncwarp();
@@ -1229,8 +1259,7 @@ __global__ void __launch_bounds__(384, 1)
               }
             }
             // Scores that are read once and held: a share of a tile, or with two
-            // row tiles and an 8-bit pool the second half, over which terms of
-            // the weights lie.
+            // row tiles and an 8-bit pool the second half.
             constexpr int kHeld = kWhole ? (E4 ? 4 : 1) : kNC;
             uint32_t held[kHeld][16];
             float top;
@@ -1246,7 +1275,7 @@ __global__ void __launch_bounds__(384, 1)
                   if (c < copy * (4 / kCopies) || c >= (copy + 1) * (4 / kCopies)) {
                     if constexpr (E4) {
 #pragma unroll
-                      for (int n = 0; n < kTerms; ++n) tmem_st8(s_addr + term_column<true>(n, c >> 1) + (c & 1) * 8, none);
+                      for (int n = 0; n < kParts; ++n) tmem_st8(s_addr + c * 32 + n * 8, none);
                     } else {
                       tmem_st16(s_addr + c * 16, none);
                     }
@@ -1329,19 +1358,23 @@ __global__ void __launch_bounds__(384, 1)
             unsigned long long sum[2] = {0ull, 0ull};
             if constexpr (E4) {
               if constexpr (kWhole) {
-#pragma unroll 2
-                for (int c = 0; c < 4; ++c) {
-                  uint32_t v[16];
-                  tmem_ld16(s_addr + c * 16, v);
+#pragma unroll 1
+                for (int c = 0; c < 64; c += 32) {
+                  uint32_t v[2][16];
+                  tmem_ld16(s_addr + c, v[0]);
+                  tmem_ld16(s_addr + c + 16, v[1]);
                   tmem_wait_ld();
-                  scale_chunk(v, sc, c * 16);
-                  weigh_chunk<kTerms, !kHalves>(v, sc, c * 16, s_addr, c22, sh2, sum);
+#pragma unroll
+                  for (int z = 0; z < 2; ++z) {
+                    scale_chunk(v[z], sc, c + z * 16);
+                    weigh_chunk<kParts>(v[z], sc, c + z * 16, s_addr, c22, sh2, sum);
+                  }
                 }
                 hand_over(&s->p_ready[g][0]);
               }
               const int from = kWhole ? 64 : col0;
 #pragma unroll
-              for (int c = 0; c < kHeld; ++c) weigh_chunk<kTerms, !kHalves>(held[c], sc, from + c * 16, s_addr, c22, sh2, sum);
+              for (int c = 0; c < kHeld; ++c) weigh_chunk<kParts>(held[c], sc, from + c * 16, s_addr, c22, sh2, sum);
               l += total2(sum);
             } else if constexpr (!kWhole) {
 #pragma unroll
