@@ -563,8 +563,8 @@ int spec_verify_cache_read_device_status(uint32_t *flags_host, int clear, void *
  * infinities and NaN included.
  * 1 <= N <= 64, Hq a multiple of num_heads, Hq <= 1024, head_dim <= 256,
  * scale finite.  Scores, softmax statistics and sums are held in 32 bits;
- * the weights enter the second product rounded to q's type, or, for an
- * SV_E4M3 pool, as a sum of 8-bit terms: each within u (2^-8 for SV_BF16,
+ * the weights enter the second product rounded to q's type (SV_F16: within
+ * 2^-32 of the row's largest beside that), or, for an SV_E4M3 pool, as a sum of 8-bit terms: each within u (2^-8 for SV_BF16,
  * 2^-11 for SV_F16) of itself plus 2^-28 of the row's largest weight times the
  * largest v_scale it sees, for v_scale from 2^-94 to 2^109 (outside, small
  * weights keep fewer bits).  For such a pool q is a sum of 8-bit terms as

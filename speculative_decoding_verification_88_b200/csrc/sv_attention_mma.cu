@@ -21,10 +21,11 @@
 // The MMA warp issues S of one while the other computes its exponentials.
 // A thread owns one row, so a row's maximum and sum need no shuffles.  The
 // running maximum is only raised when a score exceeds it by 2^8: O is then
-// rescaled in tensor memory; until then weights up to 2^8 are exact enough
-// in 16 bits, and the division by the sum at the end makes up for it.
+// rescaled in tensor memory; until then weights up to 2^8 (2^15 in float16) are
+// exact enough in 16 bits, and the division by the sum at the end makes up for it.
 //
-// Weights enter the second product in the values' 16-bit type.  8-bit pools
+// Weights enter the second product in the values' 16-bit type (float16: the
+// largest near 2^7, so that 2^-32 of it is half of the smallest step).  8-bit pools
 // go into the products as they are, by the 8-bit instructions: queries are
 // scaled by a power of two a row and written as a sum of two (bfloat16) or
 // three (16-bit floats) 8-bit terms of 4 significant bits each, exact but for
@@ -75,7 +76,10 @@ constexpr int kScaleRing = kMaxStages;  // most tiles whose scales are held (8-b
 // them in the split); they count where a block has several tiles.
 constexpr int kExtra = 3;
 constexpr int kJoinThreads = 512;
-constexpr float kLazy = 8.0f;     // log2 of what a weight may exceed 1 by
+// 16-bit weights: log2 of the largest, and of what a weight may exceed it by.
+// 16-bit floats reach 2^15, and below 2^-14 lose bits: with the largest near 1
+// a weight under 2^-25 of it was zero.
+constexpr float kBaseF16 = 7.0f, kLazy = 8.0f;
 // 8-bit weights: the largest is near 2^13, and at most 2^15.5 < 57344.
 constexpr float kBase8 = 13.0f, kLazy8 = 15.5f;
 // log2 of the common factor that V's scales put on them.  Beyond these the
@@ -796,6 +800,7 @@ __global__ void __launch_bounds__(384, 1)
   // Else tiles by turns.
   constexpr bool kHalves = E4 && SPLIT == 1, kTurns = !two && !kHalves;
   constexpr bool kWhole = two || (kTurns && kCopies == 1);  // a thread weighs whole tiles
+  constexpr float kBase = std::is_same<QT, __nv_bfloat16>::value ? 0.0f : kBaseF16;
   constexpr bool kBf16 = !E4 && std::is_same<QT, __nv_bfloat16>::value;
   constexpr int kTerms = std::is_same<QT, __nv_bfloat16>::value ? 2 : 3;  // 8-bit terms of queries (e4m3),
   constexpr int kParts = kTerms + 1;                                      // and of weights (e5m2)
@@ -1325,8 +1330,8 @@ __global__ void __launch_bounds__(384, 1)
               if (__any_sync(0xffffffffu, raise)) Mn = fmaxf(M - vexp + kBase8, top) - kBase8 + ve;
               vexp = ve;
             } else {
-              raise = top > M + kLazy;
-              if (__any_sync(0xffffffffu, raise)) Mn = fmaxf(M, top);
+              raise = top > M + kBase + kLazy;
+              if (__any_sync(0xffffffffu, raise)) Mn = fmaxf(M, top - kBase);
             }
             if (Mn != M) {
               const float f = M == -INFINITY ? 0.0f : ex2f(M - Mn);

@@ -95,6 +95,17 @@ def test_a_token_that_stands_out_over_8_bit_pools(dev, qt, G, N, n, gap, size):
     within(got, want, wabs, floor, score, n, T[qt], "out")
 
 
+@pytest.mark.parametrize("G,N", [(4, 5), (26, 4), (8, 64)])
+@pytest.mark.parametrize("gap", [12.3, 19.7, 25.2])
+def test_a_token_that_stands_out_over_16_bit_floats(dev, G, N, gap):
+    """The largest weight is near 2^7, so the smallest step, 2^-24, is 2^-31 of it."""
+    n, D = 4000, 128
+    cache, table, clen, q, score = sink(n, N, G, D, "fp16", "fp16", gap, 0.0, 100.0, G)
+    want, wabs = attention64(q, cache, table, clen, chain(N))
+    got = sv.tree_attention(q, cache, table, clen)["out"]
+    within(got, want, wabs, n * 2.0 ** -32 * 300.0, score, n, T["fp16"], "out")
+
+
 @pytest.mark.parametrize("qt", ["bf16", "fp16"])
 @pytest.mark.parametrize("G", [1, 2, 7, 10, 20, 40])
 @pytest.mark.parametrize("n", [100, 126, 130, 1000])
