@@ -707,13 +707,19 @@ __device__ __forceinline__ void load_segment(const MmaParams& p, const CUtensorM
         uint32_t w[2];
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
-          float t[4];
+          w[i >> 2] = 0u;
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            t[z] = n == kTerms - 1 ? f[i + z] : leading4(f[i + z]);
-            f[i + z] -= t[z];
+          for (int z = 0; z < 4; z += 2) {
+            float &x = f[i + z], &y = f[i + z + 1];
+            const uint32_t two = n == kTerms - 1 ? e4m3_pair(x, y) : e4m3_pair(leading4(x), leading4(y));
+            w[i >> 2] |= two << (8 * z);
+            // the next terms make up for what this code rounds: below the
+            // smallest normal ones that is more than what leading4 cuts off
+            if (n < kTerms - 1) {
+              const float2 is = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3)));
+              x -= is.x, y -= is.y;
+            }
           }
-          w[i >> 2] = e4m3_pair(t[0], t[1]) | e4m3_pair(t[2], t[3]) << 16;
         }
         if (in) {
 #pragma unroll

@@ -140,3 +140,23 @@ def test_scales_of_v_far_from_one(dev, G, N, power):
     shrink = 2.0 ** -power
     within(got.double() * shrink, want * shrink, wabs * shrink, n * 2.0 ** -28 * 8.0, score_error(q, cache), n, T["bf16"],
            "out")
+
+
+@pytest.mark.parametrize("qt", ["bf16", "fp16"])
+@pytest.mark.parametrize("G", [1, 3, 50, 100, 200])
+def test_small_elements_of_queries_over_8_bit_pools(dev, qt, G):
+    """Each element of q enters within 2^-17 of its row's largest one: here 127
+    that lie between two of the smallest codes, beside one of 2^7."""
+    D, N = 128, 1
+    k = torch.ones(1, 1, D)
+    k[..., 0] = 0.0
+    cache, table, clen = one_sequence(0, N, D, T["e4m3"], k, torch.ones(1, 1, D))
+    q = torch.full((1, 1, G, D), 2.0 ** -7 * (1 + 1 / 8 + 15 / 128))
+    q[..., 0] = 2.0 ** 7
+    scale = 4.0
+    got = sv.tree_attention(q.to(T[qt]).to(dev), cache, table, clen, scale=scale, lse=True)["lse"].double().cpu()
+    row = cache.k.float()[table[0, 0].item(), 0, 0].double().cpu() * cache.k_scale[table[0, 0].item(), 0, 0].double().cpu()
+    want = scale * (q.double() @ row)
+    most = scale * (q.double().abs() @ row.abs())
+    tol = scale * 2.0 ** -17 * 2.0 ** 7 * row.abs().sum() + most * (D + 16) * 2.0 ** -23 + 2.0 ** -20 * (1 + want.abs())
+    assert ((got - want).abs() <= tol).all(), f"{((got - want).abs() / tol).max():.3g} times the bound"
