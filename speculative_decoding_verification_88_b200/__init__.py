@@ -194,7 +194,8 @@ class Workspace:
     def ensure(self, nbytes: int, stream=None):
         if nbytes <= self.nbytes:
             return self
-        self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+        with torch.cuda.stream(stream):  # (None: the current one)
+            self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
         _check(load_library().spec_verify_workspace_init(
             self.buf.data_ptr(), self.buf.numel(), _stream_ptr(stream, self.device)),
             "spec_verify_workspace_init")
@@ -584,29 +585,36 @@ def _launch(fn, what, device, stream, args):
         _check(code, what)
 
 
-def _keep(t, stream):
-    """Memory made on the current stream and used on `stream`."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+def _new(shape, dtype, device, stream, zero=False):
+    """A new tensor of the call's stream.  With `stream`, its memory must come
+    from there too: a block of the current stream may still be read by what that
+    stream has yet to do.  The current one may use the result and drop it."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        made = make(shape, dtype=dtype, device=device)
+    made.record_stream(torch.cuda.current_stream(device))
+    return made
 
 
 def _result(out, key, shape, dtype, device, stream):
     """_out, refusing a caller's tensor on another device."""
-    if out is None:
-        made = torch.empty(shape, dtype=dtype, device=device)
-    else:
-        made = _out(out, key, shape, dtype, device)
-        if made.device != device:
-            raise ValueError(f"out[{key!r}] must be on {device}")
-    return made if stream is None else _keep(made, stream)
+    if out is None or key not in out:
+        return _new(shape, dtype, device, stream)
+    made = _out(out, key, shape, dtype, device)
+    if made.device != device:
+        raise ValueError(f"out[{key!r}] must be on {device}")
+    if stream is not None:
+        made.record_stream(stream)
+    return made
 
 
 def _like(t, stream):
     """A new contiguous tensor of t's shape and type."""
-    made = torch.empty_like(t) if t.is_contiguous() else \
-        torch.empty(t.shape, dtype=t.dtype, device=t.device)
-    return made if stream is None else _keep(made, stream)
+    if stream is None and t.is_contiguous():
+        return torch.empty_like(t)
+    return _new(t.shape, t.dtype, t.device, stream)
 
 
 def _ints(t, shape, device, name):
@@ -842,9 +850,8 @@ def cache_write(cache: KVCache, page_table: torch.Tensor, cache_len: torch.Tenso
         _, qr = _rows(q, None, cache.head_dim, "q", k)
         Hq = q.shape[2]
         if q_out is None:
-            q_out = _like(q, stream)
-            if cnt is not None:
-                q_out.zero_()  # padding rows are left as they were
+            # (padding rows are left as they were)
+            q_out = _like(q, stream) if cnt is None else _new(q.shape, q.dtype, dev, stream, True)
         elif (q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.device != dev or
               not q_out.is_contiguous()):
             raise ValueError("q_out must be a contiguous tensor like q")
@@ -914,9 +921,7 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     if scale is None:
         scale = D ** -0.5
     need = _scratch_bytes(B, N, Hq, cache.num_heads, D)
-    scratch = torch.empty(need or 16, dtype=torch.uint8, device=dev)
-    if stream is not None:
-        _keep(scratch, stream)
+    scratch = _new((need or 16,), torch.uint8, dev, stream)
     _launch(lib.spec_verify_tree_attention, "spec_verify_tree_attention", dev, stream,
             (qr, code_t, cache._c, table, tstride, pages, lens, par, cnt, B, N, Hq, float(scale),
              res["out"].data_ptr(), res["lse"].data_ptr() if lse else None,
@@ -945,7 +950,7 @@ def cache_commit(cache: KVCache, page_table: torch.Tensor, cache_len: torch.Tens
         N = int(result["out_tokens"].shape[1]) if "out_tokens" in result else 64
     table, tstride, pages = _table(page_table, B, dev)
     if new_len is None:
-        new_len = _keep(torch.empty(B, dtype=torch.int32, device=dev), stream)
+        new_len = _new((B,), torch.int32, dev, stream)
     _launch(lib.spec_verify_cache_commit, "spec_verify_cache_commit", dev, stream,
             (cache._c, table, tstride, pages, lens, accepted, path, B, N,
              _ints(new_len, (B,), dev, "new_len"), _status(workspace, stream)))
