@@ -687,8 +687,8 @@ static cudaError_t launch_rotate_t(const RotateParams& p, bool e4, bool vec, int
     for (n.UP = 1; n.UP < n.units;) n.UP <<= 1;
   // As few passes as the block's size allows, with as few idle threads.
   const int rows = p.Hq + (p.write ? 2 * p.c.heads : 0);
-  n.passes = (rows * n.UP + kRotThreads - 1) / kRotThreads;
-  if (n.passes * (kRotThreads / n.UP) < rows) ++n.passes;
+  const int most = kRotThreads / n.UP;  // whole rows that a block has threads for
+  n.passes = (rows + most - 1) / most;
   n.rows = (rows + n.passes - 1) / n.passes;
   n.turn = n.rows > 32 / n.UP ? 32 / n.UP : 0;
   const int threads = (n.rows * n.UP + 31) / 32 * 32;
