@@ -456,7 +456,7 @@ typedef struct {
  * by position * inv_freq[i].  The pair is elements (i, i + rotary_dim/2), or
  * (2i, 2i+1) if `interleaved`; (a, b) -> magnitude (a cos - b sin, b cos +
  * a sin).  inv_freq: rotary_dim/2 doubles on the DEVICE.  Angles are reduced
- * in 64 bits, so far positions turn as exactly as near ones. */
+ * in twice 64 bits, so far positions turn as exactly as near ones. */
 typedef struct {
     const double *inv_freq;
     int rotary_dim; /* even, 2 .. head_dim */

@@ -20,9 +20,10 @@ namespace sv {
 // its threads first has the loads of its (up to four) units in flight, then
 // the block turns position * f into (cos, sin) pairs in shared memory, once
 // for all heads, and then the units are turned and stored.  The angle is
-// reduced as turns in 64 bits (position * f / 2 pi, minus the nearest
-// integer), so it is exact to 1e-10 turns at any 32-bit position; cos and sin
-// then work on a half turn at most.
+// reduced as turns (position * f / 2 pi, minus the nearest integer).  Near
+// position 2^31 that integer has up to 29 bits, so the product is formed as a
+// sum of two 64-bit numbers, and what is left is exact to 2^-53 turns at any
+// 32-bit position; cos and sin then work on a half turn at most.
 //
 // Rows whose parts are multiples of 16 elements on 16-byte boundaries (8-bit
 // pools: 8) move 16 bytes a load (VEC), others one element: rotary 60 against
@@ -189,6 +190,9 @@ struct RotatePlan {
 constexpr int kRotGroup = 16;     // most tokens of a group
 constexpr int kRotAngles = 1024;  // their (cos, sin) pairs: rotary_dim <= 512
 
+// 1 / 2 pi as a sum.
+constexpr double kTurn = 0.15915494309189533577, kTurnLow = -9.839338337591243e-18;
+
 // Places (dst: element offset, -1: none, -2: padding; sdst: the scales') and
 // (cos, sin) of a group of tokens.
 template <bool E4>
@@ -234,8 +238,10 @@ __device__ __forceinline__ void prepare_tokens(const RotateParams& p, const Rota
   if (!p.inv_freq) return;
   for (int i = tid; i < group * half_rd; i += blockDim.x) {
     const int k = quotient(i, n.div_half), f = i - k * half_rd;
-    const double turns = static_cast<double>(pos[k]) * __ldg(p.inv_freq + f) * 0.15915494309189533577;
-    const double half = 2.0 * (turns - rint(turns));
+    const double at = static_cast<double>(pos[k]), freq = __ldg(p.inv_freq + f);
+    const double angle = at * freq, rest = fma(at, freq, -angle);
+    const double turns = angle * kTurn, low = fma(angle, kTurn, -turns) + fma(angle, kTurnLow, rest * kTurn);
+    const double half = 2.0 * ((turns - rint(turns)) + low);
     float s, c;
     sincospif(static_cast<float>(half), &s, &c);
     s = p.inverse ? -s : s;
