@@ -56,7 +56,10 @@ __global__ void __launch_bounds__(128) attention_plain_kernel(const AttnParams p
     o[e] = 0.0f;
   }
   float m = -INFINITY, l = 0.0f;
-  const long long end = bits ? len + nodes : 0;
+  // (tokens past the capacity have no place: no look at each of them)
+  const long long cap = min(static_cast<long long>(p.c.max_pages) * p.c.page_size, 0x7fffffffll);
+  const long long end = bits ? min(len + nodes, cap) : 0;
+  if (threadIdx.x == 0 && i == 0 && h == 0 && nodes > 0 && len + nodes > cap) raise_flag(p.ctrl, kFlagCapacity);
   for (long long t = warp; t < end; t += 4) {
     if (t >= len && !(bits >> (t - len) & 1ull)) continue;
     int page, place;

@@ -160,3 +160,22 @@ def test_small_elements_of_queries_over_8_bit_pools(dev, qt, G):
     most = scale * (q.double().abs() @ row.abs())
     tol = scale * 2.0 ** -17 * 2.0 ** 7 * row.abs().sum() + most * (D + 16) * 2.0 ** -23 + 2.0 ** -20 * (1 + want.abs())
     assert ((got - want).abs() <= tol).all(), f"{((got - want).abs() / tol).max():.3g} times the bound"
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page,D,layout", [(16, 64, "hnd"), (16, 256, "hnd"), (12, 66, "padded")])
+@pytest.mark.parametrize("length", [2 ** 30, 2 ** 31 - 1])
+def test_lengths_past_the_capacity(dev, kv, page, D, layout, length):
+    """They attend to what has a place, and no loop runs past it."""
+    cache, table, clen = make([96], 0, page, 2, D, T[kv], layout)
+    table = table[:, :96 // page].contiguous()
+    q = heads(1, 3, 4, D, T["bf16"], 1)
+    ws = sv.Workspace(dev, 256)
+    clen.fill_(96)
+    want = sv.tree_attention(q, cache, table, clen, lse=True, workspace=ws)
+    assert ws.device_status() == sv.SV_FLAG_CAPACITY
+    clen.fill_(length)
+    got = sv.tree_attention(q, cache, table, clen, lse=True, workspace=ws)
+    assert ws.device_status() == sv.SV_FLAG_CAPACITY
+    assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+    assert torch.isfinite(got["out"]).all()
