@@ -588,12 +588,14 @@ int spec_verify_tree_attention(const sv_rows *q, int q_dtype, const sv_kv_cache 
  * After verification: move the accepted path's cache rows into place, in all
  * layers of the pool, and advance the lengths.  With n = accepted_len[b]
  * (clamped to [0, N-1]), the row at position L + path[b, j] moves to L + j
- * for j = 1..n, and new_len[b] = L + n + 1 (new_len may be cache_len).
+ * for j = 1..n, and new_len[b] = L + n + 1 (new_len may be cache_len or
+ * accepted_len; any other overlap with these or with path is refused).
  * path [B, N] as spec_verify_tree_greedy and spec_verify_tree_stochastic
  * write it; NULL (a chain): nothing moves.  An entry outside [j, N) is not
  * moved (SV_FLAG_INVALID_TREE), nor is one without a place or with an invalid
  * page; new_len stops at the capacity (SV_FLAG_CAPACITY).
- * 1 <= N <= 64.  One launch, two when rows may move and new_len is cache_len.
+ * 1 <= N <= 64.  One launch, two when rows may move and new_len is cache_len
+ * or accepted_len.
  */
 int spec_verify_cache_commit(const sv_kv_cache *cache, const int32_t *page_table,
                              int64_t table_stride, int max_pages, const int32_t *cache_len,

@@ -935,7 +935,7 @@ def cache_commit(cache: KVCache, page_table: torch.Tensor, cache_len: torch.Tens
     """After a verify call: move the accepted path's cache rows, in all layers
     of the pool, from positions cache_len[b] + path[b, j] to cache_len[b] + j,
     and return the new lengths cache_len + accepted_len + 1 (in `new_len`,
-    which may be cache_len).  `result` is what tree_greedy or tree_stochastic
+    which may be cache_len or the result's accepted_len).  `result` is what tree_greedy or tree_stochastic
     returned; results without a path (a chain) only advance the lengths."""
     lib = load_library()
     acc, path = result["accepted_len"], result.get("path")

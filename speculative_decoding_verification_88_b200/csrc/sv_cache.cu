@@ -922,9 +922,9 @@ __global__ void __launch_bounds__(256) cache_commit_kernel(const CacheCommitPara
     if (j == 0) moves = __popc(in[0]) + __popc(in[1]);
   }
   __syncthreads();
-  // When new_len is cache_len, which other blocks may still have to read, the
-  // lengths are written by a grid of their own instead.
-  if (p.new_len != p.cache_len && blockIdx.x == 0 && threadIdx.x == 0) write_len(p, b, n, len);
+  // When new_len is cache_len or accepted_len, which other blocks may still
+  // have to read, the lengths are written by a grid of their own instead.
+  if (!p.apart && blockIdx.x == 0 && threadIdx.x == 0) write_len(p, b, n, len);
   const int per_head = words + (p.c.ks ? 1 : 0);
   const long long items = static_cast<long long>(p.c.layers) * 2 * p.c.heads * per_head;
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < items; i += gridDim.x * 256ll) {
@@ -958,7 +958,7 @@ __global__ void cache_len_kernel(const CacheCommitParams p) {
   dep_enter();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= p.B) return;
-  write_len(p, b, min(max(__ldg(p.accepted + b), 0), p.N - 1), max(0, p.cache_len[b]));
+  write_len(p, b, min(max(p.accepted[b], 0), p.N - 1), max(0, p.cache_len[b]));
 }
 
 cudaError_t launch_cache_commit(const CacheCommitParams& p, int es, bool vec, int sms, cudaStream_t st) {
@@ -976,7 +976,7 @@ cudaError_t launch_cache_commit(const CacheCommitParams& p, int es, bool vec, in
                                                    : wb == 2 ? cache_commit_kernel<uint16_t>
                                                              : cache_commit_kernel<uint8_t>;
     const cudaError_t e = counted(launch_k(SV_PDL >= 2, k, grid, dim3(256), 0, st, p, words, es), 1);
-    if (e != cudaSuccess || p.new_len != p.cache_len) return e;
+    if (e != cudaSuccess || !p.apart) return e;
   }
   return counted(
       launch_k(SV_PDL >= 2, cache_len_kernel, dim3((p.B + 127) / 128), dim3(128), 0, st, p), 1);

@@ -72,6 +72,7 @@ struct CacheCommitParams {
   const int* path;  // nullable
   int B, N;
   int* new_len;
+  bool apart;  // new_len is cache_len or accepted
   Ctrl* ctrl;
 };
 

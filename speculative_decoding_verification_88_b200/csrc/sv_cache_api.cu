@@ -16,6 +16,10 @@ bool type_ok(int dtype, bool f32, bool e4m3) {
   return dtype == SV_BF16 || dtype == SV_F16 || (f32 && dtype == SV_F32) || (e4m3 && dtype == SV_E4M3);
 }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4 * m && y < x + 4 * n;
+}
 bool strides_ok(const sv_rows* r) { return r->stride_b >= 0 && r->stride_n >= 0 && r->stride_h >= 0; }
 // Row starts of a strided tensor all on `bytes` boundaries.
 bool rows_on(const sv_rows* r, int es, int bytes) {
@@ -250,10 +254,15 @@ extern "C" int spec_verify_cache_commit(const sv_kv_cache* cache, const int32_t*
   if (!aligned(cache_len, 4) || !aligned(accepted_len, 4) || !aligned(path, 4) || !aligned(new_len, 4) ||
       !aligned(workspace, 16))
     return SV_ERR_MISALIGNED;
+  const bool apart = new_len == cache_len || new_len == accepted_len;
+  if ((new_len != cache_len && overlap(new_len, B, cache_len, B)) ||
+      (new_len != accepted_len && overlap(new_len, B, accepted_len, B)) ||
+      (path && overlap(new_len, B, path, static_cast<int64_t>(B) * N)))
+    return SV_ERR_INVALID_ARG;
   CacheCommitParams p{};
   p.c = view(cache, page_table, table_stride, max_pages);
   p.cache_len = cache_len, p.accepted = accepted_len, p.path = path;
-  p.B = B, p.N = N, p.new_len = new_len;
+  p.B = B, p.N = N, p.new_len = new_len, p.apart = apart;
   if (const int e = ctrl_of(workspace, &p.ctrl)) return e;
   const int es = bytes_of(cache->dtype);
   const bool vec = cache->head_dim * es % 16 == 0 && pool_on(cache, es, 16);

@@ -225,3 +225,12 @@ def test_bindings_refuse_cpu_tensors():
         sv.Rotary(torch.zeros(32, dtype=torch.float64))
     with pytest.raises(TypeError):
         sv.rotary(t, torch.zeros(2, 16, dtype=torch.int32), None)
+
+
+def test_cache_commit_refuses_overlapping_lengths(lib):
+    """new_len may be cache_len or accepted_len, and overlaps nothing otherwise."""
+    apart = dict(lens=A, acc=A + 64, path=A + 128, new=A + 256)
+    for bad in (dict(new=A + 4), dict(new=A - 4), dict(new=A + 60), dict(new=A + 68), dict(new=A + 128),
+                dict(new=A + 128 + 4 * 5)):
+        assert call(lib, "cache_commit", **{**apart, **bad}) == INVALID, bad
+    assert call(lib, "cache_commit", **{**apart, "new": A + 4, "path": None}) == INVALID
