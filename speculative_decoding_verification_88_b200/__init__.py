@@ -798,12 +798,14 @@ def _table(page_table, B, device):
     return t.data_ptr(), stride[0], shape[1]
 
 
-def _status(workspace, stream):
+def _status(workspace, device, stream):
     """Where a call reports its flags: the workspace, or the device's own word (None)."""
     if workspace is None:
         return None
     if workspace.buf is None:
         workspace.ensure(256, stream)
+    if workspace.buf.device != device:
+        raise ValueError(f"the workspace must be on {device}")
     return workspace.buf.data_ptr()
 
 
@@ -858,7 +860,7 @@ def cache_write(cache: KVCache, page_table: torch.Tensor, cache_len: torch.Tenso
         qo = q_out.data_ptr()
     _launch(lib.spec_verify_cache_write, "spec_verify_cache_write", dev, stream,
             (cache._c, table, tstride, pages, lens, par, cnt, kr, vr, code_t, B, N,
-             None if rope is None else rope._c, qr, Hq, qo, _status(workspace, stream)))
+             None if rope is None else rope._c, qr, Hq, qo, _status(workspace, dev, stream)))
     return q_out
 
 
@@ -883,7 +885,7 @@ def cache_read(cache: KVCache, page_table: torch.Tensor, offsets: torch.Tensor, 
         return res
     _launch(lib.spec_verify_cache_read, "spec_verify_cache_read", dev, stream,
             (cache._c, table, tstride, pages, offs, st0, B, int(total), res["k"].data_ptr(),
-             res["v"].data_ptr(), _TYPES[dtype], _status(workspace, stream)))
+             res["v"].data_ptr(), _TYPES[dtype], _status(workspace, dev, stream)))
     return res
 
 
@@ -925,7 +927,7 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor,
     _launch(lib.spec_verify_tree_attention, "spec_verify_tree_attention", dev, stream,
             (qr, code_t, cache._c, table, tstride, pages, lens, par, cnt, B, N, Hq, float(scale),
              res["out"].data_ptr(), res["lse"].data_ptr() if lse else None,
-             _status(workspace, stream), scratch.data_ptr(), scratch.shape[0]))
+             _status(workspace, dev, stream), scratch.data_ptr(), scratch.shape[0]))
     return res
 
 
@@ -953,5 +955,5 @@ def cache_commit(cache: KVCache, page_table: torch.Tensor, cache_len: torch.Tens
         new_len = _new((B,), torch.int32, dev, stream)
     _launch(lib.spec_verify_cache_commit, "spec_verify_cache_commit", dev, stream,
             (cache._c, table, tstride, pages, lens, accepted, path, B, N,
-             _ints(new_len, (B,), dev, "new_len"), _status(workspace, stream)))
+             _ints(new_len, (B,), dev, "new_len"), _status(workspace, dev, stream)))
     return new_len

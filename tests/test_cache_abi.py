@@ -234,3 +234,13 @@ def test_cache_commit_refuses_overlapping_lengths(lib):
                 dict(new=A + 128 + 4 * 5)):
         assert call(lib, "cache_commit", **{**apart, **bad}) == INVALID, bad
     assert call(lib, "cache_commit", **{**apart, "new": A + 4, "path": None}) == INVALID
+
+
+def test_a_workspace_of_another_device_is_refused():
+    """Kernels write their flags there: only memory of the call's device will do."""
+    class Elsewhere:
+        buf = torch.zeros(256, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        sv._status(Elsewhere, torch.device("cuda:0"), None)
+    assert sv._status(Elsewhere, torch.device("cpu"), None) == Elsewhere.buf.data_ptr()
+    assert sv._status(None, torch.device("cuda:0"), None) is None
