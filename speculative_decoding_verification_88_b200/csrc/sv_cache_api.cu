@@ -1,6 +1,5 @@
 // sv_cache_api.cu -- C ABI of the cache-side calls (include/spec_verify.h):
 // argument validation, frequencies, dispatch and the status word.
-#include <atomic>
 #include <cmath>
 
 #include "spec_verify.h"
@@ -83,17 +82,13 @@ int sms() {
 __device__ Ctrl g_status;
 
 // The control block of a call: the workspace's, or the current device's own.
+// Its address is looked up by every call (on the host, under 0.1 us): one kept
+// from before the device's primary context was reset would be stale.
 int ctrl_of(void* workspace, Ctrl** ctrl) {
   *ctrl = static_cast<Ctrl*>(workspace);
   if (workspace) return SV_OK;
-  static std::atomic<void*> known[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return SV_ERR_CUDA;
-  void* at = dev < 64 ? known[dev].load(std::memory_order_relaxed) : nullptr;
-  if (!at) {
-    if (cudaGetSymbolAddress(&at, g_status) != cudaSuccess || !at) return SV_ERR_CUDA;
-    if (dev < 64) known[dev].store(at, std::memory_order_relaxed);
-  }
+  void* at = nullptr;
+  if (cudaGetSymbolAddress(&at, g_status) != cudaSuccess || !at) return SV_ERR_CUDA;
   *ctrl = static_cast<Ctrl*>(at);
   return SV_OK;
 }
