@@ -582,6 +582,11 @@ __device__ __forceinline__ void weigh_chunk(const uint32_t (&v)[16], const Scale
   for (int n = 0; n < TERMS; ++n) tmem_st4(s_addr + (col & ~31) + 8 * n + (col & 16) / 4, out[n]);
 }
 
+// The root of 2^d, d <= 0, to be multiplied by twice.  The reference of an 8-bit
+// pool's weights follows V's scales, by up to 2^215, and their sum may be as
+// large as 2^126: 2^d alone may be zero when its product with the sum is not.
+__device__ __forceinline__ float half_step(float d) { return ex2f(0.5f * d); }
+
 // Puts -inf where a column is masked (bit i of word c allows column 32 c + i),
 // before the two passes.  8-bit pools: K's scales enter here, so that a scale
 // of a masked column does not matter, and the passes take ones.
@@ -1340,8 +1345,9 @@ __global__ void __launch_bounds__(384, 1)
               if (__any_sync(0xffffffffu, raise)) Mn = fmaxf(M, top - kBase);
             }
             if (Mn != M) {
-              const float f = M == -INFINITY ? 0.0f : ex2f(M - Mn);
+              const float f = M == -INFINITY ? 0.0f : E4 ? half_step(M - Mn) : ex2f(M - Mn);
               l *= f;
+              if (E4) l *= f;
             }
             // the first tile's product overwrites O
             if (t > (kTurns ? 1 : 0) && __any_sync(0xffffffffu, Mn != M)) {
@@ -1429,7 +1435,10 @@ __global__ void __launch_bounds__(384, 1)
           }
 #pragma unroll
           for (int z = 0; z < 2 * kCopies; ++z)
-            if (x[z].y != 0.0f) sum += x[z].y * (x[z].x == top ? 1.0f : ex2f(x[z].x - top));
+            if (x[z].y != 0.0f) {
+              const float f = x[z].x == top ? 1.0f : E4 ? half_step(x[z].x - top) : ex2f(x[z].x - top);
+              sum += (E4 ? x[z].y * f : x[z].y) * f;
+            }
           const float2 x0 = s->ml[0][r], x1 = s->ml[1][r];
           f0 = x0.y == 0.0f ? 0.0f : x0.x == top ? 1.0f : ex2f(x0.x - top);
           f1 = x1.y == 0.0f ? 0.0f : x1.x == top ? 1.0f : ex2f(x1.x - top);
@@ -1541,7 +1550,7 @@ __global__ void __launch_bounds__(384, 1)
 // grid's block j + 1 left in its plan.  The blocks whose boundaries cut one
 // item share its rows' columns (runs of 8), so that each reads about as much
 // as one share wrote.
-template <typename QT, int DP>
+template <typename QT, int DP, bool E4>
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __grid_constant__ MmaParams p) {
   dep_enter();
   const AttnParams& a = p.a;
@@ -1593,16 +1602,19 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
       float top = M;
 #pragma unroll
       for (int z = 0; z < kAhead; ++z) top = fmaxf(top, ml[z].x);
-      const float keep = M == top ? 1.0f : ex2f(M - top);
-      L *= keep;
+      const float step = M == top ? 1.0f : E4 ? half_step(M - top) : ex2f(M - top);
+      const float keep = E4 ? step * step : step;
+      L *= step;
+      if (E4) L *= step;
 #pragma unroll
       for (int x = 0; x < 8; ++x) o[x] = keep == 0.0f ? 0.0f : o[x] * keep;
       M = top;
 #pragma unroll
       for (int z = 0; z < kAhead; ++z) {
         if (ml[z].y == 0.0f) continue;
-        const float f = ml[z].x == M ? 1.0f : ex2f(ml[z].x - M);
-        L = fmaf(ml[z].y, f, L);
+        const float s = ml[z].x == M ? 1.0f : E4 ? half_step(ml[z].x - M) : ex2f(ml[z].x - M);
+        const float f = E4 ? s * s : s;
+        L = fmaf(E4 ? ml[z].y * s : ml[z].y, s, L);
         if (f == 0.0f) continue;
         o[0] = fmaf(y0[z].x, f, o[0]), o[1] = fmaf(y0[z].y, f, o[1]), o[2] = fmaf(y0[z].z, f, o[2]);
         o[3] = fmaf(y0[z].w, f, o[3]), o[4] = fmaf(y1[z].x, f, o[4]), o[5] = fmaf(y1[z].y, f, o[5]);
@@ -1731,7 +1743,7 @@ cudaError_t launch_mma(MmaParams& p, const CUtensorMap (&maps)[5], int grid, cud
                        maps[3], maps[4]),
               1);
   if (e != cudaSuccess || grid < 2) return e;
-  return counted(launch_k(SV_PDL >= 1, attention_join_kernel<QT, DP>, dim3(grid - 1), dim3(kJoinThreads), 0, st, p), 1);
+  return counted(launch_k(SV_PDL >= 1, attention_join_kernel<QT, DP, E4>, dim3(grid - 1), dim3(kJoinThreads), 0, st, p), 1);
 }
 
 template <typename QT, bool E4>

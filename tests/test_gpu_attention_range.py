@@ -179,3 +179,28 @@ def test_lengths_past_the_capacity(dev, kv, page, D, layout, length):
     assert ws.device_status() == sv.SV_FLAG_CAPACITY
     assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
     assert torch.isfinite(got["out"]).all()
+
+
+@pytest.mark.parametrize("G,N", [(4, 2), (12, 4), (100, 1), (8, 64)])
+@pytest.mark.parametrize("n", [250, 1000, 30000])
+@pytest.mark.parametrize("small,large", [(-85, 60), (-40, 90), (-85, 105)])
+def test_scales_of_v_far_from_one_another(dev, G, N, n, small, large):
+    """Tokens whose V is next to nothing beside others' still count in the sum of
+    the weights: every second 128 tokens are 2^(large - small) times the size."""
+    D = 64
+    g = torch.Generator().manual_seed(n)
+    k, v = (torch.randn(n + N, 1, D, generator=g) for _ in range(2))
+    cache, table, clen = one_sequence(n, N, D, T["e4m3"], k, v)
+    power = torch.where(torch.arange(n + N) // 128 % 2 == 0, small, large).double()
+    page = table[0].long()[torch.arange(n + N, device=dev) // cache.page_size]
+    cache.v_scale[page, 0, torch.arange(n + N, device=dev) % cache.page_size] *= (2.0 ** power).float().to(dev)
+    q = heads(1, N, G, D, T["bf16"], 2)
+    want, wabs = attention64(q, cache, table, clen, chain(N))
+    got = sv.tree_attention(q, cache, table, clen, lse=True)
+    within(got["out"].double() * 2.0 ** -large, want * 2.0 ** -large, wabs * 2.0 ** -large, n * 2.0 ** -28 * 8.0,
+           score_error(q, cache), n, T["bf16"], "out")
+    # the sum alone does not depend on V at all
+    cache.v_scale.nan_to_num_().fill_(1.0)
+    alone = sv.tree_attention(q, cache, table, clen, lse=True)["lse"]
+    # each within twice the exponential's and the sums' roundings of 32 bits
+    assert (got["lse"] - alone).abs().max().item() <= 2 * (2.0 ** -20 * (1 + alone.abs().max().item()) + n * 2.0 ** -23)
