@@ -18,8 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libspecverify.so")
-# The same sources built with every global index checked against its buffer
-# (SV_DEBUG_BOUNDS): a violation raises SV_FLAG_BOUNDS instead of an access.
+# The same sources built with every global index of the verify kernels checked
+# against its buffer (SV_DEBUG_BOUNDS): a violation raises SV_FLAG_BOUNDS instead of an access.
 # For tests, in place of a memory checker; never the default library.
 BOUNDS_LIB_PATH = os.path.join(LIB_DIR, "libspecverify_bounds.so")
 

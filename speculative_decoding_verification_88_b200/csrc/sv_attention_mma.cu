@@ -38,7 +38,8 @@
 // is near 2^13 and the smallest step 2^-16, so that the absolute error stays
 // below 2^-28 of the largest weight and scale.  (Two or three e4m3 terms, whose
 // smallest step is 2^-9 under 2^6, took 143 us instead of 166 for the long
-// chains below and lost such contexts: a tenth of the result at 4000 tokens.)
+// chains below, calls in one graph, and lost such contexts: a tenth of the
+// result at 4000 tokens.)
 // An 8-bit product of n terms costs n/2 of a 16-bit one, and K and V
 // cross shared memory once, without a widened copy (widening them to 16 bits
 // first, by four warps, bound the kernel by shared memory: 2450 cycles a tile
@@ -50,8 +51,8 @@
 //   64 trees of 26 nodes, 32 query heads, 700 to 4096 tokens, 16 bits: 143 us,
 //     4.6 TB/s of K and V: memory, and the blocks' ends (106 to 124 us) and
 //     the joining grid (7 us) behind it;
-//   2 chains of 5, 64 query heads, 125,000 tokens, 8 bits: 168 us, 3.2 TB/s:
-//     the turns of the products (1024 cycles a tile) and the softmax, 2050
+//   2 chains of 5, 64 query heads, 125,000 tokens, 8 bits: 191 us, 2.8 TB/s:
+//     the turns of the products (1280 cycles a tile) and the softmax, 2600
 //     cycles a tile in all;
 //   8 trees of 64, 64 query heads, 3750 tokens, 16 bits: 85 us, 0.69 PFLOP/s:
 //     the same turns (twice 1024 cycles of 3800 a tile), and joining (11 us).
@@ -806,8 +807,8 @@ __global__ void __launch_bounds__(384, 1)
   constexpr int kCopies = two ? 1 : SPLIT;
   // How the softmax warpgroups share the tiles.  Two row tiles: each its rows of
   // every tile.  8-bit pools with 65 to 128 rows: each half of every tile's
-  // tokens, with an output of its own (104 rows: 160 us for 184 with tiles by
-  // turns; 40 rows in two copies 157 for 142, 16 bits the same either way).
+  // tokens, with an output of its own (104 rows: 186 us for 204 with tiles by
+  // turns; 40 rows 276 for 179 as two copies by turns; 16 bits the same either way).
   // Else tiles by turns.
   constexpr bool kHalves = E4 && SPLIT == 1, kTurns = !two && !kHalves;
   constexpr bool kWhole = two || (kTurns && kCopies == 1);  // a thread weighs whole tiles
@@ -1790,8 +1791,8 @@ cudaError_t launch_attention_mma(const AttnParams& a, int q_dtype, int cache_dty
   p.zero = a.c2 == 0.0f;
   p.a.c2 = p.zero ? 1.0f : a.c2 < 0.0f ? -a.c2 : a.c2;
   // Few rows: copies of them share a tile's columns.  Two 125,000-token
-  // sequences, 20 rows (us, 1 / 2 / 4 copies): 8 bits 207 / 132 / 130, 64
-  // sequences 155 / 116 / 108; 16 bits 170 / 160 / 161.
+  // sequences, 20 rows (us, 1 / 2 / 4 copies): 8 bits 277 / 170 / 152, 64
+  // sequences 175 / 134 / 117; 16 bits 170 / 160 / 161.
   p.split = p.R <= 32 && cache_dtype == 3 ? 4 : p.R <= 64 ? 2 : p.R <= kTile ? 1 : 0;
   CUtensorMap maps[5] = {};
   bool ok = pool_map(&maps[0], a.c, a.c.k, cache_dtype, p.box, p.head_first) &&

@@ -874,7 +874,7 @@ cudaError_t launch_cache_read(const CacheReadParams& p, int cache_dtype, int out
 // time.  Row j only receives from rows after j, so a row is always read before
 // it is overwritten (those of one four are read before any of them is
 // written), and no two threads touch the same bytes.  64 paths of up to 8
-// nodes in 32 layers: 17 us, with single elements 57.
+// nodes in 32 layers: 18 us, with single elements 57.
 
 __device__ __forceinline__ void write_len(const CacheCommitParams& p, int b, int n, long long len) {
   const long long end = len + n + 1;

@@ -25,10 +25,11 @@ constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.442695040888963407f;
 
 // ------------------------------------------------------------ bounds checks
-// A build with SV_DEBUG_BOUNDS defined checks every global index the kernels
-// form (logit offsets of each chunk and gather, workspace slots, tokens,
-// outputs) against the extent of its buffer.  A violation raises
-// kFlagBounds in the status word, records the first offending source line in
+// A build with SV_DEBUG_BOUNDS defined checks every global index that the
+// verify kernels form (logit offsets of each chunk and gather, workspace slots,
+// tokens, outputs) against the extent of its buffer; the cache-side kernels
+// check pages and places against the pool and its table in every build, and
+// nothing more in this one.  A violation raises kFlagBounds in the status word, records the first offending source line in
 // the control block's first spare word, and the access is skipped, so that an
 // index error shows up as a status bit rather than a fault.  Release builds
 // compile every check to `true`.
