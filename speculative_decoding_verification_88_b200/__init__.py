@@ -194,8 +194,7 @@ class Workspace:
     def ensure(self, nbytes: int, stream=None):
         if nbytes <= self.nbytes:
             return self
-        with torch.cuda.stream(stream):  # (None: the current one)
-            self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+        self.buf = _new((max(nbytes, 256),), torch.uint8, self.device, stream)
         _check(load_library().spec_verify_workspace_init(
             self.buf.data_ptr(), self.buf.numel(), _stream_ptr(stream, self.device)),
             "spec_verify_workspace_init")

@@ -108,3 +108,58 @@ def test_results_of_another_stream_may_be_dropped_while_read(dev):
     more = [sv.rotary(q * 2, pos, rope, stream=other) for _ in range(4)]
     torch.cuda.synchronize()
     assert torch.equal(kept, want) and len(more) == 4
+
+
+def test_a_captured_step_with_a_second_stream(dev):
+    """A graph whose calls run on a stream forked from the captured one, replayed
+    on new contents, gives what eager calls give."""
+    B, N = 2, 6
+    cache, table, clen = make([90, 17], 64, 16, 2, 64, T["e4m3"])
+    twin = sv.KVCache(*(x.clone() for x in (cache.k, cache.v, cache.k_scale, cache.v_scale)))
+    q, k, v = (heads(B, N, h, 64, T["bf16"], h) for h in (4, 2, 2))
+    count = torch.tensor([6, 3], dtype=torch.int32, device=dev)
+    parent = trees(B, N, 1)
+    rope = sv.rotary_frequencies(64, device=dev)
+    other = torch.cuda.Stream()
+
+    def step(c, stream):
+        turned = sv.cache_write(c, table, clen, k, v, parent=parent, count=count, rope=rope, q=q, stream=stream)
+        got = sv.tree_attention(turned, c, table, clen, parent, count=count, lse=True, stream=stream)
+        return turned, got["out"], got["lse"]
+
+    step(twin, None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        other.wait_stream(torch.cuda.current_stream())
+        outs = step(cache, other)
+        torch.cuda.current_stream().wait_stream(other)
+        total = outs[1].float().sum()
+    for s in range(4):
+        q.copy_(heads(B, N, 4, 64, T["bf16"], 10 + s))
+        k.copy_(heads(B, N, 2, 64, T["bf16"], 20 + s))
+        count.copy_(torch.tensor([s + 1, 6 - s], dtype=torch.int32))
+        graph.replay()
+        want = step(twin, None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        assert torch.equal(total, want[1].float().sum())
+
+
+def test_a_workspace_that_grows_while_two_streams_use_it(dev):
+    """The buffer that a larger one replaces is not handed out before both the
+    given and the current stream are done with it."""
+    other = torch.cuda.Stream()
+    ws = sv.Workspace(dev)
+    ws.ensure(4096, other)
+    torch.cuda.synchronize()
+    old = ws.buf.data_ptr()
+    ws.buf.fill_(7)
+    kept = torch.zeros_like(ws.buf)
+    torch.cuda._sleep(BUSY)
+    kept.copy_(ws.buf)
+    ws.ensure(1 << 16, other)
+    with torch.cuda.stream(other):
+        more = [torch.zeros(4096, dtype=torch.uint8, device=dev) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert (kept == 7).all() and old not in [t.data_ptr() for t in more]
