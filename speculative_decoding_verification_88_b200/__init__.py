@@ -646,7 +646,8 @@ class KVCache:
     [layers, pages, ...]) of one floating type with any strides but a contiguous
     last axis, the same for both; float8_e4m3fn pools come with float32 scales
     [pages, heads, page_size] (or [layers, ...]).  Page tables are passed to the
-    calls.  `KVCache.empty` allocates one with each head's page contiguous."""
+    calls.  cache_commit moves rows in all layers; the other calls use layer 0
+    (`layer(i)` is another one's pool).  `KVCache.empty` allocates one with each head's page contiguous."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "device", "page_size", "num_heads", "head_dim",
                  "layers", "_c")
